@@ -90,7 +90,9 @@ typedef enum {
     CK_ERR_UNSUPPORTED_DEVICE = 7, /* current device is not compute capability 10.3 */
     CK_ERR_CUDA = 8,               /* a CUDA runtime call or launch failed */
     CK_ERR_TIMEOUT = 9,            /* a device-side wait ran out (ck_poll_device_status) */
-    CK_ERR_INVALID = 10            /* an enum argument has an unknown value */
+    CK_ERR_INVALID = 10,           /* an enum argument has an unknown value (attention: a scale or eps too) */
+    CK_ERR_INDEX = 11              /* a position, slot, page or length on the device was out of range
+                                    * (ck_poll_device_status) */
 } ck_status;
 
 typedef enum { CK_F32 = 0, CK_BF16 = 1 } ck_dtype;
@@ -128,6 +130,13 @@ typedef enum {
      * itself (ck_swiglu_mlp) [P1: Motivation]. */
     CK_WLAYOUT_GEMM_F16_GLU = 5
 } ck_wlayout;
+
+/* Which elements of a head the position rotation pairs (r = rot_dim <= D;
+ * elements r .. D-1 pass through). */
+typedef enum {
+    CK_ROPE_HALF = 0,       /* (x[i], x[i + r/2]), i < r/2 */
+    CK_ROPE_INTERLEAVED = 1 /* (x[2i], x[2i + 1]), i < r/2 */
+} ck_rope_mode;
 
 /* Operations whose workspace size ck_workspace_bytes reports. */
 typedef enum {
@@ -413,10 +422,133 @@ CK_API ck_status ck_packed_gemv_dequant(const int8_t *xq, const float *sx, int64
                                         ck_stream_t stream);
 
 /*
+ * The attention of a block: what runs between the qkv linear and the
+ * attention-out linear.  q, k, v and the outputs are bf16; a token's heads lie
+ * next to each other (D elements each) and tokens are a leading dimension ld*
+ * apart (elements, a multiple of 8, at least heads * D), so the pieces of a
+ * packed qkv projection are passed as pointers into its rows.  Every sum, norm
+ * and softmax statistic is f32.
+ *
+ * Indexes that live on the device (positions, slots, pages, lengths) are
+ * checked where they are used: one out of range is never followed; it records
+ * CK_ERR_INDEX in the device status word (ck_poll_device_status), and what the
+ * entry point's comment says happens to the rows it concerns.
+ */
+
+/*
+ * RMS norm of every query and key head, then the position rotation, in one
+ * pass.  For a head's row x (D elements):
+ *   y[d] = x[d] * rsqrt(mean(x^2) + eps) * w[d]         (w NULL: y = x)
+ *   (y[a], y[b]) -> (y[a] c[i] - y[b] s[i], y[b] c[i] + y[a] s[i])
+ * over the pairs (a, b) of `mode`, c[i] = cos_sin[pos, i], s[i] =
+ * cos_sin[pos, rot_dim/2 + i], pos = positions[token]; f32 throughout, rounded
+ * once.
+ *   q, k      : bf16, T tokens of Hq / Hk heads; k NULL with Hk = 0: q alone.
+ *   wq, wk    : [D] of type wdt (f32 or bf16), NULL: no norm of that side.
+ *   cos_sin   : f32 [max_pos, rot_dim], NULL with rot_dim = 0: no rotation
+ *               (positions is then not read and may be NULL).
+ *   q_out, k_out : bf16, leading dimensions ldqo / ldko; q_out may be q with
+ *               ldqo = ldq (in place), likewise k_out; otherwise an output
+ *               must not overlap an input.
+ * D a multiple of 16 up to 256, rot_dim a multiple of 16 up to D.  A token
+ * whose position is out of [0, max_pos) records CK_ERR_INDEX and is not
+ * written.  Errors: CK_ERR_NULL, CK_ERR_SHAPE, CK_ERR_DTYPE (wdt),
+ * CK_ERR_INVALID (mode; eps negative or not finite), CK_ERR_ALIGN,
+ * CK_ERR_UNSUPPORTED_DEVICE, CK_ERR_CUDA.
+ */
+CK_API ck_status ck_qk_norm_rope(const void *q, int64_t ldq, int64_t Hq, const void *wq,
+                                 const void *k, int64_t ldk, int64_t Hk, const void *wk,
+                                 ck_dtype wdt, int64_t T, int64_t D, float eps,
+                                 const float *cos_sin, int64_t max_pos, int64_t rot_dim,
+                                 ck_rope_mode mode, const int32_t *positions, void *q_out,
+                                 int64_t ldqo, void *k_out, int64_t ldko, ck_stream_t stream);
+
+/*
+ * Append T tokens' keys and values to a paged cache, the keys normed and
+ * rotated on the way (as ck_qk_norm_rope; wk NULL: no norm, cos_sin NULL with
+ * rot_dim 0: no rotation).
+ *   k_cache, v_cache : bf16 [pages, Hkv, page_size, D] (a page holds each
+ *               head's page_size rows next to each other).
+ *   slots     : int64 [T], page * page_size + row of each token; a negative
+ *               slot skips the token (padding).  Two tokens of one call must
+ *               not name the same slot.
+ * page_size 1 .. 65536.  A slot past the cache or a position out of range
+ * records CK_ERR_INDEX and that token is not written.  Errors as
+ * ck_qk_norm_rope.
+ */
+CK_API ck_status ck_kv_append(const void *k, int64_t ldk, const void *v, int64_t ldv, int64_t T,
+                              int64_t Hkv, int64_t D, const void *wk, ck_dtype wdt, float eps,
+                              const float *cos_sin, int64_t max_pos, int64_t rot_dim,
+                              ck_rope_mode mode, const int32_t *positions, const int64_t *slots,
+                              void *k_cache, void *v_cache, int64_t pages, int64_t page_size,
+                              ck_stream_t stream);
+
+/*
+ * Attention of B sequences that share a prefix, over a paged cache.  Sequence
+ * b has Lq query tokens, the last Lq of its own seq_lens[b] cached tokens
+ * (their keys and values appended before the call).  Query token i of b sees
+ * the whole prefix and its own tokens 0 .. seq_lens[b] - Lq + i:
+ *   out = sum_j softmax_j(scale * q . k_j) v_j     (no key seen: out = 0).
+ * The prefix is read once for the rows of all sequences together; its result
+ * and each sequence's own are joined by their softmax statistics.
+ *   q, out    : bf16, B * Lq tokens of Hq heads (ldq, ldo); Hq = G * Hkv,
+ *               G <= 128, query heads G h .. G h + G - 1 read key head h.
+ *   k_cache, v_cache : as ck_kv_append; page_size 16, 32, 64 or 128; at most
+ *               2^31 - 1 rows (pages * Hkv * page_size).
+ *   prefix_pages : int32 [ceil(prefix_len / page_size)], NULL when prefix_len
+ *               is 0; rows past prefix_len in its last page are not read as keys.
+ *   block_table : int32 [B, table_stride], row b the pages of sequence b's own
+ *               tokens (entries past its length are not read); NULL when
+ *               max_seq_len is 0.
+ *   seq_lens  : int32 [B], each at most max_seq_len; NULL when that is 0.
+ *   scale     : > 0 and finite.
+ *   ws        : ck_prefix_attention_workspace_bytes(...) bytes.
+ * D is 64 or 128.  What cached rows past a length hold is of no consequence
+ * (NaN among it).  A length out of [0, max_seq_len] is taken as the nearer
+ * end, a page out of [0, pages) as rows of zeros, and either records
+ * CK_ERR_INDEX.  Errors: CK_ERR_NULL, CK_ERR_SHAPE, CK_ERR_INVALID (scale),
+ * CK_ERR_ALIGN, CK_ERR_WORKSPACE, CK_ERR_UNSUPPORTED_DEVICE, CK_ERR_CUDA.
+ */
+CK_API ck_status ck_prefix_attention(const void *q, int64_t ldq, int64_t B, int64_t Lq, int64_t Hq,
+                                     int64_t Hkv, int64_t D, const void *k_cache,
+                                     const void *v_cache, int64_t pages, int64_t page_size,
+                                     const int32_t *prefix_pages, int64_t prefix_len,
+                                     const int32_t *block_table, int64_t table_stride,
+                                     const int32_t *seq_lens, int64_t max_seq_len, float scale,
+                                     void *out, int64_t ldo, void *ws, size_t ws_bytes,
+                                     ck_stream_t stream);
+/* Workspace bytes of that call (0 for sizes that it refuses). */
+CK_API size_t ck_prefix_attention_workspace_bytes(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv,
+                                                  int64_t D, int64_t prefix_len,
+                                                  int64_t max_seq_len);
+
+/*
+ * Cross attention: Lq query tokens of each of B sequences against the Lk
+ * states of an encoder (text states of an image block, an encoder-decoder's
+ * decode step), of which the first kv_lens[b] are real:
+ *   out = sum_{j < kv_lens[b]} softmax_j(scale * q . k_j) v_j   (0 if none).
+ *   q, out    : bf16, B * Lq tokens of Hq heads (ldq, ldo), as above.
+ *   k, v      : bf16, B * Lk tokens of Hkv heads (ldk, ldv); Lk may be 0.
+ *   kv_lens   : int32 [B], NULL: Lk for all.  A length out of [0, Lk] is taken
+ *               as the nearer end and records CK_ERR_INDEX.
+ * D is 64 or 128.  What padded states hold is of no consequence.  Errors as
+ * ck_prefix_attention.
+ */
+CK_API ck_status ck_cross_attention(const void *q, int64_t ldq, const void *k, int64_t ldk,
+                                    const void *v, int64_t ldv, int64_t B, int64_t Lq, int64_t Lk,
+                                    int64_t Hq, int64_t Hkv, int64_t D, const int32_t *kv_lens,
+                                    float scale, void *out, int64_t ldo, void *ws, size_t ws_bytes,
+                                    ck_stream_t stream);
+/* Workspace bytes of that call (0 where it needs none). */
+CK_API size_t ck_cross_attention_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq,
+                                                 int64_t Hkv, int64_t D);
+
+/*
  * Synchronizes `stream`, then reads and clears the device status word that
  * bounded device-side waits write.  Returns CK_OK, CK_ERR_TIMEOUT (a kernel
- * gave up waiting and finished early; its outputs are not valid) or
- * CK_ERR_CUDA (the synchronization itself failed).
+ * gave up waiting and finished early; its outputs are not valid),
+ * CK_ERR_INDEX (a device-side index was out of range) or CK_ERR_CUDA (the
+ * synchronization itself failed).
  */
 CK_API ck_status ck_poll_device_status(ck_stream_t stream);
 

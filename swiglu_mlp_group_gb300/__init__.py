@@ -1,4 +1,5 @@
-"""GB300 (sm_103a) ConvRot INT8 W8A8 linear, fused SwiGLU MLP and small-M GEMV.
+"""GB300 (sm_103a) ConvRot INT8 W8A8 linear, fused SwiGLU MLP, small-M GEMV and the
+attention between a block's qkv and output projections.
 
 Python binding of the C ABI in ``include/ck.h`` (library ``libck_gb300.so``).
 The ``ck_*`` functions below are the C entry points themselves (ctypes); the
@@ -24,7 +25,7 @@ __all__ = [
     "CkError", "lib", "library_path", "build",
     "CK_OK", "CK_ERR_NULL", "CK_ERR_SHAPE", "CK_ERR_DTYPE", "CK_ERR_GROUP", "CK_ERR_ALIGN",
     "CK_ERR_WORKSPACE", "CK_ERR_UNSUPPORTED_DEVICE", "CK_ERR_CUDA", "CK_ERR_TIMEOUT",
-    "CK_ERR_INVALID", "CK_F32", "CK_BF16", "CK_ACT_NONE", "CK_ACT_SWIGLU",
+    "CK_ERR_INVALID", "CK_ERR_INDEX", "CK_ROPE_HALF", "CK_ROPE_INTERLEAVED", "CK_F32", "CK_BF16", "CK_ACT_NONE", "CK_ACT_SWIGLU",
     "CK_WLAYOUT_ROWMAJOR_I8", "CK_WLAYOUT_GEMM_F16", "CK_WLAYOUT_GEMV_PACKED",
     "CK_WLAYOUT_GEMV_PACKED_W6", "CK_WLAYOUT_GEMV_PACKED_W4", "CK_WLAYOUT_GEMM_F16_GLU",
     "GEMV_LAYOUT_OF_BITS",
@@ -32,12 +33,17 @@ __all__ = [
     "quantize_weight", "rotate_quantize_act", "prepare_weight", "int8_linear", "swiglu_mlp",
     "gemv_smallM", "quantize_weight_bits", "packed_gemv_dequant", "debug_int8_gemm_s32", "poll_device_status", "set_wait_timeout_ns",
     "set_launch_overlap", "debug_stalled_wait", "workspace_bytes",
+    "qk_norm_rope", "kv_append", "prefix_attention", "prefix_attention_workspace", "cross_attention",
+    "cross_attention_workspace",
 ]
 
 # ck_status
 CK_OK, CK_ERR_NULL, CK_ERR_SHAPE, CK_ERR_DTYPE, CK_ERR_GROUP, CK_ERR_ALIGN = 0, 1, 2, 3, 4, 5
 CK_ERR_WORKSPACE, CK_ERR_UNSUPPORTED_DEVICE, CK_ERR_CUDA, CK_ERR_TIMEOUT, CK_ERR_INVALID = (
     6, 7, 8, 9, 10)
+CK_ERR_INDEX = 11
+# ck_rope_mode
+CK_ROPE_HALF, CK_ROPE_INTERLEAVED = 0, 1
 # ck_dtype, ck_input_act, ck_wlayout, ck_op
 CK_F32, CK_BF16 = 0, 1
 CK_ACT_NONE, CK_ACT_SWIGLU = 0, 1
@@ -48,6 +54,7 @@ GEMV_LAYOUT_OF_BITS = {8: CK_WLAYOUT_GEMV_PACKED, 6: CK_WLAYOUT_GEMV_PACKED_W6,
                        4: CK_WLAYOUT_GEMV_PACKED_W4}
 CK_OP_INT8_LINEAR, CK_OP_SWIGLU_MLP, CK_OP_GEMV_SMALLM, CK_OP_DEBUG_GEMM_S32 = 0, 1, 2, 3
 
+_ROPES = {"half": CK_ROPE_HALF, "interleaved": CK_ROPE_INTERLEAVED}
 _ACTS = {"none": CK_ACT_NONE, "swiglu": CK_ACT_SWIGLU}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -55,6 +62,7 @@ _lock = threading.Lock()
 _lib = None
 
 _i64, _vp, _sz, _int = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+_f32 = ctypes.c_float
 # name -> (restype, argtypes), in the order of include/ck.h
 _SIGNATURES = {
     "ck_status_string": (ctypes.c_char_p, [_int]),
@@ -80,6 +88,16 @@ _SIGNATURES = {
     "ck_packed_gemv_smallM": (_int, [_vp, _i64, _i64, _i64, _int, _vp, _int, _i64, _int, _vp, _vp,
                                      _vp, _vp, _sz, _vp]),
     "ck_packed_gemv_dequant": (_int, [_vp, _vp, _i64, _i64, _vp, _int, _i64, _vp, _vp, _vp, _vp]),
+    "ck_qk_norm_rope": (_int, [_vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _int, _i64, _i64, _f32, _vp,
+                               _i64, _i64, _int, _vp, _vp, _i64, _vp, _i64, _vp]),
+    "ck_kv_append": (_int, [_vp, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _int, _f32, _vp, _i64, _i64,
+                            _int, _vp, _vp, _vp, _vp, _i64, _i64, _vp]),
+    "ck_prefix_attention": (_int, [_vp, _i64, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _vp,
+                                   _i64, _vp, _i64, _vp, _i64, _f32, _vp, _i64, _vp, _sz, _vp]),
+    "ck_prefix_attention_workspace_bytes": (_sz, [_i64] * 7),
+    "ck_cross_attention": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _i64, _i64, _i64,
+                                  _vp, _f32, _vp, _i64, _vp, _sz, _vp]),
+    "ck_cross_attention_workspace_bytes": (_sz, [_i64] * 6),
     "ck_poll_device_status": (_int, [_vp]),
     "ck_set_wait_timeout_ns": (None, [ctypes.c_uint64]),
     "ck_set_launch_overlap": (None, [_int]),
@@ -399,6 +417,205 @@ def packed_gemv_dequant(xq, sx, Wpacked, wlayout: int, N: int, bias=None, out=No
     return y
 
 
+# ---------------------------------------------------------------------------
+# attention
+# ---------------------------------------------------------------------------
+
+def _token_stride(x, what: str) -> int:
+    """Elements from one token of x ([..., heads, D] bf16 on the GPU) to the next: its heads lie next to
+    each other, its tokens at one stride throughout."""
+    torch = _torch()
+    if x.dtype != torch.bfloat16 or not x.is_cuda:
+        raise ValueError(f"{what} must be a bf16 CUDA tensor")
+    H, D = x.shape[-2], x.shape[-1]
+    st = x.stride()
+    ld = H * D if x.shape[-3] == 1 else st[-3]
+    if x.dim() == 4:
+        if x.shape[1] == 1:
+            ld = H * D if x.shape[0] == 1 else st[0]
+        elif x.shape[0] > 1 and st[0] != x.shape[1] * ld:
+            raise ValueError(f"{what}: tokens must lie at one stride over batch and length")
+    if (D > 1 and st[-1] != 1) or (H > 1 and st[-2] != D):
+        raise ValueError(f"{what}: the heads of a token must lie next to each other")
+    return ld
+
+
+def _typed(t, dtype, what: str, shape=None):
+    """Data pointer of an optional contiguous CUDA tensor of the given type (and shape)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous CUDA tensor of {dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{what} must have shape {shape}, not {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _new(shape, dtype, like, stream):
+    """A new tensor that belongs to the stream the call runs on."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _rotation(cos_sin, positions, T: int, mode: str):
+    """(table pointer, max_pos, rot_dim, mode, positions pointer) of the rotation arguments."""
+    torch = _torch()
+    if mode not in _ROPES:
+        raise ValueError("mode must be 'half' or 'interleaved'")
+    if cos_sin is None:
+        return None, 0, 0, _ROPES[mode], None
+    if positions is None:
+        raise ValueError("a rotation needs positions")
+    return (_typed(cos_sin, torch.float32, "cos_sin"), cos_sin.shape[0], cos_sin.shape[1], _ROPES[mode],
+            _typed(positions, torch.int32, "positions", (T,)))
+
+
+def _norm_weights(D: int, **ws):
+    """(ck_dtype, pointers...) of optional norm weights [D], one type for all."""
+    torch = _torch()
+    types = {w.dtype for w in ws.values() if w is not None}
+    if len(types) > 1 or not types <= {torch.float32, torch.bfloat16}:
+        raise ValueError("norm weights must be f32 or bf16, one type for all")
+    dt = torch.float32 if types == {torch.float32} else torch.bfloat16
+    return (CK_F32 if dt == torch.float32 else CK_BF16,
+            *(_typed(w, dt, name, (D,)) for name, w in ws.items()))
+
+
+def qk_norm_rope(q, k, cos_sin=None, positions=None, wq=None, wk=None, eps: float = 1e-6,
+                 mode: str = "half", q_out=None, k_out=None, stream=None):
+    """RMS norm of each query / key head (where wq / wk is given) and the position rotation
+    (where cos_sin is) in one pass -> (q_out, k_out).
+
+    q [T, Hq, D], k [T, Hk, D] or None, bf16: views of a packed projection's rows will do.  cos_sin f32
+    [max_pos, rot_dim] (cosines, then sines), positions int32 [T].  q_out=q, k_out=k work in place."""
+    torch = _torch()
+    T, Hq, D = q.shape
+    Hk = 0 if k is None else k.shape[1]
+    if k is not None and (k.shape[0] != T or k.shape[2] != D):
+        raise ValueError("q and k must have the same tokens and head size")
+    ldq = _token_stride(q, "q")
+    ldk = _token_stride(k, "k") if k is not None else 0
+    table, max_pos, rot, rope, pos = _rotation(cos_sin, positions, T, mode)
+    wdt, pq, pk = _norm_weights(D, wq=wq, wk=wk)
+    if q_out is None:
+        q_out = _new((T, Hq, D), torch.bfloat16, q, stream)
+    elif q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    if k is not None and k_out is None:
+        k_out = _new((T, Hk, D), torch.bfloat16, q, stream)
+    elif k is not None and k_out.shape != k.shape:
+        raise ValueError("k_out must have k's shape")
+    elif k is None:
+        k_out = None
+    _check(lib().ck_qk_norm_rope(
+        q.data_ptr(), ldq, Hq, pq, _ptr(k), ldk, Hk, pk, wdt, T, D, eps, table, max_pos, rot, rope, pos,
+        q_out.data_ptr(), _token_stride(q_out, "q_out"), _ptr(k_out),
+        _token_stride(k_out, "k_out") if k_out is not None else 0, _stream(stream)), "ck_qk_norm_rope")
+    return q_out, k_out
+
+
+def _cache_shape(k_cache, v_cache):
+    torch = _torch()
+    _typed(k_cache, torch.bfloat16, "k_cache")
+    _typed(v_cache, torch.bfloat16, "v_cache", tuple(k_cache.shape))
+    if k_cache.dim() != 4:
+        raise ValueError("a cache is [pages, Hkv, page_size, D]")
+    return k_cache.shape
+
+
+def kv_append(k, v, k_cache, v_cache, slots, cos_sin=None, positions=None, wk=None, eps: float = 1e-6,
+              mode: str = "half", stream=None) -> None:
+    """Write T tokens' keys (normed where wk is given, rotated where cos_sin is) and values into the
+    pages of a cache.
+
+    k, v [T, Hkv, D] bf16 (views of a packed projection's rows will do); k_cache, v_cache bf16
+    [pages, Hkv, page_size, D]; slots int64 [T] = page * page_size + row, negative: skip the token."""
+    torch = _torch()
+    T, H, D = k.shape
+    pages, Hc, page_size, Dc = _cache_shape(k_cache, v_cache)
+    if v.shape != k.shape or (Hc, Dc) != (H, D):
+        raise ValueError("k, v and the caches must have the same heads and head size")
+    table, max_pos, rot, rope, pos = _rotation(cos_sin, positions, T, mode)
+    wdt, pk = _norm_weights(D, wk=wk)
+    _check(lib().ck_kv_append(
+        k.data_ptr(), _token_stride(k, "k"), v.data_ptr(), _token_stride(v, "v"), T, H, D, pk, wdt, eps,
+        table, max_pos, rot, rope, pos, _typed(slots, torch.int64, "slots", (T,)), k_cache.data_ptr(),
+        v_cache.data_ptr(), pages, page_size, _stream(stream)), "ck_kv_append")
+
+
+def prefix_attention_workspace(q, k_cache, prefix_len: int, max_seq_len: int, stream=None):
+    """A workspace for prefix_attention calls of these sizes (q [B, Lq, Hq, D])."""
+    B, Lq, Hq, D = q.shape
+    n = int(lib().ck_prefix_attention_workspace_bytes(B, Lq, Hq, k_cache.shape[1], D, prefix_len, max_seq_len))
+    return _new((max(n, 16),), _torch().uint8, q, stream)
+
+
+def prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, block_table, seq_lens,
+                     max_seq_len: int, scale: float | None = None, out=None, workspace=None, stream=None):
+    """Attention of B sequences behind a shared prefix over a paged cache -> bf16 [B, Lq, Hq, D].
+
+    q [B, Lq, Hq, D] bf16: the last Lq of each sequence's seq_lens[b] own cached tokens; token i sees the
+    prefix and the own tokens 0 .. seq_lens[b] - Lq + i.  prefix_pages int32 [ceil(prefix_len / page_size)],
+    block_table int32 [B, >= ceil(max_seq_len / page_size)], seq_lens int32 [B].  scale: 1 / sqrt(D) if None."""
+    torch = _torch()
+    B, Lq, Hq, D = q.shape
+    pages, H, page_size, Dc = _cache_shape(k_cache, v_cache)
+    if Dc != D:
+        raise ValueError("q and the caches must have the same head size")
+    ldq = _token_stride(q, "q")
+    pp = _typed(prefix_pages, torch.int32, "prefix_pages")
+    if prefix_len > 0 and (pp is None or prefix_pages.numel() * page_size < prefix_len):
+        raise ValueError("prefix_pages must hold prefix_len tokens")
+    bt = _typed(block_table, torch.int32, "block_table")
+    if max_seq_len > 0 and (bt is None or block_table.dim() != 2 or block_table.shape[0] != B):
+        raise ValueError("block_table must have a row for every sequence")
+    if out is None:
+        out = _new((B, Lq, Hq, D), torch.bfloat16, q, stream)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    ws = workspace if workspace is not None else prefix_attention_workspace(q, k_cache, prefix_len, max_seq_len,
+                                                                            stream)
+    _check(lib().ck_prefix_attention(
+        q.data_ptr(), ldq, B, Lq, Hq, H, D, k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size, pp,
+        prefix_len, bt, block_table.shape[1] if bt is not None else 0,
+        _typed(seq_lens, torch.int32, "seq_lens", (B,)), max_seq_len, D ** -0.5 if scale is None else scale,
+        out.data_ptr(), _token_stride(out, "out"), ws.data_ptr(), ws.numel(), _stream(stream)),
+        "ck_prefix_attention")
+    return out
+
+
+def cross_attention_workspace(q, k, stream=None):
+    """A workspace for cross_attention calls of these sizes (q [B, Lq, Hq, D], k [B, Lk, Hkv, D])."""
+    B, Lq, Hq, D = q.shape
+    n = int(lib().ck_cross_attention_workspace_bytes(B, Lq, k.shape[1], Hq, k.shape[2], D))
+    return _new((max(n, 16),), _torch().uint8, q, stream)
+
+
+def cross_attention(q, k, v, kv_lens=None, scale: float | None = None, out=None, workspace=None, stream=None):
+    """Attention of q [B, Lq, Hq, D] over states k, v [B, Lk, Hkv, D], the first kv_lens[b] (int32 [B];
+    None: all) of them real -> bf16 [B, Lq, Hq, D].  scale: 1 / sqrt(D) if None."""
+    torch = _torch()
+    B, Lq, Hq, D = q.shape
+    if k.shape != v.shape or k.dim() != 4 or k.shape[0] != B or k.shape[3] != D:
+        raise ValueError("k and v must be [B, Lk, Hkv, D] of q's batch and head size")
+    Lk, H = k.shape[1], k.shape[2]
+    if out is None:
+        out = _new((B, Lq, Hq, D), torch.bfloat16, q, stream)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    ws = workspace if workspace is not None else cross_attention_workspace(q, k, stream)
+    ldk, ldv = (_token_stride(k, "k"), _token_stride(v, "v")) if Lk > 0 else (0, 0)
+    _check(lib().ck_cross_attention(
+        q.data_ptr(), _token_stride(q, "q"), _ptr(k), ldk, _ptr(v), ldv, B, Lq, Lk, Hq, H, D,
+        _typed(kv_lens, torch.int32, "kv_lens", (B,)), D ** -0.5 if scale is None else scale,
+        out.data_ptr(), _token_stride(out, "out"), ws.data_ptr(), ws.numel(), _stream(stream)),
+        "ck_cross_attention")
+    return out
+
+
 def debug_int8_gemm_s32(xq, Wq, stream=None):
     """Raw int32 accumulators of the GEMM engine (test hook)."""
     torch = _torch()
@@ -427,7 +644,7 @@ def debug_gemv_s32(xq, Wpacked, wlayout: int, N: int, stream=None):
 
 
 def poll_device_status(stream=None) -> int:
-    """Synchronize the stream; CK_OK or CK_ERR_TIMEOUT from the device status word."""
+    """Synchronize the stream; CK_OK, CK_ERR_TIMEOUT or CK_ERR_INDEX from the device status word."""
     return int(lib().ck_poll_device_status(_stream(stream)))
 
 

@@ -9,6 +9,7 @@
 
 #include "ck.h"
 #include "internal.h"
+#include "ptx.cuh"
 #include "trace.h"
 
 namespace {
@@ -199,6 +200,8 @@ CK_API const char *ck_status_string(ck_status st) {
         case CK_ERR_CUDA: return "CK_ERR_CUDA: a CUDA call or kernel launch failed";
         case CK_ERR_TIMEOUT: return "CK_ERR_TIMEOUT: a device-side wait ran out";
         case CK_ERR_INVALID: return "CK_ERR_INVALID: unknown enum value";
+        case CK_ERR_INDEX:
+            return "CK_ERR_INDEX: a position, slot, page or length on the device was out of range";
     }
     return "unknown ck_status";
 }
@@ -552,7 +555,7 @@ CK_API ck_status ck_poll_device_status(ck_stream_t stream) {
         const unsigned int zero = 0;
         if (cudaMemcpy(status, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
             return CK_ERR_CUDA;
-        return CK_ERR_TIMEOUT;
+        return (v & ck::kDeviceStatusTimeout) ? CK_ERR_TIMEOUT : CK_ERR_INDEX;
     }
     return CK_OK;
 }

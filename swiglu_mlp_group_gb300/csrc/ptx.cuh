@@ -11,6 +11,8 @@ namespace ck {
 
 // Bit set in the device status word when a bounded wait ran out.
 constexpr unsigned int kDeviceStatusTimeout = 1u;
+// Bit set in it when an index read on the device was out of range.
+constexpr unsigned int kDeviceStatusIndex = 2u;
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
