@@ -503,7 +503,7 @@ CK_API ck_status ck_kv_append(const void *k, int64_t ldk, const void *v, int64_t
  *   seq_lens  : int32 [B], each at most max_seq_len; NULL when that is 0.
  *   scale     : > 0 and finite.
  *   ws        : ck_prefix_attention_workspace_bytes(...) bytes.
- * D is 64 or 128.  What cached rows past a length hold is of no consequence
+ * D is 64 or 128; lengths at most 2^30.  What cached rows past a length hold is of no consequence
  * (NaN among it).  A length out of [0, max_seq_len] is taken as the nearer
  * end, a page out of [0, pages) as rows of zeros, and either records
  * CK_ERR_INDEX.  Errors: CK_ERR_NULL, CK_ERR_SHAPE, CK_ERR_INVALID (scale),
@@ -531,7 +531,7 @@ CK_API size_t ck_prefix_attention_workspace_bytes(int64_t B, int64_t Lq, int64_t
  *   k, v      : bf16, B * Lk tokens of Hkv heads (ldk, ldv); Lk may be 0.
  *   kv_lens   : int32 [B], NULL: Lk for all.  A length out of [0, Lk] is taken
  *               as the nearer end and records CK_ERR_INDEX.
- * D is 64 or 128.  What padded states hold is of no consequence.  Errors as
+ * D is 64 or 128; Lk at most 2^30 and B * Lk below 2^31.  What padded states hold is of no consequence.  Errors as
  * ck_prefix_attention.
  */
 CK_API ck_status ck_cross_attention(const void *q, int64_t ldq, const void *k, int64_t ldk,

@@ -1,121 +1,730 @@
 // attention.cu -- attention over a shared prefix and each sequence's own keys
-// (paged), or over an encoder's states (dense): one warp a query row.
+// (paged), or over an encoder's states (dense), on tcgen05.
 //
 //   x_j = scale * q . k_j,   m = max_j x_j,   out = sum_j e^(x_j - m) v_j / sum_j e^(x_j - m)
-// in one pass over the keys: m and the sum are carried, and the sums so far are
-// scaled by e^(m_old - m_new) where m grows.  A lane scores one key of 32, then
-// the warp adds the 32 value rows, each lane its own elements.
+// in one pass over the keys: a running maximum and sum per query row, and an
+// accumulator in TMEM that is scaled where the maximum grows.
+//
+// Rows.  The G query heads of a key head read the same keys, so a tile of 128
+// MMA rows holds 128 / G query tokens x G heads.  Against the prefix the tokens
+// of all sequences are rows of the same product: each prefix key is read once
+// for the whole batch, which is what makes the shared part a matrix product
+// instead of B vector ones.
+//
+// Items.  The work is a list of items -- rows of one key head x a chunk of keys
+// -- that a persistent grid walks with a stride.  More than one row tile makes
+// a wide item: two row tiles against the same key tiles.  Otherwise an item is
+// narrow: one row tile, its key tiles taken alternately by the two halves of
+// the pipeline.  Chunks (and the halves of a narrow item) leave partial sums
+// with their maximum in the workspace; a second kernel joins them.
+//
+// Pipeline (one CTA per SM, 10 warps).  Two streams, each with its own S and O
+// in TMEM and four softmax warps, so that the tensor core works on one while
+// the other is in its softmax:
+//   warps 0..3, 4..7 : softmax of stream 0 / 1, a thread per row: S from TMEM,
+//                      maximum, exponentials, P back to TMEM (over S) as bf16.
+//   warp 8           : TMA: query tiles, and K and V tiles into a ring.
+//   warp 9           : MMA issue: S = Q K^T of step k + 1 ahead of O += P V of
+//                      step k; steps alternate between the streams.
+// P is rounded to bf16 for the second product, the operand type of V; its sum
+// is taken in f32 before that rounding.
 #include <math.h>
 
 #include "attention.h"
 #include "head_norm_rope.cuh"
+#include "launch_util.h"
 #include "ptx.cuh"
 
 namespace ck {
 namespace {
 
-constexpr int kRowsPerBlock = 4;
+constexpr int kRows = 128;     // rows of a query tile
+constexpr int kKeys = 128;     // keys of a key tile
+constexpr int kThreads = 320;  // 8 softmax warps, TMA, MMA
+constexpr int kTmemCols = 512;
+constexpr float kLog2e = 1.4426950408889634f;
+// The accumulator is rescaled only when a row's maximum has grown by more than
+// 2^8: until then its exponentials are taken against the old maximum, at most
+// 256 instead of 1, which f32 sums and bf16's exponent range take unharmed.
+constexpr float kRescaleLog2 = 8.f;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kRowsPerBlock) attention_rows_kernel(const AttentionArgs a) {
-    __shared__ float sq[kRowsPerBlock][D];
+struct Cfg {
+    static constexpr int kHalves = D / 64;         // 128-byte swizzle columns of a tile
+    static constexpr int kHalfBytes = kKeys * 128;
+    static constexpr int kTileBytes = kHalves * kHalfBytes;
+    static constexpr int kSlots = D == 128 ? 5 : 10;  // ring of K and V tiles: 160 KB
+    static constexpr int kBarBytes = 256;
+    static constexpr size_t kSmemBytes = static_cast<size_t>(2 + kSlots) * kTileBytes + kBarBytes + 1024;
+};
+
+// What the kernels take: sizes, pointers and the split of the work.
+struct Work {
+    uint16_t *out;
+    int64_t ldo;
+    int B, Lq, Hkv, G, T;  // T = B * Lq tokens
+    int page_size;         // 0: dense
+    int pages;
+    const int32_t *prefix_pages, *block_table, *lens;
+    int64_t table_stride;
+    int prefix_len, max_len;
+    bool causal;
+    float scale_log2;  // scale * log2(e)
+    // prefix items: rt_p row items x Hkv x split_p chunks; own: rt_o x Hkv x B x split_o
+    int wide_p, wide_o, tok_p, tok_o;  // tok: query tokens of one tile
+    int rt_p, rt_o, chunk_p, chunk_o;  // chunk: keys
+    int items_p, items;
+    int slots_p, slots;                // partial results of a row; slots = 0: written to out directly
+    float *part_o;                     // [slots][T * Hq][D]
+    float2 *part_ml;                   // [slots][T * Hq]: log2-scaled maximum, sum
+    unsigned int *status;
+    unsigned long long timeout_ns;
+};
+
+struct Item {
+    int b;             // sequence; -1: prefix
+    int h;             // key head
+    int tok0, tok_end; // its query tokens
+    int tok;           // tokens of one tile
+    int key0, nkeys;   // its keys
+    int lim0, lim_step;  // token t sees the keys below lim0 + lim_step * t
+    int slot;
+    bool wide;
+};
+
+// The length of sequence b; out of range: the nearer end (`bad` is set).
+__device__ __forceinline__ int own_len(const Work &w, int b, bool &bad) {
+    if (!w.lens) return w.max_len;
+    const int n = w.lens[b];
+    bad = n < 0 || n > w.max_len;
+    return min(max(n, 0), w.max_len);
+}
+
+__device__ __forceinline__ Item decode(const Work &w, int idx, bool &bad_len) {
+    Item it;
+    bad_len = false;
+    if (idx < w.items_p) {
+        const int rt = idx % w.rt_p;
+        int r = idx / w.rt_p;
+        it.h = r % w.Hkv;
+        r /= w.Hkv;
+        it.b = -1;
+        it.wide = w.wide_p;
+        it.tok = w.tok_p;
+        it.tok0 = rt * it.tok * (it.wide ? 2 : 1);
+        it.tok_end = min(w.T, it.tok0 + it.tok * (it.wide ? 2 : 1));
+        it.key0 = r * w.chunk_p;
+        it.nkeys = min(w.chunk_p, w.prefix_len - it.key0);
+        it.lim0 = w.prefix_len, it.lim_step = 0;
+        it.slot = it.wide ? r : 2 * r;
+    } else {
+        idx -= w.items_p;
+        const int rt = idx % w.rt_o;
+        int r = idx / w.rt_o;
+        it.h = r % w.Hkv;
+        r /= w.Hkv;
+        it.b = r % w.B;
+        r /= w.B;
+        it.wide = w.wide_o;
+        it.tok = w.tok_o;
+        const int first = it.b * w.Lq;
+        it.tok0 = first + rt * it.tok * (it.wide ? 2 : 1);
+        it.tok_end = min(first + w.Lq, it.tok0 + it.tok * (it.wide ? 2 : 1));
+        const int len = own_len(w, it.b, bad_len);
+        it.lim_step = w.causal ? 1 : 0;
+        it.lim0 = w.causal ? len - w.Lq + 1 - first : len;
+        it.key0 = r * w.chunk_o;
+        const int last = min(len, it.lim0 + it.lim_step * (it.tok_end - 1));
+        it.nkeys = max(0, min(w.chunk_o, last - it.key0));
+        it.slot = w.slots_p + (it.wide ? r : 2 * r);
+    }
+    return it;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_constant__ CUtensorMap qmap_o,
+                 const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                 const __grid_constant__ Work w) {
+    using C = Cfg<D>;
+    constexpr int NS = C::kSlots;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_s = smem_u32(smem_raw);
+    const uint32_t pad = (1024u - (raw_s & 1023u)) & 1023u;
+    uint8_t *smem = smem_raw + pad;
+    const uint32_t smem_s = raw_s + pad;
+    auto sQ = [&](int i) { return smem_s + i * C::kTileBytes; };
+    auto sKV = [&](int s) { return smem_s + (2 + s) * C::kTileBytes; };
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + (2 + NS) * C::kTileBytes);
+    const uint32_t bars_s = smem_s + (2 + NS) * C::kTileBytes;
+    auto kv_full = [&](int s) { return bars_s + 8u * s; };
+    auto kv_empty = [&](int s) { return bars_s + 8u * (NS + s); };
+    auto q_full = [&](int i) { return bars_s + 8u * (2 * NS + i); };
+    auto q_empty = [&](int i) { return bars_s + 8u * (2 * NS + 2 + i); };
+    auto s_full = [&](int i) { return bars_s + 8u * (2 * NS + 4 + i); };  // S of a step is in TMEM
+    auto p_full = [&](int i) { return bars_s + 8u * (2 * NS + 6 + i); };  // P of a step is in TMEM
+    auto o_full = [&](int i) { return bars_s + 8u * (2 * NS + 8 + i); };  // its P V is in O
+    const uint32_t done_bar = bars_s + 8u * (2 * NS + 10);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * NS + 11);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    static_assert(8 * (2 * NS + 11) + 8 <= C::kBarBytes);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const WaitCtl ctl{abort_flag, w.status, w.timeout_ns};
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(kv_full(s), 1);
+            mbar_init(kv_empty(s), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full(i), 1);
+            mbar_init(q_empty(i), 1);
+            mbar_init(s_full(i), 1);
+            mbar_init(p_full(i), 4);
+            mbar_init(o_full(i), 1);
+        }
+        mbar_init(done_bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    auto tS = [&](int st) { return tmem + 128u * st; };
+    auto tO = [&](int st) { return tmem + 256u + static_cast<uint32_t>(D) * st; };
     pdl_launch_dependents();
     pdl_wait();
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsPerBlock + warp;
-    if (row >= a.B * a.Lq * a.Hq) return;
-    const int64_t t = row / a.Hq;
-    const int hq = static_cast<int>(row - t * a.Hq), h = hq / a.G;
-    const int64_t b = t / a.Lq, i = t - b * a.Lq;
-    constexpr int E = D / 32;
-    for (int e = 0; e < E; ++e) {
-        const uint32_t u = a.q[t * a.ldq + static_cast<int64_t>(hq) * D + lane * E + e];
-        sq[warp][lane * E + e] = __uint_as_float(u << 16) * a.scale;
-    }
-    __syncwarp();
-    int64_t len = a.max_len;
-    if (a.lens) {
-        len = a.lens[b];
-        if (len < 0 || len > a.max_len) {
-            if (lane == 0) atomicOr(a.status, kDeviceStatusIndex);
-            len = len < 0 ? 0 : a.max_len;
+
+    // Every role walks the same items and key tiles with the same counters:
+    // J, key tiles so far (K in ring position 2 J, V in 2 J + 1); step, S tiles
+    // so far (its parity is the stream); narrow items so far (their query
+    // buffer), and the uses of each query buffer.
+    if (warp == 8) {
+        // ------------------------------------------------------------ TMA
+        uint32_t seq = 0, nar = 0;
+        uint32_t qc[2] = {0, 0};
+        bool ok = true;
+        if (elect_one()) {
+            tma_prefetch_desc(&qmap_p);
+            tma_prefetch_desc(&qmap_o);
+            tma_prefetch_desc(&kmap);
+            tma_prefetch_desc(&vmap);
         }
-    }
-    float m = -INFINITY, l = 0.f, o[E] = {};
-    auto pass = [&](int64_t n, bool prefix) {
-        for (int64_t j0 = 0; j0 < n; j0 += 32) {
-            const int64_t j = j0 + lane;
-            int64_t ko = -1, vo = -1;  // offsets of this lane's key and value row (-1: a row of zeros)
-            if (j < n) {
-                if (a.pages > 0) {
-                    const int32_t page = prefix ? a.prefix_pages[j / a.page_size]
-                                                : a.block_table[b * a.table_stride + j / a.page_size];
-                    if (page >= 0 && page < a.pages)
-                        ko = vo = ((static_cast<int64_t>(page) * a.Hkv + h) * a.page_size + j % a.page_size) * D;
-                    else
-                        atomicOr(a.status, kDeviceStatusIndex);
-                } else {
-                    ko = (b * a.max_len + j) * a.ldk + static_cast<int64_t>(h) * D;
-                    vo = (b * a.max_len + j) * a.ldv + static_cast<int64_t>(h) * D;
-                }
-            }
-            float x = -INFINITY;
-            if (j < n) {
-                x = 0.f;
-                if (ko >= 0)
-                    for (int d = 0; d < D; d += 8) {
-                        float kv[8];
-                        unpack8(*reinterpret_cast<const uint4 *>(a.k + ko + d), kv);
-                        for (int e = 0; e < 8; ++e) x = fmaf(sq[warp][d + e], kv[e], x);
+        __syncwarp();
+        for (int idx = blockIdx.x; idx < w.items && ok; idx += gridDim.x) {
+            bool bad = false;
+            const Item it = decode(w, idx, bad);
+            if (bad && lane == 0) atomicOr(w.status, kDeviceStatusIndex);
+            const int ntiles = (it.nkeys + kKeys - 1) / kKeys;
+            const int32_t *table = it.b < 0 ? w.prefix_pages : w.block_table + it.b * w.table_stride;
+            for (int j = 0; j < ntiles && ok; ++j) {
+                const int key = it.key0 + j * kKeys;
+                const int valid = min(kKeys, it.nkeys - j * kKeys);
+                int npages = 0, row = 0;
+                if (w.page_size > 0) {
+                    npages = (valid + w.page_size - 1) / w.page_size;
+                    if (lane < npages) {
+                        const int page = table[key / w.page_size + lane];
+                        const bool in = page >= 0 && page < w.pages;
+                        if (!in) atomicOr(w.status, kDeviceStatusIndex);
+                        // past the cache's rows: TMA fills zeros
+                        row = ((in ? page : w.pages) * w.Hkv + (in ? it.h : 0)) * w.page_size;
                     }
+                }
+                for (int kv = 0; kv < 2; ++kv) {
+                    const int s = seq % NS;
+                    ok = __all_sync(0xffffffffu, mbar_wait(kv_empty(s), ((seq / NS) & 1) ^ 1, ctl));
+                    if (!ok) break;
+                    const CUtensorMap *map = kv == 0 ? &kmap : &vmap;
+                    if (w.page_size > 0) {
+                        if (elect_one())
+                            mbar_arrive_expect_tx(kv_full(s), npages * w.page_size * 128 * C::kHalves);
+                        __syncwarp();
+                        if (lane < npages) {
+                            for (int hf = 0; hf < C::kHalves; ++hf)
+                                tma_load_2d(sKV(s) + hf * C::kHalfBytes + lane * w.page_size * 128, map, kv_full(s),
+                                            hf * 64, row);
+                        }
+                        __syncwarp();
+                    } else if (elect_one()) {
+                        mbar_arrive_expect_tx(kv_full(s), C::kTileBytes);
+                        for (int hf = 0; hf < C::kHalves; ++hf)
+                            tma_load_2d(sKV(s) + hf * C::kHalfBytes, map, kv_full(s), it.h * D + hf * 64,
+                                        it.b * w.max_len + key);
+                    }
+                    __syncwarp();
+                    ++seq;
+                    if (kv == 0 && j == 0) {
+                        // the item's query tiles, behind its first K tile: the
+                        // buffers are free once the last item's S are done
+                        const CUtensorMap *qm = it.b < 0 ? &qmap_p : &qmap_o;
+                        for (int i = 0; i < (it.wide ? 2 : 1) && ok; ++i) {
+                            const int buf = it.wide ? i : static_cast<int>(nar & 1);
+                            ok = __all_sync(0xffffffffu, mbar_wait(q_empty(buf), (qc[buf] & 1) ^ 1, ctl));
+                            if (!ok) break;
+                            if (elect_one()) {
+                                mbar_arrive_expect_tx(q_full(buf), it.tok * w.G * 128 * C::kHalves);
+                                for (int hf = 0; hf < C::kHalves; ++hf)
+                                    tma_load_3d(sQ(buf) + hf * C::kHalfBytes, qm, q_full(buf), hf * 64, it.h * w.G,
+                                                it.tok0 + i * it.tok);
+                            }
+                            __syncwarp();
+                            ++qc[buf];
+                        }
+                    }
+                }
             }
-            float top = x;
-            for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-            const float m_new = fmaxf(m, top);
-            const float base = m_new == -INFINITY ? 0.f : m_new;
-            const float p = expf(x - base), f = expf(m - base);
-            float sum = p;
-            for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-            l = l * f + sum;
-            m = m_new;
-            for (int e = 0; e < E; ++e) o[e] *= f;
-            for (int s = 0; s < 32 && j0 + s < n; ++s) {
-                const float ps = __shfl_sync(0xffffffffu, p, s);
-                const int64_t at = __shfl_sync(0xffffffffu, vo, s);
-                if (at < 0) continue;
-                for (int e = 0; e < E; ++e) {
-                    const uint32_t u = a.v[at + lane * E + e];
-                    o[e] = fmaf(ps, __uint_as_float(u << 16), o[e]);
+            if (!it.wide && ntiles > 0) ++nar;
+        }
+        if (*abort_flag && elect_one()) {
+            // let the copies still in flight land before the CTA exits
+            for (uint32_t q = seq > NS ? seq - NS : 0; q < seq; ++q)
+                mbar_wait_drain(kv_full(q % NS), (q / NS) & 1, w.timeout_ns, w.status);
+            for (int i = 0; i < 2; ++i)
+                if (qc[i] > 0) mbar_wait_drain(q_full(i), (qc[i] - 1) & 1, w.timeout_ns, w.status);
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ------------------------------------------------------------ MMA
+        constexpr uint32_t idesc_qk = idesc_bf16_f32(kRows, kKeys, false);
+        constexpr uint32_t idesc_pv = idesc_bf16_f32(kRows, D, true);
+        struct Step {
+            int st, vslot, ksteps;
+            uint32_t vparity, pparity;
+            bool first, release;
+        };
+        Step prev{};
+        bool have = false, ok = true;
+        uint32_t J = 0, step = 0, nar = 0;
+        uint32_t qc[2] = {0, 0}, sc[2] = {0, 0};
+        auto pv = [&](const Step &p) {
+            if (!__all_sync(0xffffffffu, mbar_wait(p_full(p.st), p.pparity, ctl))) return false;
+            if (!__all_sync(0xffffffffu, mbar_wait(kv_full(p.vslot), p.vparity, ctl))) return false;
+            tc_fence_after_sync();
+            if (elect_one()) {
+                const uint64_t vd = sdesc_mnmajor_sw128(sKV(p.vslot), C::kHalfBytes);
+                for (int ks = 0; ks < p.ksteps; ++ks)
+                    mma_f16_ts(tO(p.st), tS(p.st) + 8u * ks, vd + 128u * ks, idesc_pv, !p.first || ks > 0 ? 1u : 0u);
+                mma_commit(o_full(p.st));
+                if (p.release) mma_commit(kv_empty(p.vslot));
+            }
+            __syncwarp();
+            return true;
+        };
+        for (int idx = blockIdx.x; idx < w.items && ok; idx += gridDim.x) {
+            bool bad;
+            const Item it = decode(w, idx, bad);
+            const int ntiles = (it.nkeys + kKeys - 1) / kKeys;
+            const int subs = it.wide ? 2 : 1;
+            for (int j = 0; j < ntiles && ok; ++j, ++J) {
+                const int kslot = (2 * J) % NS, vslot = (2 * J + 1) % NS;
+                for (int sub = 0; sub < subs; ++sub, ++step) {
+                    const int st = step & 1;
+                    const int buf = it.wide ? st : static_cast<int>(nar & 1);
+                    ok = __all_sync(0xffffffffu, mbar_wait(kv_full(kslot), (2 * J / NS) & 1, ctl));
+                    if (!ok) break;
+                    if (j == 0) {
+                        ok = __all_sync(0xffffffffu, mbar_wait(q_full(buf), qc[buf] & 1, ctl));
+                        if (!ok) break;
+                        ++qc[buf];
+                    }
+                    tc_fence_after_sync();
+                    if (elect_one()) {
+                        const uint64_t qd = sdesc_kmajor_sw128(sQ(buf)), kd = sdesc_kmajor_sw128(sKV(kslot));
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            const uint32_t off = (ks / 4) * (C::kHalfBytes / 16) + 2u * (ks % 4);
+                            mma_f16_ss(tS(st), qd + off, kd + off, idesc_qk, ks > 0 ? 1u : 0u);
+                        }
+                        mma_commit(s_full(st));
+                        if (sub == subs - 1) mma_commit(kv_empty(kslot));
+                        if (j == ntiles - 1) mma_commit(q_empty(buf));
+                    }
+                    __syncwarp();
+                    if (have) {
+                        ok = pv(prev);
+                        if (!ok) break;
+                    }
+                    const int valid = min(kKeys, it.nkeys - j * kKeys);
+                    prev = Step{st,
+                                vslot,
+                                (valid + 15) / 16,
+                                ((2 * J + 1) / NS) & 1,
+                                sc[st] & 1,
+                                it.wide ? j == 0 : j < 2,
+                                sub == subs - 1};
+                    ++sc[st];
+                    have = true;
+                }
+            }
+            if (!it.wide && ntiles > 0) ++nar;
+        }
+        if (have && ok) pv(prev);
+        // no MMA may be in flight when TMEM is released
+        if (elect_one()) {
+            mma_commit(done_bar);
+            mbar_wait_drain(done_bar, 0, w.timeout_ns, w.status);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax
+        const int st = warp >> 2;
+        const int row = threadIdx.x & 127;
+        const int row_tok = row / w.G, row_g = row - row_tok * w.G;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t ts = tS(st) + lanes, to = tO(st) + lanes;
+        const int Hq = w.Hkv * w.G;
+        const int64_t rows = static_cast<int64_t>(w.T) * Hq;
+        const float c = w.scale_log2;
+        uint32_t J = 0, step = 0, cnt = 0;
+        bool ok = true;
+        for (int idx = blockIdx.x; idx < w.items && ok; idx += gridDim.x) {
+            bool bad;
+            const Item it = decode(w, idx, bad);
+            const int ntiles = (it.nkeys + kKeys - 1) / kKeys;
+            const int tok = it.tok0 + (it.wide ? st * it.tok : 0) + row_tok;
+            const bool live = row_tok < it.tok && tok < it.tok_end;
+            const bool warp_live = __any_sync(0xffffffffu, live);
+            const int limit = it.lim0 + it.lim_step * tok;
+            float mref = -INFINITY, l = 0.f;
+            int done = 0;  // tiles of this stream
+            for (int j = 0; j < ntiles; ++j, ++J) {
+                if (!it.wide) {
+                    if (static_cast<int>(step++ & 1) != st) continue;
+                }
+                ok = __all_sync(0xffffffffu, mbar_wait(s_full(st), cnt & 1, ctl));
+                if (!ok) break;
+                tc_fence_after_sync();
+                const int key = j * kKeys;
+                const int valid = min(kKeys, it.nkeys - key);
+                if (valid & 15) {
+                    // The last 16 keys of P V reach past the real ones: P is 0
+                    // there, but 0 x NaN is not, so those rows of V are cleared.
+                    const uint32_t vseq = 2 * J + 1;
+                    ok = __all_sync(0xffffffffu, mbar_wait(kv_full(vseq % NS), (vseq / NS) & 1, ctl));
+                    if (!ok) break;
+                    const int n = (16 - (valid & 15)) * 8;  // 16-byte pieces of a half
+                    for (int i = row; i < n * C::kHalves; i += 128) {
+                        const int hf = i / n, r = i - hf * n;
+                        *reinterpret_cast<uint4 *>(smem + (2 + vseq % NS) * C::kTileBytes + hf * C::kHalfBytes +
+                                                   valid * 128 + r * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+                if (warp_live) {
+                    const int vis = live ? min(max(limit - it.key0 - key, 0), valid) : 0;
+                    uint32_t sr[4][32];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(ts + 32u * q, sr[q]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_wait_ld(sr[q]);
+                    if (__any_sync(0xffffffffu, vis < kKeys)) {
+#pragma unroll
+                        for (int i = 0; i < kKeys; ++i)
+                            if (i >= vis) sr[i / 32][i % 32] = 0xff800000u;  // -inf
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < kKeys; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(sr[i / 32][i % 32]));
+                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    if (done == 0) {
+                        mref = mt;
+                    } else {
+                        const float m_new = fmaxf(mref, mt);
+                        const bool grow = (m_new - mref) * c > kRescaleLog2;
+                        if (__any_sync(0xffffffffu, grow)) {
+                            const float f = grow ? ex2((mref - m_new) * c) : 1.f;
+                            ok = __all_sync(0xffffffffu, mbar_wait(o_full(st), (cnt - 1) & 1, ctl));
+                            if (!ok) break;
+                            tc_fence_after_sync();
+#pragma unroll
+                            for (int q = 0; q < D / 32; ++q) {
+                                uint32_t o[32];
+                                tmem_ld_32x32b_x32(to + 32u * q, o);
+                                tmem_wait_ld(o);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                tmem_st_32x32b_x32(to + 32u * q, o);
+                            }
+                            l *= f;
+                            if (grow) mref = m_new;
+                        }
+                    }
+                    const float mc = mref == -INFINITY ? 0.f : mref * c;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        uint32_t p[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int e = hf * 64 + 2 * i;
+                            const float a = ex2(fmaf(__uint_as_float(sr[e / 32][e % 32]), c, -mc));
+                            const float b = ex2(fmaf(__uint_as_float(sr[e / 32][e % 32 + 1]), c, -mc));
+                            sum[i & 1] += a;
+                            sum[2 + (i & 1)] += b;
+                            p[i] = pack2(a, b);
+                        }
+                        tmem_st_32x32b_x32(ts + 32u * hf, p);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_wait_st();
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(st));
+                ++cnt;
+                ++done;
+            }
+            if (!ok) break;
+            if (it.wide) step += 2 * ntiles;
+            // the item's result
+            if (done > 0) {
+                ok = __all_sync(0xffffffffu, mbar_wait(o_full(st), (cnt - 1) & 1, ctl));
+                if (!ok) break;
+                tc_fence_after_sync();
+            }
+            if (warp_live) {
+                const int64_t at = static_cast<int64_t>(tok) * Hq + it.h * w.G + row_g;
+                if (w.slots > 0) {
+                    const int64_t pr = (it.slot + (it.wide ? 0 : st)) * rows + at;
+                    if (live) w.part_ml[pr] = make_float2(mref == -INFINITY ? mref : mref * c, l);
+                    if (done > 0) {
+#pragma unroll
+                        for (int q = 0; q < D / 32; ++q) {
+                            uint32_t o[32];
+                            tmem_ld_32x32b_x32(to + 32u * q, o);
+                            tmem_wait_ld(o);
+                            if (live) {
+                                uint4 *dst = reinterpret_cast<uint4 *>(w.part_o + pr * D + 32 * q);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            }
+                        }
+                    }
+                } else {
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    uint16_t *dst = w.out + tok * w.ldo + static_cast<int64_t>(it.h * w.G + row_g) * D;
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q) {
+                        uint32_t o[32];
+                        if (done > 0) {
+                            tmem_ld_32x32b_x32(to + 32u * q, o);
+                            tmem_wait_ld(o);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = 0;
+                        }
+                        if (live) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                float x[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[8 * i + e]) * inv;
+                                *reinterpret_cast<uint4 *>(dst + 32 * q + 8 * i) = pack8(x);
+                            }
+                        }
+                    }
                 }
             }
         }
-    };
-    if (a.prefix_len > 0) pass(a.prefix_len, true);
-    int64_t own = a.causal ? len - a.Lq + i + 1 : len;
-    pass(own < 0 ? 0 : own, false);
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    for (int e = 0; e < E; ++e) {
-        const __nv_bfloat16 r = __float2bfloat16_rn(o[e] * inv);
-        a.out[t * a.ldo + static_cast<int64_t>(hq) * D + lane * E + e] = *reinterpret_cast<const uint16_t *>(&r);
     }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over a row's partial
+// results (M their largest m); a warp per row.  Parts with l = 0 saw no key and
+// have no o.
+template <int D>
+__global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ Work w) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int Hq = w.Hkv * w.G;
+    const int64_t rows = static_cast<int64_t>(w.T) * Hq;
+    const int lane = threadIdx.x & 31;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (row >= rows) return;
+    constexpr int E = D / 32;
+    float M = -INFINITY;
+    for (int s = 0; s < w.slots; ++s) {
+        const float2 ml = w.part_ml[s * rows + row];
+        if (ml.y != 0.f) M = fmaxf(M, ml.x);
+    }
+    float L = 0.f, o[E] = {};
+    for (int s = 0; s < w.slots; ++s) {
+        const float2 ml = w.part_ml[s * rows + row];
+        if (ml.y == 0.f) continue;
+        const float f = ex2(ml.x - M);
+        L = fmaf(f, ml.y, L);
+        const float *src = w.part_o + (s * rows + row) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(f, src[e], o[e]);
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const int64_t tok = row / Hq;
+    uint16_t *dst = w.out + tok * w.ldo + (row - tok * Hq) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<uint32_t *>(dst + e) = pack2(o[e] * inv, o[e + 1] * inv);
+}
+
+// Planned for this many SMs whatever the device has, so that the workspace is a
+// function of the sizes alone.
+constexpr int kPlanSms = 152;
+
+int div_up(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+
+// How the work is cut.  Rows come first: two row tiles an item where there are
+// more than one.  Keys are cut where the rows alone leave SMs idle, into at
+// least 4 tiles a chunk (a chunk's partial result costs about as much to write
+// and join as half a key tile to read).
+Work plan(const AttentionArgs &a) {
+    Work w = {};
+    w.B = static_cast<int>(a.B), w.Lq = static_cast<int>(a.Lq), w.T = static_cast<int>(a.B * a.Lq);
+    w.Hkv = a.Hkv, w.G = a.G;
+    w.prefix_len = static_cast<int>(a.prefix_len), w.max_len = static_cast<int>(a.max_len);
+    w.causal = a.causal;
+    const int tokens = kRows / a.G;
+    w.tok_p = w.T < tokens ? w.T : tokens;
+    w.tok_o = w.Lq < tokens ? w.Lq : tokens;
+    w.wide_p = w.T > tokens, w.wide_o = w.Lq > tokens;
+    w.rt_p = div_up(w.T, w.tok_p * (w.wide_p ? 2 : 1));
+    w.rt_o = div_up(w.Lq, w.tok_o * (w.wide_o ? 2 : 1));
+    const int64_t tiles_p = div_up(w.prefix_len, kKeys), tiles_o = div_up(w.max_len, kKeys);
+    const int64_t base_p = static_cast<int64_t>(w.rt_p) * w.Hkv, base_o = static_cast<int64_t>(w.rt_o) * w.Hkv * w.B;
+    // tiles of a chunk: the whole work spread over twice the SMs
+    const int64_t steps = base_p * tiles_p * (w.wide_p ? 2 : 1) + base_o * tiles_o * (w.wide_o ? 2 : 1);
+    const int64_t share = steps / (2 * kPlanSms) + 1;
+    auto chunk = [&](int64_t tiles, bool wide) {
+        int64_t n = wide ? (share + 1) / 2 : share;
+        if (n < 4) n = 4;
+        if (n > tiles) n = tiles;
+        const int64_t parts = (tiles + n - 1) / n;
+        return (tiles + parts - 1) / parts;  // equal parts
+    };
+    int64_t split_p = 0, split_o = 0;
+    if (tiles_p > 0) {
+        const int64_t n = chunk(tiles_p, w.wide_p);
+        w.chunk_p = static_cast<int>(n) * kKeys;
+        split_p = (tiles_p + n - 1) / n;
+    }
+    if (tiles_o > 0) {
+        const int64_t n = chunk(tiles_o, w.wide_o);
+        w.chunk_o = static_cast<int>(n) * kKeys;
+        split_o = (tiles_o + n - 1) / n;
+    }
+    // no key at all: one empty own chunk writes the zeros
+    if (split_p + split_o == 0) split_o = 1, w.chunk_o = kKeys;
+    w.items_p = static_cast<int>(base_p * split_p);
+    w.items = static_cast<int>(w.items_p + base_o * split_o);
+    w.slots_p = static_cast<int>(split_p) * (w.wide_p ? 1 : 2);
+    w.slots = w.slots_p + static_cast<int>(split_o) * (w.wide_o ? 1 : 2);
+    if (w.slots == 1) w.slots_p = w.slots = 0;
+    return w;
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+size_t ml_bytes(const Work &w) { return round256(static_cast<size_t>(w.slots) * w.T * w.Hkv * w.G * sizeof(float2)); }
+
+bool row_map(CUtensorMap *m, const AttentionArgs &a, int tokens) {
+    const uint64_t dims[3] = {static_cast<uint64_t>(a.D), static_cast<uint64_t>(a.Hq),
+                              static_cast<uint64_t>(a.B * a.Lq)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(a.D) * 2, static_cast<uint64_t>(a.ldq) * 2};
+    const uint32_t box[3] = {64, static_cast<uint32_t>(a.G), static_cast<uint32_t>(tokens)};
+    return tensor_map_bf16(m, a.q, 3, dims, strides, box);
+}
+
+bool key_map(CUtensorMap *m, const AttentionArgs &a, const uint16_t *p, int64_t ld) {
+    uint64_t dims[2], strides[1];
+    uint32_t box[2] = {64, kKeys};
+    if (a.pages > 0) {
+        dims[0] = static_cast<uint64_t>(a.D);
+        dims[1] = static_cast<uint64_t>(a.pages * a.Hkv * a.page_size);
+        strides[0] = static_cast<uint64_t>(a.D) * 2;
+        box[1] = static_cast<uint32_t>(a.page_size);
+    } else {
+        dims[0] = static_cast<uint64_t>(a.Hkv) * a.D;
+        dims[1] = static_cast<uint64_t>(a.B * a.max_len);
+        strides[0] = static_cast<uint64_t>(ld) * 2;
+    }
+    return tensor_map_bf16(m, p, 2, dims, strides, box);
+}
+
+template <int D>
+cudaError_t launch(const AttentionArgs &a, Work &w, const LaunchCtx &ctx) {
+    CUtensorMap qp, qo, km, vm;
+    if (!row_map(&qp, a, w.tok_p) || !row_map(&qo, a, w.tok_o)) return cudaErrorInvalidValue;
+    if (a.k) {
+        if (!key_map(&km, a, a.k, a.ldk) || !key_map(&vm, a, a.v, a.ldv)) return cudaErrorInvalidValue;
+    } else {
+        km = vm = qo;  // no key at all: never used
+    }
+    auto kern = attention_kernel<D>;
+    constexpr size_t smem = Cfg<D>::kSmemBytes;
+    if (cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), static_cast<int>(smem));
+        e != cudaSuccess)
+        return e;
+    const int sms = sm_count();
+    if (sms < 1) return cudaErrorInvalidDevice;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(w.items < sms ? w.items : sms));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = ctx.stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = ctx.pdl ? 1 : 0;
+    if (cudaError_t e = cudaLaunchKernelEx(&cfg, kern, qp, qo, km, vm, w); e != cudaSuccess) return e;
+    if (w.slots == 0) return cudaSuccess;
+    const int64_t rows = static_cast<int64_t>(w.T) * w.Hkv * w.G;
+    cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, attention_join_kernel<D>, w);
 }
 
 }  // namespace
 
-size_t attention_workspace_bytes(const AttentionArgs &) { return 0; }
+size_t attention_workspace_bytes(const AttentionArgs &a) {
+    const Work w = plan(a);
+    if (w.slots == 0) return 0;
+    return ml_bytes(w) + static_cast<size_t>(w.slots) * w.T * w.Hkv * w.G * a.D * sizeof(float);
+}
 
 cudaError_t launch_attention(const AttentionArgs &a, const LaunchCtx &ctx) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((a.B * a.Lq * a.Hq + kRowsPerBlock - 1) / kRowsPerBlock));
-    cfg.blockDim = dim3(32 * kRowsPerBlock);
-    cfg.stream = ctx.stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = ctx.pdl ? 1 : 0;
-    return a.D == 64 ? cudaLaunchKernelEx(&cfg, attention_rows_kernel<64>, a)
-                     : cudaLaunchKernelEx(&cfg, attention_rows_kernel<128>, a);
+    Work w = plan(a);
+    w.out = a.out, w.ldo = a.ldo;
+    w.page_size = a.pages > 0 ? a.page_size : 0, w.pages = static_cast<int>(a.pages);
+    w.prefix_pages = a.prefix_pages, w.block_table = a.block_table, w.lens = a.lens, w.table_stride = a.table_stride;
+    w.scale_log2 = a.scale * kLog2e;
+    if (w.slots > 0) {
+        w.part_ml = static_cast<float2 *>(a.ws);
+        w.part_o = reinterpret_cast<float *>(static_cast<char *>(a.ws) + ml_bytes(w));
+    }
+    w.status = ctx.status;
+    w.timeout_ns = ctx.timeout_ns;
+    return a.D == 64 ? launch<64>(a, w, ctx) : launch<128>(a, w, ctx);
 }
 
 }  // namespace ck

@@ -13,6 +13,7 @@ namespace {
 
 constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxHeads = 1 << 16;
+constexpr int64_t kMaxKeys = int64_t{1} << 30;  // longest prefix, sequence or encoder length
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 const uint16_t *bits(const void *p) { return static_cast<const uint16_t *>(p); }
@@ -153,8 +154,8 @@ CK_API ck_status ck_kv_append(const void *k, int64_t ldk, const void *v, int64_t
 
 CK_API size_t ck_prefix_attention_workspace_bytes(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D,
                                                   int64_t prefix_len, int64_t max_seq_len) {
-    if (!attention_sizes(B, Lq, Hq, Hkv, D) || prefix_len < 0 || max_seq_len < 0 || prefix_len > kMaxRows ||
-        max_seq_len > kMaxRows)
+    if (!attention_sizes(B, Lq, Hq, Hkv, D) || prefix_len < 0 || max_seq_len < 0 || prefix_len > kMaxKeys ||
+        max_seq_len > kMaxKeys)
         return 0;
     return ck::attention_workspace_bytes(prefix_sizes(B, Lq, Hq, Hkv, D, prefix_len, max_seq_len));
 }
@@ -174,7 +175,7 @@ CK_API ck_status ck_prefix_attention(const void *q, int64_t ldq, int64_t B, int6
     if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return CK_ERR_SHAPE;
     if (pages < 1 || pages > kMaxRows || pages * page_size > kMaxRows || pages * page_size * Hkv > kMaxRows)
         return CK_ERR_SHAPE;
-    if (prefix_len < 0 || max_seq_len < 0 || prefix_len > kMaxRows || max_seq_len > kMaxRows) return CK_ERR_SHAPE;
+    if (prefix_len < 0 || max_seq_len < 0 || prefix_len > kMaxKeys || max_seq_len > kMaxKeys) return CK_ERR_SHAPE;
     if (max_seq_len > 0 && (table_stride < 1 || table_stride > kMaxRows || max_seq_len > table_stride * page_size))
         return CK_ERR_SHAPE;
     if (!aligned16(q) || !aligned16(out) || !aligned16(k_cache) || !aligned16(v_cache)) return CK_ERR_ALIGN;
@@ -187,7 +188,7 @@ CK_API ck_status ck_prefix_attention(const void *q, int64_t ldq, int64_t B, int6
 
 CK_API size_t ck_cross_attention_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv,
                                                  int64_t D) {
-    if (!attention_sizes(B, Lq, Hq, Hkv, D) || Lk < 0 || Lk > kMaxRows || B * Lk > kMaxRows) return 0;
+    if (!attention_sizes(B, Lq, Hq, Hkv, D) || Lk < 0 || Lk > kMaxKeys || B * Lk > kMaxRows) return 0;
     return ck::attention_workspace_bytes(cross_sizes(B, Lq, Lk, Hq, Hkv, D));
 }
 
@@ -199,7 +200,7 @@ CK_API ck_status ck_cross_attention(const void *q, int64_t ldq, const void *k, i
     if (!q || !out || (Lk > 0 && (!k || !v))) return CK_ERR_NULL;
     if (!(scale > 0.f) || !isfinite(scale)) return CK_ERR_INVALID;
     if (!attention_sizes(B, Lq, Hq, Hkv, D)) return CK_ERR_SHAPE;
-    if (Lk < 0 || Lk > kMaxRows || B * Lk > kMaxRows) return CK_ERR_SHAPE;
+    if (Lk < 0 || Lk > kMaxKeys || B * Lk > kMaxRows) return CK_ERR_SHAPE;
     if (!token_rows(ldq, Hq, D) || !token_rows(ldo, Hq, D)) return CK_ERR_SHAPE;
     if (Lk > 0 && (!token_rows(ldk, Hkv, D) || !token_rows(ldv, Hkv, D))) return CK_ERR_SHAPE;
     if (!aligned16(q) || !aligned16(out) || !aligned16(k) || !aligned16(v)) return CK_ERR_ALIGN;

@@ -203,6 +203,19 @@ bool tensor_map_2d(CUtensorMap *map, const void *ptr, CUtensorMapDataType dtype,
     return true;
 }
 
+bool tensor_map_bf16(CUtensorMap *map, const void *ptr, int rank, const uint64_t *dims,
+                     const uint64_t *strides, const uint32_t *box) {
+    auto encode = encode_fn();
+    if (!encode || rank < 2 || rank > 3) return false;
+    cuuint64_t d[3], st[2];
+    cuuint32_t bx[3], estr[3] = {1, 1, 1};
+    for (int i = 0; i < rank; ++i) d[i] = dims[i], bx[i] = box[i];
+    for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i];
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void *>(ptr),
+                  d, st, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 MapCacheStats map_cache_stats() {
     std::lock_guard<std::mutex> lock(g_map_mu);
     return MapCacheStats{g_map_hits, g_map_misses};

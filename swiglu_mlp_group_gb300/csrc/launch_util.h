@@ -40,6 +40,12 @@ bool tensor_map_2d(CUtensorMap *map, const void *ptr, CUtensorMapDataType dtype,
                    int64_t rows, int64_t cols, int box_cols, int box_rows,
                    CUtensorMapSwizzle swizzle);
 
+// A bf16 tensor map of rank 2 or 3, 128-byte swizzle, out-of-range elements
+// read as zero: dims and box innermost first, strides in bytes of dims 1 ...
+// Encoded on the spot, never cached.
+bool tensor_map_bf16(CUtensorMap *map, const void *ptr, int rank, const uint64_t *dims,
+                     const uint64_t *strides, const uint32_t *box);
+
 // Host-side counters of the map cache (tests and the bench read them).
 struct MapCacheStats {
     uint64_t hits, misses;
