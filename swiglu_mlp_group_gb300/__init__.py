@@ -421,22 +421,26 @@ def packed_gemv_dequant(xq, sx, Wpacked, wlayout: int, N: int, bias=None, out=No
 # attention
 # ---------------------------------------------------------------------------
 
-def _token_stride(x, what: str) -> int:
-    """Elements from one token of x ([..., heads, D] bf16 on the GPU) to the next: its heads lie next to
-    each other, its tokens at one stride throughout."""
-    torch = _torch()
-    if x.dtype != torch.bfloat16 or not x.is_cuda:
+def _token_stride(x, shape, what: str) -> int:
+    """Elements from one token of x (bf16 [..., heads, D] on the GPU, of this shape) to the next: its heads
+    lie next to each other, its tokens at one stride throughout."""
+    if x.dtype is not _torch().bfloat16 or not x.is_cuda:
         raise ValueError(f"{what} must be a bf16 CUDA tensor")
-    H, D = x.shape[-2], x.shape[-1]
     st = x.stride()
-    ld = H * D if x.shape[-3] == 1 else st[-3]
-    if x.dim() == 4:
-        if x.shape[1] == 1:
-            ld = H * D if x.shape[0] == 1 else st[0]
-        elif x.shape[0] > 1 and st[0] != x.shape[1] * ld:
-            raise ValueError(f"{what}: tokens must lie at one stride over batch and length")
-    if (D > 1 and st[-1] != 1) or (H > 1 and st[-2] != D):
+    H, D = shape[-2], shape[-1]
+    ld = H * D
+    if (st[-2] != D and H > 1) or (st[-1] != 1 and D > 1):
         raise ValueError(f"{what}: the heads of a token must lie next to each other")
+    if len(shape) == 4:
+        B, n = shape[0], shape[1]
+        if n > 1:
+            ld = st[1]
+            if B > 1 and st[0] != n * ld:
+                raise ValueError(f"{what}: tokens must lie at one stride over batch and length")
+        elif B > 1:
+            ld = st[0]
+    elif shape[0] > 1:
+        ld = st[0]
     return ld
 
 
@@ -444,11 +448,19 @@ def _typed(t, dtype, what: str, shape=None):
     """Data pointer of an optional contiguous CUDA tensor of the given type (and shape)."""
     if t is None:
         return None
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous CUDA tensor of {dtype}")
-    if shape is not None and tuple(t.shape) != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what} must have shape {shape}, not {tuple(t.shape)}")
     return t.data_ptr()
+
+
+def _run_stream(stream, like) -> int:
+    """The stream a call runs on: the one given, or the current one of like's device (its handle alone:
+    building a Stream object for it takes 3 us of a small call's 10)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(like.get_device())
 
 
 def _new(shape, dtype, like, stream):
@@ -463,25 +475,30 @@ def _new(shape, dtype, like, stream):
 def _rotation(cos_sin, positions, T: int, mode: str):
     """(table pointer, max_pos, rot_dim, mode, positions pointer) of the rotation arguments."""
     torch = _torch()
-    if mode not in _ROPES:
+    rope = _ROPES.get(mode)
+    if rope is None:
         raise ValueError("mode must be 'half' or 'interleaved'")
     if cos_sin is None:
-        return None, 0, 0, _ROPES[mode], None
+        return None, 0, 0, rope, None
     if positions is None:
         raise ValueError("a rotation needs positions")
-    return (_typed(cos_sin, torch.float32, "cos_sin"), cos_sin.shape[0], cos_sin.shape[1], _ROPES[mode],
+    max_pos, rot = cos_sin.shape
+    return (_typed(cos_sin, torch.float32, "cos_sin"), max_pos, rot, rope,
             _typed(positions, torch.int32, "positions", (T,)))
 
 
-def _norm_weights(D: int, **ws):
-    """(ck_dtype, pointers...) of optional norm weights [D], one type for all."""
+def _norm_weight(w, D: int, what: str, dtype):
+    """Data pointer of an optional norm weight [D] of the given type."""
+    return None if w is None else _typed(w, dtype, what, (D,))
+
+
+def _weight_type(*ws):
+    """(torch type, ck_dtype) of optional norm weights: f32 if the first one given is, else bf16."""
     torch = _torch()
-    types = {w.dtype for w in ws.values() if w is not None}
-    if len(types) > 1 or not types <= {torch.float32, torch.bfloat16}:
-        raise ValueError("norm weights must be f32 or bf16, one type for all")
-    dt = torch.float32 if types == {torch.float32} else torch.bfloat16
-    return (CK_F32 if dt == torch.float32 else CK_BF16,
-            *(_typed(w, dt, name, (D,)) for name, w in ws.items()))
+    for w in ws:
+        if w is not None:
+            return (torch.float32, CK_F32) if w.dtype is torch.float32 else (torch.bfloat16, CK_BF16)
+    return torch.bfloat16, CK_BF16
 
 
 def qk_norm_rope(q, k, cos_sin=None, positions=None, wq=None, wk=None, eps: float = 1e-6,
@@ -490,40 +507,51 @@ def qk_norm_rope(q, k, cos_sin=None, positions=None, wq=None, wk=None, eps: floa
     (where cos_sin is) in one pass -> (q_out, k_out).
 
     q [T, Hq, D], k [T, Hk, D] or None, bf16: views of a packed projection's rows will do.  cos_sin f32
-    [max_pos, rot_dim] (cosines, then sines), positions int32 [T].  q_out=q, k_out=k work in place."""
+    [max_pos, rot_dim] (cosines, then sines), positions int32 [T].  wq, wk [D], f32 or bf16 alike.
+    q_out=q, k_out=k work in place."""
     torch = _torch()
-    T, Hq, D = q.shape
-    Hk = 0 if k is None else k.shape[1]
-    if k is not None and (k.shape[0] != T or k.shape[2] != D):
-        raise ValueError("q and k must have the same tokens and head size")
-    ldq = _token_stride(q, "q")
-    ldk = _token_stride(k, "k") if k is not None else 0
+    shape = q.shape
+    T, Hq, D = shape
+    ldq = _token_stride(q, shape, "q")
     table, max_pos, rot, rope, pos = _rotation(cos_sin, positions, T, mode)
-    wdt, pq, pk = _norm_weights(D, wq=wq, wk=wk)
+    dt, wdt = _weight_type(wq, wk)
     if q_out is None:
-        q_out = _new((T, Hq, D), torch.bfloat16, q, stream)
-    elif q_out.shape != q.shape:
+        q_out, ldqo = _new(shape, torch.bfloat16, q, stream), Hq * D
+    elif q_out.shape != shape:
         raise ValueError("q_out must have q's shape")
-    if k is not None and k_out is None:
-        k_out = _new((T, Hk, D), torch.bfloat16, q, stream)
-    elif k is not None and k_out.shape != k.shape:
-        raise ValueError("k_out must have k's shape")
-    elif k is None:
-        k_out = None
-    _check(lib().ck_qk_norm_rope(
-        q.data_ptr(), ldq, Hq, pq, _ptr(k), ldk, Hk, pk, wdt, T, D, eps, table, max_pos, rot, rope, pos,
-        q_out.data_ptr(), _token_stride(q_out, "q_out"), _ptr(k_out),
-        _token_stride(k_out, "k_out") if k_out is not None else 0, _stream(stream)), "ck_qk_norm_rope")
+    else:
+        ldqo = _token_stride(q_out, shape, "q_out")
+    if k is None:
+        k_out = pk = pko = None
+        Hk = ldk = ldko = 0
+    else:
+        kshape = k.shape
+        Hk = kshape[1]
+        if kshape[0] != T or kshape[2] != D:
+            raise ValueError("q and k must have the same tokens and head size")
+        ldk = _token_stride(k, kshape, "k")
+        if k_out is None:
+            k_out, ldko = _new(kshape, torch.bfloat16, q, stream), Hk * D
+        elif k_out.shape != kshape:
+            raise ValueError("k_out must have k's shape")
+        else:
+            ldko = _token_stride(k_out, kshape, "k_out")
+        pk, pko = k.data_ptr(), k_out.data_ptr()
+    st = lib().ck_qk_norm_rope(
+        q.data_ptr(), ldq, Hq, _norm_weight(wq, D, "wq", dt), pk, ldk, Hk, _norm_weight(wk, D, "wk", dt), wdt, T, D,
+        eps, table, max_pos, rot, rope, pos, q_out.data_ptr(), ldqo, pko, ldko, _run_stream(stream, q))
+    if st != CK_OK:
+        raise CkError(st, "ck_qk_norm_rope")
     return q_out, k_out
 
 
-def _cache_shape(k_cache, v_cache):
-    torch = _torch()
-    _typed(k_cache, torch.bfloat16, "k_cache")
-    _typed(v_cache, torch.bfloat16, "v_cache", tuple(k_cache.shape))
-    if k_cache.dim() != 4:
+def _caches(k_cache, v_cache):
+    """(shape, pointers) of a paged cache: contiguous bf16 [pages, Hkv, page_size, D], twice."""
+    bf16 = _torch().bfloat16
+    shape = k_cache.shape
+    if len(shape) != 4:
         raise ValueError("a cache is [pages, Hkv, page_size, D]")
-    return k_cache.shape
+    return shape, _typed(k_cache, bf16, "k_cache"), _typed(v_cache, bf16, "v_cache", shape)
 
 
 def kv_append(k, v, k_cache, v_cache, slots, cos_sin=None, positions=None, wk=None, eps: float = 1e-6,
@@ -533,17 +561,19 @@ def kv_append(k, v, k_cache, v_cache, slots, cos_sin=None, positions=None, wk=No
 
     k, v [T, Hkv, D] bf16 (views of a packed projection's rows will do); k_cache, v_cache bf16
     [pages, Hkv, page_size, D]; slots int64 [T] = page * page_size + row, negative: skip the token."""
-    torch = _torch()
-    T, H, D = k.shape
-    pages, Hc, page_size, Dc = _cache_shape(k_cache, v_cache)
-    if v.shape != k.shape or (Hc, Dc) != (H, D):
+    shape = k.shape
+    T, H, D = shape
+    (pages, Hc, page_size, Dc), pkc, pvc = _caches(k_cache, v_cache)
+    if v.shape != shape or Hc != H or Dc != D:
         raise ValueError("k, v and the caches must have the same heads and head size")
     table, max_pos, rot, rope, pos = _rotation(cos_sin, positions, T, mode)
-    wdt, pk = _norm_weights(D, wk=wk)
-    _check(lib().ck_kv_append(
-        k.data_ptr(), _token_stride(k, "k"), v.data_ptr(), _token_stride(v, "v"), T, H, D, pk, wdt, eps,
-        table, max_pos, rot, rope, pos, _typed(slots, torch.int64, "slots", (T,)), k_cache.data_ptr(),
-        v_cache.data_ptr(), pages, page_size, _stream(stream)), "ck_kv_append")
+    dt, wdt = _weight_type(wk)
+    st = lib().ck_kv_append(
+        k.data_ptr(), _token_stride(k, shape, "k"), v.data_ptr(), _token_stride(v, shape, "v"), T, H, D,
+        _norm_weight(wk, D, "wk", dt), wdt, eps, table, max_pos, rot, rope, pos,
+        _typed(slots, _torch().int64, "slots", (T,)), pkc, pvc, pages, page_size, _run_stream(stream, k))
+    if st != CK_OK:
+        raise CkError(st, "ck_kv_append")
 
 
 def prefix_attention_workspace(q, k_cache, prefix_len: int, max_seq_len: int, stream=None):
@@ -561,29 +591,35 @@ def prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, block_t
     prefix and the own tokens 0 .. seq_lens[b] - Lq + i.  prefix_pages int32 [ceil(prefix_len / page_size)],
     block_table int32 [B, >= ceil(max_seq_len / page_size)], seq_lens int32 [B].  scale: 1 / sqrt(D) if None."""
     torch = _torch()
-    B, Lq, Hq, D = q.shape
-    pages, H, page_size, Dc = _cache_shape(k_cache, v_cache)
+    shape = q.shape
+    B, Lq, Hq, D = shape
+    (pages, H, page_size, Dc), pkc, pvc = _caches(k_cache, v_cache)
     if Dc != D:
         raise ValueError("q and the caches must have the same head size")
-    ldq = _token_stride(q, "q")
-    pp = _typed(prefix_pages, torch.int32, "prefix_pages")
+    ldq = _token_stride(q, shape, "q")
+    i32 = torch.int32
+    pp = _typed(prefix_pages, i32, "prefix_pages")
     if prefix_len > 0 and (pp is None or prefix_pages.numel() * page_size < prefix_len):
         raise ValueError("prefix_pages must hold prefix_len tokens")
-    bt = _typed(block_table, torch.int32, "block_table")
-    if max_seq_len > 0 and (bt is None or block_table.dim() != 2 or block_table.shape[0] != B):
-        raise ValueError("block_table must have a row for every sequence")
+    bt, width = _typed(block_table, i32, "block_table"), 0
+    if bt is not None:
+        if block_table.dim() != 2 or block_table.shape[0] != B:
+            raise ValueError("block_table must have a row for every sequence")
+        width = block_table.shape[1]
     if out is None:
-        out = _new((B, Lq, Hq, D), torch.bfloat16, q, stream)
-    elif out.shape != q.shape:
+        out, ldo = _new(shape, torch.bfloat16, q, stream), Hq * D
+    elif out.shape != shape:
         raise ValueError("out must have q's shape")
+    else:
+        ldo = _token_stride(out, shape, "out")
     ws = workspace if workspace is not None else prefix_attention_workspace(q, k_cache, prefix_len, max_seq_len,
                                                                             stream)
-    _check(lib().ck_prefix_attention(
-        q.data_ptr(), ldq, B, Lq, Hq, H, D, k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size, pp,
-        prefix_len, bt, block_table.shape[1] if bt is not None else 0,
-        _typed(seq_lens, torch.int32, "seq_lens", (B,)), max_seq_len, D ** -0.5 if scale is None else scale,
-        out.data_ptr(), _token_stride(out, "out"), ws.data_ptr(), ws.numel(), _stream(stream)),
-        "ck_prefix_attention")
+    st = lib().ck_prefix_attention(
+        q.data_ptr(), ldq, B, Lq, Hq, H, D, pkc, pvc, pages, page_size, pp, prefix_len, bt, width,
+        _typed(seq_lens, i32, "seq_lens", (B,)), max_seq_len, D ** -0.5 if scale is None else scale,
+        out.data_ptr(), ldo, ws.data_ptr(), ws.numel(), _run_stream(stream, q))
+    if st != CK_OK:
+        raise CkError(st, "ck_prefix_attention")
     return out
 
 
@@ -598,21 +634,26 @@ def cross_attention(q, k, v, kv_lens=None, scale: float | None = None, out=None,
     """Attention of q [B, Lq, Hq, D] over states k, v [B, Lk, Hkv, D], the first kv_lens[b] (int32 [B];
     None: all) of them real -> bf16 [B, Lq, Hq, D].  scale: 1 / sqrt(D) if None."""
     torch = _torch()
-    B, Lq, Hq, D = q.shape
-    if k.shape != v.shape or k.dim() != 4 or k.shape[0] != B or k.shape[3] != D:
+    shape, kshape = q.shape, k.shape
+    B, Lq, Hq, D = shape
+    if v.shape != kshape or len(kshape) != 4 or kshape[0] != B or kshape[3] != D:
         raise ValueError("k and v must be [B, Lk, Hkv, D] of q's batch and head size")
-    Lk, H = k.shape[1], k.shape[2]
+    Lk, H = kshape[1], kshape[2]
+    ldq = _token_stride(q, shape, "q")
+    ldk, ldv = (_token_stride(k, kshape, "k"), _token_stride(v, kshape, "v")) if Lk > 0 else (0, 0)
     if out is None:
-        out = _new((B, Lq, Hq, D), torch.bfloat16, q, stream)
-    elif out.shape != q.shape:
+        out, ldo = _new(shape, torch.bfloat16, q, stream), Hq * D
+    elif out.shape != shape:
         raise ValueError("out must have q's shape")
+    else:
+        ldo = _token_stride(out, shape, "out")
     ws = workspace if workspace is not None else cross_attention_workspace(q, k, stream)
-    ldk, ldv = (_token_stride(k, "k"), _token_stride(v, "v")) if Lk > 0 else (0, 0)
-    _check(lib().ck_cross_attention(
-        q.data_ptr(), _token_stride(q, "q"), _ptr(k), ldk, _ptr(v), ldv, B, Lq, Lk, Hq, H, D,
+    st = lib().ck_cross_attention(
+        q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, B, Lq, Lk, Hq, H, D,
         _typed(kv_lens, torch.int32, "kv_lens", (B,)), D ** -0.5 if scale is None else scale,
-        out.data_ptr(), _token_stride(out, "out"), ws.data_ptr(), ws.numel(), _stream(stream)),
-        "ck_cross_attention")
+        out.data_ptr(), ldo, ws.data_ptr(), ws.numel(), _run_stream(stream, q))
+    if st != CK_OK:
+        raise CkError(st, "ck_cross_attention")
     return out
 
 

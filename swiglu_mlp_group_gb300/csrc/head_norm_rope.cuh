@@ -78,10 +78,11 @@ __device__ __forceinline__ void load_rotation(Rotation &r, const float *row, int
     }
 }
 
-// The group's row x normed (w != null) and rotated in place.  Every lane of
-// the warp calls it; lanes past D / 8 hold zeros.
+// The group's row x normed (where `mine`) and rotated in place.  Every lane of
+// the warp calls it with the same `norm` and `rotate` (the lanes exchange
+// values; rows of one warp may differ in `mine`); lanes past D / 8 hold zeros.
 template <int L, bool INTERLEAVED>
-__device__ __forceinline__ void norm_rotate(float (&x)[8], bool norm, const float (&w)[8], float inv_d,
+__device__ __forceinline__ void norm_rotate(float (&x)[8], bool norm, bool mine, const float (&w)[8], float inv_d,
                                             float eps, bool rotate, const Rotation &r) {
     if (norm) {
         float ss = 0.f;
@@ -91,7 +92,7 @@ __device__ __forceinline__ void norm_rotate(float (&x)[8], bool norm, const floa
         for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, L);
         const float f = rsqrtf(fmaf(ss, inv_d, eps));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = x[j] * f * w[j];
+        for (int j = 0; j < 8; ++j) x[j] = mine ? x[j] * f * w[j] : x[j];
     }
     if (!rotate) return;  // uniform over the grid
     if constexpr (INTERLEAVED) {
