@@ -40,7 +40,10 @@ namespace {
 
 constexpr int kRows = 128;     // rows of a query tile
 constexpr int kKeys = 128;     // keys of a key tile
-constexpr int kThreads = 320;  // 8 softmax warps, TMA, MMA
+constexpr int kThreads = 384;  // 8 softmax warps, TMA, MMA, 2 idle (register shares go by 4 warps)
+// Registers a thread: 168 at launch; the softmax holds a row of 128 scores.
+// 256 x 208 + 128 x 88 = 384 x 168.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 // The accumulator is rescaled only when a row's maximum has grown by more than
@@ -54,7 +57,7 @@ struct Cfg {
     static constexpr int kHalfBytes = kKeys * 128;
     static constexpr int kTileBytes = kHalves * kHalfBytes;
     static constexpr int kSlots = D == 128 ? 5 : 10;  // ring of K and V tiles: 160 KB
-    static constexpr int kBarBytes = 256;
+    static constexpr int kBarBytes = 512;
     static constexpr size_t kSmemBytes = static_cast<size_t>(2 + kSlots) * kTileBytes + kBarBytes + 1024;
 };
 
@@ -147,6 +150,36 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// The largest of 32 scores (keys 32 Q .. of a tile), those from key `vis` on
+// first set to -inf, into four running maxima.
+template <int Q>
+__device__ __forceinline__ void row_max(uint32_t (&x)[32], bool masked, int vis, float (&mx)[4]) {
+    if (masked) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (32 * Q + i >= vis) x[i] = 0xff800000u;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+        mx[i / 2 & 3] = max3(mx[i / 2 & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+}
+
+// P of 32 keys: 2^(x c - mc), added to `sum` in f32 and stored as bf16.
+__device__ __forceinline__ void weights(const uint32_t (&x)[32], float c, float mc, uint64_t (&sum)[2],
+                                        uint32_t taddr) {
+    const uint64_t cc = f32x2(c, c), mm = f32x2(-mc, -mc);
+    uint32_t p[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float a, b;
+        f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), cc, mm), a, b);
+        a = ex2(a), b = ex2(b);
+        sum[i & 1] = add_f32x2(sum[i & 1], f32x2(a, b));
+        p[i] = pack2(a, b);
+    }
+    tmem_st_32x32b_x16(taddr, p);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_constant__ CUtensorMap qmap_o,
@@ -168,12 +201,13 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
     auto q_full = [&](int i) { return bars_s + 8u * (2 * NS + i); };
     auto q_empty = [&](int i) { return bars_s + 8u * (2 * NS + 2 + i); };
     auto s_full = [&](int i) { return bars_s + 8u * (2 * NS + 4 + i); };  // S of a step is in TMEM
-    auto p_full = [&](int i) { return bars_s + 8u * (2 * NS + 6 + i); };  // P of a step is in TMEM
-    auto o_full = [&](int i) { return bars_s + 8u * (2 * NS + 8 + i); };  // its P V is in O
-    const uint32_t done_bar = bars_s + 8u * (2 * NS + 10);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * NS + 11);
+    // P of a step is in TMEM: its first 64 keys, the others
+    auto p_full = [&](int i, int half) { return bars_s + 8u * (2 * NS + 6 + 2 * i + half); };
+    auto o_full = [&](int i) { return bars_s + 8u * (2 * NS + 10 + i); };  // its P V is in O
+    const uint32_t done_bar = bars_s + 8u * (2 * NS + 12);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * NS + 13);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    static_assert(8 * (2 * NS + 11) + 8 <= C::kBarBytes);
+    static_assert(8 * (2 * NS + 13) + 8 <= C::kBarBytes);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -188,7 +222,8 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             mbar_init(q_full(i), 1);
             mbar_init(q_empty(i), 1);
             mbar_init(s_full(i), 1);
-            mbar_init(p_full(i), 4);
+            mbar_init(p_full(i, 0), 4);
+            mbar_init(p_full(i, 1), 4);
             mbar_init(o_full(i), 1);
         }
         mbar_init(done_bar, 1);
@@ -212,174 +247,198 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
     // J, key tiles so far (K in ring position 2 J, V in 2 J + 1); step, S tiles
     // so far (its parity is the stream); narrow items so far (their query
     // buffer), and the uses of each query buffer.
-    if (warp == 8) {
-        // ------------------------------------------------------------ TMA
-        uint32_t seq = 0, nar = 0;
-        uint32_t qc[2] = {0, 0};
-        bool ok = true;
-        if (elect_one()) {
-            tma_prefetch_desc(&qmap_p);
-            tma_prefetch_desc(&qmap_o);
-            tma_prefetch_desc(&kmap);
-            tma_prefetch_desc(&vmap);
-        }
-        __syncwarp();
-        for (int idx = blockIdx.x; idx < w.items && ok; idx += gridDim.x) {
-            bool bad = false;
-            const Item it = decode(w, idx, bad);
-            if (bad && lane == 0) atomicOr(w.status, kDeviceStatusIndex);
-            const int ntiles = (it.nkeys + kKeys - 1) / kKeys;
-            const int32_t *table = it.b < 0 ? w.prefix_pages : w.block_table + it.b * w.table_stride;
-            for (int j = 0; j < ntiles && ok; ++j) {
-                const int key = it.key0 + j * kKeys;
-                const int valid = min(kKeys, it.nkeys - j * kKeys);
-                int npages = 0, row = 0;
-                if (w.page_size > 0) {
-                    npages = (valid + w.page_size - 1) / w.page_size;
-                    if (lane < npages) {
-                        const int page = table[key / w.page_size + lane];
-                        const bool in = page >= 0 && page < w.pages;
-                        if (!in) atomicOr(w.status, kDeviceStatusIndex);
-                        // past the cache's rows: TMA fills zeros
-                        row = ((in ? page : w.pages) * w.Hkv + (in ? it.h : 0)) * w.page_size;
-                    }
-                }
-                for (int kv = 0; kv < 2; ++kv) {
-                    const int s = seq % NS;
-                    ok = __all_sync(0xffffffffu, mbar_wait(kv_empty(s), ((seq / NS) & 1) ^ 1, ctl));
-                    if (!ok) break;
-                    const CUtensorMap *map = kv == 0 ? &kmap : &vmap;
-                    if (w.page_size > 0) {
-                        if (elect_one())
-                            mbar_arrive_expect_tx(kv_full(s), npages * w.page_size * 128 * C::kHalves);
-                        __syncwarp();
-                        if (lane < npages) {
-                            for (int hf = 0; hf < C::kHalves; ++hf)
-                                tma_load_2d(sKV(s) + hf * C::kHalfBytes + lane * w.page_size * 128, map, kv_full(s),
-                                            hf * 64, row);
-                        }
-                        __syncwarp();
-                    } else if (elect_one()) {
-                        mbar_arrive_expect_tx(kv_full(s), C::kTileBytes);
-                        for (int hf = 0; hf < C::kHalves; ++hf)
-                            tma_load_2d(sKV(s) + hf * C::kHalfBytes, map, kv_full(s), it.h * D + hf * 64,
-                                        it.b * w.max_len + key);
-                    }
-                    __syncwarp();
-                    ++seq;
-                    if (kv == 0 && j == 0) {
-                        // the item's query tiles, behind its first K tile: the
-                        // buffers are free once the last item's S are done
-                        const CUtensorMap *qm = it.b < 0 ? &qmap_p : &qmap_o;
-                        for (int i = 0; i < (it.wide ? 2 : 1) && ok; ++i) {
-                            const int buf = it.wide ? i : static_cast<int>(nar & 1);
-                            ok = __all_sync(0xffffffffu, mbar_wait(q_empty(buf), (qc[buf] & 1) ^ 1, ctl));
-                            if (!ok) break;
-                            if (elect_one()) {
-                                mbar_arrive_expect_tx(q_full(buf), it.tok * w.G * 128 * C::kHalves);
-                                for (int hf = 0; hf < C::kHalves; ++hf)
-                                    tma_load_3d(sQ(buf) + hf * C::kHalfBytes, qm, q_full(buf), hf * 64, it.h * w.G,
-                                                it.tok0 + i * it.tok);
-                            }
-                            __syncwarp();
-                            ++qc[buf];
-                        }
-                    }
-                }
-            }
-            if (!it.wide && ntiles > 0) ++nar;
-        }
-        if (*abort_flag && elect_one()) {
-            // let the copies still in flight land before the CTA exits
-            for (uint32_t q = seq > NS ? seq - NS : 0; q < seq; ++q)
-                mbar_wait_drain(kv_full(q % NS), (q / NS) & 1, w.timeout_ns, w.status);
-            for (int i = 0; i < 2; ++i)
-                if (qc[i] > 0) mbar_wait_drain(q_full(i), (qc[i] - 1) & 1, w.timeout_ns, w.status);
-        }
-        __syncwarp();
-    } else if (warp == 9) {
-        // ------------------------------------------------------------ MMA
-        constexpr uint32_t idesc_qk = idesc_bf16_f32(kRows, kKeys, false);
-        constexpr uint32_t idesc_pv = idesc_bf16_f32(kRows, D, true);
-        struct Step {
-            int st, vslot, ksteps;
-            uint32_t vparity, pparity;
-            bool first, release;
-        };
-        Step prev{};
-        bool have = false, ok = true;
-        uint32_t J = 0, step = 0, nar = 0;
-        uint32_t qc[2] = {0, 0}, sc[2] = {0, 0};
-        auto pv = [&](const Step &p) {
-            if (!__all_sync(0xffffffffu, mbar_wait(p_full(p.st), p.pparity, ctl))) return false;
-            if (!__all_sync(0xffffffffu, mbar_wait(kv_full(p.vslot), p.vparity, ctl))) return false;
-            tc_fence_after_sync();
+    if (warp >= 8) {
+        setmaxnreg_dec<kOtherRegs>();  // by all four warps at once
+        if (warp == 8) {
+            // ------------------------------------------------------------ TMA
+            uint32_t seq = 0, nar = 0;
+            uint32_t qc[2] = {0, 0};
+            bool ok = true;
             if (elect_one()) {
-                const uint64_t vd = sdesc_mnmajor_sw128(sKV(p.vslot), C::kHalfBytes);
-                for (int ks = 0; ks < p.ksteps; ++ks)
-                    mma_f16_ts(tO(p.st), tS(p.st) + 8u * ks, vd + 128u * ks, idesc_pv, !p.first || ks > 0 ? 1u : 0u);
-                mma_commit(o_full(p.st));
-                if (p.release) mma_commit(kv_empty(p.vslot));
+                tma_prefetch_desc(&qmap_p);
+                tma_prefetch_desc(&qmap_o);
+                tma_prefetch_desc(&kmap);
+                tma_prefetch_desc(&vmap);
             }
             __syncwarp();
-            return true;
-        };
-        for (int idx = blockIdx.x; idx < w.items && ok; idx += gridDim.x) {
-            bool bad;
-            const Item it = decode(w, idx, bad);
-            const int ntiles = (it.nkeys + kKeys - 1) / kKeys;
-            const int subs = it.wide ? 2 : 1;
-            for (int j = 0; j < ntiles && ok; ++j, ++J) {
-                const int kslot = (2 * J) % NS, vslot = (2 * J + 1) % NS;
-                for (int sub = 0; sub < subs; ++sub, ++step) {
-                    const int st = step & 1;
-                    const int buf = it.wide ? st : static_cast<int>(nar & 1);
-                    ok = __all_sync(0xffffffffu, mbar_wait(kv_full(kslot), (2 * J / NS) & 1, ctl));
-                    if (!ok) break;
-                    if (j == 0) {
-                        ok = __all_sync(0xffffffffu, mbar_wait(q_full(buf), qc[buf] & 1, ctl));
-                        if (!ok) break;
-                        ++qc[buf];
+#pragma unroll 1
+            for (int idx = blockIdx.x; idx < w.items && ok; idx += gridDim.x) {
+                bool bad = false;
+                const Item it = decode(w, idx, bad);
+                if (bad && lane == 0) atomicOr(w.status, kDeviceStatusIndex);
+                const int ntiles = (it.nkeys + kKeys - 1) / kKeys;
+                const int32_t *table = it.b < 0 ? w.prefix_pages : w.block_table + it.b * w.table_stride;
+#pragma unroll 1
+                for (int j = 0; j < ntiles && ok; ++j) {
+                    const int key = it.key0 + j * kKeys;
+                    const int valid = min(kKeys, it.nkeys - j * kKeys);
+                    int npages = 0, row = 0;
+                    if (w.page_size > 0) {
+                        npages = (valid + w.page_size - 1) / w.page_size;
+                        if (lane < npages) {
+                            const int page = table[key / w.page_size + lane];
+                            const bool in = page >= 0 && page < w.pages;
+                            if (!in) atomicOr(w.status, kDeviceStatusIndex);
+                            // past the cache's rows: TMA fills zeros
+                            row = ((in ? page : w.pages) * w.Hkv + (in ? it.h : 0)) * w.page_size;
+                        }
                     }
+#pragma unroll 1
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const int s = seq % NS;
+                        ok = __all_sync(0xffffffffu, mbar_wait(kv_empty(s), ((seq / NS) & 1) ^ 1, ctl));
+                        if (!ok) break;
+                        const CUtensorMap *map = kv == 0 ? &kmap : &vmap;
+                        if (w.page_size > 0) {
+                            if (elect_one())
+                                mbar_arrive_expect_tx(kv_full(s), npages * w.page_size * 128 * C::kHalves);
+                            __syncwarp();
+                            if (lane < npages) {
+#pragma unroll 1
+        #pragma unroll 1
+                            for (int hf = 0; hf < C::kHalves; ++hf)
+                                    tma_load_2d(sKV(s) + hf * C::kHalfBytes + lane * w.page_size * 128, map, kv_full(s),
+                                                hf * 64, row);
+                            }
+                            __syncwarp();
+                        } else if (elect_one()) {
+                            mbar_arrive_expect_tx(kv_full(s), C::kTileBytes);
+#pragma unroll 1
+                            for (int hf = 0; hf < C::kHalves; ++hf)
+                                tma_load_2d(sKV(s) + hf * C::kHalfBytes, map, kv_full(s), it.h * D + hf * 64,
+                                            it.b * w.max_len + key);
+                        }
+                        __syncwarp();
+                        ++seq;
+                        if (kv == 0 && j == 0) {
+                            // the item's query tiles, behind its first K tile: the
+                            // buffers are free once the last item's S are done
+                            const CUtensorMap *qm = it.b < 0 ? &qmap_p : &qmap_o;
+#pragma unroll 1
+                            for (int i = 0; i < (it.wide ? 2 : 1) && ok; ++i) {
+                                const int buf = it.wide ? i : static_cast<int>(nar & 1);
+                                ok = __all_sync(0xffffffffu, mbar_wait(q_empty(buf), (qc[buf] & 1) ^ 1, ctl));
+                                if (!ok) break;
+                                if (elect_one()) {
+                                    mbar_arrive_expect_tx(q_full(buf), it.tok * w.G * 128 * C::kHalves);
+        #pragma unroll 1
+        #pragma unroll 1
+                            for (int hf = 0; hf < C::kHalves; ++hf)
+                                        tma_load_3d(sQ(buf) + hf * C::kHalfBytes, qm, q_full(buf), hf * 64, it.h * w.G,
+                                                    it.tok0 + i * it.tok);
+                                }
+                                __syncwarp();
+                                ++qc[buf];
+                            }
+                        }
+                    }
+                }
+                if (!it.wide && ntiles > 0) ++nar;
+            }
+            if (*abort_flag && elect_one()) {
+                // let the copies still in flight land before the CTA exits
+                for (uint32_t q = seq > NS ? seq - NS : 0; q < seq; ++q)
+                    mbar_wait_drain(kv_full(q % NS), (q / NS) & 1, w.timeout_ns, w.status);
+                for (int i = 0; i < 2; ++i)
+                    if (qc[i] > 0) mbar_wait_drain(q_full(i), (qc[i] - 1) & 1, w.timeout_ns, w.status);
+            }
+            __syncwarp();
+        } else if (warp == 9) {
+            // ------------------------------------------------------------ MMA
+            constexpr uint32_t idesc_qk = idesc_bf16_f32(kRows, kKeys, false);
+            constexpr uint32_t idesc_pv = idesc_bf16_f32(kRows, D, true);
+            struct Step {
+                int st, vslot, ksteps;
+                uint32_t vparity, pparity;
+                bool first, release;
+            };
+            Step prev{};
+            bool have = false, ok = true;
+            uint32_t J = 0, step = 0, nar = 0;
+            uint32_t qc[2] = {0, 0}, sc[2] = {0, 0};
+            auto pv = [&](const Step &p) {
+                if (!__all_sync(0xffffffffu, mbar_wait(kv_full(p.vslot), p.vparity, ctl))) return false;
+                const uint64_t vd = sdesc_mnmajor_sw128(sKV(p.vslot), C::kHalfBytes);
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(p_full(p.st, half), p.pparity, ctl))) return false;
                     tc_fence_after_sync();
                     if (elect_one()) {
-                        const uint64_t qd = sdesc_kmajor_sw128(sQ(buf)), kd = sdesc_kmajor_sw128(sKV(kslot));
-#pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks) {
-                            const uint32_t off = (ks / 4) * (C::kHalfBytes / 16) + 2u * (ks % 4);
-                            mma_f16_ss(tS(st), qd + off, kd + off, idesc_qk, ks > 0 ? 1u : 0u);
+                        const int end = min(p.ksteps, 4 * half + 4);
+#pragma unroll 1
+                        for (int ks = 4 * half; ks < end; ++ks)
+                            mma_f16_ts(tO(p.st), tS(p.st) + 8u * ks, vd + 128u * ks, idesc_pv,
+                                       !p.first || ks > 0 ? 1u : 0u);
+                        if (half == 1) {
+                            mma_commit(o_full(p.st));
+                            if (p.release) mma_commit(kv_empty(p.vslot));
                         }
-                        mma_commit(s_full(st));
-                        if (sub == subs - 1) mma_commit(kv_empty(kslot));
-                        if (j == ntiles - 1) mma_commit(q_empty(buf));
                     }
                     __syncwarp();
-                    if (have) {
-                        ok = pv(prev);
-                        if (!ok) break;
-                    }
-                    const int valid = min(kKeys, it.nkeys - j * kKeys);
-                    prev = Step{st,
-                                vslot,
-                                (valid + 15) / 16,
-                                ((2 * J + 1) / NS) & 1,
-                                sc[st] & 1,
-                                it.wide ? j == 0 : j < 2,
-                                sub == subs - 1};
-                    ++sc[st];
-                    have = true;
                 }
+                return true;
+            };
+#pragma unroll 1
+            for (int idx = blockIdx.x; idx < w.items && ok; idx += gridDim.x) {
+                bool bad;
+                const Item it = decode(w, idx, bad);
+                const int ntiles = (it.nkeys + kKeys - 1) / kKeys;
+                const int subs = it.wide ? 2 : 1;
+#pragma unroll 1
+                for (int j = 0; j < ntiles && ok; ++j, ++J) {
+                    const int kslot = (2 * J) % NS, vslot = (2 * J + 1) % NS;
+#pragma unroll 1
+                    for (int sub = 0; sub < subs; ++sub, ++step) {
+                        const int st = step & 1;
+                        const int buf = it.wide ? st : static_cast<int>(nar & 1);
+                        ok = __all_sync(0xffffffffu, mbar_wait(kv_full(kslot), (2 * J / NS) & 1, ctl));
+                        if (!ok) break;
+                        if (j == 0) {
+                            ok = __all_sync(0xffffffffu, mbar_wait(q_full(buf), qc[buf] & 1, ctl));
+                            if (!ok) break;
+                            ++qc[buf];
+                        }
+                        tc_fence_after_sync();
+                        if (elect_one()) {
+                            const uint64_t qd = sdesc_kmajor_sw128(sQ(buf)), kd = sdesc_kmajor_sw128(sKV(kslot));
+#pragma unroll
+                            for (int ks = 0; ks < D / 16; ++ks) {
+                                const uint32_t off = (ks / 4) * (C::kHalfBytes / 16) + 2u * (ks % 4);
+                                mma_f16_ss(tS(st), qd + off, kd + off, idesc_qk, ks > 0 ? 1u : 0u);
+                            }
+                            mma_commit(s_full(st));
+                            if (sub == subs - 1) mma_commit(kv_empty(kslot));
+                            if (j == ntiles - 1) mma_commit(q_empty(buf));
+                        }
+                        __syncwarp();
+                        if (have) {
+                            ok = pv(prev);
+                            if (!ok) break;
+                        }
+                        const int valid = min(kKeys, it.nkeys - j * kKeys);
+                        prev = Step{st,
+                                    vslot,
+                                    (valid + 15) / 16,
+                                    ((2 * J + 1) / NS) & 1,
+                                    sc[st] & 1,
+                                    it.wide ? j == 0 : j < 2,
+                                    sub == subs - 1};
+                        ++sc[st];
+                        have = true;
+                    }
+                }
+                if (!it.wide && ntiles > 0) ++nar;
             }
-            if (!it.wide && ntiles > 0) ++nar;
+            if (have && ok) pv(prev);
+            // no MMA may be in flight when TMEM is released
+            if (elect_one()) {
+                mma_commit(done_bar);
+                mbar_wait_drain(done_bar, 0, w.timeout_ns, w.status);
+            }
+            __syncwarp();
         }
-        if (have && ok) pv(prev);
-        // no MMA may be in flight when TMEM is released
-        if (elect_one()) {
-            mma_commit(done_bar);
-            mbar_wait_drain(done_bar, 0, w.timeout_ns, w.status);
-        }
-        __syncwarp();
     } else {
+        setmaxnreg_inc<kSoftmaxRegs>();
         // ------------------------------------------------------------ softmax
         const int st = warp >> 2;
         const int row = threadIdx.x & 127;
@@ -424,21 +483,30 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                     }
                     fence_proxy_async_smem();
                 }
+                uint32_t sr[4][32];
+                uint64_t sum[2] = {0, 0};
+                float mc = 0.f;
+                auto arrive = [&](int half) {
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full(st, half));
+                };
                 if (warp_live) {
                     const int vis = live ? min(max(limit - it.key0 - key, 0), valid) : 0;
-                    uint32_t sr[4][32];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(ts + 32u * q, sr[q]);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_wait_ld(sr[q]);
-                    if (__any_sync(0xffffffffu, vis < kKeys)) {
-#pragma unroll
-                        for (int i = 0; i < kKeys; ++i)
-                            if (i >= vis) sr[i / 32][i % 32] = 0xff800000u;  // -inf
-                    }
+                    tmem_ld_32x32b_x32(ts, sr[0]);
+                    tmem_ld_32x32b_x32(ts + 32u, sr[1]);
+                    tmem_wait_ld(sr[0]);
+                    tmem_wait_ld(sr[1]);
+                    tmem_ld_32x32b_x32(ts + 64u, sr[2]);
+                    tmem_ld_32x32b_x32(ts + 96u, sr[3]);
+                    const bool masked = __any_sync(0xffffffffu, vis < kKeys);
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int i = 0; i < kKeys; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(sr[i / 32][i % 32]));
+                    row_max<0>(sr[0], masked, vis, mx);
+                    row_max<1>(sr[1], masked, vis, mx);
+                    tmem_wait_ld(sr[2]);
+                    tmem_wait_ld(sr[3]);
+                    row_max<2>(sr[2], masked, vis, mx);
+                    row_max<3>(sr[3], masked, vis, mx);
                     const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     if (done == 0) {
                         mref = mt;
@@ -450,41 +518,36 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                             ok = __all_sync(0xffffffffu, mbar_wait(o_full(st), (cnt - 1) & 1, ctl));
                             if (!ok) break;
                             tc_fence_after_sync();
+#pragma unroll 1
+                            for (int q = 0; q < D / 16; ++q) {
+                                uint32_t o[16];
+                                tmem_ld_32x32b_x16(to + 16u * q, o);
+                                tmem_wait_ld16(o);
 #pragma unroll
-                            for (int q = 0; q < D / 32; ++q) {
-                                uint32_t o[32];
-                                tmem_ld_32x32b_x32(to + 32u * q, o);
-                                tmem_wait_ld(o);
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                tmem_st_32x32b_x32(to + 32u * q, o);
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                tmem_st_32x32b_x16(to + 16u * q, o);
                             }
                             l *= f;
                             if (grow) mref = m_new;
                         }
                     }
-                    const float mc = mref == -INFINITY ? 0.f : mref * c;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        uint32_t p[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int e = hf * 64 + 2 * i;
-                            const float a = ex2(fmaf(__uint_as_float(sr[e / 32][e % 32]), c, -mc));
-                            const float b = ex2(fmaf(__uint_as_float(sr[e / 32][e % 32 + 1]), c, -mc));
-                            sum[i & 1] += a;
-                            sum[2 + (i & 1)] += b;
-                            p[i] = pack2(a, b);
-                        }
-                        tmem_st_32x32b_x32(ts + 32u * hf, p);
-                    }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    mc = mref == -INFINITY ? 0.f : mref * c;
+                    weights(sr[0], c, mc, sum, ts + 0u);
+                    weights(sr[1], c, mc, sum, ts + 16u);
                     tmem_wait_st();
                 }
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_full(st));
+                arrive(0);
+                if (warp_live) {
+                    weights(sr[2], c, mc, sum, ts + 32u);
+                    weights(sr[3], c, mc, sum, ts + 48u);
+                    tmem_wait_st();
+                }
+                arrive(1);
+                if (warp_live) {
+                    float a, b;
+                    f32x2_split(add_f32x2(sum[0], sum[1]), a, b);
+                    l += a + b;
+                }
                 ++cnt;
                 ++done;
             }
