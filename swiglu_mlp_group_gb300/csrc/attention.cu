@@ -345,91 +345,107 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             __syncwarp();
         } else if (warp == 9) {
             // ------------------------------------------------------------ MMA
+            // The whole warp runs the loop and one elected lane issues; counters
+            // and descriptors are kept uniform over the warp (a key count that
+            // was read from memory goes through a shuffle for that) and the K
+            // steps of a tile are unrolled: with the K steps of P V in a loop
+            // and lane-wise counters the issue of a step took 2300 cycles for
+            // 1024 of tensor work.
             constexpr uint32_t idesc_qk = idesc_bf16_f32(kRows, kKeys, false);
             constexpr uint32_t idesc_pv = idesc_bf16_f32(kRows, D, true);
-            struct Step {
-                int st, vslot, ksteps;
-                uint32_t vparity, pparity;
-                bool first, release;
-            };
-            Step prev{};
-            bool have = false, ok = true;
-            uint32_t J = 0, step = 0, nar = 0;
-            uint32_t qc[2] = {0, 0}, sc[2] = {0, 0};
-            auto pv = [&](const Step &p) {
-                if (!__all_sync(0xffffffffu, mbar_wait(kv_full(p.vslot), p.vparity, ctl))) return false;
-                const uint64_t vd = sdesc_mnmajor_sw128(sKV(p.vslot), C::kHalfBytes);
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(p_full(p.st, half), p.pparity, ctl))) return false;
-                    tc_fence_after_sync();
-                    if (elect_one()) {
-                        const int end = min(p.ksteps, 4 * half + 4);
-#pragma unroll 1
-                        for (int ks = 4 * half; ks < end; ++ks)
-                            mma_f16_ts(tO(p.st), tS(p.st) + 8u * ks, vd + 128u * ks, idesc_pv,
-                                       !p.first || ks > 0 ? 1u : 0u);
-                        if (half == 1) {
-                            mma_commit(o_full(p.st));
-                            if (p.release) mma_commit(kv_empty(p.vslot));
-                        }
-                    }
-                    __syncwarp();
+            constexpr uint32_t tile_desc = C::kTileBytes / 16;
+            const uint64_t qd0 = sdesc_kmajor_sw128(sQ(0));
+            const uint64_t kd0 = sdesc_kmajor_sw128(sKV(0));
+            const uint64_t vd0 = sdesc_mnmajor_sw128(sKV(0), C::kHalfBytes);
+            bool ok = true;
+            int J = 0, step = 0, nar = 0;
+            int kslot = 0;       // ring position of the tile's K; V is the next
+            uint32_t kpar = 0;   // its parity
+            uint32_t qpar = 0;   // bit i: parity of query buffer i
+            uint32_t ppar = 0;   // bit i: parity of stream i's P
+            // the step whose P V is due
+            int p_st = -1, p_slot = 0, p_ksteps = 0;
+            uint32_t p_par = 0;
+            bool p_first = false, p_release = false;
+            auto pv = [&]() {
+                if (!__all_sync(0xffffffffu, mbar_wait(kv_full(p_slot), p_par, ctl))) return false;
+                const uint64_t vd = vd0 + static_cast<uint32_t>(p_slot) * tile_desc;
+                const uint32_t o = tO(p_st), p = tS(p_st);
+                const uint32_t par = (ppar >> p_st) & 1;
+                if (!__all_sync(0xffffffffu, mbar_wait(p_full(p_st, 0), par, ctl))) return false;
+                tc_fence_after_sync();
+                if (elect_one()) {
+                    mma_f16_ts(o, p, vd, idesc_pv, p_first ? 0u : 1u);
+#pragma unroll
+                    for (int ks = 1; ks < 4; ++ks)
+                        if (ks < p_ksteps) mma_f16_ts(o, p + 8u * ks, vd + 128u * ks, idesc_pv, 1u);
                 }
+                __syncwarp();
+                if (!__all_sync(0xffffffffu, mbar_wait(p_full(p_st, 1), par, ctl))) return false;
+                tc_fence_after_sync();
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 4; ks < 8; ++ks)
+                        if (ks < p_ksteps) mma_f16_ts(o, p + 8u * ks, vd + 128u * ks, idesc_pv, 1u);
+                    mma_commit(o_full(p_st));
+                    if (p_release) mma_commit(kv_empty(p_slot));
+                }
+                __syncwarp();
+                ppar ^= 1u << p_st;
                 return true;
             };
 #pragma unroll 1
             for (int idx = blockIdx.x; idx < w.items && ok; idx += gridDim.x) {
                 bool bad;
                 const Item it = decode(w, idx, bad);
-                const int ntiles = (it.nkeys + kKeys - 1) / kKeys;
+                const int nkeys = __shfl_sync(0xffffffffu, it.nkeys, 0);
+                const int ntiles = (nkeys + kKeys - 1) / kKeys;
                 const int subs = it.wide ? 2 : 1;
 #pragma unroll 1
                 for (int j = 0; j < ntiles && ok; ++j, ++J) {
-                    const int kslot = (2 * J) % NS, vslot = (2 * J + 1) % NS;
+                    const int vslot = kslot + 1 == NS ? 0 : kslot + 1;
+                    const uint32_t vpar = kslot + 1 == NS ? kpar ^ 1 : kpar;
+                    ok = __all_sync(0xffffffffu, mbar_wait(kv_full(kslot), kpar, ctl));
+                    if (!ok) break;
 #pragma unroll 1
                     for (int sub = 0; sub < subs; ++sub, ++step) {
                         const int st = step & 1;
-                        const int buf = it.wide ? st : static_cast<int>(nar & 1);
-                        ok = __all_sync(0xffffffffu, mbar_wait(kv_full(kslot), (2 * J / NS) & 1, ctl));
-                        if (!ok) break;
+                        const int buf = it.wide ? st : nar & 1;
                         if (j == 0) {
-                            ok = __all_sync(0xffffffffu, mbar_wait(q_full(buf), qc[buf] & 1, ctl));
+                            ok = __all_sync(0xffffffffu, mbar_wait(q_full(buf), (qpar >> buf) & 1, ctl));
                             if (!ok) break;
-                            ++qc[buf];
+                            qpar ^= 1u << buf;
                         }
                         tc_fence_after_sync();
                         if (elect_one()) {
-                            const uint64_t qd = sdesc_kmajor_sw128(sQ(buf)), kd = sdesc_kmajor_sw128(sKV(kslot));
+                            const uint64_t qd = qd0 + static_cast<uint32_t>(buf) * tile_desc;
+                            const uint64_t kd = kd0 + static_cast<uint32_t>(kslot) * tile_desc;
+                            const uint32_t s = tS(st);
 #pragma unroll
                             for (int ks = 0; ks < D / 16; ++ks) {
                                 const uint32_t off = (ks / 4) * (C::kHalfBytes / 16) + 2u * (ks % 4);
-                                mma_f16_ss(tS(st), qd + off, kd + off, idesc_qk, ks > 0 ? 1u : 0u);
+                                mma_f16_ss(s, qd + off, kd + off, idesc_qk, ks > 0 ? 1u : 0u);
                             }
                             mma_commit(s_full(st));
                             if (sub == subs - 1) mma_commit(kv_empty(kslot));
                             if (j == ntiles - 1) mma_commit(q_empty(buf));
                         }
                         __syncwarp();
-                        if (have) {
-                            ok = pv(prev);
+                        if (p_st >= 0) {
+                            ok = pv();
                             if (!ok) break;
                         }
-                        const int valid = min(kKeys, it.nkeys - j * kKeys);
-                        prev = Step{st,
-                                    vslot,
-                                    (valid + 15) / 16,
-                                    ((2 * J + 1) / NS) & 1,
-                                    sc[st] & 1,
-                                    it.wide ? j == 0 : j < 2,
-                                    sub == subs - 1};
-                        ++sc[st];
-                        have = true;
+                        p_st = st, p_slot = vslot, p_par = vpar;
+                        p_ksteps = (min(kKeys, nkeys - j * kKeys) + 15) / 16;
+                        p_first = it.wide ? j == 0 : j < 2;
+                        p_release = sub == subs - 1;
                     }
+                    kslot += 2;
+                    if (kslot >= NS) kslot -= NS, kpar ^= 1;
                 }
                 if (!it.wide && ntiles > 0) ++nar;
             }
-            if (have && ok) pv(prev);
+            if (p_st >= 0 && ok) pv();
             // no MMA may be in flight when TMEM is released
             if (elect_one()) {
                 mma_commit(done_bar);
