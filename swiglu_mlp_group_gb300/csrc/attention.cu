@@ -18,14 +18,14 @@
 // the pipeline.  Chunks (and the halves of a narrow item) leave partial sums
 // with their maximum in the workspace; a second kernel joins them.
 //
-// Pipeline (one CTA per SM, 10 warps).  Two streams, each with its own S and O
+// Pipeline (one CTA per SM, 11 warps).  Two streams, each with its own S and O
 // in TMEM and four softmax warps, so that the tensor core works on one while
 // the other is in its softmax:
 //   warps 0..3, 4..7 : softmax of stream 0 / 1, a thread per row: S from TMEM,
 //                      maximum, exponentials, P back to TMEM (over S) as bf16.
 //   warp 8           : TMA: query tiles, and K and V tiles into a ring.
-//   warp 9           : MMA issue: S = Q K^T of step k + 1 ahead of O += P V of
-//                      step k; steps alternate between the streams.
+//   warps 9, 10      : MMA issue: S = Q K^T, O += P V.  Their steps alternate
+//                      between the streams.
 // P is rounded to bf16 for the second product, the operand type of V; its sum
 // is taken in f32 before that rounding.
 #include <math.h>
@@ -40,7 +40,8 @@ namespace {
 
 constexpr int kRows = 128;     // rows of a query tile
 constexpr int kKeys = 128;     // keys of a key tile
-constexpr int kThreads = 384;  // 8 softmax warps, TMA, MMA, 2 idle (register shares go by 4 warps)
+constexpr int kTmaWarp = 8, kQkWarp = 9, kPvWarp = 10;
+constexpr int kThreads = 384;  // 8 softmax warps, TMA, 2 MMA, 1 idle (register shares go by 4 warps)
 // Registers a thread: 168 at launch; the softmax holds a row of 128 scores.
 // 256 x 208 + 128 x 88 = 384 x 168.
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
@@ -209,7 +210,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     static_assert(8 * (2 * NS + 13) + 8 <= C::kBarBytes);
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // uniform for the compiler too
     const int lane = threadIdx.x & 31;
     const WaitCtl ctl{abort_flag, w.status, w.timeout_ns};
 
@@ -226,11 +227,11 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             mbar_init(p_full(i, 1), 4);
             mbar_init(o_full(i), 1);
         }
-        mbar_init(done_bar, 1);
+        mbar_init(done_bar, 2);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 9) {
+    if (warp == kQkWarp) {
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
         tmem_relinquish();
     }
@@ -247,12 +248,12 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
     // J, key tiles so far (K in ring position 2 J, V in 2 J + 1); step, S tiles
     // so far (its parity is the stream); narrow items so far (their query
     // buffer), and the uses of each query buffer.
-    if (warp >= 8) {
+    if (warp >= kTmaWarp) {
         setmaxnreg_dec<kOtherRegs>();  // by all four warps at once
-        if (warp == 8) {
+        if (warp == kTmaWarp) {
             // ------------------------------------------------------------ TMA
             uint32_t seq = 0, nar = 0;
-            uint32_t qc[2] = {0, 0};
+            uint32_t qpar = 0, qused = 0;  // bit i: parity of query buffer i's next use, used at all
             bool ok = true;
             if (elect_one()) {
                 tma_prefetch_desc(&qmap_p);
@@ -286,7 +287,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
 #pragma unroll 1
                     for (int kv = 0; kv < 2; ++kv) {
                         const int s = seq % NS;
-                        ok = __all_sync(0xffffffffu, mbar_wait(kv_empty(s), ((seq / NS) & 1) ^ 1, ctl));
+                        ok = __all_sync(0xffffffffu, mbar_wait_spin(kv_empty(s), ((seq / NS) & 1) ^ 1, ctl));
                         if (!ok) break;
                         const CUtensorMap *map = kv == 0 ? &kmap : &vmap;
                         if (w.page_size > 0) {
@@ -317,7 +318,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
 #pragma unroll 1
                             for (int i = 0; i < (it.wide ? 2 : 1) && ok; ++i) {
                                 const int buf = it.wide ? i : static_cast<int>(nar & 1);
-                                ok = __all_sync(0xffffffffu, mbar_wait(q_empty(buf), (qc[buf] & 1) ^ 1, ctl));
+                                ok = __all_sync(0xffffffffu, mbar_wait_spin(q_empty(buf), ((qpar >> buf) & 1) ^ 1, ctl));
                                 if (!ok) break;
                                 if (elect_one()) {
                                     mbar_arrive_expect_tx(q_full(buf), it.tok * w.G * 128 * C::kHalves);
@@ -328,7 +329,8 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                                                     it.tok0 + i * it.tok);
                                 }
                                 __syncwarp();
-                                ++qc[buf];
+                                qpar ^= 1u << buf;
+                                qused |= 1u << buf;
                             }
                         }
                     }
@@ -340,60 +342,35 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                 for (uint32_t q = seq > NS ? seq - NS : 0; q < seq; ++q)
                     mbar_wait_drain(kv_full(q % NS), (q / NS) & 1, w.timeout_ns, w.status);
                 for (int i = 0; i < 2; ++i)
-                    if (qc[i] > 0) mbar_wait_drain(q_full(i), (qc[i] - 1) & 1, w.timeout_ns, w.status);
+                    if ((qused >> i) & 1) mbar_wait_drain(q_full(i), ((qpar >> i) & 1) ^ 1, w.timeout_ns, w.status);
             }
             __syncwarp();
-        } else if (warp == 9) {
+        } else if (warp == kQkWarp || warp == kPvWarp) {
             // ------------------------------------------------------------ MMA
-            // The whole warp runs the loop and one elected lane issues; counters
-            // and descriptors are kept uniform over the warp (a key count that
-            // was read from memory goes through a shuffle for that) and the K
-            // steps of a tile are unrolled: with the K steps of P V in a loop
-            // and lane-wise counters the issue of a step took 2300 cycles for
-            // 1024 of tensor work.
+            // One warp issues S = Q K^T of every step, one O += P V; both take
+            // the steps in the same order, which alternates between the streams
+            // and so keeps one in its softmax while the other's products run.
+            // (A poll of a barrier takes some 120 cycles, and a commit returns
+            // when the products before it have nearly run: one warp for both
+            // spent 1800 cycles on a step's 1024 of tensor work; a warp for each
+            // stream let the streams fall into step.)  The whole warp runs the
+            // loop and one elected lane issues; counters and descriptors are
+            // kept uniform over the warp -- a key count that was read from
+            // memory goes through a shuffle for that -- and the K steps of a
+            // tile are unrolled.
             constexpr uint32_t idesc_qk = idesc_bf16_f32(kRows, kKeys, false);
             constexpr uint32_t idesc_pv = idesc_bf16_f32(kRows, D, true);
             constexpr uint32_t tile_desc = C::kTileBytes / 16;
+            const bool is_qk = warp == kQkWarp;
             const uint64_t qd0 = sdesc_kmajor_sw128(sQ(0));
             const uint64_t kd0 = sdesc_kmajor_sw128(sKV(0));
             const uint64_t vd0 = sdesc_mnmajor_sw128(sKV(0), C::kHalfBytes);
             bool ok = true;
-            int J = 0, step = 0, nar = 0;
-            int kslot = 0;       // ring position of the tile's K; V is the next
-            uint32_t kpar = 0;   // its parity
-            uint32_t qpar = 0;   // bit i: parity of query buffer i
-            uint32_t ppar = 0;   // bit i: parity of stream i's P
-            // the step whose P V is due
-            int p_st = -1, p_slot = 0, p_ksteps = 0;
-            uint32_t p_par = 0;
-            bool p_first = false, p_release = false;
-            auto pv = [&]() {
-                if (!__all_sync(0xffffffffu, mbar_wait(kv_full(p_slot), p_par, ctl))) return false;
-                const uint64_t vd = vd0 + static_cast<uint32_t>(p_slot) * tile_desc;
-                const uint32_t o = tO(p_st), p = tS(p_st);
-                const uint32_t par = (ppar >> p_st) & 1;
-                if (!__all_sync(0xffffffffu, mbar_wait(p_full(p_st, 0), par, ctl))) return false;
-                tc_fence_after_sync();
-                if (elect_one()) {
-                    mma_f16_ts(o, p, vd, idesc_pv, p_first ? 0u : 1u);
-#pragma unroll
-                    for (int ks = 1; ks < 4; ++ks)
-                        if (ks < p_ksteps) mma_f16_ts(o, p + 8u * ks, vd + 128u * ks, idesc_pv, 1u);
-                }
-                __syncwarp();
-                if (!__all_sync(0xffffffffu, mbar_wait(p_full(p_st, 1), par, ctl))) return false;
-                tc_fence_after_sync();
-                if (elect_one()) {
-#pragma unroll
-                    for (int ks = 4; ks < 8; ++ks)
-                        if (ks < p_ksteps) mma_f16_ts(o, p + 8u * ks, vd + 128u * ks, idesc_pv, 1u);
-                    mma_commit(o_full(p_st));
-                    if (p_release) mma_commit(kv_empty(p_slot));
-                }
-                __syncwarp();
-                ppar ^= 1u << p_st;
-                return true;
-            };
+            int step = 0, nar = 0;
+            int slot = is_qk ? 0 : 1;  // ring position of the tile's K / V
+            uint32_t par = 0;          // its parity
+            uint32_t qpar = 0;         // bit i: parity of query buffer i
+            uint32_t spar = 0;         // bit i: QK: parity of stream i's next O; PV: of its P
 #pragma unroll 1
             for (int idx = blockIdx.x; idx < w.items && ok; idx += gridDim.x) {
                 bool bad;
@@ -402,50 +379,90 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                 const int ntiles = (nkeys + kKeys - 1) / kKeys;
                 const int subs = it.wide ? 2 : 1;
 #pragma unroll 1
-                for (int j = 0; j < ntiles && ok; ++j, ++J) {
-                    const int vslot = kslot + 1 == NS ? 0 : kslot + 1;
-                    const uint32_t vpar = kslot + 1 == NS ? kpar ^ 1 : kpar;
-                    ok = __all_sync(0xffffffffu, mbar_wait(kv_full(kslot), kpar, ctl));
+                for (int j = 0; j < ntiles && ok; ++j) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_spin(kv_full(slot), par, ctl));
                     if (!ok) break;
+                    const int valid = min(kKeys, nkeys - j * kKeys);
+                    const uint64_t kvd = (is_qk ? kd0 : vd0) + static_cast<uint32_t>(slot) * tile_desc;
+                    if (is_qk) {
 #pragma unroll 1
-                    for (int sub = 0; sub < subs; ++sub, ++step) {
-                        const int st = step & 1;
-                        const int buf = it.wide ? st : nar & 1;
-                        if (j == 0) {
-                            ok = __all_sync(0xffffffffu, mbar_wait(q_full(buf), (qpar >> buf) & 1, ctl));
-                            if (!ok) break;
-                            qpar ^= 1u << buf;
-                        }
-                        tc_fence_after_sync();
-                        if (elect_one()) {
-                            const uint64_t qd = qd0 + static_cast<uint32_t>(buf) * tile_desc;
-                            const uint64_t kd = kd0 + static_cast<uint32_t>(kslot) * tile_desc;
-                            const uint32_t s = tS(st);
-#pragma unroll
-                            for (int ks = 0; ks < D / 16; ++ks) {
-                                const uint32_t off = (ks / 4) * (C::kHalfBytes / 16) + 2u * (ks % 4);
-                                mma_f16_ss(s, qd + off, kd + off, idesc_qk, ks > 0 ? 1u : 0u);
+                        for (int sub = 0; sub < subs; ++sub, ++step) {
+                            const int st = step & 1;
+                            const int buf = it.wide ? st : nar & 1;
+                            if (j == 0) {
+                                ok = __all_sync(0xffffffffu, mbar_wait_spin(q_full(buf), (qpar >> buf) & 1, ctl));
+                                if (!ok) break;
+                                qpar ^= 1u << buf;
                             }
-                            mma_commit(s_full(st));
-                            if (sub == subs - 1) mma_commit(kv_empty(kslot));
-                            if (j == ntiles - 1) mma_commit(q_empty(buf));
+                            if (step >= 2) {
+                                // P of the stream's last step, which lies over S, has been used
+                                ok = __all_sync(0xffffffffu, mbar_wait_spin(o_full(st), (spar >> st) & 1, ctl));
+                                if (!ok) break;
+                                spar ^= 1u << st;
+                            }
+                            tc_fence_after_sync();
+                            if (elect_one()) {
+                                const uint64_t qd = qd0 + static_cast<uint32_t>(buf) * tile_desc;
+                                const uint32_t s = tS(st);
+#pragma unroll
+                                for (int ks = 0; ks < D / 16; ++ks) {
+                                    const uint32_t off = (ks / 4) * (C::kHalfBytes / 16) + 2u * (ks % 4);
+                                    mma_f16_ss(s, qd + off, kvd + off, idesc_qk, ks > 0 ? 1u : 0u);
+                                }
+                                mma_commit(s_full(st));
+                                if (sub == subs - 1) mma_commit(kv_empty(slot));
+                                if (j == ntiles - 1) mma_commit(q_empty(buf));
+                            }
+                            __syncwarp();
                         }
-                        __syncwarp();
-                        if (p_st >= 0) {
-                            ok = pv();
+                    } else {
+                        if (valid & 15) {
+                            // The last 16 keys of P V reach past the real ones: P
+                            // is 0 there, but 0 x NaN is not, so those rows of V
+                            // are cleared.
+                            const int n = (16 - (valid & 15)) * 8;  // 16-byte pieces of a swizzle column
+                            for (int i = lane; i < n * C::kHalves; i += 32) {
+                                const int hf = i / n, r = i - hf * n;
+                                *reinterpret_cast<uint4 *>(smem + (2 + slot) * C::kTileBytes + hf * C::kHalfBytes +
+                                                           valid * 128 + r * 16) = make_uint4(0, 0, 0, 0);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+#pragma unroll 1
+                        for (int sub = 0; sub < subs; ++sub, ++step) {
+                            const int st = step & 1;
+                            const uint32_t o = tO(st), p = tS(st);
+                            const bool first = it.wide ? j == 0 : j < 2;
+                            ok = __all_sync(0xffffffffu, mbar_wait_spin(p_full(st, 0), (spar >> st) & 1, ctl));
                             if (!ok) break;
+                            tc_fence_after_sync();
+                            if (elect_one()) {
+                                mma_f16_ts(o, p, kvd, idesc_pv, first ? 0u : 1u);
+#pragma unroll
+                                for (int ks = 1; ks < 4; ++ks)
+                                    if (16 * ks < valid) mma_f16_ts(o, p + 8u * ks, kvd + 128u * ks, idesc_pv, 1u);
+                            }
+                            __syncwarp();
+                            ok = __all_sync(0xffffffffu, mbar_wait_spin(p_full(st, 1), (spar >> st) & 1, ctl));
+                            if (!ok) break;
+                            tc_fence_after_sync();
+                            if (elect_one()) {
+#pragma unroll
+                                for (int ks = 4; ks < 8; ++ks)
+                                    if (16 * ks < valid) mma_f16_ts(o, p + 8u * ks, kvd + 128u * ks, idesc_pv, 1u);
+                                mma_commit(o_full(st));
+                                if (sub == subs - 1) mma_commit(kv_empty(slot));
+                            }
+                            __syncwarp();
+                            spar ^= 1u << st;
                         }
-                        p_st = st, p_slot = vslot, p_par = vpar;
-                        p_ksteps = (min(kKeys, nkeys - j * kKeys) + 15) / 16;
-                        p_first = it.wide ? j == 0 : j < 2;
-                        p_release = sub == subs - 1;
                     }
-                    kslot += 2;
-                    if (kslot >= NS) kslot -= NS, kpar ^= 1;
+                    slot += 2;
+                    if (slot >= NS) slot -= NS, par ^= 1;
                 }
                 if (!it.wide && ntiles > 0) ++nar;
             }
-            if (p_st >= 0 && ok) pv();
             // no MMA may be in flight when TMEM is released
             if (elect_one()) {
                 mma_commit(done_bar);
@@ -464,7 +481,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
         const int Hq = w.Hkv * w.G;
         const int64_t rows = static_cast<int64_t>(w.T) * Hq;
         const float c = w.scale_log2;
-        uint32_t J = 0, step = 0, cnt = 0;
+        uint32_t step = 0, cnt = 0;
         bool ok = true;
         for (int idx = blockIdx.x; idx < w.items && ok; idx += gridDim.x) {
             bool bad;
@@ -476,29 +493,15 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             const int limit = it.lim0 + it.lim_step * tok;
             float mref = -INFINITY, l = 0.f;
             int done = 0;  // tiles of this stream
-            for (int j = 0; j < ntiles; ++j, ++J) {
+            for (int j = 0; j < ntiles; ++j) {
                 if (!it.wide) {
                     if (static_cast<int>(step++ & 1) != st) continue;
                 }
-                ok = __all_sync(0xffffffffu, mbar_wait(s_full(st), cnt & 1, ctl));
+                ok = __all_sync(0xffffffffu, mbar_wait_spin(s_full(st), cnt & 1, ctl));
                 if (!ok) break;
                 tc_fence_after_sync();
                 const int key = j * kKeys;
                 const int valid = min(kKeys, it.nkeys - key);
-                if (valid & 15) {
-                    // The last 16 keys of P V reach past the real ones: P is 0
-                    // there, but 0 x NaN is not, so those rows of V are cleared.
-                    const uint32_t vseq = 2 * J + 1;
-                    ok = __all_sync(0xffffffffu, mbar_wait(kv_full(vseq % NS), (vseq / NS) & 1, ctl));
-                    if (!ok) break;
-                    const int n = (16 - (valid & 15)) * 8;  // 16-byte pieces of a half
-                    for (int i = row; i < n * C::kHalves; i += 128) {
-                        const int hf = i / n, r = i - hf * n;
-                        *reinterpret_cast<uint4 *>(smem + (2 + vseq % NS) * C::kTileBytes + hf * C::kHalfBytes +
-                                                   valid * 128 + r * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                }
                 uint32_t sr[4][32];
                 uint64_t sum[2] = {0, 0};
                 float mc = 0.f;
@@ -531,9 +534,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                         const bool grow = (m_new - mref) * c > kRescaleLog2;
                         if (__any_sync(0xffffffffu, grow)) {
                             const float f = grow ? ex2((mref - m_new) * c) : 1.f;
-                            ok = __all_sync(0xffffffffu, mbar_wait(o_full(st), (cnt - 1) & 1, ctl));
-                            if (!ok) break;
-                            tc_fence_after_sync();
+                            // S of this tile was issued when P V of the last one was done: O is at rest
 #pragma unroll 1
                             for (int q = 0; q < D / 16; ++q) {
                                 uint32_t o[16];
@@ -571,7 +572,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             if (it.wide) step += 2 * ntiles;
             // the item's result
             if (done > 0) {
-                ok = __all_sync(0xffffffffu, mbar_wait(o_full(st), (cnt - 1) & 1, ctl));
+                ok = __all_sync(0xffffffffu, mbar_wait_spin(o_full(st), (cnt - 1) & 1, ctl));
                 if (!ok) break;
                 tc_fence_after_sync();
             }
@@ -624,7 +625,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
 
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kQkWarp) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, kTmemCols);
     }
