@@ -205,10 +205,11 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
     // P of a step is in TMEM: its first 64 keys, the others
     auto p_full = [&](int i, int half) { return bars_s + 8u * (2 * NS + 6 + 2 * i + half); };
     auto o_full = [&](int i) { return bars_s + 8u * (2 * NS + 10 + i); };  // its P V is in O
-    const uint32_t done_bar = bars_s + 8u * (2 * NS + 12);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * NS + 13);
+    auto pv_issued = [&](int i) { return bars_s + 8u * (2 * NS + 12 + i); };
+    const uint32_t done_bar = bars_s + 8u * (2 * NS + 14);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * NS + 15);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    static_assert(8 * (2 * NS + 13) + 8 <= C::kBarBytes);
+    static_assert(8 * (2 * NS + 15) + 8 <= C::kBarBytes);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // uniform for the compiler too
     const int lane = threadIdx.x & 31;
@@ -226,6 +227,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             mbar_init(p_full(i, 0), 4);
             mbar_init(p_full(i, 1), 4);
             mbar_init(o_full(i), 1);
+            mbar_init(pv_issued(i), 1);
         }
         mbar_init(done_bar, 2);
         *abort_flag = 0;
@@ -370,7 +372,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             int slot = is_qk ? 0 : 1;  // ring position of the tile's K / V
             uint32_t par = 0;          // its parity
             uint32_t qpar = 0;         // bit i: parity of query buffer i
-            uint32_t spar = 0;         // bit i: QK: parity of stream i's next O; PV: of its P
+            uint32_t spar = 0;         // bit i: parity of stream i: QK: its P V issued; PV: its P
 #pragma unroll 1
             for (int idx = blockIdx.x; idx < w.items && ok; idx += gridDim.x) {
                 bool bad;
@@ -395,8 +397,10 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                                 qpar ^= 1u << buf;
                             }
                             if (step >= 2) {
-                                // P of the stream's last step, which lies over S, has been used
-                                ok = __all_sync(0xffffffffu, mbar_wait_spin(o_full(st), (spar >> st) & 1, ctl));
+                                // P V of the stream's last step, whose P lies over
+                                // S, is in the tensor core's queue: in order, this
+                                // product comes after it
+                                ok = __all_sync(0xffffffffu, mbar_wait_spin(pv_issued(st), (spar >> st) & 1, ctl));
                                 if (!ok) break;
                                 spar ^= 1u << st;
                             }
@@ -451,6 +455,8 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
 #pragma unroll
                                 for (int ks = 4; ks < 8; ++ks)
                                     if (16 * ks < valid) mma_f16_ts(o, p + 8u * ks, kvd + 128u * ks, idesc_pv, 1u);
+                                tc_fence_before_sync();
+                                mbar_arrive(pv_issued(st));
                                 mma_commit(o_full(st));
                                 if (sub == subs - 1) mma_commit(kv_empty(slot));
                             }
@@ -534,7 +540,9 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                         const bool grow = (m_new - mref) * c > kRescaleLog2;
                         if (__any_sync(0xffffffffu, grow)) {
                             const float f = grow ? ex2((mref - m_new) * c) : 1.f;
-                            // S of this tile was issued when P V of the last one was done: O is at rest
+                            ok = __all_sync(0xffffffffu, mbar_wait_spin(o_full(st), (cnt - 1) & 1, ctl));
+                            if (!ok) break;
+                            tc_fence_after_sync();
 #pragma unroll 1
                             for (int q = 0; q < D / 16; ++q) {
                                 uint32_t o[16];
