@@ -31,6 +31,7 @@
 #include <math.h>
 
 #include "attention.h"
+#include "gemm_epilogue.cuh"
 #include "head_norm_rope.cuh"
 #include "launch_util.h"
 #include "ptx.cuh"
@@ -45,6 +46,9 @@ constexpr int kThreads = 384;  // 8 softmax warps, TMA, 2 MMA, 1 idle (register 
 // Registers a thread: 168 at launch; the softmax holds a row of 128 scores.
 // 256 x 208 + 128 x 88 = 384 x 168.
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+// Keys of a tile whose P is handed over first: P V of them runs while the last
+// exponentials are taken.
+constexpr int kFirstKeys = 96;
 constexpr int kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 // The accumulator is rescaled only when a row's maximum has grown by more than
@@ -202,7 +206,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
     auto q_full = [&](int i) { return bars_s + 8u * (2 * NS + i); };
     auto q_empty = [&](int i) { return bars_s + 8u * (2 * NS + 2 + i); };
     auto s_full = [&](int i) { return bars_s + 8u * (2 * NS + 4 + i); };  // S of a step is in TMEM
-    // P of a step is in TMEM: its first 64 keys, the others
+    // P of a step is in TMEM: its first kFirstKeys keys, the others
     auto p_full = [&](int i, int half) { return bars_s + 8u * (2 * NS + 6 + 2 * i + half); };
     auto o_full = [&](int i) { return bars_s + 8u * (2 * NS + 10 + i); };  // its P V is in O
     auto pv_issued = [&](int i) { return bars_s + 8u * (2 * NS + 12 + i); };
@@ -444,7 +448,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                             if (elect_one()) {
                                 mma_f16_ts(o, p, kvd, idesc_pv, first ? 0u : 1u);
 #pragma unroll
-                                for (int ks = 1; ks < 4; ++ks)
+                                for (int ks = 1; ks < kFirstKeys / 16; ++ks)
                                     if (16 * ks < valid) mma_f16_ts(o, p + 8u * ks, kvd + 128u * ks, idesc_pv, 1u);
                             }
                             __syncwarp();
@@ -453,7 +457,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                             tc_fence_after_sync();
                             if (elect_one()) {
 #pragma unroll
-                                for (int ks = 4; ks < 8; ++ks)
+                                for (int ks = kFirstKeys / 16; ks < 8; ++ks)
                                     if (16 * ks < valid) mma_f16_ts(o, p + 8u * ks, kvd + 128u * ks, idesc_pv, 1u);
                                 tc_fence_before_sync();
                                 mbar_arrive(pv_issued(st));
@@ -559,11 +563,11 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                     mc = mref == -INFINITY ? 0.f : mref * c;
                     weights(sr[0], c, mc, sum, ts + 0u);
                     weights(sr[1], c, mc, sum, ts + 16u);
+                    weights(sr[2], c, mc, sum, ts + 32u);
                     tmem_wait_st();
                 }
                 arrive(0);
                 if (warp_live) {
-                    weights(sr[2], c, mc, sum, ts + 32u);
                     weights(sr[3], c, mc, sum, ts + 48u);
                     tmem_wait_st();
                 }
@@ -585,28 +589,25 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                 tc_fence_after_sync();
             }
             if (warp_live) {
+                // Stored through a 4 x 4 transpose of 16-byte pieces within each
+                // quad of lanes: an instruction then writes 64 bytes of 8 rows
+                // instead of 16 bytes of 32.
                 const int64_t at = static_cast<int64_t>(tok) * Hq + it.h * w.G + row_g;
-                if (w.slots > 0) {
-                    const int64_t pr = (it.slot + (it.wide ? 0 : st)) * rows + at;
-                    if (live) w.part_ml[pr] = make_float2(mref == -INFINITY ? mref : mref * c, l);
-                    if (done > 0) {
+                const bool part = w.slots > 0;
+                const int64_t pr = part ? (it.slot + (it.wide ? 0 : st)) * rows + at : 0;
+                if (part && live) w.part_ml[pr] = make_float2(mref == -INFINITY ? mref : mref * c, l);
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const int64_t mine = part ? pr * D : tok * w.ldo + static_cast<int64_t>(it.h * w.G + row_g) * D;
+                const int qi = lane & 3;
+                int64_t off[4];
+                bool on[4];
 #pragma unroll
-                        for (int q = 0; q < D / 32; ++q) {
-                            uint32_t o[32];
-                            tmem_ld_32x32b_x32(to + 32u * q, o);
-                            tmem_wait_ld(o);
-                            if (live) {
-                                uint4 *dst = reinterpret_cast<uint4 *>(w.part_o + pr * D + 32 * q);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                            }
-                        }
-                    }
-                } else {
-                    const float inv = l == 0.f ? 0.f : 1.f / l;
-                    uint16_t *dst = w.out + tok * w.ldo + static_cast<int64_t>(it.h * w.G + row_g) * D;
-#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    off[k] = __shfl_sync(0xffffffffu, mine, (lane & ~3) + k);
+                    on[k] = __shfl_sync(0xffffffffu, live, (lane & ~3) + k);
+                }
+                if (done > 0 || !part) {
+#pragma unroll 1
                     for (int q = 0; q < D / 32; ++q) {
                         uint32_t o[32];
                         if (done > 0) {
@@ -616,14 +617,30 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
 #pragma unroll
                             for (int i = 0; i < 32; ++i) o[i] = 0;
                         }
-                        if (live) {
+                        if (part) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                float x[8];
+                            for (int g = 0; g < 2; ++g) {
+                                uint32_t p[16];
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[8 * i + e]) * inv;
-                                *reinterpret_cast<uint4 *>(dst + 32 * q + 8 * i) = pack8(x);
+                                for (int i = 0; i < 16; ++i) p[i] = o[16 * g + i];
+                                ep::quad_transpose(p, qi);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    if (on[k])
+                                        *reinterpret_cast<uint4 *>(w.part_o + off[k] + 32 * q + 16 * g + 4 * qi) =
+                                            make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
                             }
+                        } else {
+                            uint32_t p[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                p[i] = pack2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+                            ep::quad_transpose(p, qi);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (on[k])
+                                    *reinterpret_cast<uint4 *>(w.out + off[k] + 32 * q + 8 * qi) =
+                                        make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
                         }
                     }
                 }
