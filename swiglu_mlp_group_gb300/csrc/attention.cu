@@ -11,12 +11,17 @@
 // for the whole batch, which is what makes the shared part a matrix product
 // instead of B vector ones.
 //
-// Items.  The work is a list of items -- rows of one key head x a chunk of keys
-// -- that a persistent grid walks with a stride.  More than one row tile makes
-// a wide item: two row tiles against the same key tiles.  Otherwise an item is
-// narrow: one row tile, its key tiles taken alternately by the two halves of
-// the pipeline.  Chunks (and the halves of a narrow item) leave partial sums
-// with their maximum in the workspace; a second kernel joins them.
+// Items.  A group is the row tiles of one key head that go together, against
+// the prefix or against a sequence's own keys; an item is a group x a run of its
+// key tiles.  More than one row tile makes a group wide: two row tiles against
+// the same key tiles.  A narrow item's key tiles are taken alternately by the two
+// halves of the pipeline, which add up what they have at its end.
+// Every CTA gets an equal share of the whole work (Share below): an equal run of
+// the prefix of a group, and a run of the sequence of all groups' own key tiles,
+// cut where its share ends.  Pieces of a row leave partial sums with their
+// maximum in the workspace, and a second kernel joins them.  Without a prefix,
+// and with groups enough for every SM or keys for two tiles at most, whole
+// groups are dealt out and written directly.
 //
 // Pipeline (one CTA per SM, 11 warps).  Two streams, each with its own S and O
 // in TMEM and four softmax warps, so that the tensor core works on one while
@@ -62,8 +67,15 @@ struct Cfg {
     static constexpr int kHalfBytes = kKeys * 128;
     static constexpr int kTileBytes = kHalves * kHalfBytes;
     static constexpr int kSlots = D == 128 ? 5 : 10;  // ring of K and V tiles: 160 KB
-    static constexpr int kBarBytes = 512;
-    static constexpr size_t kSmemBytes = static_cast<size_t>(2 + kSlots) * kTileBytes + kBarBytes + 1024;
+    static constexpr int kBarBytes = 512;  // barriers, TMEM address, abort flag, Share
+    // maximum and sum of a row, [stream][row]: what the streams of a narrow item
+    // tell each other (before the first item: the work's division)
+    static constexpr int kExchangeBytes = 2 * kRows * 8;
+    // the last 512: tiles start at a multiple of 1024 also where the block's
+    // shared memory starts at one of 512
+    static constexpr size_t kSmemBytes =
+        static_cast<size_t>(2 + kSlots) * kTileBytes + kBarBytes + kExchangeBytes + 512;
+    static_assert(kSmemBytes <= 227 * 1024);
 };
 
 // What the kernels take: sizes, pointers and the split of the work.
@@ -78,16 +90,29 @@ struct Work {
     int prefix_len, max_len;
     bool causal;
     float scale_log2;  // scale * log2(e)
-    // prefix items: rt_p row items x Hkv x split_p chunks; own: rt_o x Hkv x B x split_o
-    int wide_p, wide_o, tok_p, tok_o;  // tok: query tokens of one tile
-    int rt_p, rt_o, chunk_p, chunk_o;  // chunk: keys
-    int items_p, items;
-    int slots_p, slots;                // partial results of a row; slots = 0: written to out directly
-    float *part_o;                     // [slots][T * Hq][D]
-    float2 *part_ml;                   // [slots][T * Hq]: log2-scaled maximum, sum
+    // groups: rt_p x Hkv against the prefix, rt_o x Hkv x B against own keys
+    bool wide_p, wide_o;
+    int tok_p, tok_o;  // query tokens of one tile
+    int rt_p, rt_o;
+    int tiles_p, tiles_o;  // key tiles of the prefix, of the longest sequence
+    bool direct;           // own groups whole, nothing to join
+    int sms;               // CTAs to share the work among
+    int cost_p, cost_o;    // cost of a key tile (a group's or item's own is kItemCost)
+    int min_o;             // own tiles a CTA is given at least, if any
+    int slots_p, slots_o;  // most parts of a row: against the prefix, own
+    int *parts;            // [0]: parts of a prefix group; then [B][Hkv][rt_o]: of each own group that has keys
+    float *part_o;         // [slots_p + slots_o][T * Hq][D]
+    float2 *part_ml;       // the same [..][..]: log2-scaled maximum, sum
     unsigned int *status;
     unsigned long long timeout_ns;
 };
+
+// Cost units: a sixteenth of a narrow key tile's time (cost_o of one).  A wide
+// tile is 3/2 of one: it is bound by its products and exponentials (2465 cycles,
+// two row tiles), a narrow one by the K and V it streams -- 64 KB, 2790 cycles
+// when all SMs stream at once, some 1300 alone.  An item's query loads and
+// result cost about one narrow tile.
+constexpr int kTileCost = 16, kWideTileCost = 24, kItemCost = 16;
 
 struct Item {
     int b;             // sequence; -1: prefix
@@ -96,58 +121,201 @@ struct Item {
     int tok;           // tokens of one tile
     int key0, nkeys;   // its keys
     int lim0, lim_step;  // token t sees the keys below lim0 + lim_step * t
-    int slot;
+    int slot;            // where its partial result goes
+    int own_parts;       // the last piece of an own group: how many there are, else 0
     bool wide;
+    bool whole;          // all keys of its rows: written to out
 };
 
-// The length of sequence b; out of range: the nearer end (`bad` is set).
-__device__ __forceinline__ int own_len(const Work &w, int b, bool &bad) {
-    if (!w.lens) return w.max_len;
-    const int n = w.lens[b];
-    bad = n < 0 || n > w.max_len;
-    return min(max(n, 0), w.max_len);
+// What this CTA does, worked out once.
+struct Share {
+    int parts_p, chunk_p, items_p;  // a prefix group's parts, tiles of one, parts of all groups
+    int ctas;                       // CTAs that take part
+    // own key tiles from (sequence, group of it, tile) to (.., .., ..)
+    int b_lo, r_lo, t_lo, b_hi, r_hi, t_hi;
+    int part_lo;                    // number of the first piece within its group
+};
+
+// The length of sequence b; out of range: the nearer end.
+__device__ __forceinline__ int own_len(const Work &w, int b) {
+    return w.lens ? min(max(w.lens[b], 0), w.max_len) : w.max_len;
+}
+__device__ __forceinline__ int tiles_of(int keys) { return (keys + kKeys - 1) / kKeys; }
+
+// The work's division, by all threads of the block (`scratch`: 1 KB of shared
+// memory).  Prefix groups are cut into equal parts of at most a CTA's share, dealt out in
+// turn -- row tiles of the same keys side by side, so that they pass over them
+// together and the keys are read from HBM once -- and own tiles, in order, fill
+// every CTA's share up.
+template <int THREADS>
+__device__ void divide(const Work &w, Share &sh, int64_t *scratch) {
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    constexpr int kWarps = THREADS / 32;
+    const int groups = w.Hkv * w.rt_o;  // of one sequence
+    // own cost up to this thread's run of sequences
+    const int run = w.tiles_o > 0 ? (w.B + THREADS - 1) / THREADS : 0;
+    const int b0 = min(t * run, w.B), b1 = min(b0 + run, w.B);
+    auto group_cost = [&](int b) { return kItemCost + tiles_of(own_len(w, b)) * w.cost_o; };
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        mine += static_cast<int64_t>(groups) * group_cost(b);
+    }
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) scratch[warp] = upto;
+    if (t == 0) sh.b_lo = sh.b_hi = w.B, sh.r_lo = sh.t_lo = sh.r_hi = sh.t_hi = sh.part_lo = 0;
+    __syncthreads();
+    int64_t own = 0;
+    for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) upto += scratch[i];
+        own += scratch[i];
+    }
+    const int64_t before = upto - mine;
+
+    // CTAs that take part: two narrow tiles each at least
+    const int64_t group_p = kItemCost + static_cast<int64_t>(w.tiles_p) * w.cost_p;
+    const int64_t prefix = w.tiles_p > 0 ? static_cast<int64_t>(w.rt_p) * w.Hkv * group_p : 0;
+    const int64_t least = kItemCost + 2 * kTileCost;
+    const int n = static_cast<int>(min(static_cast<int64_t>(w.sms), max((prefix + own) / least, static_cast<int64_t>(1))));
+    const int64_t share = (prefix + own + n - 1) / n;
+    // prefix: equal parts of at most a share
+    int parts = 0, chunk = 0, items = 0;
+    int64_t part_cost = 0;
+    if (w.tiles_p > 0) {
+        const int64_t room = max(share - kItemCost, static_cast<int64_t>(w.cost_p));
+        parts = static_cast<int>(min((static_cast<int64_t>(w.tiles_p) * w.cost_p + room - 1) / room,
+                                     static_cast<int64_t>(w.slots_p)));
+        chunk = (w.tiles_p + parts - 1) / parts;
+        parts = (w.tiles_p + chunk - 1) / chunk;
+        items = parts * w.rt_p * w.Hkv;
+        part_cost = kItemCost + static_cast<int64_t>(chunk) * w.cost_p;
+    }
+    // own: CTAs below `many` have one prefix part more than the others; each has
+    // len_a or len_b of the own cost
+    const int each = items / n, many = items - each * n;
+    const int64_t least_o = static_cast<int64_t>(w.min_o) * w.cost_o;
+    int64_t room_a = share - (each + 1) * part_cost, room_b = share - each * part_cost;
+    if (room_a < least_o || many == 0) room_a = 0;
+    if (room_b < least_o) room_a = room_b = share;  // too little for its own CTAs: all take some
+    const int64_t room = many * room_a + (n - many) * room_b;
+    const int64_t len_a = room_a == 0 ? 0 : max(least_o, (room_a * own + room - 1) / room);
+    const int64_t len_b = max(least_o, (room_b * own + room - 1) / room);
+    auto start = [&](int64_t cta) { return cta < many ? cta * len_a : many * len_a + (cta - many) * len_b; };
+    const int cta = blockIdx.x;
+    const int64_t lo = min(cta < n ? start(cta) : own, own), hi = min(cta < n ? start(cta + 1) : own, own);
+    if (t == 0) {
+        sh.parts_p = parts, sh.chunk_p = chunk, sh.items_p = items, sh.ctas = n;
+        if (cta == 0) w.parts[0] = parts;
+    }
+    // the tile at or behind a cost: by the thread whose sequences hold it
+    int64_t at = before;
+    if (mine > 0 && ((lo >= before && lo < upto) || (hi >= before && hi < upto))) {
+        for (int b = b0; b < b1; ++b) {
+            const int64_t g = group_cost(b), all = g * groups;
+            for (int end = 0; end < 2; ++end) {
+                const int64_t x = (end ? hi : lo) - at;
+                if (x < 0 || x >= all) continue;
+                const int r = static_cast<int>(x / g);
+                const int64_t off = x - r * g - kItemCost;
+                const int tile = off <= 0 ? 0 : static_cast<int>((off + w.cost_o - 1) / w.cost_o);
+                if (end) {
+                    sh.b_hi = b, sh.r_hi = r, sh.t_hi = tile;
+                } else {
+                    sh.b_lo = b, sh.r_lo = r, sh.t_lo = tile;
+                    const int64_t first = at + r * g + kItemCost;  // its first tile
+                    const int64_t of = first < many * len_a ? first / len_a : many + (first - many * len_a) / len_b;
+                    if (tile > 0) sh.part_lo = min(static_cast<int>(cta - of), w.slots_o - 1);
+                }
+            }
+            at += all;
+        }
+    }
+    __syncthreads();
 }
 
-__device__ __forceinline__ Item decode(const Work &w, int idx, bool &bad_len) {
-    Item it;
-    bad_len = false;
-    if (idx < w.items_p) {
-        const int rt = idx % w.rt_p;
-        int r = idx / w.rt_p;
-        it.h = r % w.Hkv;
-        r /= w.Hkv;
-        it.b = -1;
-        it.wide = w.wide_p;
-        it.tok = w.tok_p;
-        it.tok0 = rt * it.tok * (it.wide ? 2 : 1);
-        it.tok_end = min(w.T, it.tok0 + it.tok * (it.wide ? 2 : 1));
-        it.key0 = r * w.chunk_p;
-        it.nkeys = min(w.chunk_p, w.prefix_len - it.key0);
-        it.lim0 = w.prefix_len, it.lim_step = 0;
-        it.slot = it.wide ? r : 2 * r;
-    } else {
-        idx -= w.items_p;
-        const int rt = idx % w.rt_o;
-        int r = idx / w.rt_o;
-        it.h = r % w.Hkv;
-        r /= w.Hkv;
-        it.b = r % w.B;
-        r /= w.B;
+// The items of this CTA, one after the other; every role walks them alike.
+struct Walk {
+    int next_p, b, r, tiles, len;
+
+    __device__ Walk(const Work &w, const Share &sh)
+        : next_p(blockIdx.x), b(w.direct ? 0 : sh.b_lo), r(w.direct ? 0 : sh.r_lo), tiles(-1), len(0) {}
+
+    // Tiles t0 .. t1 - 1 of group r of sequence b.
+    __device__ void own_item(const Work &w, Item &it, int t0, int t1) const {
+        const int rt = r % w.rt_o;
+        it.h = r / w.rt_o;
+        it.b = b;
         it.wide = w.wide_o;
         it.tok = w.tok_o;
-        const int first = it.b * w.Lq;
-        it.tok0 = first + rt * it.tok * (it.wide ? 2 : 1);
-        it.tok_end = min(first + w.Lq, it.tok0 + it.tok * (it.wide ? 2 : 1));
-        const int len = own_len(w, it.b, bad_len);
+        const int first = b * w.Lq, rows = it.tok * (it.wide ? 2 : 1);
+        it.tok0 = first + rt * rows;
+        it.tok_end = min(first + w.Lq, it.tok0 + rows);
         it.lim_step = w.causal ? 1 : 0;
         it.lim0 = w.causal ? len - w.Lq + 1 - first : len;
-        it.key0 = r * w.chunk_o;
+        it.key0 = t0 * kKeys;
         const int last = min(len, it.lim0 + it.lim_step * (it.tok_end - 1));
-        it.nkeys = max(0, min(w.chunk_o, last - it.key0));
-        it.slot = w.slots_p + (it.wide ? r : 2 * r);
+        it.nkeys = max(0, min(t1 * kKeys, last) - it.key0);
     }
-    return it;
-}
+
+    __device__ bool next(const Work &w, const Share &sh, Item &it) {
+        if (w.direct) {
+            const int groups = w.Hkv * w.rt_o;
+            if (next_p >= groups * w.B) return false;
+            b = next_p / groups;
+            r = next_p - b * groups;
+            len = own_len(w, b);
+            own_item(w, it, 0, tiles_of(len));
+            it.whole = true;
+            it.slot = it.own_parts = 0;
+            next_p += gridDim.x;
+            return true;
+        }
+        if (next_p < sh.items_p) {
+            const int rt = next_p % w.rt_p, hc = next_p / w.rt_p;
+            it.h = hc / sh.parts_p;
+            it.slot = hc - it.h * sh.parts_p;
+            it.b = -1;
+            it.wide = w.wide_p;
+            it.tok = w.tok_p;
+            const int rows = it.tok * (it.wide ? 2 : 1);
+            it.tok0 = rt * rows;
+            it.tok_end = min(w.T, it.tok0 + rows);
+            it.key0 = it.slot * sh.chunk_p * kKeys;
+            it.nkeys = min(sh.chunk_p * kKeys, w.prefix_len - it.key0);
+            it.lim0 = w.prefix_len, it.lim_step = 0;
+            it.own_parts = 0;
+            it.whole = false;
+            next_p += sh.ctas;
+            if (static_cast<int>(blockIdx.x) >= sh.ctas) next_p = sh.items_p;
+            else return true;
+        }
+        while (b < sh.b_hi || (b == sh.b_hi && (r < sh.r_hi || (r == sh.r_hi && sh.t_hi > 0)))) {
+            if (tiles < 0) {
+                len = own_len(w, b);
+                tiles = tiles_of(len);
+            }
+            const bool first = b == sh.b_lo && r == sh.r_lo;
+            const bool end = b == sh.b_hi && r == sh.r_hi;
+            const int t0 = first ? sh.t_lo : 0, t1 = end ? min(sh.t_hi, tiles) : tiles;
+            const bool some = t0 < t1;
+            if (some) {
+                const int part = first ? sh.part_lo : 0;
+                own_item(w, it, t0, t1);
+                it.whole = w.tiles_p == 0 && t0 == 0 && t1 == tiles;
+                it.slot = w.slots_p + part;
+                it.own_parts = t1 == tiles ? part + 1 : 0;
+            }
+            if (tiles == 0) r = w.Hkv * w.rt_o - 1;  // none of its groups has any
+            if (++r == w.Hkv * w.rt_o) ++b, r = 0, tiles = -1;
+            if (some) return true;
+        }
+        return false;
+    }
+};
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -210,10 +378,14 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
     auto p_full = [&](int i, int half) { return bars_s + 8u * (2 * NS + 6 + 2 * i + half); };
     auto o_full = [&](int i) { return bars_s + 8u * (2 * NS + 10 + i); };  // its P V is in O
     auto pv_issued = [&](int i) { return bars_s + 8u * (2 * NS + 12 + i); };
-    const uint32_t done_bar = bars_s + 8u * (2 * NS + 14);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * NS + 15);
+    // the same rows' warps of both streams are at the end of a narrow item
+    auto met = [&](int q) { return bars_s + 8u * (2 * NS + 14 + q); };
+    const uint32_t done_bar = bars_s + 8u * (2 * NS + 18);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * NS + 19);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    static_assert(8 * (2 * NS + 15) + 8 <= C::kBarBytes);
+    Share &share = *reinterpret_cast<Share *>(tmem_slot + 2);
+    static_assert(8 * (2 * NS + 19) + 8 + sizeof(Share) <= C::kBarBytes);
+    float2 *const xml = reinterpret_cast<float2 *>(smem + (2 + NS) * C::kTileBytes + C::kBarBytes);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // uniform for the compiler too
     const int lane = threadIdx.x & 31;
@@ -233,6 +405,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             mbar_init(o_full(i), 1);
             mbar_init(pv_issued(i), 1);
         }
+        for (int q = 0; q < 4; ++q) mbar_init(met(q), 2);
         mbar_init(done_bar, 2);
         *abort_flag = 0;
         fence_mbar_init();
@@ -249,6 +422,11 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
     auto tO = [&](int st) { return tmem + 256u + static_cast<uint32_t>(D) * st; };
     pdl_launch_dependents();
     pdl_wait();
+    if (blockIdx.x == 0 && w.lens) {
+        for (int b = threadIdx.x; b < w.B; b += kThreads)
+            if (w.lens[b] < 0 || w.lens[b] > w.max_len) atomicOr(w.status, kDeviceStatusIndex);
+    }
+    if (!w.direct) divide<kThreads>(w, share, reinterpret_cast<int64_t *>(xml));
 
     // Every role walks the same items and key tiles with the same counters:
     // J, key tiles so far (K in ring position 2 J, V in 2 J + 1); step, S tiles
@@ -259,6 +437,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
         if (warp == kTmaWarp) {
             // ------------------------------------------------------------ TMA
             uint32_t seq = 0, nar = 0;
+            Item it;
             uint32_t qpar = 0, qused = 0;  // bit i: parity of query buffer i's next use, used at all
             bool ok = true;
             if (elect_one()) {
@@ -269,11 +448,8 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             }
             __syncwarp();
 #pragma unroll 1
-            for (int idx = blockIdx.x; idx < w.items && ok; idx += gridDim.x) {
-                bool bad = false;
-                const Item it = decode(w, idx, bad);
-                if (bad && lane == 0) atomicOr(w.status, kDeviceStatusIndex);
-                const int ntiles = (it.nkeys + kKeys - 1) / kKeys;
+            for (Walk walk(w, share); ok && walk.next(w, share, it);) {
+                const int ntiles = tiles_of(it.nkeys);
                 const int32_t *table = it.b < 0 ? w.prefix_pages : w.block_table + it.b * w.table_stride;
 #pragma unroll 1
                 for (int j = 0; j < ntiles && ok; ++j) {
@@ -302,7 +478,6 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                             __syncwarp();
                             if (lane < npages) {
 #pragma unroll 1
-        #pragma unroll 1
                             for (int hf = 0; hf < C::kHalves; ++hf)
                                     tma_load_2d(sKV(s) + hf * C::kHalfBytes + lane * w.page_size * 128, map, kv_full(s),
                                                 hf * 64, row);
@@ -328,8 +503,6 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                                 if (!ok) break;
                                 if (elect_one()) {
                                     mbar_arrive_expect_tx(q_full(buf), it.tok * w.G * 128 * C::kHalves);
-        #pragma unroll 1
-        #pragma unroll 1
                             for (int hf = 0; hf < C::kHalves; ++hf)
                                         tma_load_3d(sQ(buf) + hf * C::kHalfBytes, qm, q_full(buf), hf * 64, it.h * w.G,
                                                     it.tok0 + i * it.tok);
@@ -372,18 +545,18 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             const uint64_t kd0 = sdesc_kmajor_sw128(sKV(0));
             const uint64_t vd0 = sdesc_mnmajor_sw128(sKV(0), C::kHalfBytes);
             bool ok = true;
+            Item it;
             int step = 0, nar = 0;
             int slot = is_qk ? 0 : 1;  // ring position of the tile's K / V
             uint32_t par = 0;          // its parity
             uint32_t qpar = 0;         // bit i: parity of query buffer i
             uint32_t spar = 0;         // bit i: parity of stream i: QK: its P V issued; PV: its P
 #pragma unroll 1
-            for (int idx = blockIdx.x; idx < w.items && ok; idx += gridDim.x) {
-                bool bad;
-                const Item it = decode(w, idx, bad);
+            for (Walk walk(w, share); ok && walk.next(w, share, it);) {
                 const int nkeys = __shfl_sync(0xffffffffu, it.nkeys, 0);
-                const int ntiles = (nkeys + kKeys - 1) / kKeys;
-                const int subs = it.wide ? 2 : 1;
+                const bool wide = __shfl_sync(0xffffffffu, it.wide, 0);
+                const int ntiles = tiles_of(nkeys);
+                const int subs = wide ? 2 : 1;
 #pragma unroll 1
                 for (int j = 0; j < ntiles && ok; ++j) {
                     ok = __all_sync(0xffffffffu, mbar_wait_spin(kv_full(slot), par, ctl));
@@ -394,7 +567,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
 #pragma unroll 1
                         for (int sub = 0; sub < subs; ++sub, ++step) {
                             const int st = step & 1;
-                            const int buf = it.wide ? st : nar & 1;
+                            const int buf = wide ? st : nar & 1;
                             if (j == 0) {
                                 ok = __all_sync(0xffffffffu, mbar_wait_spin(q_full(buf), (qpar >> buf) & 1, ctl));
                                 if (!ok) break;
@@ -441,7 +614,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                         for (int sub = 0; sub < subs; ++sub, ++step) {
                             const int st = step & 1;
                             const uint32_t o = tO(st), p = tS(st);
-                            const bool first = it.wide ? j == 0 : j < 2;
+                            const bool first = wide ? j == 0 : j < 2;
                             ok = __all_sync(0xffffffffu, mbar_wait_spin(p_full(st, 0), (spar >> st) & 1, ctl));
                             if (!ok) break;
                             tc_fence_after_sync();
@@ -471,7 +644,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                     slot += 2;
                     if (slot >= NS) slot -= NS, par ^= 1;
                 }
-                if (!it.wide && ntiles > 0) ++nar;
+                if (!wide && ntiles > 0) ++nar;
             }
             // no MMA may be in flight when TMEM is released
             if (elect_one()) {
@@ -491,12 +664,18 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
         const int Hq = w.Hkv * w.G;
         const int64_t rows = static_cast<int64_t>(w.T) * Hq;
         const float c = w.scale_log2;
-        uint32_t step = 0, cnt = 0;
+        uint32_t step = 0, cnt = 0, meets = 0;
         bool ok = true;
-        for (int idx = blockIdx.x; idx < w.items && ok; idx += gridDim.x) {
-            bool bad;
-            const Item it = decode(w, idx, bad);
-            const int ntiles = (it.nkeys + kKeys - 1) / kKeys;
+        // both warps of these rows have got here (a bounded wait, unlike bar.sync)
+        auto meet = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(met(warp & 3));
+            return __all_sync(0xffffffffu, mbar_wait_spin(met(warp & 3), meets++ & 1, ctl)) != 0;
+        };
+        Item it;
+#pragma unroll 1
+        for (Walk walk(w, share); ok && walk.next(w, share, it);) {
+            const int ntiles = tiles_of(it.nkeys);
             const int tok = it.tok0 + (it.wide ? st * it.tok : 0) + row_tok;
             const bool live = row_tok < it.tok && tok < it.tok_end;
             const bool warp_live = __any_sync(0xffffffffu, live);
@@ -582,68 +761,114 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             }
             if (!ok) break;
             if (it.wide) step += 2 * ntiles;
-            // the item's result
+            // The item's result.  A wide item's rows are this stream's own.  A
+            // narrow one's are both streams': each adds up one half of the
+            // columns of the two accumulators, as a join of two parts would.
             if (done > 0) {
                 ok = __all_sync(0xffffffffu, mbar_wait_spin(o_full(st), (cnt - 1) & 1, ctl));
                 if (!ok) break;
-                tc_fence_after_sync();
             }
+            float m = mref == -INFINITY ? mref : mref * c;
+            float f_mine = 1.f, f_other = 0.f;
+            bool other = false;
+            if (!it.wide && ntiles > 1) {
+                tc_fence_before_sync();
+                xml[st * kRows + row] = make_float2(m, l);
+                ok = meet();
+                if (!ok) break;
+                const float2 o = xml[(1 - st) * kRows + row];
+                const float top = fmaxf(l != 0.f ? m : -INFINITY, o.y != 0.f ? o.x : -INFINITY);
+                f_mine = l != 0.f ? ex2(m - top) : 0.f;
+                f_other = o.y != 0.f ? ex2(o.x - top) : 0.f;
+                l = f_mine * l + f_other * o.y;
+                m = top;
+                other = true;
+            }
+            tc_fence_after_sync();
+            const bool part = !it.whole;
+            // columns of this stream; a narrow item of one tile is its stream's alone
+            const int col0 = other ? st * (D / 2) : 0, col1 = other ? col0 + D / 2 : (it.wide || done > 0 ? D : 0);
+            const bool reports = it.wide || (ntiles > 0 ? (other ? st == 0 : done > 0) : st == 0);
             if (warp_live) {
                 // Stored through a 4 x 4 transpose of 16-byte pieces within each
                 // quad of lanes: an instruction then writes 64 bytes of 8 rows
-                // instead of 16 bytes of 32.
+                // instead of 16 bytes of 32.  A few rows are not worth it.
                 const int64_t at = static_cast<int64_t>(tok) * Hq + it.h * w.G + row_g;
-                const bool part = w.slots > 0;
-                const int64_t pr = part ? (it.slot + (it.wide ? 0 : st)) * rows + at : 0;
-                if (part && live) w.part_ml[pr] = make_float2(mref == -INFINITY ? mref : mref * c, l);
-                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const int64_t pr = part ? it.slot * rows + at : 0;
+                if (part && live && reports) w.part_ml[pr] = make_float2(m, l);
+                if (it.own_parts > 0 && !w.direct && threadIdx.x == 0)
+                    w.parts[1 + (it.b * w.Hkv + it.h) * w.rt_o + (it.tok0 - it.b * w.Lq) / (it.tok * (it.wide ? 2 : 1))] =
+                        it.own_parts;
+                const bool empty = ntiles == 0;  // zeros, if written at all
+                const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
+                f_mine *= inv, f_other *= inv;
+                const bool use_mine = f_mine != 0.f, use_other = f_other != 0.f;
                 const int64_t mine = part ? pr * D : tok * w.ldo + static_cast<int64_t>(it.h * w.G + row_g) * D;
                 const int qi = lane & 3;
-                int64_t off[4];
-                bool on[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    off[k] = __shfl_sync(0xffffffffu, mine, (lane & ~3) + k);
-                    on[k] = __shfl_sync(0xffffffffu, live, (lane & ~3) + k);
-                }
-                if (done > 0 || !part) {
+                const bool few = __popc(__ballot_sync(0xffffffffu, live)) <= 8;
+                const int last = empty ? (part || !(it.wide || st == 0) ? 0 : D) : col1;
 #pragma unroll 1
-                    for (int q = 0; q < D / 32; ++q) {
-                        uint32_t o[32];
-                        if (done > 0) {
-                            tmem_ld_32x32b_x32(to + 32u * q, o);
-                            tmem_wait_ld(o);
-                        } else {
+                for (int col = col0; col < last; col += 32) {
+                    uint32_t o[32];
+                    if (empty) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = 0;
-                        }
-                        if (part) {
+                        for (int i = 0; i < 32; ++i) o[i] = 0;
+                    } else {
+                        tmem_ld_32x32b_x32(to + static_cast<uint32_t>(col), o);
+                        tmem_wait_ld(o);
 #pragma unroll
-                            for (int g = 0; g < 2; ++g) {
-                                uint32_t p[16];
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = use_mine ? __float_as_uint(__uint_as_float(o[i]) * f_mine) : 0u;
+                        if (other) {
+                            uint32_t p[32];
+                            tmem_ld_32x32b_x32(tO(1 - st) + lanes + static_cast<uint32_t>(col), p);
+                            tmem_wait_ld(p);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) p[i] = o[16 * g + i];
-                                ep::quad_transpose(p, qi);
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    if (on[k])
-                                        *reinterpret_cast<uint4 *>(w.part_o + off[k] + 32 * q + 16 * g + 4 * qi) =
-                                            make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
-                            }
-                        } else {
-                            uint32_t p[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                p[i] = pack2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-                            ep::quad_transpose(p, qi);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                if (on[k])
-                                    *reinterpret_cast<uint4 *>(w.out + off[k] + 32 * q + 8 * qi) =
-                                        make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
+                            for (int i = 0; i < 32; ++i)
+                                if (use_other)
+                                    o[i] = __float_as_uint(fmaf(__uint_as_float(p[i]), f_other, __uint_as_float(o[i])));
                         }
                     }
+                    auto put = [&](uint32_t (&p)[16], void *base, int64_t off16) {
+                        // 16 words of every row, off16: in 16-byte units from base
+                        uint4 *dst = static_cast<uint4 *>(base);
+                        if (few) {
+                            if (live) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    dst[off16 + k] = make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
+                            }
+                            return;
+                        }
+                        ep::quad_transpose(p, qi);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int64_t to_row = __shfl_sync(0xffffffffu, off16, (lane & ~3) + k);
+                            if (__shfl_sync(0xffffffffu, live, (lane & ~3) + k))
+                                dst[to_row + qi] = make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
+                        }
+                    };
+                    uint32_t p[16];
+                    if (part) {
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) p[i] = o[16 * g + i];
+                            put(p, w.part_o, (mine + col + 16 * g) / 4);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            p[i] = pack2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+                        put(p, w.out, (mine + col) / 8);
+                    }
                 }
+            }
+            if (other) {
+                // the next item's products and maxima come after the other
+                // stream has read this one's
+                tc_fence_before_sync();
+                ok = meet();
             }
         }
     }
@@ -657,36 +882,64 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
 }
 
 // out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over a row's partial
-// results (M their largest m); a warp per row.  Parts with l = 0 saw no key and
-// have no o.
+// results (M their largest m): the parts against the prefix, then the own ones;
+// a warp per row.  Parts with l = 0 saw no key and may have no o.
 template <int D>
 __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ Work w) {
     pdl_launch_dependents();
-    pdl_wait();
     const int Hq = w.Hkv * w.G;
     const int64_t rows = static_cast<int64_t>(w.T) * Hq;
     const int lane = threadIdx.x & 31;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     if (row >= rows) return;
+    const int tok = static_cast<int>(row / Hq), hq = static_cast<int>(row - static_cast<int64_t>(tok) * Hq);
+    const int b = tok / w.Lq, rt = (tok - b * w.Lq) / (w.tok_o * (w.wide_o ? 2 : 1));
+    pdl_wait();
+    const int np = w.tiles_p > 0 ? w.parts[0] : 0;
+    const int no = own_len(w, b) > 0 ? w.parts[1 + (b * w.Hkv + hq / w.G) * w.rt_o + rt] : 0;
+    if (np == 0 && no == 1) return;  // written by the item itself
+    const int n = np + no;
     constexpr int E = D / 32;
-    float M = -INFINITY;
-    for (int s = 0; s < w.slots; ++s) {
-        const float2 ml = w.part_ml[s * rows + row];
-        if (ml.y != 0.f) M = fmaxf(M, ml.x);
-    }
-    float L = 0.f, o[E] = {};
-    for (int s = 0; s < w.slots; ++s) {
-        const float2 ml = w.part_ml[s * rows + row];
-        if (ml.y == 0.f) continue;
-        const float f = ex2(ml.x - M);
-        L = fmaf(f, ml.y, L);
-        const float *src = w.part_o + (s * rows + row) * D + lane * E;
+    float M = -INFINITY, L = 0.f, o[E] = {};
+    for (int s0 = 0; s0 < n; s0 += 32) {
+        // up to 32 parts: a lane each for their maxima and sums
+        float2 ml = make_float2(-INFINITY, 0.f);
+        const int s = s0 + lane;
+        if (s < n) ml = w.part_ml[(s < np ? s : w.slots_p + s - np) * rows + row];
+        float top = ml.y != 0.f ? ml.x : -INFINITY;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(f, src[e], o[e]);
+        for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+        const float m_new = fmaxf(M, top);
+        const float f = ml.y != 0.f ? ex2(ml.x - m_new) : 0.f;
+        const float keep = L != 0.f ? ex2(M - m_new) : 0.f;
+        float sum = f * ml.y;
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+        L = L * keep + sum;
+        M = m_new;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] *= keep;
+        const int here = min(32, n - s0);
+#pragma unroll 4
+        for (int i = 0; i < here; ++i) {
+            const float fi = __shfl_sync(0xffffffffu, f, i);
+            if (fi == 0.f) continue;
+            const int si = s0 + i;
+            const float *src = w.part_o + ((si < np ? si : w.slots_p + si - np) * rows + row) * D + lane * E;
+            float x[E];
+            if constexpr (E == 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(src);
+                x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+            } else {
+                const float2 v = *reinterpret_cast<const float2 *>(src);
+                x[0] = v.x, x[1] = v.y;
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = fmaf(fi, x[e], o[e]);
+        }
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    const int64_t tok = row / Hq;
-    uint16_t *dst = w.out + tok * w.ldo + (row - tok * Hq) * D + lane * E;
+    uint16_t *dst = w.out + tok * w.ldo + static_cast<int64_t>(hq) * D + lane * E;
 #pragma unroll
     for (int e = 0; e < E; e += 2)
         *reinterpret_cast<uint32_t *>(dst + e) = pack2(o[e] * inv, o[e + 1] * inv);
@@ -698,10 +951,6 @@ constexpr int kPlanSms = 152;
 
 int div_up(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
-// How the work is cut.  Rows come first: two row tiles an item where there are
-// more than one.  Keys are cut where the rows alone leave SMs idle, into at
-// least 4 tiles a chunk (a chunk's partial result costs about as much to write
-// and join as half a key tile to read).
 Work plan(const AttentionArgs &a) {
     Work w = {};
     w.B = static_cast<int>(a.B), w.Lq = static_cast<int>(a.Lq), w.T = static_cast<int>(a.B * a.Lq);
@@ -714,41 +963,39 @@ Work plan(const AttentionArgs &a) {
     w.wide_p = w.T > tokens, w.wide_o = w.Lq > tokens;
     w.rt_p = div_up(w.T, w.tok_p * (w.wide_p ? 2 : 1));
     w.rt_o = div_up(w.Lq, w.tok_o * (w.wide_o ? 2 : 1));
-    const int64_t tiles_p = div_up(w.prefix_len, kKeys), tiles_o = div_up(w.max_len, kKeys);
+    w.tiles_p = div_up(w.prefix_len, kKeys), w.tiles_o = div_up(w.max_len, kKeys);
+    w.cost_p = w.wide_p ? kWideTileCost : kTileCost, w.cost_o = w.wide_o ? kWideTileCost : kTileCost;
+    w.sms = kPlanSms;
     const int64_t base_p = static_cast<int64_t>(w.rt_p) * w.Hkv, base_o = static_cast<int64_t>(w.rt_o) * w.Hkv * w.B;
-    // tiles of a chunk: the whole work spread over twice the SMs
-    const int64_t steps = base_p * tiles_p * (w.wide_p ? 2 : 1) + base_o * tiles_o * (w.wide_o ? 2 : 1);
-    const int64_t share = steps / (2 * kPlanSms) + 1;
-    auto chunk = [&](int64_t tiles, bool wide) {
-        int64_t n = wide ? (share + 1) / 2 : share;
-        if (n < 4) n = 4;
-        if (n > tiles) n = tiles;
-        const int64_t parts = (tiles + n - 1) / n;
-        return (tiles + parts - 1) / parts;  // equal parts
-    };
-    int64_t split_p = 0, split_o = 0;
-    if (tiles_p > 0) {
-        const int64_t n = chunk(tiles_p, w.wide_p);
-        w.chunk_p = static_cast<int>(n) * kKeys;
-        split_p = (tiles_p + n - 1) / n;
+    // Whole groups where they are many (at 4 a SM the last round leaves at most
+    // a quarter idle, about what partial results and their join would cost) or
+    // short (two tiles run side by side in a narrow group).
+    w.direct = w.tiles_p == 0 && (base_o >= 4 * kPlanSms || w.tiles_o <= 2);
+    if (w.direct) return w;
+    // a group's parts: as many as CTAs can find work in, of two tiles at least;
+    // own pieces of a sixteenth of the longest at least
+    if (w.tiles_p > 0) {
+        const int64_t most = kPlanSms / base_p + 1;
+        w.slots_p = static_cast<int>(most < w.tiles_p ? most : w.tiles_p);
     }
-    if (tiles_o > 0) {
-        const int64_t n = chunk(tiles_o, w.wide_o);
-        w.chunk_o = static_cast<int>(n) * kKeys;
-        split_o = (tiles_o + n - 1) / n;
+    if (w.tiles_o > 0) {
+        w.min_o = w.tiles_o > 32 ? div_up(w.tiles_o, 16) : 2;
+        // a piece in the middle of a group is min_o tiles at least
+        w.slots_o = (w.tiles_o - 1) / w.min_o + 2;
+    } else {
+        w.min_o = 1;
     }
-    // no key at all: one empty own chunk writes the zeros
-    if (split_p + split_o == 0) split_o = 1, w.chunk_o = kKeys;
-    w.items_p = static_cast<int>(base_p * split_p);
-    w.items = static_cast<int>(w.items_p + base_o * split_o);
-    w.slots_p = static_cast<int>(split_p) * (w.wide_p ? 1 : 2);
-    w.slots = w.slots_p + static_cast<int>(split_o) * (w.wide_o ? 1 : 2);
-    if (w.slots == 1) w.slots_p = w.slots = 0;
     return w;
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
-size_t ml_bytes(const Work &w) { return round256(static_cast<size_t>(w.slots) * w.T * w.Hkv * w.G * sizeof(float2)); }
+int64_t part_rows(const Work &w) {
+    return static_cast<int64_t>(w.slots_p + w.slots_o) * w.T * w.Hkv * w.G;
+}
+size_t parts_bytes(const Work &w) {
+    return round256((1 + static_cast<size_t>(w.B) * w.Hkv * w.rt_o) * sizeof(int));
+}
+size_t ml_bytes(const Work &w) { return round256(static_cast<size_t>(part_rows(w)) * sizeof(float2)); }
 
 bool row_map(CUtensorMap *m, const AttentionArgs &a, int tokens) {
     const uint64_t dims[3] = {static_cast<uint64_t>(a.D), static_cast<uint64_t>(a.Hq),
@@ -794,14 +1041,17 @@ cudaError_t launch(const AttentionArgs &a, Work &w, const LaunchCtx &ctx) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(w.items < sms ? w.items : sms));
+    // planned for kPlanSms; fewer SMs share the same work
+    if (sms < w.sms) w.sms = sms;
+    const int64_t groups = static_cast<int64_t>(w.rt_o) * w.Hkv * w.B;
+    cfg.gridDim = dim3(static_cast<unsigned>(w.direct && groups < sms ? groups : w.direct ? sms : w.sms));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = ctx.stream;
     cfg.attrs = attr;
     cfg.numAttrs = ctx.pdl ? 1 : 0;
     if (cudaError_t e = cudaLaunchKernelEx(&cfg, kern, qp, qo, km, vm, w); e != cudaSuccess) return e;
-    if (w.slots == 0) return cudaSuccess;
+    if (w.direct) return cudaSuccess;
     const int64_t rows = static_cast<int64_t>(w.T) * w.Hkv * w.G;
     cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));
     cfg.blockDim = dim3(256);
@@ -813,8 +1063,8 @@ cudaError_t launch(const AttentionArgs &a, Work &w, const LaunchCtx &ctx) {
 
 size_t attention_workspace_bytes(const AttentionArgs &a) {
     const Work w = plan(a);
-    if (w.slots == 0) return 0;
-    return ml_bytes(w) + static_cast<size_t>(w.slots) * w.T * w.Hkv * w.G * a.D * sizeof(float);
+    if (w.direct) return 0;
+    return parts_bytes(w) + ml_bytes(w) + static_cast<size_t>(part_rows(w)) * a.D * sizeof(float);
 }
 
 cudaError_t launch_attention(const AttentionArgs &a, const LaunchCtx &ctx) {
@@ -823,9 +1073,11 @@ cudaError_t launch_attention(const AttentionArgs &a, const LaunchCtx &ctx) {
     w.page_size = a.pages > 0 ? a.page_size : 0, w.pages = static_cast<int>(a.pages);
     w.prefix_pages = a.prefix_pages, w.block_table = a.block_table, w.lens = a.lens, w.table_stride = a.table_stride;
     w.scale_log2 = a.scale * kLog2e;
-    if (w.slots > 0) {
-        w.part_ml = static_cast<float2 *>(a.ws);
-        w.part_o = reinterpret_cast<float *>(static_cast<char *>(a.ws) + ml_bytes(w));
+    if (!w.direct) {
+        char *p = static_cast<char *>(a.ws);
+        w.parts = reinterpret_cast<int *>(p);
+        w.part_ml = reinterpret_cast<float2 *>(p + parts_bytes(w));
+        w.part_o = reinterpret_cast<float *>(p + parts_bytes(w) + ml_bytes(w));
     }
     w.status = ctx.status;
     w.timeout_ns = ctx.timeout_ns;
