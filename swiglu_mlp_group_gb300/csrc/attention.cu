@@ -700,7 +700,8 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                     if (lane == 0) mbar_arrive(p_full(st, half));
                 };
                 if (warp_live) {
-                    const int vis = live ? min(max(limit - it.key0 - key, 0), valid) : 0;
+                    // rows of no query hold what they like: not worth a mask
+                    const int vis = live ? min(max(limit - it.key0 - key, 0), valid) : kKeys;
                     tmem_ld_32x32b_x32(ts, sr[0]);
                     tmem_ld_32x32b_x32(ts + 32u, sr[1]);
                     tmem_wait_ld(sr[0]);
