@@ -16,14 +16,15 @@
 // key tiles.  More than one row tile makes a group wide: two row tiles against
 // the same key tiles.  A narrow item's key tiles are taken alternately by the two
 // halves of the pipeline, which add up what they have at its end.
-// Every CTA gets an equal share of the whole work (Share below): an equal run of
-// the prefix of a group, and a run of the sequence of all groups' own key tiles,
-// cut where its share ends.  Pieces of a row leave partial sums with their
-// maximum in the workspace, and a second kernel joins them.  Without a prefix,
-// and with groups enough for every SM or keys for two tiles at most, whole
-// groups are dealt out and written directly.
+// Little work is dealt out in fixed chunks of key tiles, an item a CTA.  Of more,
+// every CTA gets an equal share (divide below): an equal run of the prefix of a
+// group, and a run of the sequence of all groups' own key tiles, cut where its
+// share ends.  Pieces of a row leave partial sums with their maximum in the
+// workspace, and a second kernel joins them.  Without a prefix, and with groups
+// enough for every SM or keys for two tiles at most, whole groups are dealt out
+// and written directly.
 //
-// Pipeline (one CTA per SM, 11 warps).  Two streams, each with its own S and O
+// Pipeline (one CTA per SM, 12 warps).  Two streams, each with its own S and O
 // in TMEM and four softmax warps, so that the tensor core works on one while
 // the other is in its softmax:
 //   warps 0..3, 4..7 : softmax of stream 0 / 1, a thread per row: S from TMEM,
@@ -31,6 +32,8 @@
 //   warp 8           : TMA: query tiles, and K and V tiles into a ring.
 //   warps 9, 10      : MMA issue: S = Q K^T, O += P V.  Their steps alternate
 //                      between the streams.
+//   warp 11          : works the CTA's items out, ahead of the others, and hands
+//                      them round in a ring.
 // P is rounded to bf16 for the second product, the operand type of V; its sum
 // is taken in f32 before that rounding.
 #include <math.h>
@@ -46,8 +49,10 @@ namespace {
 
 constexpr int kRows = 128;     // rows of a query tile
 constexpr int kKeys = 128;     // keys of a key tile
-constexpr int kTmaWarp = 8, kQkWarp = 9, kPvWarp = 10;
-constexpr int kThreads = 384;  // 8 softmax warps, TMA, 2 MMA, 1 idle (register shares go by 4 warps)
+constexpr int kTmaWarp = 8, kQkWarp = 9, kPvWarp = 10, kWalkWarp = 11;
+constexpr int kItems = 4;    // items in the ring
+constexpr int kReaders = 11; // warps that read them
+constexpr int kThreads = 384;  // 8 softmax warps, TMA, 2 MMA, items
 // Registers a thread: 168 at launch; the softmax holds a row of 128 scores.
 // 256 x 208 + 128 x 88 = 384 x 168.
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
@@ -67,14 +72,15 @@ struct Cfg {
     static constexpr int kHalfBytes = kKeys * 128;
     static constexpr int kTileBytes = kHalves * kHalfBytes;
     static constexpr int kSlots = D == 128 ? 5 : 10;  // ring of K and V tiles: 160 KB
-    static constexpr int kBarBytes = 512;  // barriers, TMEM address, abort flag, Share
+    static constexpr int kBarBytes = 768;  // barriers, TMEM address, abort flag, Share, items
     // maximum and sum of a row, [stream][row]: what the streams of a narrow item
     // tell each other (before the first item: the work's division)
     static constexpr int kExchangeBytes = 2 * kRows * 8;
-    // the last 512: tiles start at a multiple of 1024 also where the block's
-    // shared memory starts at one of 512
+    // the last 256: tiles start at a multiple of 1024, as the block's shared
+    // memory does by its alignment; with what is left of 227 KB they also do
+    // where it starts 256 short of one
     static constexpr size_t kSmemBytes =
-        static_cast<size_t>(2 + kSlots) * kTileBytes + kBarBytes + kExchangeBytes + 512;
+        static_cast<size_t>(2 + kSlots) * kTileBytes + kBarBytes + kExchangeBytes + 256;
     static_assert(kSmemBytes <= 227 * 1024);
 };
 
@@ -96,11 +102,14 @@ struct Work {
     int rt_p, rt_o;
     int tiles_p, tiles_o;  // key tiles of the prefix, of the longest sequence
     bool direct;           // own groups whole, nothing to join
+    // Fixed chunks: parts of a group against the prefix, own (tiles of one:
+    // chunk), CTA i taking items i, i + grid, ...; chunk_o 0: shares by cost.
+    int parts_p, chunk_p, parts_o, chunk_o;
     int sms;               // CTAs to share the work among
     int cost_p, cost_o;    // cost of a key tile (a group's or item's own is kItemCost)
     int min_o;             // own tiles a CTA is given at least, if any
     int slots_p, slots_o;  // most parts of a row: against the prefix, own
-    int *parts;            // [0]: parts of a prefix group; then [B][Hkv][rt_o]: of each own group that has keys
+    int *parts;            // by cost: [0]: parts of a prefix group; then [B][Hkv][rt_o]: of each own group that has keys
     float *part_o;         // [slots_p + slots_o][T * Hq][D]
     float2 *part_ml;       // the same [..][..]: log2-scaled maximum, sum
     unsigned int *status;
@@ -122,10 +131,12 @@ struct Item {
     int key0, nkeys;   // its keys
     int lim0, lim_step;  // token t sees the keys below lim0 + lim_step * t
     int slot;            // where its partial result goes
-    int own_parts;       // the last piece of an own group: how many there are, else 0
-    bool wide;
-    bool whole;          // all keys of its rows: written to out
+    int own_parts;       // by cost, the last piece of an own group: how many there are, else 0
+    int flags;           // kWide, kWhole
 };
+constexpr int kWide = 1;
+constexpr int kWhole = 2;  // all keys of its rows: written to out
+constexpr int kEnd = -1;   // nkeys of what follows the last item
 
 // What this CTA does, worked out once.
 struct Share {
@@ -142,6 +153,13 @@ __device__ __forceinline__ int own_len(const Work &w, int b) {
 }
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + kKeys - 1) / kKeys; }
 
+// x / d; by the 32-bit division where both are that small (a 64-bit one takes
+// some 500 cycles).
+__device__ __forceinline__ int64_t quotient64(int64_t x, int64_t d) {
+    return (x | d) >> 32 == 0 ? static_cast<uint32_t>(x) / static_cast<uint32_t>(d) : x / d;
+}
+__device__ __forceinline__ int quotient(int64_t x, int64_t d) { return static_cast<int>(quotient64(x, d)); }
+
 // The work's division, by all threads of the block (`scratch`: 1 KB of shared
 // memory).  Prefix groups are cut into equal parts of at most a CTA's share, dealt out in
 // turn -- row tiles of the same keys side by side, so that they pass over them
@@ -157,9 +175,7 @@ __device__ void divide(const Work &w, Share &sh, int64_t *scratch) {
     const int b0 = min(t * run, w.B), b1 = min(b0 + run, w.B);
     auto group_cost = [&](int b) { return kItemCost + tiles_of(own_len(w, b)) * w.cost_o; };
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        mine += static_cast<int64_t>(groups) * group_cost(b);
-    }
+    for (int b = b0; b < b1; ++b) mine += static_cast<int64_t>(groups) * group_cost(b);
     int64_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -180,15 +196,14 @@ __device__ void divide(const Work &w, Share &sh, int64_t *scratch) {
     const int64_t group_p = kItemCost + static_cast<int64_t>(w.tiles_p) * w.cost_p;
     const int64_t prefix = w.tiles_p > 0 ? static_cast<int64_t>(w.rt_p) * w.Hkv * group_p : 0;
     const int64_t least = kItemCost + 2 * kTileCost;
-    const int n = static_cast<int>(min(static_cast<int64_t>(w.sms), max((prefix + own) / least, static_cast<int64_t>(1))));
-    const int64_t share = (prefix + own + n - 1) / n;
+    const int n = prefix + own >= least * w.sms ? w.sms : max(quotient(prefix + own, least), 1);
+    const int64_t share = quotient64(prefix + own + n - 1, n);
     // prefix: equal parts of at most a share
     int parts = 0, chunk = 0, items = 0;
     int64_t part_cost = 0;
     if (w.tiles_p > 0) {
         const int64_t room = max(share - kItemCost, static_cast<int64_t>(w.cost_p));
-        parts = static_cast<int>(min((static_cast<int64_t>(w.tiles_p) * w.cost_p + room - 1) / room,
-                                     static_cast<int64_t>(w.slots_p)));
+        parts = min(quotient(static_cast<int64_t>(w.tiles_p) * w.cost_p + room - 1, room), w.slots_p);
         chunk = (w.tiles_p + parts - 1) / parts;
         parts = (w.tiles_p + chunk - 1) / chunk;
         items = parts * w.rt_p * w.Hkv;
@@ -202,11 +217,14 @@ __device__ void divide(const Work &w, Share &sh, int64_t *scratch) {
     if (room_a < least_o || many == 0) room_a = 0;
     if (room_b < least_o) room_a = room_b = share;  // too little for its own CTAs: all take some
     const int64_t room = many * room_a + (n - many) * room_b;
-    const int64_t len_a = room_a == 0 ? 0 : max(least_o, (room_a * own + room - 1) / room);
-    const int64_t len_b = max(least_o, (room_b * own + room - 1) / room);
+    // (rounded up: the last CTAs get what is left)
+    const float fill = static_cast<float>(own) / static_cast<float>(room);
+    const int64_t len_a = room_a == 0 ? 0 : max(least_o, static_cast<int64_t>(static_cast<float>(room_a) * fill) + 1);
+    const int64_t len_b = max(least_o, static_cast<int64_t>(static_cast<float>(room_b) * fill) + 1);
     auto start = [&](int64_t cta) { return cta < many ? cta * len_a : many * len_a + (cta - many) * len_b; };
     const int cta = blockIdx.x;
-    const int64_t lo = min(cta < n ? start(cta) : own, own), hi = min(cta < n ? start(cta + 1) : own, own);
+    const int64_t lo = min(cta < n ? start(cta) : own, own);
+    const int64_t hi = min(cta < n - 1 ? start(cta + 1) : own, own);
     if (t == 0) {
         sh.parts_p = parts, sh.chunk_p = chunk, sh.items_p = items, sh.ctas = n;
         if (cta == 0) w.parts[0] = parts;
@@ -219,16 +237,19 @@ __device__ void divide(const Work &w, Share &sh, int64_t *scratch) {
             for (int end = 0; end < 2; ++end) {
                 const int64_t x = (end ? hi : lo) - at;
                 if (x < 0 || x >= all) continue;
-                const int r = static_cast<int>(x / g);
+                const int r = quotient(x, g);
                 const int64_t off = x - r * g - kItemCost;
-                const int tile = off <= 0 ? 0 : static_cast<int>((off + w.cost_o - 1) / w.cost_o);
+                const int tile = off <= 0 ? 0 : quotient(off + w.cost_o - 1, w.cost_o);
                 if (end) {
                     sh.b_hi = b, sh.r_hi = r, sh.t_hi = tile;
                 } else {
                     sh.b_lo = b, sh.r_lo = r, sh.t_lo = tile;
                     const int64_t first = at + r * g + kItemCost;  // its first tile
-                    const int64_t of = first < many * len_a ? first / len_a : many + (first - many * len_a) / len_b;
-                    if (tile > 0) sh.part_lo = min(static_cast<int>(cta - of), w.slots_o - 1);
+                    if (tile > 0) {
+                        const int of = first < many * len_a ? quotient(first, len_a)
+                                                            : many + quotient(first - many * len_a, len_b);
+                        sh.part_lo = min(cta - min(of, n - 1), w.slots_o - 1);
+                    }
                 }
             }
             at += all;
@@ -237,21 +258,18 @@ __device__ void divide(const Work &w, Share &sh, int64_t *scratch) {
     __syncthreads();
 }
 
-// The items of this CTA, one after the other; every role walks them alike.
+// The items of this CTA, one after the other.
 struct Walk {
-    int next_p, b, r, tiles, len;
+    int idx, b, r, tiles, len;
 
-    __device__ Walk(const Work &w, const Share &sh)
-        : next_p(blockIdx.x), b(w.direct ? 0 : sh.b_lo), r(w.direct ? 0 : sh.r_lo), tiles(-1), len(0) {}
-
-    // Tiles t0 .. t1 - 1 of group r of sequence b.
+    // Key tiles t0 .. t1 - 1 of group r of sequence b.
     __device__ void own_item(const Work &w, Item &it, int t0, int t1) const {
-        const int rt = r % w.rt_o;
         it.h = r / w.rt_o;
+        const int rt = r - it.h * w.rt_o;
         it.b = b;
-        it.wide = w.wide_o;
+        it.flags = w.wide_o ? kWide : 0;
         it.tok = w.tok_o;
-        const int first = b * w.Lq, rows = it.tok * (it.wide ? 2 : 1);
+        const int first = b * w.Lq, rows = it.tok * (w.wide_o ? 2 : 1);
         it.tok0 = first + rt * rows;
         it.tok_end = min(first + w.Lq, it.tok0 + rows);
         it.lim_step = w.causal ? 1 : 0;
@@ -259,40 +277,61 @@ struct Walk {
         it.key0 = t0 * kKeys;
         const int last = min(len, it.lim0 + it.lim_step * (it.tok_end - 1));
         it.nkeys = max(0, min(t1 * kKeys, last) - it.key0);
+        it.own_parts = 0;
+    }
+    // Part `part` of the prefix, `chunk` tiles, for row item rt of key head h.
+    __device__ void prefix_item(const Work &w, Item &it, int rt, int h, int part, int chunk) const {
+        it.b = -1;
+        it.h = h;
+        it.flags = w.wide_p ? kWide : 0;
+        it.tok = w.tok_p;
+        const int rows = it.tok * (w.wide_p ? 2 : 1);
+        it.tok0 = rt * rows;
+        it.tok_end = min(w.T, it.tok0 + rows);
+        it.key0 = part * chunk * kKeys;
+        it.nkeys = min(chunk * kKeys, w.prefix_len - it.key0);
+        it.lim0 = w.prefix_len, it.lim_step = 0;
+        it.slot = part;
+        it.own_parts = 0;
     }
 
-    __device__ bool next(const Work &w, const Share &sh, Item &it) {
-        if (w.direct) {
-            const int groups = w.Hkv * w.rt_o;
-            if (next_p >= groups * w.B) return false;
-            b = next_p / groups;
-            r = next_p - b * groups;
+    __device__ bool next_fixed(const Work &w, Item &it) {
+        const int items_p = w.rt_p * w.Hkv * w.parts_p, groups = w.Hkv * w.rt_o;
+        const int items_o = groups * w.B * w.parts_o;
+        while (idx < items_p + items_o) {
+            int i = idx;
+            idx += gridDim.x;
+            if (i < items_p) {
+                const int hc = i / w.rt_p, h = hc / w.parts_p;
+                prefix_item(w, it, i - hc * w.rt_p, h, hc - h * w.parts_p, w.chunk_p);
+                return true;
+            }
+            i -= items_p;
+            const int bc = i / groups, part = bc / w.B;
+            r = i - bc * groups;
+            b = bc - part * w.B;
             len = own_len(w, b);
-            own_item(w, it, 0, tiles_of(len));
-            it.whole = true;
-            it.slot = it.own_parts = 0;
-            next_p += gridDim.x;
+            tiles = tiles_of(len);
+            const int t0 = part * w.chunk_o, t1 = min(t0 + w.chunk_o, tiles);
+            // a chunk past its end; one without keys is an item where there is
+            // nothing else of its rows
+            if (t0 >= tiles && (t0 > 0 || w.tiles_p > 0)) continue;
+            own_item(w, it, t0, t1);
+            if (w.tiles_p == 0 && tiles <= w.chunk_o) it.flags |= kWhole;
+            it.slot = w.slots_p + part;
             return true;
         }
-        if (next_p < sh.items_p) {
-            const int rt = next_p % w.rt_p, hc = next_p / w.rt_p;
-            it.h = hc / sh.parts_p;
-            it.slot = hc - it.h * sh.parts_p;
-            it.b = -1;
-            it.wide = w.wide_p;
-            it.tok = w.tok_p;
-            const int rows = it.tok * (it.wide ? 2 : 1);
-            it.tok0 = rt * rows;
-            it.tok_end = min(w.T, it.tok0 + rows);
-            it.key0 = it.slot * sh.chunk_p * kKeys;
-            it.nkeys = min(sh.chunk_p * kKeys, w.prefix_len - it.key0);
-            it.lim0 = w.prefix_len, it.lim_step = 0;
-            it.own_parts = 0;
-            it.whole = false;
-            next_p += sh.ctas;
-            if (static_cast<int>(blockIdx.x) >= sh.ctas) next_p = sh.items_p;
-            else return true;
+        return false;
+    }
+
+    __device__ bool next_share(const Work &w, const Share &sh, Item &it) {
+        if (idx < sh.items_p && static_cast<int>(blockIdx.x) < sh.ctas) {
+            const int hc = idx / w.rt_p, h = hc / sh.parts_p;
+            prefix_item(w, it, idx - hc * w.rt_p, h, hc - h * sh.parts_p, sh.chunk_p);
+            idx += sh.ctas;
+            return true;
         }
+        const int groups = w.Hkv * w.rt_o;
         while (b < sh.b_hi || (b == sh.b_hi && (r < sh.r_hi || (r == sh.r_hi && sh.t_hi > 0)))) {
             if (tiles < 0) {
                 len = own_len(w, b);
@@ -305,12 +344,12 @@ struct Walk {
             if (some) {
                 const int part = first ? sh.part_lo : 0;
                 own_item(w, it, t0, t1);
-                it.whole = w.tiles_p == 0 && t0 == 0 && t1 == tiles;
+                if (w.tiles_p == 0 && t0 == 0 && t1 == tiles) it.flags |= kWhole;
                 it.slot = w.slots_p + part;
                 it.own_parts = t1 == tiles ? part + 1 : 0;
             }
-            if (tiles == 0) r = w.Hkv * w.rt_o - 1;  // none of its groups has any
-            if (++r == w.Hkv * w.rt_o) ++b, r = 0, tiles = -1;
+            if (tiles == 0) r = groups - 1;  // none of its groups has any
+            if (++r == groups) ++b, r = 0, tiles = -1;
             if (some) return true;
         }
         return false;
@@ -380,11 +419,14 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
     auto pv_issued = [&](int i) { return bars_s + 8u * (2 * NS + 12 + i); };
     // the same rows' warps of both streams are at the end of a narrow item
     auto met = [&](int q) { return bars_s + 8u * (2 * NS + 14 + q); };
-    const uint32_t done_bar = bars_s + 8u * (2 * NS + 18);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * NS + 19);
+    auto item_full = [&](int i) { return bars_s + 8u * (2 * NS + 18 + i); };
+    auto item_empty = [&](int i) { return bars_s + 8u * (2 * NS + 18 + kItems + i); };
+    const uint32_t done_bar = bars_s + 8u * (2 * NS + 18 + 2 * kItems);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * NS + 19 + 2 * kItems);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     Share &share = *reinterpret_cast<Share *>(tmem_slot + 2);
-    static_assert(8 * (2 * NS + 19) + 8 + sizeof(Share) <= C::kBarBytes);
+    Item *const ring = reinterpret_cast<Item *>(&share + 1);
+    static_assert(8 * (2 * NS + 19 + 2 * kItems) + 8 + sizeof(Share) + kItems * sizeof(Item) <= C::kBarBytes);
     float2 *const xml = reinterpret_cast<float2 *>(smem + (2 + NS) * C::kTileBytes + C::kBarBytes);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // uniform for the compiler too
@@ -406,6 +448,10 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             mbar_init(pv_issued(i), 1);
         }
         for (int q = 0; q < 4; ++q) mbar_init(met(q), 2);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(item_full(i), 1);
+            mbar_init(item_empty(i), kReaders);
+        }
         mbar_init(done_bar, 2);
         *abort_flag = 0;
         fence_mbar_init();
@@ -426,7 +472,19 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
         for (int b = threadIdx.x; b < w.B; b += kThreads)
             if (w.lens[b] < 0 || w.lens[b] > w.max_len) atomicOr(w.status, kDeviceStatusIndex);
     }
-    if (!w.direct) divide<kThreads>(w, share, reinterpret_cast<int64_t *>(xml));
+    if (w.chunk_o == 0) divide<kThreads>(w, share, reinterpret_cast<int64_t *>(xml));
+
+    // The next item, in every lane of a reading warp; false after the last.
+    uint32_t items = 0;
+    auto next_item = [&](Item &it) {
+        const uint32_t i = items % kItems;
+        if (!__all_sync(0xffffffffu, mbar_wait_spin(item_full(i), (items / kItems) & 1, ctl))) return false;
+        it = ring[i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(item_empty(i));
+        ++items;
+        return it.nkeys != kEnd;
+    };
 
     // Every role walks the same items and key tiles with the same counters:
     // J, key tiles so far (K in ring position 2 J, V in 2 J + 1); step, S tiles
@@ -448,8 +506,9 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             }
             __syncwarp();
 #pragma unroll 1
-            for (Walk walk(w, share); ok && walk.next(w, share, it);) {
+            while (ok && next_item(it)) {
                 const int ntiles = tiles_of(it.nkeys);
+                const bool wide = it.flags & kWide;
                 const int32_t *table = it.b < 0 ? w.prefix_pages : w.block_table + it.b * w.table_stride;
 #pragma unroll 1
                 for (int j = 0; j < ntiles && ok; ++j) {
@@ -497,8 +556,8 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                             // buffers are free once the last item's S are done
                             const CUtensorMap *qm = it.b < 0 ? &qmap_p : &qmap_o;
 #pragma unroll 1
-                            for (int i = 0; i < (it.wide ? 2 : 1) && ok; ++i) {
-                                const int buf = it.wide ? i : static_cast<int>(nar & 1);
+                            for (int i = 0; i < (wide ? 2 : 1) && ok; ++i) {
+                                const int buf = wide ? i : static_cast<int>(nar & 1);
                                 ok = __all_sync(0xffffffffu, mbar_wait_spin(q_empty(buf), ((qpar >> buf) & 1) ^ 1, ctl));
                                 if (!ok) break;
                                 if (elect_one()) {
@@ -514,7 +573,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                         }
                     }
                 }
-                if (!it.wide && ntiles > 0) ++nar;
+                if (!wide && ntiles > 0) ++nar;
             }
             if (*abort_flag && elect_one()) {
                 // let the copies still in flight land before the CTA exits
@@ -524,6 +583,25 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                     if ((qused >> i) & 1) mbar_wait_drain(q_full(i), ((qpar >> i) & 1) ^ 1, w.timeout_ns, w.status);
             }
             __syncwarp();
+        } else if (warp == kWalkWarp) {
+            // ------------------------------------------------------------ items
+            Walk walk;
+            walk.idx = blockIdx.x, walk.tiles = -1, walk.len = 0;
+            walk.b = w.chunk_o > 0 ? 0 : share.b_lo, walk.r = w.chunk_o > 0 ? 0 : share.r_lo;
+            bool more = true;
+#pragma unroll 1
+            for (uint32_t n = 0; more; ++n) {
+                Item it;
+                more = w.chunk_o > 0 ? walk.next_fixed(w, it) : walk.next_share(w, share, it);
+                if (!more) it.nkeys = kEnd;
+                const uint32_t i = n % kItems;
+                if (!__all_sync(0xffffffffu, mbar_wait_spin(item_empty(i), ((n / kItems) & 1) ^ 1, ctl))) break;
+                if (lane == 0) {
+                    ring[i] = it;
+                    mbar_arrive(item_full(i));
+                }
+                __syncwarp();
+            }
         } else if (warp == kQkWarp || warp == kPvWarp) {
             // ------------------------------------------------------------ MMA
             // One warp issues S = Q K^T of every step, one O += P V; both take
@@ -552,9 +630,9 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             uint32_t qpar = 0;         // bit i: parity of query buffer i
             uint32_t spar = 0;         // bit i: parity of stream i: QK: its P V issued; PV: its P
 #pragma unroll 1
-            for (Walk walk(w, share); ok && walk.next(w, share, it);) {
+            while (ok && next_item(it)) {
                 const int nkeys = __shfl_sync(0xffffffffu, it.nkeys, 0);
-                const bool wide = __shfl_sync(0xffffffffu, it.wide, 0);
+                const bool wide = __shfl_sync(0xffffffffu, it.flags, 0) & kWide;
                 const int ntiles = tiles_of(nkeys);
                 const int subs = wide ? 2 : 1;
 #pragma unroll 1
@@ -674,16 +752,17 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
         };
         Item it;
 #pragma unroll 1
-        for (Walk walk(w, share); ok && walk.next(w, share, it);) {
+        while (ok && next_item(it)) {
             const int ntiles = tiles_of(it.nkeys);
-            const int tok = it.tok0 + (it.wide ? st * it.tok : 0) + row_tok;
+            const bool wide = it.flags & kWide;
+            const int tok = it.tok0 + (wide ? st * it.tok : 0) + row_tok;
             const bool live = row_tok < it.tok && tok < it.tok_end;
             const bool warp_live = __any_sync(0xffffffffu, live);
             const int limit = it.lim0 + it.lim_step * tok;
             float mref = -INFINITY, l = 0.f;
             int done = 0;  // tiles of this stream
             for (int j = 0; j < ntiles; ++j) {
-                if (!it.wide) {
+                if (!wide) {
                     if (static_cast<int>(step++ & 1) != st) continue;
                 }
                 ok = __all_sync(0xffffffffu, mbar_wait_spin(s_full(st), cnt & 1, ctl));
@@ -761,7 +840,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                 ++done;
             }
             if (!ok) break;
-            if (it.wide) step += 2 * ntiles;
+            if (wide) step += 2 * ntiles;
             // The item's result.  A wide item's rows are this stream's own.  A
             // narrow one's are both streams': each adds up one half of the
             // columns of the two accumulators, as a join of two parts would.
@@ -772,7 +851,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             float m = mref == -INFINITY ? mref : mref * c;
             float f_mine = 1.f, f_other = 0.f;
             bool other = false;
-            if (!it.wide && ntiles > 1) {
+            if (!wide && ntiles > 1) {
                 tc_fence_before_sync();
                 xml[st * kRows + row] = make_float2(m, l);
                 ok = meet();
@@ -786,10 +865,10 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                 other = true;
             }
             tc_fence_after_sync();
-            const bool part = !it.whole;
+            const bool part = !(it.flags & kWhole);
             // columns of this stream; a narrow item of one tile is its stream's alone
-            const int col0 = other ? st * (D / 2) : 0, col1 = other ? col0 + D / 2 : (it.wide || done > 0 ? D : 0);
-            const bool reports = it.wide || (ntiles > 0 ? (other ? st == 0 : done > 0) : st == 0);
+            const int col0 = other ? st * (D / 2) : 0, col1 = other ? col0 + D / 2 : (wide || done > 0 ? D : 0);
+            const bool reports = wide || (ntiles > 0 ? (other ? st == 0 : done > 0) : st == 0);
             if (warp_live) {
                 // Stored through a 4 x 4 transpose of 16-byte pieces within each
                 // quad of lanes: an instruction then writes 64 bytes of 8 rows
@@ -798,7 +877,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                 const int64_t pr = part ? it.slot * rows + at : 0;
                 if (part && live && reports) w.part_ml[pr] = make_float2(m, l);
                 if (it.own_parts > 0 && !w.direct && threadIdx.x == 0)
-                    w.parts[1 + (it.b * w.Hkv + it.h) * w.rt_o + (it.tok0 - it.b * w.Lq) / (it.tok * (it.wide ? 2 : 1))] =
+                    w.parts[1 + (it.b * w.Hkv + it.h) * w.rt_o + (it.tok0 - it.b * w.Lq) / (it.tok * (wide ? 2 : 1))] =
                         it.own_parts;
                 const bool empty = ntiles == 0;  // zeros, if written at all
                 const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
@@ -807,7 +886,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                 const int64_t mine = part ? pr * D : tok * w.ldo + static_cast<int64_t>(it.h * w.G + row_g) * D;
                 const int qi = lane & 3;
                 const bool few = __popc(__ballot_sync(0xffffffffu, live)) <= 8;
-                const int last = empty ? (part || !(it.wide || st == 0) ? 0 : D) : col1;
+                const int last = empty ? (part || !(wide || st == 0) ? 0 : D) : col1;
 #pragma unroll 1
                 for (int col = col0; col < last; col += 32) {
                     uint32_t o[32];
@@ -896,8 +975,11 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
     const int tok = static_cast<int>(row / Hq), hq = static_cast<int>(row - static_cast<int64_t>(tok) * Hq);
     const int b = tok / w.Lq, rt = (tok - b * w.Lq) / (w.tok_o * (w.wide_o ? 2 : 1));
     pdl_wait();
-    const int np = w.tiles_p > 0 ? w.parts[0] : 0;
-    const int no = own_len(w, b) > 0 ? w.parts[1 + (b * w.Hkv + hq / w.G) * w.rt_o + rt] : 0;
+    const int own = tiles_of(own_len(w, b));
+    const bool fixed = w.chunk_o > 0;
+    const int np = fixed ? w.parts_p : w.tiles_p > 0 ? w.parts[0] : 0;
+    const int no = fixed ? (own + w.chunk_o - 1) / w.chunk_o
+                         : own > 0 ? w.parts[1 + (b * w.Hkv + hq / w.G) * w.rt_o + rt] : 0;
     if (np == 0 && no == 1) return;  // written by the item itself
     const int n = np + no;
     constexpr int E = D / 32;
@@ -972,7 +1054,25 @@ Work plan(const AttentionArgs &a) {
     // a quarter idle, about what partial results and their join would cost) or
     // short (two tiles run side by side in a narrow group).
     w.direct = w.tiles_p == 0 && (base_o >= 4 * kPlanSms || w.tiles_o <= 2);
-    if (w.direct) return w;
+    if (w.direct) {
+        w.parts_o = 1, w.chunk_o = w.tiles_o > 0 ? w.tiles_o : 1;
+        return w;
+    }
+    // Fixed chunks where every one has an SM of its own: the smallest of two tiles
+    // or more for which that holds, if it is no more than four or the tiles there
+    // may be keep half of the SMs busy.
+    if (base_p * (w.tiles_p > 0) + base_o * (w.tiles_o > 0) <= kPlanSms) {
+        auto items = [&](int64_t c) { return base_p * ((w.tiles_p + c - 1) / c) + base_o * ((w.tiles_o + c - 1) / c); };
+        const int64_t all = base_p * w.tiles_p + base_o * w.tiles_o;
+        int64_t c = all / kPlanSms > 2 ? all / kPlanSms : 2;
+        while (items(c) > kPlanSms) ++c;
+        if (c <= 4 || all >= c * kPlanSms / 2) {
+            w.chunk_p = w.chunk_o = static_cast<int>(c);
+            w.parts_p = w.slots_p = div_up(w.tiles_p, c);
+            w.parts_o = w.slots_o = div_up(w.tiles_o, c);
+            return w;
+        }
+    }
     // a group's parts: as many as CTAs can find work in, of two tiles at least;
     // own pieces of a sixteenth of the longest at least
     if (w.tiles_p > 0) {
@@ -1045,7 +1145,8 @@ cudaError_t launch(const AttentionArgs &a, Work &w, const LaunchCtx &ctx) {
     // planned for kPlanSms; fewer SMs share the same work
     if (sms < w.sms) w.sms = sms;
     const int64_t groups = static_cast<int64_t>(w.rt_o) * w.Hkv * w.B;
-    cfg.gridDim = dim3(static_cast<unsigned>(w.direct && groups < sms ? groups : w.direct ? sms : w.sms));
+    const int64_t most = w.chunk_o > 0 ? static_cast<int64_t>(w.rt_p) * w.Hkv * w.parts_p + groups * w.parts_o : sms;
+    cfg.gridDim = dim3(static_cast<unsigned>(most < sms ? most : w.chunk_o > 0 ? sms : w.sms));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = ctx.stream;

@@ -89,13 +89,24 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const W
     }
 }
 
-// mbar_wait that polls a while before it looks at the time: where a phase is
-// due within microseconds, reading the timer delays the wake-up.
+// mbar_wait that looks at the time and the abort flag only at every 64th poll:
+// where a phase is due within microseconds, reading the timer delays the
+// wake-up.  One short loop, for kernels with many waits.
 __device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity, const WaitCtl &ctl) {
+    uint64_t t0 = 0;
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
+    for (uint32_t n = 1;; ++n) {
         if (mbar_try_wait(bar, parity)) return true;
-    return mbar_wait(bar, parity, ctl);
+        if (n % 64 != 0) continue;
+        if (*ctl.abort_flag) return false;
+        const uint64_t t = globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > ctl.timeout_ns) {
+            *ctl.abort_flag = 1;
+            atomicOr(ctl.status, kDeviceStatusTimeout);
+            return false;
+        }
+    }
 }
 
 // Wait that ignores the CTA's abort flag, bounded in time: lets copies or MMAs
