@@ -55,7 +55,8 @@ constexpr int kReaders = 11; // warps that read them
 constexpr int kThreads = 384;  // 8 softmax warps, TMA, 2 MMA, items
 // Registers a thread: 168 at launch; the softmax holds a row of 128 scores.
 // 256 x 208 + 128 x 88 = 384 x 168.
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs == kThreads * kLaunchRegs && kThreads * kLaunchRegs <= 65536);
 // Keys of a tile whose P is handed over first: P V of them runs while the last
 // exponentials are taken.
 constexpr int kFirstKeys = 96;
@@ -466,8 +467,8 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
     const uint32_t tmem = *tmem_slot;
     auto tS = [&](int st) { return tmem + 128u * st; };
     auto tO = [&](int st) { return tmem + 256u + static_cast<uint32_t>(D) * st; };
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();  // the join may read the lengths before it waits
     if (blockIdx.x == 0 && w.lens) {
         for (int b = threadIdx.x; b < w.B; b += kThreads)
             if (w.lens[b] < 0 || w.lens[b] > w.max_len) atomicOr(w.status, kDeviceStatusIndex);
@@ -883,9 +884,30 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                 const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
                 f_mine *= inv, f_other *= inv;
                 const bool use_mine = f_mine != 0.f, use_other = f_other != 0.f;
-                const int64_t mine = part ? pr * D : tok * w.ldo + static_cast<int64_t>(it.h * w.G + row_g) * D;
+                // in 16-byte units; the rows of this lane's quad
+                const int64_t mine = part ? pr * (D / 4) : (tok * w.ldo + static_cast<int64_t>(it.h * w.G + row_g) * D) / 8;
+                uint4 *const dst = part ? reinterpret_cast<uint4 *>(w.part_o) : reinterpret_cast<uint4 *>(w.out);
                 const int qi = lane & 3;
-                const bool few = __popc(__ballot_sync(0xffffffffu, live)) <= 8;
+                int64_t off[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) off[k] = __shfl_sync(0xffffffffu, mine, (lane & ~3) + k) + qi;
+                const uint32_t lives = __ballot_sync(0xffffffffu, live), on = lives >> (lane & ~3);
+                const bool few = __popc(lives) <= 8;
+                auto put = [&](uint32_t (&p)[16], int piece) {
+                    if (few) {
+                        if (live) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                dst[mine + 4 * piece + k] = make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
+                        }
+                        return;
+                    }
+                    ep::quad_transpose(p, qi);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if ((on >> k) & 1)
+                            dst[off[k] + 4 * piece] = make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
+                };
                 const int last = empty ? (part || !(wide || st == 0) ? 0 : D) : col1;
 #pragma unroll 1
                 for (int col = col0; col < last; col += 32) {
@@ -895,13 +917,13 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                         for (int i = 0; i < 32; ++i) o[i] = 0;
                     } else {
                         tmem_ld_32x32b_x32(to + static_cast<uint32_t>(col), o);
+                        uint32_t p[32];
+                        if (other) tmem_ld_32x32b_x32(tO(1 - st) + lanes + static_cast<uint32_t>(col), p);
                         tmem_wait_ld(o);
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             o[i] = use_mine ? __float_as_uint(__uint_as_float(o[i]) * f_mine) : 0u;
                         if (other) {
-                            uint32_t p[32];
-                            tmem_ld_32x32b_x32(tO(1 - st) + lanes + static_cast<uint32_t>(col), p);
                             tmem_wait_ld(p);
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
@@ -909,38 +931,19 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                                     o[i] = __float_as_uint(fmaf(__uint_as_float(p[i]), f_other, __uint_as_float(o[i])));
                         }
                     }
-                    auto put = [&](uint32_t (&p)[16], void *base, int64_t off16) {
-                        // 16 words of every row, off16: in 16-byte units from base
-                        uint4 *dst = static_cast<uint4 *>(base);
-                        if (few) {
-                            if (live) {
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    dst[off16 + k] = make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
-                            }
-                            return;
-                        }
-                        ep::quad_transpose(p, qi);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int64_t to_row = __shfl_sync(0xffffffffu, off16, (lane & ~3) + k);
-                            if (__shfl_sync(0xffffffffu, live, (lane & ~3) + k))
-                                dst[to_row + qi] = make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
-                        }
-                    };
                     uint32_t p[16];
                     if (part) {
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
 #pragma unroll
                             for (int i = 0; i < 16; ++i) p[i] = o[16 * g + i];
-                            put(p, w.part_o, (mine + col + 16 * g) / 4);
+                            put(p, col / 16 + g);
                         }
                     } else {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             p[i] = pack2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
-                        put(p, w.out, (mine + col) / 8);
+                        put(p, col / 32);
                     }
                 }
             }
@@ -974,9 +977,9 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
     if (row >= rows) return;
     const int tok = static_cast<int>(row / Hq), hq = static_cast<int>(row - static_cast<int64_t>(tok) * Hq);
     const int b = tok / w.Lq, rt = (tok - b * w.Lq) / (w.tok_o * (w.wide_o ? 2 : 1));
-    pdl_wait();
-    const int own = tiles_of(own_len(w, b));
+    const int own = tiles_of(own_len(w, b));  // lengths are older than the kernel ahead
     const bool fixed = w.chunk_o > 0;
+    pdl_wait();
     const int np = fixed ? w.parts_p : w.tiles_p > 0 ? w.parts[0] : 0;
     const int no = fixed ? (own + w.chunk_o - 1) / w.chunk_o
                          : own > 0 ? w.parts[1 + (b * w.Hkv + hq / w.G) * w.rt_o + rt] : 0;
