@@ -102,12 +102,13 @@ struct Work {
     int tok_p, tok_o;  // query tokens of one tile
     int rt_p, rt_o;
     int tiles_p, tiles_o;  // key tiles of the prefix, of the longest sequence
+    bool too_large;        // more key tiles than can be counted: refused
     bool direct;           // own groups whole, nothing to join
     // Fixed chunks: parts of a group against the prefix, own (tiles of one:
     // chunk), CTA i taking items i, i + grid, ...; chunk_o 0: shares by cost.
     int parts_p, chunk_p, parts_o, chunk_o;
     int sms;               // CTAs to share the work among
-    int cost_p, cost_o;    // cost of a key tile (a group's or item's own is kItemCost)
+    int cost_p, cost_o, cost_item;  // of a key tile; of a group or item besides
     int min_o;             // own tiles a CTA is given at least, if any
     int slots_p, slots_o;  // most parts of a row: against the prefix, own
     int *parts;            // by cost: [0]: parts of a prefix group; then [B][Hkv][rt_o]: of each own group that has keys
@@ -123,6 +124,7 @@ struct Work {
 // when all SMs stream at once, some 1300 alone.  An item's query loads and
 // result cost about one narrow tile.
 constexpr int kTileCost = 16, kWideTileCost = 24, kItemCost = 16;
+constexpr int64_t kMostCost = int64_t{1} << 30;
 
 struct Item {
     int b;             // sequence; -1: prefix
@@ -154,101 +156,92 @@ __device__ __forceinline__ int own_len(const Work &w, int b) {
 }
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + kKeys - 1) / kKeys; }
 
-// x / d; by the 32-bit division where both are that small (a 64-bit one takes
-// some 500 cycles).
-__device__ __forceinline__ int64_t quotient64(int64_t x, int64_t d) {
-    return (x | d) >> 32 == 0 ? static_cast<uint32_t>(x) / static_cast<uint32_t>(d) : x / d;
-}
-__device__ __forceinline__ int quotient(int64_t x, int64_t d) { return static_cast<int>(quotient64(x, d)); }
-
-// The work's division, by all threads of the block (`scratch`: 1 KB of shared
-// memory).  Prefix groups are cut into equal parts of at most a CTA's share, dealt out in
-// turn -- row tiles of the same keys side by side, so that they pass over them
-// together and the keys are read from HBM once -- and own tiles, in order, fill
-// every CTA's share up.
+// The work's division, by all threads of the block (`scratch`: shared memory of
+// an int a warp).  Prefix groups are cut into equal parts of at most a CTA's
+// share, dealt out in turn -- row tiles of the same keys side by side, so that
+// they pass over them together and the keys are read from HBM once -- and own
+// tiles, in order, fill every CTA's share up.  Costs fit 30 bits (cost_shift).
 template <int THREADS>
-__device__ void divide(const Work &w, Share &sh, int64_t *scratch) {
+__device__ void divide(const Work &w, Share &sh, int *scratch) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     constexpr int kWarps = THREADS / 32;
     const int groups = w.Hkv * w.rt_o;  // of one sequence
     // own cost up to this thread's run of sequences
-    const int run = w.tiles_o > 0 ? (w.B + THREADS - 1) / THREADS : 0;
+    const int run = w.tiles_o == 0 ? 0 : w.B <= THREADS ? 1 : (w.B + THREADS - 1) / THREADS;
     const int b0 = min(t * run, w.B), b1 = min(b0 + run, w.B);
-    auto group_cost = [&](int b) { return kItemCost + tiles_of(own_len(w, b)) * w.cost_o; };
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += static_cast<int64_t>(groups) * group_cost(b);
-    int64_t upto = mine;
+    auto group_cost = [&](int b) { return w.cost_item + tiles_of(own_len(w, b)) * w.cost_o; };
+    int mine = 0, one = 0;  // one: a group's of the run's last
+    for (int b = b0; b < b1; ++b) one = group_cost(b), mine += groups * one;
+    int upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += v;
     }
     if (lane == 31) scratch[warp] = upto;
     if (t == 0) sh.b_lo = sh.b_hi = w.B, sh.r_lo = sh.t_lo = sh.r_hi = sh.t_hi = sh.part_lo = 0;
     __syncthreads();
-    int64_t own = 0;
+    int own = 0;
     for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) upto += scratch[i];
-        own += scratch[i];
+        const int v = scratch[i];
+        if (i < warp) upto += v;
+        own += v;
     }
-    const int64_t before = upto - mine;
+    const int before = upto - mine;
 
     // CTAs that take part: two narrow tiles each at least
-    const int64_t group_p = kItemCost + static_cast<int64_t>(w.tiles_p) * w.cost_p;
-    const int64_t prefix = w.tiles_p > 0 ? static_cast<int64_t>(w.rt_p) * w.Hkv * group_p : 0;
-    const int64_t least = kItemCost + 2 * kTileCost;
-    const int n = prefix + own >= least * w.sms ? w.sms : max(quotient(prefix + own, least), 1);
-    const int64_t share = quotient64(prefix + own + n - 1, n);
+    const int prefix = w.tiles_p > 0 ? w.rt_p * w.Hkv * (w.cost_item + w.tiles_p * w.cost_p) : 0;
+    const int least = w.cost_item + 2 * w.cost_o;
+    const int n = prefix + own >= least * w.sms ? w.sms : max((prefix + own) / least, 1);
+    const int share = (prefix + own + n - 1) / n;
     // prefix: equal parts of at most a share
-    int parts = 0, chunk = 0, items = 0;
-    int64_t part_cost = 0;
+    int parts = 0, chunk = 0, items = 0, part_cost = 0;
     if (w.tiles_p > 0) {
-        const int64_t room = max(share - kItemCost, static_cast<int64_t>(w.cost_p));
-        parts = min(quotient(static_cast<int64_t>(w.tiles_p) * w.cost_p + room - 1, room), w.slots_p);
+        const int room = max(share - w.cost_item, w.cost_p);
+        parts = min((w.tiles_p * w.cost_p + room - 1) / room, w.slots_p);
         chunk = (w.tiles_p + parts - 1) / parts;
         parts = (w.tiles_p + chunk - 1) / chunk;
         items = parts * w.rt_p * w.Hkv;
-        part_cost = kItemCost + static_cast<int64_t>(chunk) * w.cost_p;
+        part_cost = w.cost_item + chunk * w.cost_p;
     }
     // own: CTAs below `many` have one prefix part more than the others; each has
-    // len_a or len_b of the own cost
+    // len_a or len_b of the own cost (rounded up: the last CTAs get what is left)
     const int each = items / n, many = items - each * n;
-    const int64_t least_o = static_cast<int64_t>(w.min_o) * w.cost_o;
-    int64_t room_a = share - (each + 1) * part_cost, room_b = share - each * part_cost;
+    const int least_o = w.min_o * w.cost_o;
+    int room_a = share - (each + 1) * part_cost, room_b = share - each * part_cost;
     if (room_a < least_o || many == 0) room_a = 0;
     if (room_b < least_o) room_a = room_b = share;  // too little for its own CTAs: all take some
-    const int64_t room = many * room_a + (n - many) * room_b;
-    // (rounded up: the last CTAs get what is left)
-    const float fill = static_cast<float>(own) / static_cast<float>(room);
-    const int64_t len_a = room_a == 0 ? 0 : max(least_o, static_cast<int64_t>(static_cast<float>(room_a) * fill) + 1);
-    const int64_t len_b = max(least_o, static_cast<int64_t>(static_cast<float>(room_b) * fill) + 1);
-    auto start = [&](int64_t cta) { return cta < many ? cta * len_a : many * len_a + (cta - many) * len_b; };
+    const float fill = static_cast<float>(own) /
+                       (static_cast<float>(many) * static_cast<float>(room_a) +
+                        static_cast<float>(n - many) * static_cast<float>(room_b));
+    const int len_a = room_a == 0 ? 0 : max(least_o, static_cast<int>(static_cast<float>(room_a) * fill) + 1);
+    const int len_b = max(least_o, static_cast<int>(static_cast<float>(room_b) * fill) + 1);
+    auto start = [&](int cta) { return cta < many ? cta * len_a : many * len_a + (cta - many) * len_b; };
     const int cta = blockIdx.x;
-    const int64_t lo = min(cta < n ? start(cta) : own, own);
-    const int64_t hi = min(cta < n - 1 ? start(cta + 1) : own, own);
+    const int lo = cta < n ? min(start(cta), own) : own;
+    const int hi = cta < n - 1 ? min(start(cta + 1), own) : own;
     if (t == 0) {
         sh.parts_p = parts, sh.chunk_p = chunk, sh.items_p = items, sh.ctas = n;
         if (cta == 0) w.parts[0] = parts;
     }
     // the tile at or behind a cost: by the thread whose sequences hold it
-    int64_t at = before;
-    if (mine > 0 && ((lo >= before && lo < upto) || (hi >= before && hi < upto))) {
+    if ((lo >= before && lo < upto) || (hi >= before && hi < upto)) {
+        int at = before;
         for (int b = b0; b < b1; ++b) {
-            const int64_t g = group_cost(b), all = g * groups;
+            const int g = run == 1 ? one : group_cost(b), all = g * groups;
+#pragma unroll 1
             for (int end = 0; end < 2; ++end) {
-                const int64_t x = (end ? hi : lo) - at;
+                const int x = (end ? hi : lo) - at;
                 if (x < 0 || x >= all) continue;
-                const int r = quotient(x, g);
-                const int64_t off = x - r * g - kItemCost;
-                const int tile = off <= 0 ? 0 : quotient(off + w.cost_o - 1, w.cost_o);
+                const int r = x / g, off = x - r * g - w.cost_item;
+                const int tile = off <= 0 ? 0 : (off + w.cost_o - 1) / w.cost_o;
                 if (end) {
                     sh.b_hi = b, sh.r_hi = r, sh.t_hi = tile;
                 } else {
                     sh.b_lo = b, sh.r_lo = r, sh.t_lo = tile;
-                    const int64_t first = at + r * g + kItemCost;  // its first tile
                     if (tile > 0) {
-                        const int of = first < many * len_a ? quotient(first, len_a)
-                                                            : many + quotient(first - many * len_a, len_b);
+                        const int first = at + r * g + w.cost_item;  // its first tile
+                        const int of = first < many * len_a ? first / len_a : many + (first - many * len_a) / len_b;
                         sh.part_lo = min(cta - min(of, n - 1), w.slots_o - 1);
                     }
                 }
@@ -473,7 +466,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
         for (int b = threadIdx.x; b < w.B; b += kThreads)
             if (w.lens[b] < 0 || w.lens[b] > w.max_len) atomicOr(w.status, kDeviceStatusIndex);
     }
-    if (w.chunk_o == 0) divide<kThreads>(w, share, reinterpret_cast<int64_t *>(xml));
+    if (w.chunk_o == 0) divide<kThreads>(w, share, reinterpret_cast<int *>(xml));
 
     // The next item, in every lane of a reading warp; false after the last.
     uint32_t items = 0;
@@ -908,42 +901,61 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                         if ((on >> k) & 1)
                             dst[off[k] + 4 * piece] = make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
                 };
-                const int last = empty ? (part || !(wide || st == 0) ? 0 : D) : col1;
-#pragma unroll 1
-                for (int col = col0; col < last; col += 32) {
-                    uint32_t o[32];
-                    if (empty) {
+                if (!part && !other && !empty && col1 > 0) {
+                    // all columns of a finished row at once
+                    uint32_t o[D / 32][32];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = 0;
-                    } else {
-                        tmem_ld_32x32b_x32(to + static_cast<uint32_t>(col), o);
-                        uint32_t p[32];
-                        if (other) tmem_ld_32x32b_x32(tO(1 - st) + lanes + static_cast<uint32_t>(col), p);
-                        tmem_wait_ld(o);
+                    for (int q = 0; q < D / 32; ++q) tmem_ld_32x32b_x32(to + 32u * q, o[q]);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            o[i] = use_mine ? __float_as_uint(__uint_as_float(o[i]) * f_mine) : 0u;
-                        if (other) {
-                            tmem_wait_ld(p);
+                    for (int q = 0; q < D / 32; ++q) tmem_wait_ld(o[q]);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (use_other)
-                                    o[i] = __float_as_uint(fmaf(__uint_as_float(p[i]), f_other, __uint_as_float(o[i])));
-                        }
-                    }
-                    uint32_t p[16];
-                    if (part) {
-#pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) p[i] = o[16 * g + i];
-                            put(p, col / 16 + g);
-                        }
-                    } else {
+                    for (int q = 0; q < D / 32; ++q) {
+                        uint32_t p[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            p[i] = pack2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
-                        put(p, col / 32);
+                            p[i] = use_mine ? pack2(__uint_as_float(o[q][2 * i]) * f_mine,
+                                                    __uint_as_float(o[q][2 * i + 1]) * f_mine)
+                                            : 0u;
+                        put(p, q);
+                    }
+                } else {
+                    const int last = empty ? (part || !(wide || st == 0) ? 0 : D) : col1;
+#pragma unroll 1
+                    for (int col = col0; col < last; col += 32) {
+                        uint32_t o[32];
+                        if (empty) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = 0;
+                        } else {
+                            tmem_ld_32x32b_x32(to + static_cast<uint32_t>(col), o);
+                            uint32_t p[32];
+                            if (other) tmem_ld_32x32b_x32(tO(1 - st) + lanes + static_cast<uint32_t>(col), p);
+                            tmem_wait_ld(o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                o[i] = use_mine ? __float_as_uint(__uint_as_float(o[i]) * f_mine) : 0u;
+                            if (other) {
+                                tmem_wait_ld(p);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (use_other)
+                                        o[i] = __float_as_uint(fmaf(__uint_as_float(p[i]), f_other, __uint_as_float(o[i])));
+                            }
+                        }
+                        uint32_t p[16];
+                        if (part) {
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) p[i] = o[16 * g + i];
+                                put(p, col / 16 + g);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                p[i] = pack2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+                            put(p, col / 32);
+                        }
                     }
                 }
             }
@@ -1050,7 +1062,6 @@ Work plan(const AttentionArgs &a) {
     w.rt_p = div_up(w.T, w.tok_p * (w.wide_p ? 2 : 1));
     w.rt_o = div_up(w.Lq, w.tok_o * (w.wide_o ? 2 : 1));
     w.tiles_p = div_up(w.prefix_len, kKeys), w.tiles_o = div_up(w.max_len, kKeys);
-    w.cost_p = w.wide_p ? kWideTileCost : kTileCost, w.cost_o = w.wide_o ? kWideTileCost : kTileCost;
     w.sms = kPlanSms;
     const int64_t base_p = static_cast<int64_t>(w.rt_p) * w.Hkv, base_o = static_cast<int64_t>(w.rt_o) * w.Hkv * w.B;
     // Whole groups where they are many (at 4 a SM the last round leaves at most
@@ -1076,6 +1087,17 @@ Work plan(const AttentionArgs &a) {
             return w;
         }
     }
+    // costs in units that keep the sum of all below 2^30
+    int shift = 0;
+    auto sum = [&] {
+        w.cost_p = (w.wide_p ? kWideTileCost : kTileCost) >> shift;
+        w.cost_o = (w.wide_o ? kWideTileCost : kTileCost) >> shift;
+        w.cost_item = kItemCost >> shift;
+        return base_p * (w.cost_item + static_cast<int64_t>(w.tiles_p) * w.cost_p) +
+               base_o * (w.cost_item + static_cast<int64_t>(w.tiles_o) * w.cost_o);
+    };
+    while (sum() >= kMostCost && shift < 4) ++shift;
+    w.too_large = sum() >= kMostCost;
     // a group's parts: as many as CTAs can find work in, of two tiles at least;
     // own pieces of a sixteenth of the longest at least
     if (w.tiles_p > 0) {
@@ -1168,6 +1190,7 @@ cudaError_t launch(const AttentionArgs &a, Work &w, const LaunchCtx &ctx) {
 
 size_t attention_workspace_bytes(const AttentionArgs &a) {
     const Work w = plan(a);
+    if (w.too_large) return kAttentionTooLarge;
     if (w.direct) return 0;
     return parts_bytes(w) + ml_bytes(w) + static_cast<size_t>(part_rows(w)) * a.D * sizeof(float);
 }

@@ -67,6 +67,9 @@ struct AttentionArgs {
     void *ws;
     unsigned int *status;
 };
+// kAttentionTooLarge: more key tiles over all heads and sequences than a call
+// can count (2^30 of 128 keys).
+constexpr size_t kAttentionTooLarge = ~size_t{0};
 size_t attention_workspace_bytes(const AttentionArgs &a);
 cudaError_t launch_attention(const AttentionArgs &a, const LaunchCtx &ctx);
 

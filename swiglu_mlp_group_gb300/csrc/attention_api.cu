@@ -80,6 +80,7 @@ ck::AttentionArgs cross_sizes(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int
 ck_status run_attention(ck::AttentionArgs &a, const void *q, int64_t ldq, void *out, int64_t ldo, float scale,
                         void *ws, size_t ws_bytes, ck_stream_t stream) {
     const size_t need = ck::attention_workspace_bytes(a);
+    if (need == ck::kAttentionTooLarge) return CK_ERR_SHAPE;
     if (need > 0 && (!ws || ws_bytes < need)) return CK_ERR_WORKSPACE;
     if (need > 0 && !aligned16(ws)) return CK_ERR_ALIGN;
     unsigned int *status = nullptr;
@@ -157,7 +158,8 @@ CK_API size_t ck_prefix_attention_workspace_bytes(int64_t B, int64_t Lq, int64_t
     if (!attention_sizes(B, Lq, Hq, Hkv, D) || prefix_len < 0 || max_seq_len < 0 || prefix_len > kMaxKeys ||
         max_seq_len > kMaxKeys)
         return 0;
-    return ck::attention_workspace_bytes(prefix_sizes(B, Lq, Hq, Hkv, D, prefix_len, max_seq_len));
+    const size_t n = ck::attention_workspace_bytes(prefix_sizes(B, Lq, Hq, Hkv, D, prefix_len, max_seq_len));
+    return n == ck::kAttentionTooLarge ? 0 : n;
 }
 
 CK_API ck_status ck_prefix_attention(const void *q, int64_t ldq, int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv,
@@ -189,7 +191,8 @@ CK_API ck_status ck_prefix_attention(const void *q, int64_t ldq, int64_t B, int6
 CK_API size_t ck_cross_attention_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv,
                                                  int64_t D) {
     if (!attention_sizes(B, Lq, Hq, Hkv, D) || Lk < 0 || Lk > kMaxKeys || B * Lk > kMaxRows) return 0;
-    return ck::attention_workspace_bytes(cross_sizes(B, Lq, Lk, Hq, Hkv, D));
+    const size_t n = ck::attention_workspace_bytes(cross_sizes(B, Lq, Lk, Hq, Hkv, D));
+    return n == ck::kAttentionTooLarge ? 0 : n;
 }
 
 CK_API ck_status ck_cross_attention(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v,
