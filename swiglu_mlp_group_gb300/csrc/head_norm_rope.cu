@@ -12,154 +12,224 @@ namespace ck {
 namespace {
 
 constexpr int kThreads = 256;
-// Head rows a group of lanes has in flight at once: their 16-byte loads are all
-// issued before the first is used, and share the token's rotation factors.
-constexpr int kRowsAhead = 4;
+constexpr int kBlocksPerSm = 3;  // by their registers
+constexpr int kRows = 4;         // rows of a group of lanes in one unit of work
 
-// How a block's groups of L lanes are dealt out: 2^gp_log2 of them share a
-// token, the g-th taking its heads g, g + 2^gp_log2, ...
+// How the blocks' groups of L lanes are dealt out.  Blocks from `blocks_q` on
+// have the keys (of the append: none).  2^gp_log2 groups share a token, the g-th
+// taking its heads g, g + 2^gp_log2, ..., in `batches` units.
 struct Deal {
-    int gp_log2;
+    int blocks_q;
+    int gp_log2[2], batches[2];
 };
 
-template <int L, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormRopeArgs a, const Deal deal) {
+// The factors of a token's pairs; `ok`: it has any (and a place in the cache).
+struct Token {
+    float4 c, s;
+    int64_t at;
+    bool ok;
+};
+
+// Both passes are a copy with arithmetic, and latency is what they have to hide:
+// a token's position comes before its factors, and both before its rows can be
+// used.  A block is persistent and, while it works on one unit, has the next
+// one's rows and factors and the position after that on their way.  (Blocks of
+// one token each: 30011 tokens x 48 heads x 128 191 us, 64 KB on their way an SM
+// but for a third of a block's life; rows three units ahead through shared
+// memory, with the pairs' elements in different lanes: 247 us.)
+template <int L, bool INTERLEAVED, typename Rows>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+head_rows_kernel(const __grid_constant__ typename Rows::Args a, const __grid_constant__ Deal deal) {
     pdl_launch_dependents();
-    const int gl = threadIdx.x % L;
-    const int d0 = gl * 8;
-    const bool lane_on = d0 < a.D;
-    const int heads = a.Hq + a.Hk;
-    const int group = threadIdx.x / L;
-    const int gp = 1 << deal.gp_log2;
-    const int64_t tok = static_cast<int64_t>(blockIdx.x) * ((kThreads / L) >> deal.gp_log2) + (group >> deal.gp_log2);
-    const bool tok_on = tok < a.T;
-    const int64_t t = tok_on ? tok : 0;
-    const int h0 = group & (gp - 1);
+    const int side = static_cast<int>(blockIdx.x) < deal.blocks_q ? 0 : 1;
+    const int block = blockIdx.x - (side == 0 ? 0 : deal.blocks_q);
+    const int blocks = side == 0 ? deal.blocks_q : gridDim.x - deal.blocks_q;
+    const int gp_log2 = deal.gp_log2[side], batches = deal.batches[side];
+    const int gl = threadIdx.x % L, group = threadIdx.x / L;
+    const int per = (kThreads / L) >> gp_log2;  // tokens of a block at once
+    const Place<INTERLEAVED> p(gl, a.D, a.rot);
+    const Rows rows(a, side, 1 << gp_log2, group & ((1 << gp_log2) - 1));
+    const int64_t step = static_cast<int64_t>(blocks) * per;
+    const int64_t first = static_cast<int64_t>(block) * per;
+    const int64_t mine = first + (group >> gp_log2);
     pdl_wait();
-    const int pos = a.rot > 0 ? a.positions[t] : 0;
-    float w[2][8] = {};
-    if (lane_on) {
-        if (a.wq) load_weight8(a.wq, a.w_f32, d0, w[0]);
-        if (a.wk) load_weight8(a.wk, a.w_f32, d0, w[1]);
-    }
-    bool ok = tok_on;
-    Rotation r;
-    r.on = false, r.partner = gl;
-    // heads in rounds of kRowsAhead a group; uniform over the block
-    for (int base = 0; base < heads; base += gp * kRowsAhead) {
-        uint4 in[kRowsAhead];
+    const Pairs w = load_weights<INTERLEAVED>(rows.weight(), a.w_f32, p);
+    const bool norm = rows.weight() != nullptr;
+
+    auto load_rows = [&](int64_t t, int batch, uint4 (&v)[kRows]) {
 #pragma unroll
-        for (int i = 0; i < kRowsAhead; ++i) {
-            const int h = base + i * gp + h0;
-            in[i] = make_uint4(0, 0, 0, 0);
-            if (tok_on && lane_on && h < heads) {
-                const uint16_t *src = h < a.Hq ? a.q + t * a.ldq + static_cast<int64_t>(h) * a.D
-                                               : a.k + t * a.ldk + static_cast<int64_t>(h - a.Hq) * a.D;
-                in[i] = *reinterpret_cast<const uint4 *>(src + d0);
-            }
+        for (int i = 0; i < kRows; ++i) {
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (t < a.T && p.on && rows.has(batch, i)) v[i] = load_row<INTERLEAVED>(rows.source(t, batch, i), p);
         }
-        if (base == 0 && a.rot > 0) {
-            const bool in_table = pos >= 0 && pos < a.max_pos;
-            if (in_table)
-                load_rotation<INTERLEAVED>(r, a.cos_sin + static_cast<int64_t>(pos) * a.rot, a.rot, d0, gl);
-            else if (gl == 0 && tok_on)
-                atomicOr(a.status, kDeviceStatusIndex);
-            ok = ok && in_table;
+    };
+    struct Index {
+        int pos;
+        int64_t slot;
+    };
+    auto load_index = [&](int64_t t) {
+        Index x{0, 0};
+        if (t < a.T) {
+            if (a.rot > 0) x.pos = a.positions[t];
+            x.slot = rows.slot(t);
         }
+        return x;
+    };
+    auto load_token = [&](int64_t t, const Index &x, bool report, Token &k) {
+        k.c = make_float4(1.f, 1.f, 1.f, 1.f), k.s = make_float4(0.f, 0.f, 0.f, 0.f);
+        k.ok = t < a.T && rows.place(x.slot, report, k.at);
+        if (k.ok && a.rot > 0) {
+            const bool in_table = x.pos >= 0 && x.pos < a.max_pos;
+            if (in_table && p.rotated && p.on)
+                load_factors<INTERLEAVED>(a.cos_sin + static_cast<int64_t>(x.pos) * a.rot, a.rot, p, k.c, k.s);
+            if (!in_table && report) atomicOr(a.status, kDeviceStatusIndex);
+            k.ok = in_table;
+        }
+    };
+
+    uint4 next_rows[kRows];
+    Token next;
+    load_rows(mine, 0, next_rows);
+    load_token(mine, load_index(mine), gl == 0, next);
+    // unit + 1 and unit + 2
+    int64_t t1 = mine, t2 = mine;
+    int j1 = 0, j2 = 0;
+    auto forward = [&](int64_t &t, int &j) {
+        if (++j == batches) j = 0, t += step;
+    };
+    forward(t1, j1);
+    forward(t2, j2);
+    Index index = load_index(t1);
+    forward(t2, j2);
+    int64_t t0 = mine;
+    int j0 = 0;
+    // every group of a block makes the same rounds
+    for (int64_t block_t = first; block_t < a.T;) {
+        uint4 v[kRows];
 #pragma unroll
-        for (int i = 0; i < kRowsAhead; ++i) {
-            if (base + i * gp >= heads) break;  // uniform over the block
-            const int h = base + i * gp + h0;
-            const bool is_q = h < a.Hq;
-            float x[8], wv[8];
-            unpack8(in[i], x);
+        for (int i = 0; i < kRows; ++i) v[i] = next_rows[i];
+        const Token now = next;
+        load_rows(t1, j1, next_rows);
+        load_token(t1, index, gl == 0 && j1 == 0, next);
+        index = load_index(t2);
+        Factors k;
+        set_factors(k, w, p.rotated, now.c, now.s);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) wv[j] = is_q ? w[0][j] : w[1][j];
-            norm_rotate<L, INTERLEAVED>(x, a.wq || a.wk, (is_q ? a.wq : a.wk) != nullptr, wv, a.inv_d, a.eps, a.rot > 0, r);
-            if (ok && lane_on && h < heads) {
-                uint16_t *dst = is_q ? a.q_out + t * a.ldqo + static_cast<int64_t>(h) * a.D
-                                     : a.k_out + t * a.ldko + static_cast<int64_t>(h - a.Hq) * a.D;
-                *reinterpret_cast<uint4 *>(dst + d0) = pack8(x);
-            }
+        for (int i = 0; i < kRows; ++i) {
+            if (!rows.any(j0, i)) continue;
+            uint4 out = v[i];
+            if (!rows.plain(i))
+                out = norm_rotate<L, INTERLEAVED>(v[i], norm, a.inv_d, a.eps, a.rot < a.D, p.rotated, k);
+            if (now.ok && p.on && rows.has(j0, i)) store_row<INTERLEAVED>(rows.target(t0, now.at, j0, i), p, out);
         }
+        if (j0 + 1 == batches) block_t += step;
+        t0 = t1, j0 = j1;
+        t1 = t2, j1 = j2;
+        forward(t2, j2);
     }
 }
 
-template <int L, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs a, const Deal deal) {
-    pdl_launch_dependents();
-    const int gl = threadIdx.x % L;
-    const int d0 = gl * 8;
-    const bool lane_on = d0 < a.D;
-    const int group = threadIdx.x / L;
-    const int gp = 1 << deal.gp_log2;
-    const int64_t tok = static_cast<int64_t>(blockIdx.x) * ((kThreads / L) >> deal.gp_log2) + (group >> deal.gp_log2);
-    const bool tok_on = tok < a.T;
-    const int64_t t = tok_on ? tok : 0;
-    const int h0 = group & (gp - 1);
-    pdl_wait();
-    const int64_t slot = tok_on ? a.slots[t] : -1;
-    const int pos = a.rot > 0 ? a.positions[t] : 0;
-    float w[8] = {};
-    if (lane_on && a.wk) load_weight8(a.wk, a.w_f32, d0, w);
-    bool ok = slot >= 0 && slot < a.pages * a.page_size;
-    if (slot >= 0 && !ok && gl == 0) atomicOr(a.status, kDeviceStatusIndex);
-    const int64_t page = ok ? slot / a.page_size : 0;
-    const int64_t at0 = (page * a.Hkv * a.page_size + (slot - page * a.page_size)) * a.D + d0;
-    Rotation r;
-    r.on = false, r.partner = gl;
-    constexpr int kAhead = kRowsAhead / 2;  // keys and values
-    for (int base = 0; base < a.Hkv; base += gp * kAhead) {
-        uint4 kin[kAhead], vin[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int h = base + i * gp + h0;
-            kin[i] = vin[i] = make_uint4(0, 0, 0, 0);
-            if (ok && lane_on && h < a.Hkv) {
-                kin[i] = *reinterpret_cast<const uint4 *>(a.k + t * a.ldk + static_cast<int64_t>(h) * a.D + d0);
-                vin[i] = *reinterpret_cast<const uint4 *>(a.v + t * a.ldv + static_cast<int64_t>(h) * a.D + d0);
-            }
-        }
-        if (base == 0 && a.rot > 0 && ok) {
-            ok = pos >= 0 && pos < a.max_pos;
-            if (ok)
-                load_rotation<INTERLEAVED>(r, a.cos_sin + static_cast<int64_t>(pos) * a.rot, a.rot, d0, gl);
-            else if (gl == 0)
-                atomicOr(a.status, kDeviceStatusIndex);
-        }
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (base + i * gp >= a.Hkv) break;  // uniform over the block
-            const int h = base + i * gp + h0;
-            float x[8];
-            unpack8(kin[i], x);
-            norm_rotate<L, INTERLEAVED>(x, a.wk != nullptr, true, w, a.inv_d, a.eps, a.rot > 0, r);
-            if (ok && lane_on && h < a.Hkv) {
-                const int64_t at = at0 + static_cast<int64_t>(h) * a.page_size * a.D;
-                *reinterpret_cast<uint4 *>(a.k_cache + at) = pack8(x);
-                *reinterpret_cast<uint4 *>(a.v_cache + at) = vin[i];
-            }
-        }
+// Query heads (side 0) or key heads (side 1) of a token.
+struct QkRows {
+    using Args = NormRopeArgs;
+    const Args &a;
+    int side, gp, g, heads;
+    __device__ QkRows(const Args &args, int s, int gp_, int g_)
+        : a(args), side(s), gp(gp_), g(g_), heads(s == 0 ? args.Hq : args.Hk) {}
+    __device__ int head(int batch, int i) const { return (batch * kRows + i) * gp + g; }
+    __device__ const void *weight() const { return side == 0 ? a.wq : a.wk; }
+    __device__ const uint16_t *source(int64_t t, int batch, int i) const {
+        return (side == 0 ? a.q + t * a.ldq : a.k + t * a.ldk) + head(batch, i) * a.D;
     }
-}
+    __device__ uint16_t *target(int64_t t, int64_t, int batch, int i) const {
+        return (side == 0 ? a.q_out + t * a.ldqo : a.k_out + t * a.ldko) + head(batch, i) * a.D;
+    }
+    __device__ bool any(int batch, int i) const { return (batch * kRows + i) * gp < heads; }  // uniform
+    __device__ bool has(int batch, int i) const { return head(batch, i) < heads; }
+    __device__ bool plain(int) const { return false; }
+    __device__ int64_t slot(int64_t) const { return 0; }
+    __device__ bool place(int64_t, bool, int64_t &at) const { return at = 0, true; }
+};
+
+// Key heads of a token (the first half of a unit's rows) and its value heads.
+struct AppendRows {
+    using Args = KvAppendArgs;
+    static constexpr int kHeads = kRows / 2;
+    const Args &a;
+    int gp, g;
+    __device__ AppendRows(const Args &args, int, int gp_, int g_) : a(args), gp(gp_), g(g_) {}
+    __device__ int head(int batch, int i) const { return (batch * kHeads + i % kHeads) * gp + g; }
+    __device__ const void *weight() const { return a.wk; }
+    __device__ const uint16_t *source(int64_t t, int batch, int i) const {
+        return (i < kHeads ? a.k + t * a.ldk : a.v + t * a.ldv) + head(batch, i) * a.D;
+    }
+    __device__ uint16_t *target(int64_t, int64_t at, int batch, int i) const {
+        return (i < kHeads ? a.k_cache : a.v_cache) + at + static_cast<int64_t>(head(batch, i)) * a.page_size * a.D;
+    }
+    __device__ bool any(int batch, int i) const { return (batch * kHeads + i % kHeads) * gp < a.Hkv; }
+    __device__ bool has(int batch, int i) const { return head(batch, i) < a.Hkv; }
+    __device__ bool plain(int i) const { return i >= kHeads; }
+    __device__ int64_t slot(int64_t t) const { return a.slots[t]; }
+    // Where a slot's rows are: of head 0, its row of its page.
+    __device__ bool place(int64_t slot, bool report, int64_t &at) const {
+        at = 0;
+        if (slot < 0) return false;
+        if (slot >= a.pages * a.page_size) {
+            if (report) atomicOr(a.status, kDeviceStatusIndex);
+            return false;
+        }
+        const int64_t page = slot <= 0x7fffffff ? static_cast<uint32_t>(slot) / static_cast<uint32_t>(a.page_size)
+                                                : slot / a.page_size;
+        at = (page * a.Hkv * a.page_size + (slot - page * a.page_size)) * a.D;
+        return true;
+    }
+};
 
 // Lanes that hold a row: the power of two of at least D / 8.
 int group_lanes(int D) { return D <= 64 ? 8 : (D <= 128 ? 16 : 32); }
 
-template <typename Args>
-cudaError_t launch_rows(void (*const (&kernels)[3][2])(const Args, const Deal), const Args &a, int64_t T, int heads,
-                        bool interleaved, const LaunchCtx &ctx) {
-    const int L = group_lanes(a.D);
-    // Groups that share a token: each takes at least two of its heads, so that
-    // the token's rotation factors serve more than one row.  A few tokens leave
-    // SMs idle, so there a token's heads are spread as far as they go.
-    int gp_log2 = 0;
+// Groups of lanes that share a token of `heads` heads, a unit holding `rows` of
+// them a group: as many as leave the fewest of a unit's rows unused.  A few
+// tokens leave SMs idle, so there a token's heads are spread as far as they go.
+void deal_heads(int64_t T, int heads, int rows, int L, int *gp_log2, int *batches) {
     const int groups = kThreads / L;
-    const bool few = T * heads <= 4 * sm_count() * groups;
-    while ((1 << gp_log2) < groups && (2 << gp_log2) <= (few ? 2 * heads - 1 : heads / 2)) ++gp_log2;
-    const int64_t per = groups >> gp_log2;
+    const bool few = T * heads <= static_cast<int64_t>(4) * sm_count() * groups;
+    int best = 0, held = 1 << 30;
+    for (int n = 0; (1 << n) <= groups; ++n) {
+        const int unit = few ? 1 << n : rows << n;
+        const int places = (heads + unit - 1) / unit * unit;
+        if ((few && (1 << n) >= 2 * heads) || (!few && places > held)) continue;
+        best = n, held = places;
+    }
+    *gp_log2 = best;
+    *batches = (heads + (rows << best) - 1) / (rows << best);
+}
+
+template <typename Rows>
+cudaError_t launch_rows(const typename Rows::Args &a, const int (&heads)[2], int rows, bool interleaved,
+                        const LaunchCtx &ctx) {
+    using Kernel = void (*)(const typename Rows::Args, const Deal);
+    static const Kernel kernels[3][2] = {
+        {head_rows_kernel<8, false, Rows>, head_rows_kernel<8, true, Rows>},
+        {head_rows_kernel<16, false, Rows>, head_rows_kernel<16, true, Rows>},
+        {head_rows_kernel<32, false, Rows>, head_rows_kernel<32, true, Rows>}};
+    const int L = group_lanes(a.D);
+    const int sms = sm_count();
+    if (sms < 1) return cudaErrorInvalidDevice;
+    // blocks by the rows of each side
+    Deal deal = {};
+    int64_t blocks[2] = {0, 0};
+    for (int s = 0; s < 2; ++s) {
+        if (heads[s] == 0) continue;
+        deal_heads(a.T, heads[s], rows, L, &deal.gp_log2[s], &deal.batches[s]);
+        const int64_t per = (kThreads / L) >> deal.gp_log2[s];
+        const int64_t all = (a.T + per - 1) / per;
+        const int64_t share = static_cast<int64_t>(kBlocksPerSm) * sms * heads[s] / (heads[0] + heads[1]);
+        blocks[s] = all < share ? all : (share < 1 ? 1 : share);
+    }
+    deal.blocks_q = static_cast<int>(blocks[0]);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((T + per - 1) / per));
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks[0] + blocks[1]));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = ctx.stream;
     cudaLaunchAttribute attr[1];
@@ -167,25 +237,19 @@ cudaError_t launch_rows(void (*const (&kernels)[3][2])(const Args, const Deal), 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = ctx.pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernels[L == 8 ? 0 : (L == 16 ? 1 : 2)][interleaved ? 1 : 0], a, Deal{gp_log2});
+    return cudaLaunchKernelEx(&cfg, kernels[L == 8 ? 0 : (L == 16 ? 1 : 2)][interleaved ? 1 : 0], a, deal);
 }
 
 }  // namespace
 
 cudaError_t launch_qk_norm_rope(const NormRopeArgs &a, bool interleaved, const LaunchCtx &ctx) {
-    static void (*const kernels[3][2])(const NormRopeArgs, const Deal) = {
-        {qk_norm_rope_kernel<8, false>, qk_norm_rope_kernel<8, true>},
-        {qk_norm_rope_kernel<16, false>, qk_norm_rope_kernel<16, true>},
-        {qk_norm_rope_kernel<32, false>, qk_norm_rope_kernel<32, true>}};
-    return launch_rows(kernels, a, a.T, a.Hq + a.Hk, interleaved, ctx);
+    const int heads[2] = {a.Hq, a.Hk};
+    return launch_rows<QkRows>(a, heads, kRows, interleaved, ctx);
 }
 
 cudaError_t launch_kv_append(const KvAppendArgs &a, bool interleaved, const LaunchCtx &ctx) {
-    static void (*const kernels[3][2])(const KvAppendArgs, const Deal) = {
-        {kv_append_kernel<8, false>, kv_append_kernel<8, true>},
-        {kv_append_kernel<16, false>, kv_append_kernel<16, true>},
-        {kv_append_kernel<32, false>, kv_append_kernel<32, true>}};
-    return launch_rows(kernels, a, a.T, a.Hkv, interleaved, ctx);
+    const int heads[2] = {a.Hkv, 0};
+    return launch_rows<AppendRows>(a, heads, AppendRows::kHeads, interleaved, ctx);
 }
 
 }  // namespace ck
