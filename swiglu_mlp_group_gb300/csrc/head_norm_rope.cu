@@ -56,13 +56,10 @@ head_rows_kernel(const __grid_constant__ typename Rows::Args a, const __grid_con
     const Pairs w = load_weights<INTERLEAVED>(rows.weight(), a.w_f32, p);
     const bool norm = rows.weight() != nullptr;
 
-    auto load_rows = [&](int64_t t, int batch, uint4 (&v)[kRows]) {
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (t < a.T && p.on && rows.has(batch, i)) v[i] = load_row<INTERLEAVED>(rows.source(t, batch, i), p);
-        }
-    };
+    // A unit's rows: `rows.from(t, batch)` and every `stride` elements on (of the
+    // second half of an append's unit: the values).
+    const int stride = a.D << gp_log2;
+    auto load = [&](const uint16_t *src, int i, uint4 &v) { v = load_row<INTERLEAVED>(src + i * stride, p); };
     struct Index {
         int pos;
         int64_t slot;
@@ -76,51 +73,62 @@ head_rows_kernel(const __grid_constant__ typename Rows::Args a, const __grid_con
         return x;
     };
     auto load_token = [&](int64_t t, const Index &x, bool report, Token &k) {
-        k.c = make_float4(1.f, 1.f, 1.f, 1.f), k.s = make_float4(0.f, 0.f, 0.f, 0.f);
-        k.ok = t < a.T && rows.place(x.slot, report, k.at);
+        k.ok = t < a.T && p.on && rows.place(x.slot, report, k.at);
         if (k.ok && a.rot > 0) {
             const bool in_table = x.pos >= 0 && x.pos < a.max_pos;
-            if (in_table && p.rotated && p.on)
+            if (in_table && p.rotated)
                 load_factors<INTERLEAVED>(a.cos_sin + static_cast<int64_t>(x.pos) * a.rot, a.rot, p, k.c, k.s);
             if (!in_table && report) atomicOr(a.status, kDeviceStatusIndex);
             k.ok = in_table;
         }
     };
 
-    uint4 next_rows[kRows];
-    Token next;
-    load_rows(mine, 0, next_rows);
-    load_token(mine, load_index(mine), gl == 0, next);
-    // unit + 1 and unit + 2
-    int64_t t1 = mine, t2 = mine;
-    int j1 = 0, j2 = 0;
+    uint4 v[kRows];
+    Token token;
+    token.c = make_float4(1.f, 1.f, 1.f, 1.f), token.s = make_float4(0.f, 0.f, 0.f, 0.f);
+    token.at = 0;
     auto forward = [&](int64_t &t, int &j) {
         if (++j == batches) j = 0, t += step;
     };
+    // this unit, and the one after the next
+    int64_t t0 = mine, t1 = mine, t2;
+    int j0 = 0, j1 = 0, j2;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (mine < a.T && p.on && rows.has(0, i)) load(rows.from(mine, 0, i), i % Rows::kHeads, v[i]);
+    }
+    load_token(mine, load_index(mine), gl == 0, token);
     forward(t1, j1);
-    forward(t2, j2);
+    t2 = t1, j2 = j1;
     Index index = load_index(t1);
     forward(t2, j2);
-    int64_t t0 = mine;
-    int j0 = 0;
     // every group of a block makes the same rounds
     for (int64_t block_t = first; block_t < a.T;) {
-        uint4 v[kRows];
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) v[i] = next_rows[i];
-        const Token now = next;
-        load_rows(t1, j1, next_rows);
-        load_token(t1, index, gl == 0 && j1 == 0, next);
-        index = load_index(t2);
         Factors k;
-        set_factors(k, w, p.rotated, now.c, now.s);
+        set_factors(k, w, p.rotated, token.c, token.s);
+        const int64_t at = token.at;
+        const bool ok = token.ok;
+        load_token(t1, index, gl == 0 && j1 == 0, token);
+        index = load_index(t2);
+        const bool more = t1 < a.T && p.on;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            if (!rows.any(j0, i)) continue;
-            uint4 out = v[i];
-            if (!rows.plain(i))
-                out = norm_rotate<L, INTERLEAVED>(v[i], norm, a.inv_d, a.eps, a.rot < a.D, p.rotated, k);
-            if (now.ok && p.on && rows.has(j0, i)) store_row<INTERLEAVED>(rows.target(t0, now.at, j0, i), p, out);
+        for (int half = 0; half < kRows / Rows::kHeads; ++half) {
+            uint16_t *const dst = rows.to(t0, at, j0, half * Rows::kHeads);
+            const uint16_t *const src = rows.from(more ? t1 : 0, j1, half * Rows::kHeads);
+            const int64_t dst_stride = rows.to_stride(stride);
+#pragma unroll
+            for (int i0 = 0; i0 < Rows::kHeads; ++i0) {
+                const int i = half * Rows::kHeads + i0;
+                if (rows.any(j0, i)) {  // uniform over the block
+                    uint4 out = v[i];
+                    if (!rows.plain(i))
+                        out = norm_rotate<L, INTERLEAVED>(out, norm, a.inv_d, a.eps, a.rot < a.D, p.rotated, k);
+                    if (ok && rows.has(j0, i)) store_row<INTERLEAVED>(dst + i0 * dst_stride, p, out);
+                }
+                // its place is free for the next unit's
+                if (more && rows.has(j1, i)) load(src, i0, v[i]);
+            }
         }
         if (j0 + 1 == batches) block_t += step;
         t0 = t1, j0 = j1;
@@ -132,23 +140,25 @@ head_rows_kernel(const __grid_constant__ typename Rows::Args a, const __grid_con
 // Query heads (side 0) or key heads (side 1) of a token.
 struct QkRows {
     using Args = NormRopeArgs;
+    static constexpr int kHeads = kRows;
     const Args &a;
     int side, gp, g, heads;
     __device__ QkRows(const Args &args, int s, int gp_, int g_)
         : a(args), side(s), gp(gp_), g(g_), heads(s == 0 ? args.Hq : args.Hk) {}
     __device__ int head(int batch, int i) const { return (batch * kRows + i) * gp + g; }
     __device__ const void *weight() const { return side == 0 ? a.wq : a.wk; }
-    __device__ const uint16_t *source(int64_t t, int batch, int i) const {
-        return (side == 0 ? a.q + t * a.ldq : a.k + t * a.ldk) + head(batch, i) * a.D;
+    __device__ const uint16_t *from(int64_t t, int batch, int) const {
+        return (side == 0 ? a.q + t * a.ldq : a.k + t * a.ldk) + head(batch, 0) * a.D;
     }
-    __device__ uint16_t *target(int64_t t, int64_t, int batch, int i) const {
-        return (side == 0 ? a.q_out + t * a.ldqo : a.k_out + t * a.ldko) + head(batch, i) * a.D;
+    __device__ uint16_t *to(int64_t t, int64_t, int batch, int) const {
+        return (side == 0 ? a.q_out + t * a.ldqo : a.k_out + t * a.ldko) + head(batch, 0) * a.D;
     }
-    __device__ bool any(int batch, int i) const { return (batch * kRows + i) * gp < heads; }  // uniform
+    __device__ int64_t to_stride(int stride) const { return stride; }
+    __device__ bool any(int batch, int i) const { return (batch * kRows + i) * gp < heads; }
     __device__ bool has(int batch, int i) const { return head(batch, i) < heads; }
     __device__ bool plain(int) const { return false; }
     __device__ int64_t slot(int64_t) const { return 0; }
-    __device__ bool place(int64_t, bool, int64_t &at) const { return at = 0, true; }
+    __device__ bool place(int64_t, bool, int64_t &) const { return true; }
 };
 
 // Key heads of a token (the first half of a unit's rows) and its value heads.
@@ -160,19 +170,19 @@ struct AppendRows {
     __device__ AppendRows(const Args &args, int, int gp_, int g_) : a(args), gp(gp_), g(g_) {}
     __device__ int head(int batch, int i) const { return (batch * kHeads + i % kHeads) * gp + g; }
     __device__ const void *weight() const { return a.wk; }
-    __device__ const uint16_t *source(int64_t t, int batch, int i) const {
-        return (i < kHeads ? a.k + t * a.ldk : a.v + t * a.ldv) + head(batch, i) * a.D;
+    __device__ const uint16_t *from(int64_t t, int batch, int i) const {
+        return (i < kHeads ? a.k + t * a.ldk : a.v + t * a.ldv) + head(batch, 0) * a.D;
     }
-    __device__ uint16_t *target(int64_t, int64_t at, int batch, int i) const {
-        return (i < kHeads ? a.k_cache : a.v_cache) + at + static_cast<int64_t>(head(batch, i)) * a.page_size * a.D;
+    __device__ uint16_t *to(int64_t, int64_t at, int batch, int i) const {
+        return (i < kHeads ? a.k_cache : a.v_cache) + at + static_cast<int64_t>(head(batch, 0)) * a.page_size * a.D;
     }
+    __device__ int64_t to_stride(int stride) const { return static_cast<int64_t>(stride) * a.page_size; }
     __device__ bool any(int batch, int i) const { return (batch * kHeads + i % kHeads) * gp < a.Hkv; }
     __device__ bool has(int batch, int i) const { return head(batch, i) < a.Hkv; }
     __device__ bool plain(int i) const { return i >= kHeads; }
     __device__ int64_t slot(int64_t t) const { return a.slots[t]; }
     // Where a slot's rows are: of head 0, its row of its page.
     __device__ bool place(int64_t slot, bool report, int64_t &at) const {
-        at = 0;
         if (slot < 0) return false;
         if (slot >= a.pages * a.page_size) {
             if (report) atomicOr(a.status, kDeviceStatusIndex);
@@ -206,7 +216,7 @@ void deal_heads(int64_t T, int heads, int rows, int L, int *gp_log2, int *batche
 }
 
 template <typename Rows>
-cudaError_t launch_rows(const typename Rows::Args &a, const int (&heads)[2], int rows, bool interleaved,
+cudaError_t launch_rows(const typename Rows::Args &a, const int (&heads)[2], bool interleaved,
                         const LaunchCtx &ctx) {
     using Kernel = void (*)(const typename Rows::Args, const Deal);
     static const Kernel kernels[3][2] = {
@@ -221,7 +231,7 @@ cudaError_t launch_rows(const typename Rows::Args &a, const int (&heads)[2], int
     int64_t blocks[2] = {0, 0};
     for (int s = 0; s < 2; ++s) {
         if (heads[s] == 0) continue;
-        deal_heads(a.T, heads[s], rows, L, &deal.gp_log2[s], &deal.batches[s]);
+        deal_heads(a.T, heads[s], Rows::kHeads, L, &deal.gp_log2[s], &deal.batches[s]);
         const int64_t per = (kThreads / L) >> deal.gp_log2[s];
         const int64_t all = (a.T + per - 1) / per;
         const int64_t share = static_cast<int64_t>(kBlocksPerSm) * sms * heads[s] / (heads[0] + heads[1]);
@@ -244,12 +254,12 @@ cudaError_t launch_rows(const typename Rows::Args &a, const int (&heads)[2], int
 
 cudaError_t launch_qk_norm_rope(const NormRopeArgs &a, bool interleaved, const LaunchCtx &ctx) {
     const int heads[2] = {a.Hq, a.Hk};
-    return launch_rows<QkRows>(a, heads, kRows, interleaved, ctx);
+    return launch_rows<QkRows>(a, heads, interleaved, ctx);
 }
 
 cudaError_t launch_kv_append(const KvAppendArgs &a, bool interleaved, const LaunchCtx &ctx) {
     const int heads[2] = {a.Hkv, 0};
-    return launch_rows<AppendRows>(a, heads, AppendRows::kHeads, interleaved, ctx);
+    return launch_rows<AppendRows>(a, heads, interleaved, ctx);
 }
 
 }  // namespace ck
