@@ -134,6 +134,8 @@ def build(force: bool = False) -> str:
 def lib():
     """The loaded library.  Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()
@@ -176,9 +178,15 @@ def _check(st: int, where: str) -> None:
 # torch marshalling
 # ---------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(stream=None) -> int:
