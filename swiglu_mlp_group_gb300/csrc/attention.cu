@@ -75,7 +75,7 @@ struct Cfg {
     static constexpr int kSlots = D == 128 ? 5 : 10;  // ring of K and V tiles: 160 KB
     static constexpr int kBarBytes = 768;  // barriers, TMEM address, abort flag, Share, items
     // maximum and sum of a row, [stream][row]: what the streams of a narrow item
-    // tell each other (before the first item: the work's division)
+    // tell each other
     static constexpr int kExchangeBytes = 2 * kRows * 8;
     // the last 256: tiles start at a multiple of 1024, as the block's shared
     // memory does by its alignment; with what is left of 227 KB they also do
@@ -119,11 +119,11 @@ struct Work {
 };
 
 // Cost units: a sixteenth of a narrow key tile's time (cost_o of one).  A wide
-// tile is 3/2 of one: it is bound by its products and exponentials (2465 cycles,
-// two row tiles), a narrow one by the K and V it streams -- 64 KB, 2790 cycles
-// when all SMs stream at once, some 1300 alone.  An item's query loads and
-// result cost about one narrow tile.
-constexpr int kTileCost = 16, kWideTileCost = 24, kItemCost = 16;
+// tile is bound by its products and exponentials (2620 cycles for two row tiles),
+// a narrow one by the K and V it streams (64 KB, 2200 cycles with the SMs shared
+// between both); 21:16 divided a mixed call best of 19, 21 and 24.  An item's
+// query loads and result cost about a narrow tile.
+constexpr int kTileCost = 16, kWideTileCost = 21, kItemCost = 16;
 constexpr int64_t kMostCost = int64_t{1} << 30;
 
 struct Item {
@@ -156,38 +156,30 @@ __device__ __forceinline__ int own_len(const Work &w, int b) {
 }
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + kKeys - 1) / kKeys; }
 
-// The work's division, by all threads of the block (`scratch`: shared memory of
-// an int a warp).  Prefix groups are cut into equal parts of at most a CTA's
-// share, dealt out in turn -- row tiles of the same keys side by side, so that
-// they pass over them together and the keys are read from HBM once -- and own
-// tiles, in order, fill every CTA's share up.  Costs fit 30 bits (cost_shift).
-template <int THREADS>
-__device__ void divide(const Work &w, Share &sh, int *scratch) {
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    constexpr int kWarps = THREADS / 32;
+// The work's division, by one warp.  Prefix groups are cut into equal parts of
+// at most a CTA's share, dealt out in turn -- row tiles of the same keys side by
+// side, so that they pass over them together and the keys are read from HBM once
+// -- and own tiles, in order, fill every CTA's share up.  Costs fit 30 bits.
+__device__ void divide(const Work &w, Share &sh) {
+    const int lane = threadIdx.x & 31;
     const int groups = w.Hkv * w.rt_o;  // of one sequence
-    // own cost up to this thread's run of sequences
-    const int run = w.tiles_o == 0 ? 0 : w.B <= THREADS ? 1 : (w.B + THREADS - 1) / THREADS;
-    const int b0 = min(t * run, w.B), b1 = min(b0 + run, w.B);
+    // own cost up to this lane's run of sequences
+    const int run = w.tiles_o == 0 ? 0 : (w.B + 31) / 32;
+    const int b0 = min(lane * run, w.B), b1 = min(b0 + run, w.B);
     auto group_cost = [&](int b) { return w.cost_item + tiles_of(own_len(w, b)) * w.cost_o; };
-    int mine = 0, one = 0;  // one: a group's of the run's last
-    for (int b = b0; b < b1; ++b) one = group_cost(b), mine += groups * one;
+    int mine = 0;
+#pragma unroll 4
+    for (int b = b0; b < b1; ++b) mine += groups * group_cost(b);
     int upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += v;
     }
-    if (lane == 31) scratch[warp] = upto;
-    if (t == 0) sh.b_lo = sh.b_hi = w.B, sh.r_lo = sh.t_lo = sh.r_hi = sh.t_hi = sh.part_lo = 0;
-    __syncthreads();
-    int own = 0;
-    for (int i = 0; i < kWarps; ++i) {
-        const int v = scratch[i];
-        if (i < warp) upto += v;
-        own += v;
-    }
+    const int own = __shfl_sync(0xffffffffu, upto, 31);
     const int before = upto - mine;
+    if (lane == 0) sh.b_lo = sh.b_hi = w.B, sh.r_lo = sh.t_lo = sh.r_hi = sh.t_hi = sh.part_lo = 0;
+    __syncwarp();
 
     // CTAs that take part: two narrow tiles each at least
     const int prefix = w.tiles_p > 0 ? w.rt_p * w.Hkv * (w.cost_item + w.tiles_p * w.cost_p) : 0;
@@ -220,15 +212,15 @@ __device__ void divide(const Work &w, Share &sh, int *scratch) {
     const int cta = blockIdx.x;
     const int lo = cta < n ? min(start(cta), own) : own;
     const int hi = cta < n - 1 ? min(start(cta + 1), own) : own;
-    if (t == 0) {
+    if (lane == 0) {
         sh.parts_p = parts, sh.chunk_p = chunk, sh.items_p = items, sh.ctas = n;
         if (cta == 0) w.parts[0] = parts;
     }
-    // the tile at or behind a cost: by the thread whose sequences hold it
+    // the tile at or behind a cost: by the lane whose sequences hold it
     if ((lo >= before && lo < upto) || (hi >= before && hi < upto)) {
         int at = before;
         for (int b = b0; b < b1; ++b) {
-            const int g = run == 1 ? one : group_cost(b), all = g * groups;
+            const int g = group_cost(b), all = g * groups;
 #pragma unroll 1
             for (int end = 0; end < 2; ++end) {
                 const int x = (end ? hi : lo) - at;
@@ -249,7 +241,7 @@ __device__ void divide(const Work &w, Share &sh, int *scratch) {
             at += all;
         }
     }
-    __syncthreads();
+    __syncwarp();
 }
 
 // The items of this CTA, one after the other.
@@ -466,7 +458,6 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
         for (int b = threadIdx.x; b < w.B; b += kThreads)
             if (w.lens[b] < 0 || w.lens[b] > w.max_len) atomicOr(w.status, kDeviceStatusIndex);
     }
-    if (w.chunk_o == 0) divide<kThreads>(w, share, reinterpret_cast<int *>(xml));
 
     // The next item, in every lane of a reading warp; false after the last.
     uint32_t items = 0;
@@ -480,10 +471,9 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
         return it.nkeys != kEnd;
     };
 
-    // Every role walks the same items and key tiles with the same counters:
-    // J, key tiles so far (K in ring position 2 J, V in 2 J + 1); step, S tiles
-    // so far (its parity is the stream); narrow items so far (their query
-    // buffer), and the uses of each query buffer.
+    // Every role takes the same items and key tiles in the same order, with its
+    // own counters: ring fills (K of a tile, then V), steps (S tiles; their parity
+    // is the stream), narrow items (their parity is the query buffer).
     if (warp >= kTmaWarp) {
         setmaxnreg_dec<kOtherRegs>();  // by all four warps at once
         if (warp == kTmaWarp) {
@@ -579,6 +569,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             __syncwarp();
         } else if (warp == kWalkWarp) {
             // ------------------------------------------------------------ items
+            if (w.chunk_o == 0) divide(w, share);
             Walk walk;
             walk.idx = blockIdx.x, walk.tiles = -1, walk.len = 0;
             walk.b = w.chunk_o > 0 ? 0 : share.b_lo, walk.r = w.chunk_o > 0 ? 0 : share.r_lo;
