@@ -988,13 +988,31 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
                          : own > 0 ? w.parts[1 + (b * w.Hkv + hq / w.G) * w.rt_o + rt] : 0;
     if (np == 0 && no == 1) return;  // written by the item itself
     const int n = np + no;
-    constexpr int E = D / 32;
+    constexpr int E = D / 32, kAhead = 8;
+    auto slot_of = [&](int s) { return (s < np ? s : w.slots_p + s - np) * rows + row; };
     float M = -INFINITY, L = 0.f, o[E] = {};
     for (int s0 = 0; s0 < n; s0 += 32) {
-        // up to 32 parts: a lane each for their maxima and sums
+        // up to 32 parts: a lane each for their maxima and sums, and the first
+        // results on their way before those are known
+        const int here = min(32, n - s0);
         float2 ml = make_float2(-INFINITY, 0.f);
-        const int s = s0 + lane;
-        if (s < n) ml = w.part_ml[(s < np ? s : w.slots_p + s - np) * rows + row];
+        if (lane < here) ml = w.part_ml[slot_of(s0 + lane)];
+        float x[kAhead][E];
+        auto fetch = [&](int i0) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (i0 + k >= here) break;
+                const float *src = w.part_o + slot_of(s0 + i0 + k) * D + lane * E;
+                if constexpr (E == 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(src);
+                    x[k][0] = v.x, x[k][1] = v.y, x[k][2] = v.z, x[k][3] = v.w;
+                } else {
+                    const float2 v = *reinterpret_cast<const float2 *>(src);
+                    x[k][0] = v.x, x[k][1] = v.y;
+                }
+            }
+        };
+        fetch(0);
         float top = ml.y != 0.f ? ml.x : -INFINITY;
 #pragma unroll
         for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
@@ -1008,23 +1026,16 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
         M = m_new;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] *= keep;
-        const int here = min(32, n - s0);
-#pragma unroll 4
-        for (int i = 0; i < here; ++i) {
-            const float fi = __shfl_sync(0xffffffffu, f, i);
-            if (fi == 0.f) continue;
-            const int si = s0 + i;
-            const float *src = w.part_o + ((si < np ? si : w.slots_p + si - np) * rows + row) * D + lane * E;
-            float x[E];
-            if constexpr (E == 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(src);
-                x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-            } else {
-                const float2 v = *reinterpret_cast<const float2 *>(src);
-                x[0] = v.x, x[1] = v.y;
-            }
+        for (int i0 = 0; i0 < here; i0 += kAhead) {
+            if (i0 > 0) fetch(i0);
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = fmaf(fi, x[e], o[e]);
+            for (int k = 0; k < kAhead; ++k) {
+                if (i0 + k >= here) break;
+                const float fk = __shfl_sync(0xffffffffu, f, i0 + k);
+                if (fk == 0.f) continue;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = fmaf(fk, x[k][e], o[e]);
+            }
         }
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
