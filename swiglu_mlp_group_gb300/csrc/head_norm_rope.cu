@@ -1,7 +1,6 @@
 // head_norm_rope.cu -- the two passes between the qkv linear and attention:
 // the norm and rotation of query and key heads, and the append of keys (normed
-// and rotated on the way) and values to a paged cache.  Each reads a head's
-// row once into registers and writes it once; the bound is HBM bandwidth.
+// and rotated on the way) and values to a paged cache.
 #include "head_norm_rope.cuh"
 #include "attention.h"
 #include "internal.h"
@@ -11,9 +10,13 @@
 namespace ck {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kBlocksPerSm = 3;  // by their registers
-constexpr int kRows = 4;         // rows of a group of lanes in one unit of work
+// Rows of a group of lanes in one unit of work, and blocks that share an SM (by
+// their registers): of 2, 4 and 8 rows with 512 to 1280 threads an SM, 8 rows
+// with 640 were best at long calls (30011 tokens x 48 heads x 128: 131 us; 4 rows
+// with 768 139, 2 with 1024 170; 8 rows with 768 spill: 160).
+constexpr int kRows = 8;
+constexpr int kThreads = 128;
+constexpr int kBlocksPerSm = 5;
 
 // How the blocks' groups of L lanes are dealt out.  Blocks from `blocks_q` on
 // have the keys (of the append: none).  2^gp_log2 groups share a token, the g-th
@@ -30,13 +33,19 @@ struct Token {
     bool ok;
 };
 
-// Both passes are a copy with arithmetic, and latency is what they have to hide:
-// a token's position comes before its factors, and both before its rows can be
-// used.  A block is persistent and, while it works on one unit, has the next
-// one's rows and factors and the position after that on their way.  (Blocks of
-// one token each: 30011 tokens x 48 heads x 128 191 us, 64 KB on their way an SM
-// but for a third of a block's life; rows three units ahead through shared
-// memory, with the pairs' elements in different lanes: 247 us.)
+// Both passes are a copy with arithmetic: read once, written once, and HBM's
+// rate is the floor.  Latency is what they have to hide: a token's position comes
+// before its factors, and both before its rows can be used.  So a block is
+// persistent: while it works on one unit, the next one's factors and the position
+// after that are on their way, and a row's place is refilled from the next unit
+// as soon as it has been used.  Then instructions count (some 170 a warp for two
+// rows of 128 at first): a lane holds whole pairs, weights and factors are
+// multiplied once for all heads of a token, arithmetic is on two elements at a
+// time, and addresses are worked out once a unit.
+// Measured: 30011 tokens x 48 heads x 128 in 131 us (5.7 TB/s, 0.84 of the
+// measured copy), 4096 x 64 in 26 us (5.2 TB/s), append of 65519 tokens x 8 heads
+// in 91 us (6.1 TB/s, 0.90).  Tried and slower: a block for each token (191 us),
+// rows fetched three units ahead through shared memory (247 us).
 template <int L, bool INTERLEAVED, typename Rows>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 head_rows_kernel(const __grid_constant__ typename Rows::Args a, const __grid_constant__ Deal deal) {
