@@ -456,11 +456,11 @@ def _typed(t, dtype, what: str, shape=None):
     """Data pointer of an optional contiguous CUDA tensor of the given type (and shape)."""
     if t is None:
         return None
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous CUDA tensor of {dtype}")
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous() and (shape is None or t.shape == shape):
+        return t.data_ptr()
     if shape is not None and t.shape != shape:
-        raise ValueError(f"{what} must have shape {shape}, not {tuple(t.shape)}")
-    return t.data_ptr()
+        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    raise ValueError(f"{what} must be a contiguous CUDA tensor of {dtype}")
 
 
 def _run_stream(stream, like) -> int:
@@ -469,6 +469,15 @@ def _run_stream(stream, like) -> int:
     if stream is not None:
         return stream.cuda_stream
     return _torch()._C._cuda_getCurrentRawStream(like.get_device())
+
+
+def _new_like(x, stream):
+    """A new contiguous tensor like x (whose rows _token_stride has passed) that belongs to the call's stream."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty_like(x)  # x's tokens are contiguous or have gaps: contiguous either way
+    with torch.cuda.stream(stream):
+        return torch.empty_like(x)
 
 
 def _new(shape, dtype, like, stream):
@@ -517,14 +526,13 @@ def qk_norm_rope(q, k, cos_sin=None, positions=None, wq=None, wk=None, eps: floa
     q [T, Hq, D], k [T, Hk, D] or None, bf16: views of a packed projection's rows will do.  cos_sin f32
     [max_pos, rot_dim] (cosines, then sines), positions int32 [T].  wq, wk [D], f32 or bf16 alike.
     q_out=q, k_out=k work in place."""
-    torch = _torch()
     shape = q.shape
     T, Hq, D = shape
     ldq = _token_stride(q, shape, "q")
     table, max_pos, rot, rope, pos = _rotation(cos_sin, positions, T, mode)
     dt, wdt = _weight_type(wq, wk)
     if q_out is None:
-        q_out, ldqo = _new(shape, torch.bfloat16, q, stream), Hq * D
+        q_out, ldqo = _new_like(q, stream), Hq * D
     elif q_out.shape != shape:
         raise ValueError("q_out must have q's shape")
     else:
@@ -539,7 +547,7 @@ def qk_norm_rope(q, k, cos_sin=None, positions=None, wq=None, wk=None, eps: floa
             raise ValueError("q and k must have the same tokens and head size")
         ldk = _token_stride(k, kshape, "k")
         if k_out is None:
-            k_out, ldko = _new(kshape, torch.bfloat16, q, stream), Hk * D
+            k_out, ldko = _new_like(k, stream), Hk * D
         elif k_out.shape != kshape:
             raise ValueError("k_out must have k's shape")
         else:
@@ -615,7 +623,7 @@ def prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, block_t
             raise ValueError("block_table must have a row for every sequence")
         width = block_table.shape[1]
     if out is None:
-        out, ldo = _new(shape, torch.bfloat16, q, stream), Hq * D
+        out, ldo = _new_like(q, stream), Hq * D
     elif out.shape != shape:
         raise ValueError("out must have q's shape")
     else:
@@ -650,7 +658,7 @@ def cross_attention(q, k, v, kv_lens=None, scale: float | None = None, out=None,
     ldq = _token_stride(q, shape, "q")
     ldk, ldv = (_token_stride(k, kshape, "k"), _token_stride(v, kshape, "v")) if Lk > 0 else (0, 0)
     if out is None:
-        out, ldo = _new(shape, torch.bfloat16, q, stream), Hq * D
+        out, ldo = _new_like(q, stream), Hq * D
     elif out.shape != shape:
         raise ValueError("out must have q's shape")
     else:

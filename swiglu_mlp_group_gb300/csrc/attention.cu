@@ -1152,11 +1152,16 @@ bool key_map(CUtensorMap *m, const AttentionArgs &a, const uint16_t *p, int64_t 
 template <int D>
 cudaError_t launch(const AttentionArgs &a, Work &w, const LaunchCtx &ctx) {
     CUtensorMap qp, qo, km, vm;
-    if (!row_map(&qp, a, w.tok_p) || !row_map(&qo, a, w.tok_o)) return cudaErrorInvalidValue;
+    // maps of what the call reads; the others are never used
+    if (!row_map(&qo, a, w.tok_o)) return cudaErrorInvalidValue;
+    if (w.tiles_p == 0)
+        qp = qo;
+    else if (!row_map(&qp, a, w.tok_p))
+        return cudaErrorInvalidValue;
     if (a.k) {
         if (!key_map(&km, a, a.k, a.ldk) || !key_map(&vm, a, a.v, a.ldv)) return cudaErrorInvalidValue;
     } else {
-        km = vm = qo;  // no key at all: never used
+        km = vm = qo;  // no key at all
     }
     auto kern = attention_kernel<D>;
     constexpr size_t smem = Cfg<D>::kSmemBytes;
