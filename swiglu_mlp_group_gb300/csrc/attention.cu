@@ -36,6 +36,16 @@
 //                      them round in a ring.
 // P is rounded to bf16 for the second product, the operand type of V; its sum
 // is taken in f32 before that rounding.
+//
+// What bounds it (measured on GB300).  Wide items: the chain of a stream's tile,
+// S -> softmax (1440 cycles) -> P V -> Q K^T, some 2460 cycles for two row tiles
+// whose products take 2048; 2 x 8192 x 4093 x 32 heads of 128 in 415-430 us, 1600
+// to 1655 TFLOP/s, the rate at which a library's plain product runs under the
+// power limit (1706).  Short wide items: the store of their results besides, at
+// 26 to 32 B a cycle an SM.  Narrow items: the K and V in flight, three of the
+// ring's five 32 KB places an SM (the others hold what is being used): 5.5 to
+// 6 TB/s.  Small calls: latency, some 14 cycles for every instruction that is
+// fetched for the first time.
 #include <math.h>
 
 #include "attention.h"
@@ -58,7 +68,8 @@ constexpr int kThreads = 384;  // 8 softmax warps, TMA, 2 MMA, items
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs == kThreads * kLaunchRegs && kThreads * kLaunchRegs <= 65536);
 // Keys of a tile whose P is handed over first: P V of them runs while the last
-// exponentials are taken.
+// exponentials are taken (2 x 8192 x 4093 x 32 heads: 96 443 us, 64 502, 112 449,
+// all 128 at once 472).
 constexpr int kFirstKeys = 96;
 constexpr int kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -768,16 +779,16 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                     const int vis = live ? min(max(limit - it.key0 - key, 0), valid) : kKeys;
                     tmem_ld_32x32b_x32(ts, sr[0]);
                     tmem_ld_32x32b_x32(ts + 32u, sr[1]);
-                    tmem_wait_ld(sr[0]);
-                    tmem_wait_ld(sr[1]);
                     tmem_ld_32x32b_x32(ts + 64u, sr[2]);
                     tmem_ld_32x32b_x32(ts + 96u, sr[3]);
                     const bool masked = __any_sync(0xffffffffu, vis < kKeys);
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    row_max<0>(sr[0], masked, vis, mx);
-                    row_max<1>(sr[1], masked, vis, mx);
+                    tmem_wait_ld(sr[0]);
+                    tmem_wait_ld(sr[1]);
                     tmem_wait_ld(sr[2]);
                     tmem_wait_ld(sr[3]);
+                    row_max<0>(sr[0], masked, vis, mx);
+                    row_max<1>(sr[1], masked, vis, mx);
                     row_max<2>(sr[2], masked, vis, mx);
                     row_max<3>(sr[3], masked, vis, mx);
                     const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
