@@ -34,6 +34,8 @@
 //                      between the streams.
 //   warp 11          : works the CTA's items out, ahead of the others, and hands
 //                      them round in a ring.
+// In an item of few rows (FEW) the four warps of a stream share them: each has a
+// copy of the rows in its 32 of the tile and a quarter of the tile's keys.
 // P is rounded to bf16 for the second product, the operand type of V; its sum
 // is taken in f32 before that rounding.
 //
@@ -45,7 +47,9 @@
 // 26 to 32 B a cycle an SM.  Narrow items: the K and V in flight, three of the
 // ring's five 32 KB places an SM (the others hold what is being used): 5.5 to
 // 6 TB/s.  Small calls: latency, some 14 cycles for every instruction that is
-// fetched for the first time.
+// fetched for the first time.  Few rows: K and V, 1600
+// cycles for a key tile of 64 KB, and their items' ends, about 4000 cycles from the
+// last P on (1000 its product, 2800 the sums over streams and quarters and the store).
 #include <math.h>
 
 #include "attention.h"
@@ -71,6 +75,12 @@ static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs == kThreads * kLaunchRegs &&
 // exponentials are taken (2 x 8192 x 4093 x 32 heads: 96 443 us, 64 502, 112 449,
 // all 128 at once 472).
 constexpr int kFirstKeys = 96;
+// Query rows up to which a narrow item is one of few rows.  The call's kernel has
+// // their code where that is so of own items and none is wide: 16 x 1 x 1500 x 16
+// heads of 64 take 24.5 us without it and 20.4 with it; with wide items besides
+// (128 x 1 x 4096 behind 32768, 64 heads over 8 of 128) it is 223 and 246: a wide
+// tile, bound by its softmax, takes longer in the kernel that has both.
+constexpr int kFewRows = 16;
 constexpr int kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 // The accumulator is rescaled only when a row's maximum has grown by more than
@@ -146,10 +156,11 @@ struct Item {
     int lim0, lim_step;  // token t sees the keys below lim0 + lim_step * t
     int slot;            // where its partial result goes
     int own_parts;       // by cost, the last piece of an own group: how many there are, else 0
-    int flags;           // kWide, kWhole
+    int flags;           // kWide, kWhole, kFew
 };
 constexpr int kWide = 1;
 constexpr int kWhole = 2;  // all keys of its rows: written to out
+constexpr int kFew = 4;    // at most kFewRows query rows
 constexpr int kEnd = -1;   // nkeys of what follows the last item
 
 // What this CTA does, worked out once.
@@ -264,7 +275,7 @@ struct Walk {
         it.h = r / w.rt_o;
         const int rt = r - it.h * w.rt_o;
         it.b = b;
-        it.flags = w.wide_o ? kWide : 0;
+        it.flags = w.wide_o ? kWide : w.tok_o * w.G <= kFewRows ? kFew : 0;
         it.tok = w.tok_o;
         const int first = b * w.Lq, rows = it.tok * (w.wide_o ? 2 : 1);
         it.tok0 = first + rt * rows;
@@ -280,7 +291,7 @@ struct Walk {
     __device__ void prefix_item(const Work &w, Item &it, int rt, int h, int part, int chunk) const {
         it.b = -1;
         it.h = h;
-        it.flags = w.wide_p ? kWide : 0;
+        it.flags = w.wide_p ? kWide : w.tok_p * w.G <= kFewRows ? kFew : 0;
         it.tok = w.tok_p;
         const int rows = it.tok * (w.wide_p ? 2 : 1);
         it.tok0 = rt * rows;
@@ -389,7 +400,7 @@ __device__ __forceinline__ void weights(const uint32_t (&x)[32], float c, float 
     tmem_st_32x32b_x16(taddr, p);
 }
 
-template <int D>
+template <int D, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_constant__ CUtensorMap qmap_o,
                  const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -416,14 +427,17 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
     auto pv_issued = [&](int i) { return bars_s + 8u * (2 * NS + 12 + i); };
     // the same rows' warps of both streams are at the end of a narrow item
     auto met = [&](int q) { return bars_s + 8u * (2 * NS + 14 + q); };
-    auto item_full = [&](int i) { return bars_s + 8u * (2 * NS + 18 + i); };
-    auto item_empty = [&](int i) { return bars_s + 8u * (2 * NS + 18 + kItems + i); };
-    const uint32_t done_bar = bars_s + 8u * (2 * NS + 18 + 2 * kItems);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * NS + 19 + 2 * kItems);
+    const uint32_t met_all = bars_s + 8u * (2 * NS + 18);  // all softmax warps are at the end of an item of few rows
+    // and done with a query buffer that they have used for its results
+    auto few_free = [&](int i) { return bars_s + 8u * (2 * NS + 19 + i); };
+    auto item_full = [&](int i) { return bars_s + 8u * (2 * NS + 21 + i); };
+    auto item_empty = [&](int i) { return bars_s + 8u * (2 * NS + 21 + kItems + i); };
+    const uint32_t done_bar = bars_s + 8u * (2 * NS + 21 + 2 * kItems);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * NS + 22 + 2 * kItems);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     Share &share = *reinterpret_cast<Share *>(tmem_slot + 2);
     Item *const ring = reinterpret_cast<Item *>(&share + 1);
-    static_assert(8 * (2 * NS + 19 + 2 * kItems) + 8 + sizeof(Share) + kItems * sizeof(Item) <= C::kBarBytes);
+    static_assert(8 * (2 * NS + 22 + 2 * kItems) + 8 + sizeof(Share) + kItems * sizeof(Item) <= C::kBarBytes);
     float2 *const xml = reinterpret_cast<float2 *>(smem + (2 + NS) * C::kTileBytes + C::kBarBytes);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // uniform for the compiler too
@@ -438,6 +452,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full(i), 1);
             mbar_init(q_empty(i), 1);
+            mbar_init(few_free(i), 8);
             mbar_init(s_full(i), 1);
             mbar_init(p_full(i, 0), 4);
             mbar_init(p_full(i, 1), 4);
@@ -445,6 +460,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             mbar_init(pv_issued(i), 1);
         }
         for (int q = 0; q < 4; ++q) mbar_init(met(q), 2);
+        mbar_init(met_all, 8);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(item_full(i), 1);
             mbar_init(item_empty(i), kReaders);
@@ -492,6 +508,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             uint32_t seq = 0, nar = 0;
             Item it;
             uint32_t qpar = 0, qused = 0;  // bit i: parity of query buffer i's next use, used at all
+            uint32_t fpar = 0, qfew = 0;   // bit i: parity of its next use for a few rows' results, if its last was one
             bool ok = true;
             if (elect_one()) {
                 tma_prefetch_desc(&qmap_p);
@@ -555,11 +572,22 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                                 const int buf = wide ? i : static_cast<int>(nar & 1);
                                 ok = __all_sync(0xffffffffu, mbar_wait_spin(q_empty(buf), ((qpar >> buf) & 1) ^ 1, ctl));
                                 if (!ok) break;
+                                if (FEW && ((qfew >> buf) & 1)) {
+                                    ok = __all_sync(0xffffffffu, mbar_wait_spin(few_free(buf), (fpar >> buf) & 1, ctl));
+                                    if (!ok) break;
+                                    fpar ^= 1u << buf;
+                                }
+                                qfew = it.flags & kFew ? qfew | 1u << buf : qfew & ~(1u << buf);
                                 if (elect_one()) {
-                                    mbar_arrive_expect_tx(q_full(buf), it.tok * w.G * 128 * C::kHalves);
-                            for (int hf = 0; hf < C::kHalves; ++hf)
-                                        tma_load_3d(sQ(buf) + hf * C::kHalfBytes, qm, q_full(buf), hf * 64, it.h * w.G,
-                                                    it.tok0 + i * it.tok);
+                                    // few rows: four times, 32 rows apart
+                                    const int copies = FEW && (it.flags & kFew) ? 4 : 1;
+                                    mbar_arrive_expect_tx(q_full(buf), copies * it.tok * w.G * 128 * C::kHalves);
+#pragma unroll 1
+                                    for (int c = 0; c < copies * C::kHalves; ++c) {
+                                        const int hf = c % C::kHalves;
+                                        tma_load_3d(sQ(buf) + hf * C::kHalfBytes + c / C::kHalves * (32 * 128), qm,
+                                                    q_full(buf), hf * 64, it.h * w.G, it.tok0 + i * it.tok);
+                                    }
                                 }
                                 __syncwarp();
                                 qpar ^= 1u << buf;
@@ -738,7 +766,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
         const int Hq = w.Hkv * w.G;
         const int64_t rows = static_cast<int64_t>(w.T) * Hq;
         const float c = w.scale_log2;
-        uint32_t step = 0, cnt = 0, meets = 0;
+        uint32_t step = 0, cnt = 0, meets = 0, all_meets = 0, nar = 0;
         bool ok = true;
         // both warps of these rows have got here (a bounded wait, unlike bar.sync)
         auto meet = [&]() {
@@ -746,11 +774,195 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             if (lane == 0) mbar_arrive(met(warp & 3));
             return __all_sync(0xffffffffu, mbar_wait_spin(met(warp & 3), meets++ & 1, ctl)) != 0;
         };
+        auto meet_all = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(met_all);
+            return __all_sync(0xffffffffu, mbar_wait_spin(met_all, all_meets++ & 1, ctl)) != 0;
+        };
+        // O scaled where a row's maximum has grown past the threshold; f: by how much
+        auto rescale = [&](float f) {
+            if (!__all_sync(0xffffffffu, mbar_wait_spin(o_full(st), (cnt - 1) & 1, ctl))) return false;
+            tc_fence_after_sync();
+#pragma unroll 1
+            for (int q = 0; q < D / 16; ++q) {
+                uint32_t o[16];
+                tmem_ld_32x32b_x16(to + 16u * q, o);
+                tmem_wait_ld16(o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st_32x32b_x16(to + 16u * q, o);
+            }
+            return true;
+        };
+        auto arrive = [&](int half) {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full(st, half));
+        };
+        const int quarter = warp & 3;
+        // of an item of few rows (lanes from kFewRows on help at its end only)
+        const int few_row = lane % kFewRows, few_tok = few_row / w.G, few_g = few_row - few_tok * w.G;
         Item it;
 #pragma unroll 1
         while (ok && next_item(it)) {
             const int ntiles = tiles_of(it.nkeys);
             const bool wide = it.flags & kWide;
+            const int buf = nar & 1;
+            if (!wide && ntiles > 0) ++nar;
+            if (FEW && (it.flags & kFew) && ntiles > 0) {
+                // A few rows would leave all but one of a stream's warps idle: they
+                // are in the tile four times, 32 rows apart, and each warp takes a
+                // quarter of a tile's keys, with maxima and sums of its own; P of
+                // the other keys is 0 in its rows.  A tile's softmax is a quarter as
+                // long, and K and V stay in the ring for as much less.
+                const int tok = it.tok0 + few_tok;
+                const bool row_live = few_tok < it.tok && tok < it.tok_end;
+                const bool live = row_live && lane < kFewRows;
+                const int limit = it.lim0 + it.lim_step * tok - it.key0 - 32 * quarter;
+                float mref = -INFINITY, l = 0.f;
+                int done = 0;
+#pragma unroll 1
+                for (int j = 0; j < ntiles; ++j) {
+                    if (static_cast<int>(step++ & 1) != st) continue;
+                    ok = __all_sync(0xffffffffu, mbar_wait_spin(s_full(st), cnt & 1, ctl));
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const int key = j * kKeys;
+                    const int vis = live ? min(limit - key, it.nkeys - key - 32 * quarter) : 32;
+                    uint32_t x[32];
+                    tmem_ld_32x32b_x32(ts + 32u * quarter, x);
+                    const bool masked = __any_sync(0xffffffffu, vis < 32);
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    tmem_wait_ld(x);
+                    row_max<0>(x, masked, vis, mx);
+                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    if (done == 0) {
+                        mref = mt;
+                    } else {
+                        const float m_new = fmaxf(mref, mt);
+                        const bool grow = live && (m_new - mref) * c > kRescaleLog2;
+                        if (__any_sync(0xffffffffu, grow)) {
+                            const float f = grow ? ex2((mref - m_new) * c) : 1.f;
+                            ok = rescale(f);
+                            if (!ok) break;
+                            l *= f;
+                            if (grow) mref = m_new;
+                        }
+                    }
+                    const float mc = mref == -INFINITY ? 0.f : mref * c;
+                    uint64_t sum[2] = {0, 0};
+                    weights(x, c, mc, sum, ts + 16u * quarter);
+                    uint32_t zero[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) zero[i] = 0;
+#pragma unroll
+                    for (int q = 1; q < 4; ++q) tmem_st_32x32b_x16(ts + 16u * ((quarter + q) & 3), zero);
+                    float a, b;
+                    f32x2_split(add_f32x2(sum[0], sum[1]), a, b);
+                    l += a + b;
+                    tmem_wait_st();
+                    arrive(0);
+                    arrive(1);
+                    ++cnt;
+                    ++done;
+                }
+                if (!ok) break;
+                if (done > 0) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_spin(o_full(st), (cnt - 1) & 1, ctl));
+                    if (!ok) break;
+                }
+                // The result: eight parts of a row, by stream and quarter.  Each
+                // warp adds up its quarter's two streams for half of the columns
+                // and puts them where the item's queries were, which are not
+                // needed any more; then it adds up the quarters for an eighth of
+                // the columns, two lanes a row, and stores them.
+                tc_fence_before_sync();
+                xml[st * kRows + 32 * quarter + lane] = make_float2(mref == -INFINITY ? mref : mref * c, l);
+                ok = meet_all();
+                if (!ok) break;
+                tc_fence_after_sync();
+                const bool part = !(it.flags & kWhole);
+                const int only = ntiles == 1 ? static_cast<int>((step - 1) & 1) : -1;  // the one stream with a tile
+                float *const scratch = reinterpret_cast<float *>(smem + buf * C::kTileBytes);
+                float m = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 o = xml[32 * i + few_row];
+                    if (o.y != 0.f) m = fmaxf(m, o.x);
+                }
+                float f0 = 0.f, f1 = 0.f;  // of this quarter's streams
+                l = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 o = xml[32 * i + few_row];
+                    const float fi = o.y != 0.f ? ex2(o.x - m) : 0.f;
+                    l += fi * o.y;
+                    if (i == quarter) f0 = fi;
+                    if (i == 4 + quarter) f1 = fi;
+                }
+#pragma unroll 1
+                for (int col = st * (D / 2); col < (st + 1) * (D / 2); col += 32) {
+                    uint32_t o[32];
+                    float v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+#pragma unroll 1
+                    for (int s2 = 0; s2 < 2; ++s2) {
+                        if (only >= 0 && only != s2) continue;
+                        const float f = s2 == 0 ? f0 : f1;
+                        tmem_ld_32x32b_x32(tO(s2) + lanes + static_cast<uint32_t>(col), o);
+                        tmem_wait_ld(o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = f != 0.f ? fmaf(__uint_as_float(o[i]), f, v[i]) : v[i];
+                    }
+                    if (lane < kFewRows) {
+                        // pieces of 16 bytes, turned by the row against bank conflicts
+                        float4 *dst = reinterpret_cast<float4 *>(scratch + (quarter * kFewRows + lane) * D + col);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            dst[i ^ (lane & 7)] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    }
+                }
+                tc_fence_before_sync();
+                fence_proxy_async_smem();
+                ok = meet_all();
+                if (!ok) break;
+                const int Hq_row = it.h * w.G + few_g;
+                const int64_t pr = part ? it.slot * rows + static_cast<int64_t>(tok) * Hq + Hq_row : 0;
+                if (part && live && warp == 0) w.part_ml[pr] = make_float2(m, l);
+                if (it.own_parts > 0 && threadIdx.x == 0)
+                    w.parts[1 + (it.b * w.Hkv + it.h) * w.rt_o + (it.tok0 - it.b * w.Lq) / it.tok] = it.own_parts;
+                if (row_live) {
+                    // D / 8 columns of this warp, half of them of this lane
+                    constexpr int kPieces = D / 64;
+                    const int piece0 = (st * (D / 2) + quarter * (D / 8)) / 4 + (lane >> 4) * kPieces;
+                    const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
+                    float4 sum4[kPieces];
+#pragma unroll
+                    for (int k = 0; k < kPieces; ++k) {
+                        sum4[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        const int piece = piece0 + k;
+#pragma unroll
+                        for (int o = 0; o < 4; ++o) {
+                            const float4 x = reinterpret_cast<const float4 *>(
+                                scratch + (o * kFewRows + few_row) * D)[(piece & ~7) + ((piece & 7) ^ (few_row & 7))];
+                            sum4[k].x += x.x, sum4[k].y += x.y, sum4[k].z += x.z, sum4[k].w += x.w;
+                        }
+                        if (part) {
+                            reinterpret_cast<float4 *>(w.part_o + pr * D)[piece] = sum4[k];
+                        } else {
+                            uint2 *dst = reinterpret_cast<uint2 *>(w.out + tok * w.ldo + static_cast<int64_t>(Hq_row) * D);
+                            dst[piece] = make_uint2(pack2(sum4[k].x * inv, sum4[k].y * inv),
+                                                    pack2(sum4[k].z * inv, sum4[k].w * inv));
+                        }
+                    }
+                }
+                // every warp has read its sums before the next queries come
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(few_free(buf));
+                continue;
+            }
             const int tok = it.tok0 + (wide ? st * it.tok : 0) + row_tok;
             const bool live = row_tok < it.tok && tok < it.tok_end;
             const bool warp_live = __any_sync(0xffffffffu, live);
@@ -769,11 +981,6 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                 uint32_t sr[4][32];
                 uint64_t sum[2] = {0, 0};
                 float mc = 0.f;
-                auto arrive = [&](int half) {
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(p_full(st, half));
-                };
                 if (warp_live) {
                     // rows of no query hold what they like: not worth a mask
                     const int vis = live ? min(max(limit - it.key0 - key, 0), valid) : kKeys;
@@ -799,18 +1006,8 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                         const bool grow = (m_new - mref) * c > kRescaleLog2;
                         if (__any_sync(0xffffffffu, grow)) {
                             const float f = grow ? ex2((mref - m_new) * c) : 1.f;
-                            ok = __all_sync(0xffffffffu, mbar_wait_spin(o_full(st), (cnt - 1) & 1, ctl));
+                            ok = rescale(f);
                             if (!ok) break;
-                            tc_fence_after_sync();
-#pragma unroll 1
-                            for (int q = 0; q < D / 16; ++q) {
-                                uint32_t o[16];
-                                tmem_ld_32x32b_x16(to + 16u * q, o);
-                                tmem_wait_ld16(o);
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                tmem_st_32x32b_x16(to + 16u * q, o);
-                            }
                             l *= f;
                             if (grow) mref = m_new;
                         }
@@ -1174,7 +1371,9 @@ cudaError_t launch(const AttentionArgs &a, Work &w, const LaunchCtx &ctx) {
     } else {
         km = vm = qo;  // no key at all
     }
-    auto kern = attention_kernel<D>;
+    // few rows against each sequence's own keys, and no wide items besides
+    const bool few = !w.wide_o && w.tok_o * w.G <= kFewRows && (w.tiles_p == 0 || !w.wide_p);
+    auto kern = few ? attention_kernel<D, true> : attention_kernel<D, false>;
     constexpr size_t smem = Cfg<D>::kSmemBytes;
     if (cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), static_cast<int>(smem));
         e != cudaSuccess)

@@ -234,6 +234,34 @@ def test_cross_head_layouts(Hq, H, Lq):
     check_cross(Hq, 3, Lq, 150, Hq, H, 64, [150, 1, 149])
 
 
+# up to 16 query rows a key head and just above, and more groups than SMs: every CTA takes several in turn
+@pytest.mark.parametrize("Lq,G", [(1, 1), (1, 8), (3, 5), (16, 1), (2, 8), (17, 1), (3, 6)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_few_rows_many_groups(Lq, G, D):
+    lens = [(37 * b) % 700 for b in range(50)]
+    check_cross(Lq + G, 50, Lq, 700, 8 * G, 8, D, lens)
+    check_prefix(Lq * G, 50, Lq, 2 * G, 2, D, 32, 0, lens)
+
+
+# scores that grow with the keys, for some rows only: a running maximum that moves in every tile, or in one quarter of it
+@pytest.mark.parametrize("Lq", [1, 4, 40])
+@pytest.mark.parametrize("every", [1, 37, 128])
+@pytest.mark.parametrize("D", [64, 128])
+def test_cross_growing_scores(Lq, every, D):
+    dev = device()
+    B, Lk, H = 3, 1100, 4
+    g = ref.gen(Lq + every)
+    q, k, v = ref.randn(g, B, Lq, H, D), ref.randn(g, B, Lk, H, D), ref.randn(g, B, Lk, H, D)
+    q[:, ::3] = -q[:, ::3]
+    # up to 2 sqrt(D): scores whose f32 sums the bound still allows for
+    k[:, ::every] = q[:, -1:, :] * torch.linspace(0, 2, Lk)[::every].view(1, -1, 1, 1).to(q.dtype)
+    q, k, v = q.to(dev), k.to(dev), v.to(dev)
+    out = ck.cross_attention(q, k, v)
+    want, mag = ref.attend(q, list(k), list(v), [[Lk] * Lq] * B, D ** -0.5)
+    poll_ok()
+    ref.assert_attention(out, want, mag)
+
+
 def test_cross_more_rows_than_a_wave():
     check_cross(21, 2, 2500, 300, 6, 3, 128, [300, 299])
     check_cross(22, 1, 1, 5000, 4, 4, 128, None)
