@@ -33,7 +33,7 @@
 //   warps 9, 10      : MMA issue: S = Q K^T, O += P V.  Their steps alternate
 //                      between the streams.
 //   warp 11          : works the CTA's items out, ahead of the others, and hands
-//                      them round in a ring.
+//                      them round in a ring; sends finished rows out by TMA.
 // In an item of few rows (FEW) the four warps of a stream share them: each has a
 // copy of the rows in its 32 of the tile and a quarter of the tile's keys.
 // P is rounded to bf16 for the second product, the operand type of V; its sum
@@ -43,13 +43,13 @@
 // S -> softmax (1440 cycles) -> P V -> Q K^T, some 2460 cycles for two row tiles
 // whose products take 2048; 2 x 8192 x 4093 x 32 heads of 128 in 415-430 us, 1600
 // to 1655 TFLOP/s, the rate at which a library's plain product runs under the
-// power limit (1706).  Short wide items: the store of their results besides, at
-// 26 to 32 B a cycle an SM.  Narrow items: the K and V in flight, three of the
-// ring's five 32 KB places an SM (the others hold what is being used): 5.5 to
-// 6 TB/s.  Small calls: latency, some 14 cycles for every instruction that is
-// fetched for the first time.  Few rows: K and V, 1600
-// cycles for a key tile of 64 KB, and their items' ends, about 4000 cycles from the
-// last P on (1000 its product, 2800 the sums over streams and quarters and the store).
+// power limit (1706).  Short wide items: their starts and ends besides.  Narrow
+// items: the K and V in flight, three of the ring's five 32 KB places an SM (the
+// others hold what is being used): 5.5 to 6 TB/s.  Few rows: K and V, 1600 cycles
+// for a key tile of 64 KB, and their items' ends, about 4000 cycles from the last P
+// on (1000 its product, 2800 the sums over streams and quarters and the store).
+// Small calls: latency, some 14 cycles for every instruction that is fetched for
+// the first time.
 #include <math.h>
 
 #include "attention.h"
@@ -364,6 +364,13 @@ struct Walk {
     }
 };
 
+// Whole rows of a wide item: stored through the ring, beside the next item's first
+// tiles (2 x 4096 x 333 x 32 heads of 128: 43.3 us from registers, 41.2 so; 2 x 8192 x
+// 4093: 427, 420; of one tile, of more than two alike).
+__device__ __forceinline__ bool staged(int flags, int ntiles) {
+    return (flags & (kWide | kWhole)) == (kWide | kWhole) && ntiles > 0;
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -404,7 +411,7 @@ template <int D, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_constant__ CUtensorMap qmap_o,
                  const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                 const __grid_constant__ Work w) {
+                 const __grid_constant__ CUtensorMap omap, const __grid_constant__ Work w) {
     using C = Cfg<D>;
     constexpr int NS = C::kSlots;
     extern __shared__ uint8_t smem_raw[];
@@ -430,19 +437,22 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
     const uint32_t met_all = bars_s + 8u * (2 * NS + 18);  // all softmax warps are at the end of an item of few rows
     // and done with a query buffer that they have used for its results
     auto few_free = [&](int i) { return bars_s + 8u * (2 * NS + 19 + i); };
-    auto item_full = [&](int i) { return bars_s + 8u * (2 * NS + 21 + i); };
-    auto item_empty = [&](int i) { return bars_s + 8u * (2 * NS + 21 + kItems + i); };
-    const uint32_t done_bar = bars_s + 8u * (2 * NS + 21 + 2 * kItems);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * NS + 22 + 2 * kItems);
+    auto staged_full = [&](int i) { return bars_s + 8u * (2 * NS + 21 + i); };  // a stream's result is in the ring
+    auto item_full = [&](int i) { return bars_s + 8u * (2 * NS + 23 + i); };
+    auto item_empty = [&](int i) { return bars_s + 8u * (2 * NS + 23 + kItems + i); };
+    const uint32_t done_bar = bars_s + 8u * (2 * NS + 23 + 2 * kItems);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * NS + 24 + 2 * kItems);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     Share &share = *reinterpret_cast<Share *>(tmem_slot + 2);
     Item *const ring = reinterpret_cast<Item *>(&share + 1);
-    static_assert(8 * (2 * NS + 22 + 2 * kItems) + 8 + sizeof(Share) + kItems * sizeof(Item) <= C::kBarBytes);
+    static_assert(8 * (2 * NS + 24 + 2 * kItems) + 8 + sizeof(Share) + kItems * sizeof(Item) <= C::kBarBytes);
     float2 *const xml = reinterpret_cast<float2 *>(smem + (2 + NS) * C::kTileBytes + C::kBarBytes);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // uniform for the compiler too
     const int lane = threadIdx.x & 31;
     const WaitCtl ctl{abort_flag, w.status, w.timeout_ns};
+    // waits that may last for an item, at 2 us a tile
+    const WaitCtl item_ctl{abort_flag, w.status, w.timeout_ns + 2000ull * max(w.tiles_p, w.tiles_o)};
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
@@ -453,6 +463,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             mbar_init(q_full(i), 1);
             mbar_init(q_empty(i), 1);
             mbar_init(few_free(i), 8);
+            mbar_init(staged_full(i), 4);
             mbar_init(s_full(i), 1);
             mbar_init(p_full(i, 0), 4);
             mbar_init(p_full(i, 1), 4);
@@ -490,7 +501,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
     uint32_t items = 0;
     auto next_item = [&](Item &it) {
         const uint32_t i = items % kItems;
-        if (!__all_sync(0xffffffffu, mbar_wait_spin(item_full(i), (items / kItems) & 1, ctl))) return false;
+        if (!__all_sync(0xffffffffu, mbar_wait_spin(item_full(i), (items / kItems) & 1, item_ctl))) return false;
         it = ring[i];
         __syncwarp();
         if (lane == 0) mbar_arrive(item_empty(i));
@@ -499,7 +510,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
     };
 
     // Every role takes the same items and key tiles in the same order, with its
-    // own counters: ring fills (K of a tile, then V), steps (S tiles; their parity
+    // own counters: ring fills (K of a tile, then V; staged() ones' results), steps (S tiles; their parity
     // is the stream), narrow items (their parity is the query buffer).
     if (warp >= kTmaWarp) {
         setmaxnreg_dec<kOtherRegs>();  // by all four warps at once
@@ -596,6 +607,17 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                         }
                     }
                 }
+                if (!FEW && staged(it.flags, ntiles)) {
+                    // two places for its results, nothing to load
+#pragma unroll 1
+                    for (int i = 0; i < 2 && ok; ++i, ++seq) {
+                        const int s = seq % NS;
+                        ok = __all_sync(0xffffffffu, mbar_wait_spin(kv_empty(s), ((seq / NS) & 1) ^ 1, ctl));
+                        if (!ok) break;
+                        if (lane == 0) mbar_arrive(kv_full(s));
+                        __syncwarp();
+                    }
+                }
                 if (!wide && ntiles > 0) ++nar;
             }
             if (*abort_flag && elect_one()) {
@@ -612,20 +634,58 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             Walk walk;
             walk.idx = blockIdx.x, walk.tiles = -1, walk.len = 0;
             walk.b = w.chunk_o > 0 ? 0 : share.b_lo, walk.r = w.chunk_o > 0 ? 0 : share.r_lo;
-            bool more = true;
+            // An item's staged results, when the softmax has put them into the
+            // ring: out by TMA, which leaves rows past the sequence's queries
+            // out, and the places back to the loader.
+            uint32_t fills = 0, stages = 0;
+            auto store = [&](const Item &it) {
+                const int ntiles = tiles_of(it.nkeys);
+                fills += 2 * ntiles;
+                if (!staged(it.flags, ntiles)) return true;
 #pragma unroll 1
-            for (uint32_t n = 0; more; ++n) {
+                for (int st = 0; st < 2; ++st, ++fills) {
+                    const int s = fills % NS;
+                    if (!__all_sync(0xffffffffu, mbar_wait_spin(staged_full(st), stages & 1, item_ctl))) return false;
+                    const int first = it.tok0 + st * it.tok;  // its first token
+                    if (lane == 0) {
+                        if (first < it.tok_end) {
+#pragma unroll 1
+                            for (int hf = 0; hf < C::kHalves; ++hf)
+                                tma_store_4d(&omap, sKV(s) + hf * C::kHalfBytes, hf * 64, it.h * w.G, first - it.b * w.Lq,
+                                             it.b);
+                            bulk_commit();
+                            bulk_wait_read();
+                        }
+                        mbar_arrive(kv_empty(s));
+                    }
+                    __syncwarp();
+                }
+                ++stages;
+                return true;
+            };
+            bool more = true, ok = true;
+            uint32_t n = 0, sent = 0;  // items in the ring so far, looked after by store()
+#pragma unroll 1
+            for (; more; ++n) {
                 Item it;
                 more = w.chunk_o > 0 ? walk.next_fixed(w, it) : walk.next_share(w, share, it);
                 if (!more) it.nkeys = kEnd;
                 const uint32_t i = n % kItems;
-                if (!__all_sync(0xffffffffu, mbar_wait_spin(item_empty(i), ((n / kItems) & 1) ^ 1, ctl))) break;
+                ok = __all_sync(0xffffffffu, mbar_wait_spin(item_empty(i), ((n / kItems) & 1) ^ 1, item_ctl));
+                if (!ok) break;
                 if (lane == 0) {
                     ring[i] = it;
                     mbar_arrive(item_full(i));
                 }
                 __syncwarp();
+                if (!FEW && n - sent == kItems - 1) ok = store(ring[sent++ % kItems]);  // the oldest in the ring
+                if (!ok) break;
             }
+            if (!FEW) {
+                while (ok && sent < n) ok = store(ring[sent++ % kItems]);
+                if (lane == 0) bulk_wait();
+            }
+            __syncwarp();
         } else if (warp == kQkWarp || warp == kPvWarp) {
             // ------------------------------------------------------------ MMA
             // One warp issues S = Q K^T of every step, one O += P V; both take
@@ -656,7 +716,8 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
 #pragma unroll 1
             while (ok && next_item(it)) {
                 const int nkeys = __shfl_sync(0xffffffffu, it.nkeys, 0);
-                const bool wide = __shfl_sync(0xffffffffu, it.flags, 0) & kWide;
+                const int flags = __shfl_sync(0xffffffffu, it.flags, 0);
+                const bool wide = flags & kWide;
                 const int ntiles = tiles_of(nkeys);
                 const int subs = wide ? 2 : 1;
 #pragma unroll 1
@@ -746,6 +807,10 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                     slot += 2;
                     if (slot >= NS) slot -= NS, par ^= 1;
                 }
+                if (!FEW && staged(flags, ntiles)) {
+                    slot += 2;
+                    if (slot >= NS) slot -= NS, par ^= 1;
+                }
                 if (!wide && ntiles > 0) ++nar;
             }
             // no MMA may be in flight when TMEM is released
@@ -767,6 +832,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
         const int64_t rows = static_cast<int64_t>(w.T) * Hq;
         const float c = w.scale_log2;
         uint32_t step = 0, cnt = 0, meets = 0, all_meets = 0, nar = 0;
+        uint32_t fills = 0;
         bool ok = true;
         // both warps of these rows have got here (a bounded wait, unlike bar.sync)
         auto meet = [&]() {
@@ -1034,12 +1100,52 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             }
             if (!ok) break;
             if (wide) step += 2 * ntiles;
+            fills += 2 * ntiles;
             // The item's result.  A wide item's rows are this stream's own.  A
             // narrow one's are both streams': each adds up one half of the
             // columns of the two accumulators, as a join of two parts would.
             if (done > 0) {
                 ok = __all_sync(0xffffffffu, mbar_wait_spin(o_full(st), (cnt - 1) & 1, ctl));
                 if (!ok) break;
+            }
+            if (it.own_parts > 0 && !w.direct && threadIdx.x == 0)
+                w.parts[1 + (it.b * w.Hkv + it.h) * w.rt_o + (it.tok0 - it.b * w.Lq) / (it.tok * (wide ? 2 : 1))] =
+                    it.own_parts;
+            if (!FEW && staged(it.flags, ntiles)) {
+                // Finished rows go to a place of the ring that the loader has
+                // passed over, laid out as the query tile; the walking warp
+                // sends them out.
+                const int s = (fills + st) % NS;
+                ok = __all_sync(0xffffffffu, mbar_wait_spin(kv_full(s), ((fills + st) / NS) & 1, ctl));
+                if (!ok) break;
+                fills += 2;
+                tc_fence_after_sync();
+                if (warp_live) {
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    uint32_t o[D / 32][32];
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q) tmem_ld_32x32b_x32(to + 32u * q, o[q]);
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q) tmem_wait_ld(o[q]);
+                    uint8_t *const dst = smem + (2 + s) * C::kTileBytes + row * 128;
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            p[i] = inv != 0.f ? pack2(__uint_as_float(o[q][2 * i]) * inv,
+                                                      __uint_as_float(o[q][2 * i + 1]) * inv)
+                                              : 0u;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            *reinterpret_cast<uint4 *>(dst + (q / 2) * C::kHalfBytes + (((q & 1) * 4 + k) ^ (row & 7)) * 16) =
+                                make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(staged_full(st));
+                continue;
             }
             float m = mref == -INFINITY ? mref : mref * c;
             float f_mine = 1.f, f_other = 0.f;
@@ -1069,9 +1175,6 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                 const int64_t at = static_cast<int64_t>(tok) * Hq + it.h * w.G + row_g;
                 const int64_t pr = part ? it.slot * rows + at : 0;
                 if (part && live && reports) w.part_ml[pr] = make_float2(m, l);
-                if (it.own_parts > 0 && !w.direct && threadIdx.x == 0)
-                    w.parts[1 + (it.b * w.Hkv + it.h) * w.rt_o + (it.tok0 - it.b * w.Lq) / (it.tok * (wide ? 2 : 1))] =
-                        it.own_parts;
                 const bool empty = ntiles == 0;  // zeros, if written at all
                 const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
                 f_mine *= inv, f_other *= inv;
@@ -1341,6 +1444,17 @@ bool row_map(CUtensorMap *m, const AttentionArgs &a, int tokens) {
     return tensor_map_bf16(m, a.q, 3, dims, strides, box);
 }
 
+// The same rows of the result, by sequence: a tile's rows past its queries are
+// outside.
+bool out_map(CUtensorMap *m, const AttentionArgs &a, int tokens) {
+    const uint64_t ld = static_cast<uint64_t>(a.ldo) * 2;
+    const uint64_t dims[4] = {static_cast<uint64_t>(a.D), static_cast<uint64_t>(a.Hq), static_cast<uint64_t>(a.Lq),
+                              static_cast<uint64_t>(a.B)};
+    const uint64_t strides[3] = {static_cast<uint64_t>(a.D) * 2, ld, ld * static_cast<uint64_t>(a.Lq)};
+    const uint32_t box[4] = {64, static_cast<uint32_t>(a.G), static_cast<uint32_t>(tokens), 1};
+    return tensor_map_bf16(m, a.out, 4, dims, strides, box);
+}
+
 bool key_map(CUtensorMap *m, const AttentionArgs &a, const uint16_t *p, int64_t ld) {
     uint64_t dims[2], strides[1];
     uint32_t box[2] = {64, kKeys};
@@ -1359,7 +1473,7 @@ bool key_map(CUtensorMap *m, const AttentionArgs &a, const uint16_t *p, int64_t 
 
 template <int D>
 cudaError_t launch(const AttentionArgs &a, Work &w, const LaunchCtx &ctx) {
-    CUtensorMap qp, qo, km, vm;
+    CUtensorMap qp, qo, km, vm, om;
     // maps of what the call reads; the others are never used
     if (!row_map(&qo, a, w.tok_o)) return cudaErrorInvalidValue;
     if (w.tiles_p == 0)
@@ -1371,6 +1485,10 @@ cudaError_t launch(const AttentionArgs &a, Work &w, const LaunchCtx &ctx) {
     } else {
         km = vm = qo;  // no key at all
     }
+    if (!w.wide_o)
+        om = qo;
+    else if (!out_map(&om, a, w.tok_o))
+        return cudaErrorInvalidValue;
     // few rows against each sequence's own keys, and no wide items besides
     const bool few = !w.wide_o && w.tok_o * w.G <= kFewRows && (w.tiles_p == 0 || !w.wide_p);
     auto kern = few ? attention_kernel<D, true> : attention_kernel<D, false>;
@@ -1394,7 +1512,7 @@ cudaError_t launch(const AttentionArgs &a, Work &w, const LaunchCtx &ctx) {
     cfg.stream = ctx.stream;
     cfg.attrs = attr;
     cfg.numAttrs = ctx.pdl ? 1 : 0;
-    if (cudaError_t e = cudaLaunchKernelEx(&cfg, kern, qp, qo, km, vm, w); e != cudaSuccess) return e;
+    if (cudaError_t e = cudaLaunchKernelEx(&cfg, kern, qp, qo, km, vm, om, w); e != cudaSuccess) return e;
     if (w.direct) return cudaSuccess;
     const int64_t rows = static_cast<int64_t>(w.T) * w.Hkv * w.G;
     cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));

@@ -206,9 +206,9 @@ bool tensor_map_2d(CUtensorMap *map, const void *ptr, CUtensorMapDataType dtype,
 bool tensor_map_bf16(CUtensorMap *map, const void *ptr, int rank, const uint64_t *dims,
                      const uint64_t *strides, const uint32_t *box) {
     auto encode = encode_fn();
-    if (!encode || rank < 2 || rank > 3) return false;
-    cuuint64_t d[3], st[2];
-    cuuint32_t bx[3], estr[3] = {1, 1, 1};
+    if (!encode || rank < 2 || rank > 4) return false;
+    cuuint64_t d[4], st[3];
+    cuuint32_t bx[4], estr[4] = {1, 1, 1, 1};
     for (int i = 0; i < rank; ++i) d[i] = dims[i], bx[i] = box[i];
     for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i];
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void *>(ptr),

@@ -40,7 +40,7 @@ bool tensor_map_2d(CUtensorMap *map, const void *ptr, CUtensorMapDataType dtype,
                    int64_t rows, int64_t cols, int box_cols, int box_rows,
                    CUtensorMapSwizzle swizzle);
 
-// A bf16 tensor map of rank 2 or 3, 128-byte swizzle, out-of-range elements
+// A bf16 tensor map of rank 2 to 4, 128-byte swizzle, out-of-range elements
 // read as zero: dims and box innermost first, strides in bytes of dims 1 ...
 // Encoded on the spot, never cached.
 bool tensor_map_bf16(CUtensorMap *map, const void *ptr, int rank, const uint64_t *dims,

@@ -268,6 +268,26 @@ def test_cross_more_rows_than_a_wave():
     check_cross(23, 40, 1, 40, 4, 4, 64, None, packed=False)
 
 
+# results into rows of a wider tensor: nothing beside them, before the first or behind the last is written
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Lq,Hq,H", [(300, 6, 2), (261, 4, 4), (170, 5, 1), (20, 16, 2), (2, 128, 1)])
+@pytest.mark.parametrize("Lk", [1, 150, 700])
+def test_cross_out_of_wider_rows(Lq, Hq, H, Lk, D):
+    dev = device()
+    B, wide = 3, Hq * D + 64
+    g = ref.gen(Lq + Lk)
+    q = ref.randn(g, B, Lq, Hq, D, std=1.5).to(dev)
+    k, v = ref.randn(g, B, Lk, H, D).to(dev), ref.randn(g, B, Lk, H, D).to(dev)
+    guarded = torch.full((B * Lq + 2, wide), 7.0, dtype=torch.bfloat16, device=dev)
+    out = guarded[1:-1, 32:32 + Hq * D].view(B, Lq, Hq, D)
+    ck.cross_attention(q, k, v, out=out)
+    want, mag = ref.attend(q, list(k), list(v), [[Lk] * Lq] * B, D ** -0.5)
+    poll_ok()
+    ref.assert_attention(out, want, mag)
+    guarded[1:-1, 32:32 + Hq * D] = 7.0
+    assert (guarded == 7.0).all()
+
+
 def test_cross_no_states():
     dev = device()
     q = ref.randn(ref.gen(24), 2, 3, 4, 64).to(dev)
