@@ -699,7 +699,6 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             // kept uniform over the warp -- a key count that was read from
             // memory goes through a shuffle for that -- and the K steps of a
             // tile are unrolled.
-            constexpr uint32_t idesc_qk = idesc_bf16_f32(kRows, kKeys, false);
             constexpr uint32_t idesc_pv = idesc_bf16_f32(kRows, D, true);
             constexpr uint32_t tile_desc = C::kTileBytes / 16;
             const bool is_qk = warp == kQkWarp;
@@ -727,6 +726,8 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                     const int valid = min(kKeys, nkeys - j * kKeys);
                     const uint64_t kvd = (is_qk ? kd0 : vd0) + static_cast<uint32_t>(slot) * tile_desc;
                     if (is_qk) {
+                        // no more columns of S than there are keys
+                        const uint32_t idesc_qk = idesc_bf16_f32(kRows, (valid + 15) & ~15, false);
 #pragma unroll 1
                         for (int sub = 0; sub < subs; ++sub, ++step) {
                             const int st = step & 1;
@@ -1054,16 +1055,16 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                     tmem_ld_32x32b_x32(ts + 32u, sr[1]);
                     tmem_ld_32x32b_x32(ts + 64u, sr[2]);
                     tmem_ld_32x32b_x32(ts + 96u, sr[3]);
-                    const bool masked = __any_sync(0xffffffffu, vis < kKeys);
+                    const int all_see = __reduce_min_sync(0xffffffffu, vis);
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                     tmem_wait_ld(sr[0]);
                     tmem_wait_ld(sr[1]);
                     tmem_wait_ld(sr[2]);
                     tmem_wait_ld(sr[3]);
-                    row_max<0>(sr[0], masked, vis, mx);
-                    row_max<1>(sr[1], masked, vis, mx);
-                    row_max<2>(sr[2], masked, vis, mx);
-                    row_max<3>(sr[3], masked, vis, mx);
+                    row_max<0>(sr[0], all_see < 32, vis, mx);
+                    row_max<1>(sr[1], all_see < 64, vis, mx);
+                    row_max<2>(sr[2], all_see < 96, vis, mx);
+                    row_max<3>(sr[3], all_see < 128, vis, mx);
                     const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     if (done == 0) {
                         mref = mt;
@@ -1085,7 +1086,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                     tmem_wait_st();
                 }
                 arrive(0);
-                if (warp_live) {
+                if (warp_live && valid > kFirstKeys) {  // else no product reads them
                     weights(sr[3], c, mc, sum, ts + 48u);
                     tmem_wait_st();
                 }
