@@ -1123,24 +1123,27 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                 tc_fence_after_sync();
                 if (warp_live) {
                     const float inv = l == 0.f ? 0.f : 1.f / l;
-                    uint32_t o[D / 32][32];
+                    uint8_t *dst = smem + (2 + s) * C::kTileBytes + row * 128;
+#pragma unroll 1
+                    for (int hf = 0; hf < C::kHalves; ++hf, dst += C::kHalfBytes) {
+                        uint32_t o[2][32];
+                        tmem_ld_32x32b_x32(to + 64u * hf, o[0]);
+                        tmem_ld_32x32b_x32(to + 64u * hf + 32u, o[1]);
+                        tmem_wait_ld(o[0]);
+                        tmem_wait_ld(o[1]);
 #pragma unroll
-                    for (int q = 0; q < D / 32; ++q) tmem_ld_32x32b_x32(to + 32u * q, o[q]);
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t p[16];
 #pragma unroll
-                    for (int q = 0; q < D / 32; ++q) tmem_wait_ld(o[q]);
-                    uint8_t *const dst = smem + (2 + s) * C::kTileBytes + row * 128;
+                            for (int i = 0; i < 16; ++i)
+                                p[i] = inv != 0.f ? pack2(__uint_as_float(o[q][2 * i]) * inv,
+                                                          __uint_as_float(o[q][2 * i + 1]) * inv)
+                                                  : 0u;
 #pragma unroll
-                    for (int q = 0; q < D / 32; ++q) {
-                        uint32_t p[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            p[i] = inv != 0.f ? pack2(__uint_as_float(o[q][2 * i]) * inv,
-                                                      __uint_as_float(o[q][2 * i + 1]) * inv)
-                                              : 0u;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            *reinterpret_cast<uint4 *>(dst + (q / 2) * C::kHalfBytes + (((q & 1) * 4 + k) ^ (row & 7)) * 16) =
-                                make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
+                            for (int k = 0; k < 4; ++k)
+                                *reinterpret_cast<uint4 *>(dst + ((q * 4 + k) ^ (row & 7)) * 16) =
+                                    make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
+                        }
                     }
                     fence_proxy_async_smem();
                 }
