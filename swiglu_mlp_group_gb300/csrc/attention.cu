@@ -949,7 +949,6 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                 if (!ok) break;
                 tc_fence_after_sync();
                 const bool part = !(it.flags & kWhole);
-                const int only = ntiles == 1 ? static_cast<int>((step - 1) & 1) : -1;  // the one stream with a tile
                 float *const scratch = reinterpret_cast<float *>(smem + buf * C::kTileBytes);
                 float m = -INFINITY;
 #pragma unroll
@@ -969,18 +968,17 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                 }
 #pragma unroll 1
                 for (int col = st * (D / 2); col < (st + 1) * (D / 2); col += 32) {
-                    uint32_t o[32];
+                    uint32_t o[32], p[32];
                     float v[32];
+                    tmem_ld_32x32b_x32(tO(0) + lanes + static_cast<uint32_t>(col), o);
+                    tmem_ld_32x32b_x32(tO(1) + lanes + static_cast<uint32_t>(col), p);
+                    tmem_wait_ld(o);
+                    tmem_wait_ld(p);
+                    // a stream without a weight may hold what it likes
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
-#pragma unroll 1
-                    for (int s2 = 0; s2 < 2; ++s2) {
-                        if (only >= 0 && only != s2) continue;
-                        const float f = s2 == 0 ? f0 : f1;
-                        tmem_ld_32x32b_x32(tO(s2) + lanes + static_cast<uint32_t>(col), o);
-                        tmem_wait_ld(o);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = f != 0.f ? fmaf(__uint_as_float(o[i]), f, v[i]) : v[i];
+                    for (int i = 0; i < 32; ++i) {
+                        v[i] = f0 != 0.f ? __uint_as_float(o[i]) * f0 : 0.f;
+                        if (f1 != 0.f) v[i] = fmaf(__uint_as_float(p[i]), f1, v[i]);
                     }
                     if (lane < kFewRows) {
                         // pieces of 16 bytes, turned by the row against bank conflicts
