@@ -1399,6 +1399,7 @@ Work plan(const AttentionArgs &a) {
             w.chunk_p = w.chunk_o = static_cast<int>(c);
             w.parts_p = w.slots_p = div_up(w.tiles_p, c);
             w.parts_o = w.slots_o = div_up(w.tiles_o, c);
+            w.direct = w.tiles_p == 0 && w.parts_o == 1;  // every group whole after all: nothing to join
             return w;
         }
     }
