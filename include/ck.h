@@ -540,7 +540,7 @@ CK_API ck_status ck_cross_attention(const void *q, int64_t ldq, const void *k, i
                                     int64_t Hq, int64_t Hkv, int64_t D, const int32_t *kv_lens,
                                     float scale, void *out, int64_t ldo, void *ws, size_t ws_bytes,
                                     ck_stream_t stream);
-/* Workspace bytes of that call (0 where it needs none). */
+/* Workspace bytes of that call, whatever the lengths (0 where it needs none). */
 CK_API size_t ck_cross_attention_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq,
                                                  int64_t Hkv, int64_t D);
 

@@ -1379,10 +1379,18 @@ Work plan(const AttentionArgs &a) {
     w.tiles_p = div_up(w.prefix_len, kKeys), w.tiles_o = div_up(w.max_len, kKeys);
     w.sms = kPlanSms;
     const int64_t base_p = static_cast<int64_t>(w.rt_p) * w.Hkv, base_o = static_cast<int64_t>(w.rt_o) * w.Hkv * w.B;
-    // Whole groups where they are many (at 4 a SM the last round leaves at most
-    // a quarter idle, about what partial results and their join would cost) or
-    // short (two tiles run side by side in a narrow group).
-    w.direct = w.tiles_p == 0 && (base_o >= 4 * kPlanSms || w.tiles_o <= 2);
+    // Whole groups where there are more than SMs and their lengths are one, or
+    // short enough that a long one among them costs less than partial results
+    // and their join; of two tiles always (they run side by side in a narrow
+    // group).  us, whole against shares: even, 2 x 4096 x 500 x 8 heads of 128 20
+    // / 47, 2 x 4096 x 4000 x 14 140 / 186, 56 x 1 x 2000 x 8 70 / 80, 70 x 1 x
+    // 4000 x 8 167 / 176; one query token, lengths drawn evenly to 1000: 128 x 8
+    // heads 60 / 62, to 2000 97 / 92, to 4000 183 / 167, one 4000 among 250s 50 /
+    // 35; 8 x 1024 x 8 heads to 2000 40 / 58, to 4000 71 / 85, one 4000 among
+    // 250s 52 / 45.  Many wide groups level their lengths out, and a join passes
+    // over all their rows.
+    const int64_t most = w.wide_o ? (base_o >= 4 * kPlanSms ? w.tiles_o : 32) : 16;
+    w.direct = w.tiles_p == 0 && (w.tiles_o <= 2 || (base_o > kPlanSms && (!a.ragged || w.tiles_o <= most)));
     if (w.direct) {
         w.parts_o = 1, w.chunk_o = w.tiles_o > 0 ? w.tiles_o : 1;
         return w;

@@ -52,6 +52,7 @@ struct AttentionArgs {
     int64_t ldq, ldo;
     int64_t B, Lq;
     int Hq, Hkv, G, D;
+    bool ragged;  // lengths of own keys may differ; the workspace is sized for that
     const uint16_t *k, *v;  // the cache, or the dense states
     int64_t ldk, ldv;       // dense
     int64_t pages;          // paged; 0: dense

@@ -56,6 +56,7 @@ bool attention_sizes(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D) 
 
 ck::AttentionArgs attention_sizes_only(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D) {
     ck::AttentionArgs a = {};
+    a.ragged = true;
     a.B = B, a.Lq = Lq;
     a.Hq = static_cast<int>(Hq), a.Hkv = static_cast<int>(Hkv), a.G = static_cast<int>(Hq / Hkv);
     a.D = static_cast<int>(D);
@@ -210,6 +211,7 @@ CK_API ck_status ck_cross_attention(const void *q, int64_t ldq, const void *k, i
     ck::AttentionArgs a = cross_sizes(B, Lq, Lk, Hq, Hkv, D);
     a.k = bits(k), a.v = bits(v), a.ldk = ldk, a.ldv = ldv;
     a.lens = Lk > 0 ? kv_lens : nullptr;
+    a.ragged = a.lens != nullptr;
     return run_attention(a, q, ldq, out, ldo, scale, ws, ws_bytes, stream);
 }
 

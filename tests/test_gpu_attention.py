@@ -262,6 +262,14 @@ def test_cross_growing_scores(Lq, every, D):
     ref.assert_attention(out, want, mag)
 
 
+# more groups than SMs over long states: whole where the lengths are one, in shares where they are not
+@pytest.mark.parametrize("B,Lq,Lk,H", [(21, 1, 2300, 8), (23, 20, 2100, 8), (2, 1300, 4300, 14)])
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_cross_many_groups_long(B, Lq, Lk, H, ragged, D):
+    check_cross(B + D, B, Lq, Lk, H, H, D, [(911 * b) % (Lk + 1) for b in range(B - 1)] + [Lk] if ragged else None)
+
+
 def test_cross_more_rows_than_a_wave():
     check_cross(21, 2, 2500, 300, 6, 3, 128, [300, 299])
     check_cross(22, 1, 1, 5000, 4, 4, 128, None)
