@@ -20,9 +20,9 @@
 // every CTA gets an equal share (divide below): an equal run of the prefix of a
 // group, and a run of the sequence of all groups' own key tiles, cut where its
 // share ends.  Pieces of a row leave partial sums with their maximum in the
-// workspace, and a second kernel joins them.  Without a prefix, and with groups
-// enough for every SM or keys for two tiles at most, whole groups are dealt out
-// and written directly.
+// workspace, and a second kernel joins them.  Without a prefix, and with more
+// groups than SMs of about one length or keys for two tiles at most, whole groups
+// are dealt out and written directly.
 //
 // Pipeline (one CTA per SM, 12 warps).  Two streams, each with its own S and O
 // in TMEM and four softmax warps, so that the tensor core works on one while
@@ -77,7 +77,7 @@ static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs == kThreads * kLaunchRegs &&
 constexpr int kFirstKeys = 96;
 // Query rows up to which a narrow item is one of few rows.  The call's kernel has
 // // their code where that is so of own items and none is wide: 16 x 1 x 1500 x 16
-// heads of 64 take 24.5 us without it and 20.4 with it; with wide items besides
+// heads of 64 take 22.4 us without it and 17.2 with it; with wide items besides
 // (128 x 1 x 4096 behind 32768, 64 heads over 8 of 128) it is 223 and 246: a wide
 // tile, bound by its softmax, takes longer in the kernel that has both.
 constexpr int kFewRows = 16;
