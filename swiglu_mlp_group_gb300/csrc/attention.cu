@@ -437,15 +437,21 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
     const uint32_t met_all = bars_s + 8u * (2 * NS + 18);  // all softmax warps are at the end of an item of few rows
     // and done with a query buffer that they have used for its results
     auto few_free = [&](int i) { return bars_s + 8u * (2 * NS + 19 + i); };
-    auto staged_full = [&](int i) { return bars_s + 8u * (2 * NS + 21 + i); };  // a stream's result is in the ring
-    auto item_full = [&](int i) { return bars_s + 8u * (2 * NS + 23 + i); };
-    auto item_empty = [&](int i) { return bars_s + 8u * (2 * NS + 23 + kItems + i); };
-    const uint32_t done_bar = bars_s + 8u * (2 * NS + 23 + 2 * kItems);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * NS + 24 + 2 * kItems);
+    auto item_full = [&](int i) { return bars_s + 8u * (2 * NS + 21 + i); };
+    auto item_empty = [&](int i) { return bars_s + 8u * (2 * NS + 21 + kItems + i); };
+    // A stream's result is in the ring: a barrier for each place of an item.
+    // The softmax warps never wait for the walking warp, which may be items
+    // behind while there are free places for K, V and results.  But the walking
+    // warp hands an item's place out again only after it has waited here for
+    // what was in it, so that no phase can pass unseen.
+    auto staged_full = [&](int st, uint32_t i) { return bars_s + 8u * (2 * NS + 21 + (2 + st) * kItems + i); };
+    const uint32_t done_bar = bars_s + 8u * (2 * NS + 21 + 4 * kItems);
+    constexpr int kBars = 2 * NS + 22 + 4 * kItems;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     Share &share = *reinterpret_cast<Share *>(tmem_slot + 2);
     Item *const ring = reinterpret_cast<Item *>(&share + 1);
-    static_assert(8 * (2 * NS + 24 + 2 * kItems) + 8 + sizeof(Share) + kItems * sizeof(Item) <= C::kBarBytes);
+    static_assert(8 * kBars + 8 + sizeof(Share) + kItems * sizeof(Item) <= C::kBarBytes);
     float2 *const xml = reinterpret_cast<float2 *>(smem + (2 + NS) * C::kTileBytes + C::kBarBytes);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // uniform for the compiler too
@@ -463,7 +469,6 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             mbar_init(q_full(i), 1);
             mbar_init(q_empty(i), 1);
             mbar_init(few_free(i), 8);
-            mbar_init(staged_full(i), 4);
             mbar_init(s_full(i), 1);
             mbar_init(p_full(i, 0), 4);
             mbar_init(p_full(i, 1), 4);
@@ -475,6 +480,8 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
         for (int i = 0; i < kItems; ++i) {
             mbar_init(item_full(i), 1);
             mbar_init(item_empty(i), kReaders);
+            mbar_init(staged_full(0, i), 4);
+            mbar_init(staged_full(1, i), 4);
         }
         mbar_init(done_bar, 2);
         *abort_flag = 0;
@@ -637,15 +644,18 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             // An item's staged results, when the softmax has put them into the
             // ring: out by TMA, which leaves rows past the sequence's queries
             // out, and the places back to the loader.
-            uint32_t fills = 0, stages = 0;
-            auto store = [&](const Item &it) {
+            uint32_t fills = 0, spar = 0;  // spar bit i: parity of the next staged item in place i
+            auto store = [&](uint32_t place) {
+                const Item &it = ring[place];
                 const int ntiles = tiles_of(it.nkeys);
                 fills += 2 * ntiles;
                 if (!staged(it.flags, ntiles)) return true;
 #pragma unroll 1
                 for (int st = 0; st < 2; ++st, ++fills) {
                     const int s = fills % NS;
-                    if (!__all_sync(0xffffffffu, mbar_wait_spin(staged_full(st), stages & 1, item_ctl))) return false;
+                    if (!__all_sync(0xffffffffu,
+                                    mbar_wait_spin(staged_full(st, place), (spar >> place) & 1, item_ctl)))
+                        return false;
                     const int first = it.tok0 + st * it.tok;  // its first token
                     if (lane == 0) {
                         if (first < it.tok_end) {
@@ -660,7 +670,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                     }
                     __syncwarp();
                 }
-                ++stages;
+                spar ^= 1u << place;
                 return true;
             };
             bool more = true, ok = true;
@@ -678,11 +688,11 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                     mbar_arrive(item_full(i));
                 }
                 __syncwarp();
-                if (!FEW && n - sent == kItems - 1) ok = store(ring[sent++ % kItems]);  // the oldest in the ring
+                if (!FEW && n - sent == kItems - 1) ok = store(sent++ % kItems);  // the oldest in the ring
                 if (!ok) break;
             }
             if (!FEW) {
-                while (ok && sent < n) ok = store(ring[sent++ % kItems]);
+                while (ok && sent < n) ok = store(sent++ % kItems);
                 if (lane == 0) bulk_wait();
             }
             __syncwarp();
@@ -1146,7 +1156,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(staged_full(st));
+                if (lane == 0) mbar_arrive(staged_full(st, (items - 1) % kItems));
                 continue;
             }
             float m = mref == -INFINITY ? mref : mref * c;
