@@ -1306,9 +1306,11 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
     const int own = tiles_of(own_len(w, b));  // lengths are older than the kernel ahead
     const bool fixed = w.chunk_o > 0;
     pdl_wait();
-    const int np = fixed ? w.parts_p : w.tiles_p > 0 ? w.parts[0] : 0;
+    // Where a wait ran out in the kernel ahead a count may not have been written:
+    // no more parts than have a place.
+    const int np = fixed ? w.parts_p : w.tiles_p > 0 ? min(max(w.parts[0], 0), w.slots_p) : 0;
     const int no = fixed ? (own + w.chunk_o - 1) / w.chunk_o
-                         : own > 0 ? w.parts[1 + (b * w.Hkv + hq / w.G) * w.rt_o + rt] : 0;
+                         : own > 0 ? min(max(w.parts[1 + (b * w.Hkv + hq / w.G) * w.rt_o + rt], 0), w.slots_o) : 0;
     if (np == 0 && no == 1) return;  // written by the item itself
     const int n = np + no;
     constexpr int E = D / 32, kAhead = 8;
