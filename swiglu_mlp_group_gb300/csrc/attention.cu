@@ -627,8 +627,9 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                 }
                 if (!wide && ntiles > 0) ++nar;
             }
-            if (*abort_flag && elect_one()) {
-                // let the copies still in flight land before the CTA exits
+            if (elect_one()) {
+                // The last copies have landed before the CTA exits, also where a
+                // wait of another warp runs out after this one is through.
                 for (uint32_t q = seq > NS ? seq - NS : 0; q < seq; ++q)
                     mbar_wait_drain(kv_full(q % NS), (q / NS) & 1, w.timeout_ns, w.status);
                 for (int i = 0; i < 2; ++i)

@@ -110,10 +110,12 @@ __device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity, co
 }
 
 // Wait that ignores the CTA's abort flag, bounded in time: lets copies or MMAs
-// already in flight finish before the CTA exits.
+// already in flight finish before the CTA exits.  They take microseconds; a
+// limit of a wait that is shorter than 100 ms does not cut them off.
 __device__ __forceinline__ bool mbar_wait_drain(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
                                                 unsigned int *status) {
     if (mbar_try_wait(bar, parity)) return true;
+    if (timeout_ns < 100000000ull) timeout_ns = 100000000ull;
     const uint64_t t0 = globaltimer_ns();
     while (!mbar_try_wait(bar, parity)) {
         if (globaltimer_ns() - t0 > timeout_ns) {

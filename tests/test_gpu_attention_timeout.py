@@ -56,3 +56,26 @@ def test_counts_of_parts_that_were_never_written():
     again = call()
     poll_ok()
     assert torch.equal(again, good)
+
+
+@pytest.mark.parametrize("limit", [1, 1_000, 20_000])
+def test_copies_in_flight_at_a_short_limit(limit):
+    """Whether a wait runs out or none does, no copy outlives its block: calls at short limits, each with its
+    successor close behind, and then a right one."""
+    dev = device()
+    call, check = many_empty(60_000)
+    g = ref.gen(52)
+    q, k, v = (ref.randn(g, 2, n, 8, 128).to(dev) for n in (700, 400, 400))
+    want, mag = ref.attend(q, list(k), list(v), [[400] * 700] * 2, 128 ** -0.5)
+    poll_ok()
+    ck.set_wait_timeout_ns(limit)
+    try:
+        for _ in range(10):
+            call()
+            ck.cross_attention(q, k, v)
+        assert ck.poll_device_status() in (ck.CK_OK, ck.CK_ERR_TIMEOUT)
+    finally:
+        ck.set_wait_timeout_ns(0)
+    ref.assert_attention(ck.cross_attention(q, k, v), want, mag)
+    check(call())
+    poll_ok()
