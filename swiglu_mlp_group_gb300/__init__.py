@@ -429,11 +429,21 @@ def packed_gemv_dequant(xq, sx, Wpacked, wlayout: int, N: int, bias=None, out=No
 # attention
 # ---------------------------------------------------------------------------
 
-def _token_stride(x, shape, what: str) -> int:
-    """Elements from one token of x (bf16 [..., heads, D] on the GPU, of this shape) to the next: its heads
-    lie next to each other, its tokens at one stride throughout."""
-    if x.dtype is not _torch().bfloat16 or not x.is_cuda:
+def _call_device(x, what: str) -> int:
+    """Index of the device of a call: x's.  The library launches on the current one, so it has to be that."""
+    dev = x.get_device()
+    if dev < 0:
         raise ValueError(f"{what} must be a bf16 CUDA tensor")
+    if dev != _torch().cuda.current_device():
+        raise ValueError(f"{what} is on cuda:{dev}, which is not the current device")
+    return dev
+
+
+def _token_stride(x, shape, what: str, dev: int) -> int:
+    """Elements from one token of x (bf16 [..., heads, D] on the call's device, of this shape) to the next: its
+    heads lie next to each other, its tokens at one stride throughout."""
+    if x.dtype is not _torch().bfloat16 or x.get_device() != dev:
+        raise ValueError(f"{what} must be a bf16 tensor on cuda:{dev}")
     st = x.stride()
     H, D = shape[-2], shape[-1]
     ld = H * D
@@ -452,23 +462,30 @@ def _token_stride(x, shape, what: str) -> int:
     return ld
 
 
-def _typed(t, dtype, what: str, shape=None):
-    """Data pointer of an optional contiguous CUDA tensor of the given type (and shape)."""
+def _typed(t, dtype, what: str, dev: int, shape=None):
+    """Data pointer of an optional contiguous tensor of the given type (and shape) on the call's device."""
     if t is None:
         return None
-    if t.dtype is dtype and t.is_cuda and t.is_contiguous() and (shape is None or t.shape == shape):
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and (shape is None or t.shape == shape):
         return t.data_ptr()
     if shape is not None and t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    raise ValueError(f"{what} must be a contiguous CUDA tensor of {dtype}")
+    raise ValueError(f"{what} must be a contiguous tensor of {dtype} on cuda:{dev}")
 
 
-def _run_stream(stream, like) -> int:
-    """The stream a call runs on: the one given, or the current one of like's device (its handle alone:
-    building a Stream object for it takes 3 us of a small call's 10)."""
+def _given_workspace(ws, dev: int):
+    """A caller's workspace: any contiguous memory on the call's device."""
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    return ws
+
+
+def _run_stream(stream, dev: int) -> int:
+    """The stream a call runs on: the one given, or the device's current one (its handle alone: building a
+    Stream object for it takes 3 us of a small call's 10)."""
     if stream is not None:
         return stream.cuda_stream
-    return _torch()._C._cuda_getCurrentRawStream(like.get_device())
+    return _torch()._C._cuda_getCurrentRawStream(dev)
 
 
 def _new_like(x, stream):
@@ -489,7 +506,7 @@ def _new(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _rotation(cos_sin, positions, T: int, mode: str):
+def _rotation(cos_sin, positions, T: int, mode: str, dev: int):
     """(table pointer, max_pos, rot_dim, mode, positions pointer) of the rotation arguments."""
     torch = _torch()
     rope = _ROPES.get(mode)
@@ -500,13 +517,13 @@ def _rotation(cos_sin, positions, T: int, mode: str):
     if positions is None:
         raise ValueError("a rotation needs positions")
     max_pos, rot = cos_sin.shape
-    return (_typed(cos_sin, torch.float32, "cos_sin"), max_pos, rot, rope,
-            _typed(positions, torch.int32, "positions", (T,)))
+    return (_typed(cos_sin, torch.float32, "cos_sin", dev), max_pos, rot, rope,
+            _typed(positions, torch.int32, "positions", dev, (T,)))
 
 
-def _norm_weight(w, D: int, what: str, dtype):
+def _norm_weight(w, D: int, what: str, dtype, dev: int):
     """Data pointer of an optional norm weight [D] of the given type."""
-    return None if w is None else _typed(w, dtype, what, (D,))
+    return None if w is None else _typed(w, dtype, what, dev, (D,))
 
 
 def _weight_type(*ws):
@@ -528,15 +545,16 @@ def qk_norm_rope(q, k, cos_sin=None, positions=None, wq=None, wk=None, eps: floa
     q_out=q, k_out=k work in place."""
     shape = q.shape
     T, Hq, D = shape
-    ldq = _token_stride(q, shape, "q")
-    table, max_pos, rot, rope, pos = _rotation(cos_sin, positions, T, mode)
+    dev = _call_device(q, "q")
+    ldq = _token_stride(q, shape, "q", dev)
+    table, max_pos, rot, rope, pos = _rotation(cos_sin, positions, T, mode, dev)
     dt, wdt = _weight_type(wq, wk)
     if q_out is None:
         q_out, ldqo = _new_like(q, stream), Hq * D
     elif q_out.shape != shape:
         raise ValueError("q_out must have q's shape")
     else:
-        ldqo = _token_stride(q_out, shape, "q_out")
+        ldqo = _token_stride(q_out, shape, "q_out", dev)
     if k is None:
         k_out = pk = pko = None
         Hk = ldk = ldko = 0
@@ -545,29 +563,29 @@ def qk_norm_rope(q, k, cos_sin=None, positions=None, wq=None, wk=None, eps: floa
         Hk = kshape[1]
         if kshape[0] != T or kshape[2] != D:
             raise ValueError("q and k must have the same tokens and head size")
-        ldk = _token_stride(k, kshape, "k")
+        ldk = _token_stride(k, kshape, "k", dev)
         if k_out is None:
             k_out, ldko = _new_like(k, stream), Hk * D
         elif k_out.shape != kshape:
             raise ValueError("k_out must have k's shape")
         else:
-            ldko = _token_stride(k_out, kshape, "k_out")
+            ldko = _token_stride(k_out, kshape, "k_out", dev)
         pk, pko = k.data_ptr(), k_out.data_ptr()
     st = lib().ck_qk_norm_rope(
-        q.data_ptr(), ldq, Hq, _norm_weight(wq, D, "wq", dt), pk, ldk, Hk, _norm_weight(wk, D, "wk", dt), wdt, T, D,
-        eps, table, max_pos, rot, rope, pos, q_out.data_ptr(), ldqo, pko, ldko, _run_stream(stream, q))
+        q.data_ptr(), ldq, Hq, _norm_weight(wq, D, "wq", dt, dev), pk, ldk, Hk, _norm_weight(wk, D, "wk", dt, dev), wdt,
+        T, D, eps, table, max_pos, rot, rope, pos, q_out.data_ptr(), ldqo, pko, ldko, _run_stream(stream, dev))
     if st != CK_OK:
         raise CkError(st, "ck_qk_norm_rope")
     return q_out, k_out
 
 
-def _caches(k_cache, v_cache):
+def _caches(k_cache, v_cache, dev: int):
     """(shape, pointers) of a paged cache: contiguous bf16 [pages, Hkv, page_size, D], twice."""
     bf16 = _torch().bfloat16
     shape = k_cache.shape
     if len(shape) != 4:
         raise ValueError("a cache is [pages, Hkv, page_size, D]")
-    return shape, _typed(k_cache, bf16, "k_cache"), _typed(v_cache, bf16, "v_cache", shape)
+    return shape, _typed(k_cache, bf16, "k_cache", dev), _typed(v_cache, bf16, "v_cache", dev, shape)
 
 
 def kv_append(k, v, k_cache, v_cache, slots, cos_sin=None, positions=None, wk=None, eps: float = 1e-6,
@@ -579,15 +597,16 @@ def kv_append(k, v, k_cache, v_cache, slots, cos_sin=None, positions=None, wk=No
     [pages, Hkv, page_size, D]; slots int64 [T] = page * page_size + row, negative: skip the token."""
     shape = k.shape
     T, H, D = shape
-    (pages, Hc, page_size, Dc), pkc, pvc = _caches(k_cache, v_cache)
+    dev = _call_device(k, "k")
+    (pages, Hc, page_size, Dc), pkc, pvc = _caches(k_cache, v_cache, dev)
     if v.shape != shape or Hc != H or Dc != D:
         raise ValueError("k, v and the caches must have the same heads and head size")
-    table, max_pos, rot, rope, pos = _rotation(cos_sin, positions, T, mode)
+    table, max_pos, rot, rope, pos = _rotation(cos_sin, positions, T, mode, dev)
     dt, wdt = _weight_type(wk)
     st = lib().ck_kv_append(
-        k.data_ptr(), _token_stride(k, shape, "k"), v.data_ptr(), _token_stride(v, shape, "v"), T, H, D,
-        _norm_weight(wk, D, "wk", dt), wdt, eps, table, max_pos, rot, rope, pos,
-        _typed(slots, _torch().int64, "slots", (T,)), pkc, pvc, pages, page_size, _run_stream(stream, k))
+        k.data_ptr(), _token_stride(k, shape, "k", dev), v.data_ptr(), _token_stride(v, shape, "v", dev), T, H, D,
+        _norm_weight(wk, D, "wk", dt, dev), wdt, eps, table, max_pos, rot, rope, pos,
+        _typed(slots, _torch().int64, "slots", dev, (T,)), pkc, pvc, pages, page_size, _run_stream(stream, dev))
     if st != CK_OK:
         raise CkError(st, "ck_kv_append")
 
@@ -609,15 +628,16 @@ def prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, block_t
     torch = _torch()
     shape = q.shape
     B, Lq, Hq, D = shape
-    (pages, H, page_size, Dc), pkc, pvc = _caches(k_cache, v_cache)
+    dev = _call_device(q, "q")
+    (pages, H, page_size, Dc), pkc, pvc = _caches(k_cache, v_cache, dev)
     if Dc != D:
         raise ValueError("q and the caches must have the same head size")
-    ldq = _token_stride(q, shape, "q")
+    ldq = _token_stride(q, shape, "q", dev)
     i32 = torch.int32
-    pp = _typed(prefix_pages, i32, "prefix_pages")
+    pp = _typed(prefix_pages, i32, "prefix_pages", dev)
     if prefix_len > 0 and (pp is None or prefix_pages.numel() * page_size < prefix_len):
         raise ValueError("prefix_pages must hold prefix_len tokens")
-    bt, width = _typed(block_table, i32, "block_table"), 0
+    bt, width = _typed(block_table, i32, "block_table", dev), 0
     if bt is not None:
         if block_table.dim() != 2 or block_table.shape[0] != B:
             raise ValueError("block_table must have a row for every sequence")
@@ -627,13 +647,13 @@ def prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, block_t
     elif out.shape != shape:
         raise ValueError("out must have q's shape")
     else:
-        ldo = _token_stride(out, shape, "out")
-    ws = workspace if workspace is not None else prefix_attention_workspace(q, k_cache, prefix_len, max_seq_len,
-                                                                            stream)
+        ldo = _token_stride(out, shape, "out", dev)
+    ws = (_given_workspace(workspace, dev) if workspace is not None else
+          prefix_attention_workspace(q, k_cache, prefix_len, max_seq_len, stream))
     st = lib().ck_prefix_attention(
         q.data_ptr(), ldq, B, Lq, Hq, H, D, pkc, pvc, pages, page_size, pp, prefix_len, bt, width,
-        _typed(seq_lens, i32, "seq_lens", (B,)), max_seq_len, D ** -0.5 if scale is None else scale,
-        out.data_ptr(), ldo, ws.data_ptr(), ws.numel(), _run_stream(stream, q))
+        _typed(seq_lens, i32, "seq_lens", dev, (B,)), max_seq_len, D ** -0.5 if scale is None else scale,
+        out.data_ptr(), ldo, ws.data_ptr(), ws.nbytes, _run_stream(stream, dev))
     if st != CK_OK:
         raise CkError(st, "ck_prefix_attention")
     return out
@@ -655,19 +675,20 @@ def cross_attention(q, k, v, kv_lens=None, scale: float | None = None, out=None,
     if v.shape != kshape or len(kshape) != 4 or kshape[0] != B or kshape[3] != D:
         raise ValueError("k and v must be [B, Lk, Hkv, D] of q's batch and head size")
     Lk, H = kshape[1], kshape[2]
-    ldq = _token_stride(q, shape, "q")
-    ldk, ldv = (_token_stride(k, kshape, "k"), _token_stride(v, kshape, "v")) if Lk > 0 else (0, 0)
+    dev = _call_device(q, "q")
+    ldq = _token_stride(q, shape, "q", dev)
+    ldk, ldv = (_token_stride(k, kshape, "k", dev), _token_stride(v, kshape, "v", dev)) if Lk > 0 else (0, 0)
     if out is None:
         out, ldo = _new_like(q, stream), Hq * D
     elif out.shape != shape:
         raise ValueError("out must have q's shape")
     else:
-        ldo = _token_stride(out, shape, "out")
-    ws = workspace if workspace is not None else cross_attention_workspace(q, k, stream)
+        ldo = _token_stride(out, shape, "out", dev)
+    ws = _given_workspace(workspace, dev) if workspace is not None else cross_attention_workspace(q, k, stream)
     st = lib().ck_cross_attention(
         q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, B, Lq, Lk, Hq, H, D,
-        _typed(kv_lens, torch.int32, "kv_lens", (B,)), D ** -0.5 if scale is None else scale,
-        out.data_ptr(), ldo, ws.data_ptr(), ws.numel(), _run_stream(stream, q))
+        _typed(kv_lens, torch.int32, "kv_lens", dev, (B,)), D ** -0.5 if scale is None else scale,
+        out.data_ptr(), ldo, ws.data_ptr(), ws.nbytes, _run_stream(stream, dev))
     if st != CK_OK:
         raise CkError(st, "ck_cross_attention")
     return out
