@@ -1414,8 +1414,15 @@ Work plan(const AttentionArgs &a) {
     if (base_p * (w.tiles_p > 0) + base_o * (w.tiles_o > 0) <= kPlanSms) {
         auto items = [&](int64_t c) { return base_p * ((w.tiles_p + c - 1) / c) + base_o * ((w.tiles_o + c - 1) / c); };
         const int64_t all = base_p * w.tiles_p + base_o * w.tiles_o;
+        // items(c) falls with c and is no more than SMs for whole groups
         int64_t c = all / kPlanSms > 2 ? all / kPlanSms : 2;
-        while (items(c) > kPlanSms) ++c;
+        for (int64_t hi = w.tiles_p > w.tiles_o ? w.tiles_p : w.tiles_o; c < hi;) {
+            const int64_t mid = c + (hi - c) / 2;
+            if (items(mid) > kPlanSms)
+                c = mid + 1;
+            else
+                hi = mid;
+        }
         if (c <= 4 || all >= c * kPlanSms / 2) {
             w.chunk_p = w.chunk_o = static_cast<int>(c);
             w.parts_p = w.slots_p = div_up(w.tiles_p, c);
