@@ -503,9 +503,11 @@ CK_API ck_status ck_kv_append(const void *k, int64_t ldk, const void *v, int64_t
  *   seq_lens  : int32 [B], each at most max_seq_len; NULL when that is 0.
  *   scale     : > 0 and finite.
  *   ws        : ck_prefix_attention_workspace_bytes(...) bytes.
- * D is 64 or 128; lengths at most 2^30.  What cached rows past a length hold is of no consequence
- * (NaN among it); a value within it that is not finite makes the results over it
- * NaN or infinite.  A length out of [0, max_seq_len] is taken as the nearer
+ * D is 64 or 128; lengths at most 2^30.  What a query does not see is of no
+ * consequence to its result, whatever it holds (rows past a length, tokens
+ * behind its own); a value that it sees and that is not finite makes its result
+ * NaN or infinite, in the value's column or, a key, in all (unless its weight
+ * vanishes beside another part's of the row).  A length out of [0, max_seq_len] is taken as the nearer
  * end, a page out of [0, pages) as rows of zeros, and either records
  * CK_ERR_INDEX.  Errors: CK_ERR_NULL, CK_ERR_SHAPE, CK_ERR_INVALID (scale),
  * CK_ERR_ALIGN, CK_ERR_WORKSPACE, CK_ERR_UNSUPPORTED_DEVICE, CK_ERR_CUDA.

@@ -94,7 +94,8 @@ struct Cfg {
     static constexpr int kHalfBytes = kKeys * 128;
     static constexpr int kTileBytes = kHalves * kHalfBytes;
     static constexpr int kSlots = D == 128 ? 5 : 10;  // ring of K and V tiles: 160 KB
-    static constexpr int kBarBytes = 768;  // barriers, TMEM address, abort flag, Share, items
+    // barriers, TMEM address, abort flag, Share, items, what is known of bad values
+    static constexpr int kBarBytes = D == 128 ? 768 : 1024;
     // maximum and sum of a row, [stream][row]: what the streams of a narrow item
     // tell each other
     static constexpr int kExchangeBytes = 2 * kRows * 8;
@@ -153,14 +154,15 @@ struct Item {
     int tok0, tok_end; // its query tokens
     int tok;           // tokens of one tile
     int key0, nkeys;   // its keys
-    int lim0, lim_step;  // token t sees the keys below lim0 + lim_step * t
+    int lim0;          // a token sees the keys below lim0, of a causal item token t those below lim0 + t
     int slot;            // where its partial result goes
     int own_parts;       // by cost, the last piece of an own group: how many there are, else 0
-    int flags;           // kWide, kWhole, kFew
+    int flags;           // kWide, kWhole, kFew, kCausal
 };
 constexpr int kWide = 1;
 constexpr int kWhole = 2;  // all keys of its rows: written to out
 constexpr int kFew = 4;    // at most kFewRows query rows
+constexpr int kCausal = 8;
 constexpr int kEnd = -1;   // nkeys of what follows the last item
 
 // What this CTA does, worked out once.
@@ -177,6 +179,23 @@ __device__ __forceinline__ int own_len(const Work &w, int b) {
     return w.lens ? min(max(w.lens[b], 0), w.max_len) : w.max_len;
 }
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + kKeys - 1) / kKeys; }
+// Token t of the item sees the keys below.
+__device__ __forceinline__ int limit_of(const Item &it, int t) { return it.lim0 + (it.flags & kCausal ? t : 0); }
+// The item's keys that all of its rows see: from here on (below nkeys) are those
+// that only later query tokens see, at most 255 of them.
+__device__ __forceinline__ int seen_by_all(const Item &it) { return limit_of(it, it.tok0) - it.key0; }
+constexpr int kNoneBad = 255;
+
+// Is one of two bf16 values infinite or NaN?
+__device__ __forceinline__ bool not_finite(uint32_t two) {
+    return (((two & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0;
+}
+// Pairwise the larger of |a| and |b|, NaN if one is.
+__device__ __forceinline__ uint32_t abs_max(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b & 0x7fff7fffu));
+    return r;
+}
 
 // The work's division, by one warp.  Prefix groups are cut into equal parts of
 // at most a CTA's share, dealt out in turn -- row tiles of the same keys side by
@@ -275,15 +294,14 @@ struct Walk {
         it.h = r / w.rt_o;
         const int rt = r - it.h * w.rt_o;
         it.b = b;
-        it.flags = w.wide_o ? kWide : w.tok_o * w.G <= kFewRows ? kFew : 0;
+        it.flags = (w.wide_o ? kWide : w.tok_o * w.G <= kFewRows ? kFew : 0) | (w.causal ? kCausal : 0);
         it.tok = w.tok_o;
         const int first = b * w.Lq, rows = it.tok * (w.wide_o ? 2 : 1);
         it.tok0 = first + rt * rows;
         it.tok_end = min(first + w.Lq, it.tok0 + rows);
-        it.lim_step = w.causal ? 1 : 0;
         it.lim0 = w.causal ? len - w.Lq + 1 - first : len;
         it.key0 = t0 * kKeys;
-        const int last = min(len, it.lim0 + it.lim_step * (it.tok_end - 1));
+        const int last = min(len, limit_of(it, it.tok_end - 1));
         it.nkeys = max(0, min(t1 * kKeys, last) - it.key0);
         it.own_parts = 0;
     }
@@ -298,7 +316,7 @@ struct Walk {
         it.tok_end = min(w.T, it.tok0 + rows);
         it.key0 = part * chunk * kKeys;
         it.nkeys = min(chunk * kKeys, w.prefix_len - it.key0);
-        it.lim0 = w.prefix_len, it.lim_step = 0;
+        it.lim0 = w.prefix_len;
         it.slot = part;
         it.own_parts = 0;
     }
@@ -407,7 +425,11 @@ __device__ __forceinline__ void weights(const uint32_t (&x)[32], float c, float 
     tmem_st_32x32b_x16(taddr, p);
 }
 
-template <int D, bool FEW>
+// FEW: has the code for items of few rows.  LATER: for values that are not finite
+// among keys that only later query tokens of an item see (causal calls of more
+// than one query token; cross attention over 4093 keys would take 454 us with it
+// instead of 443, over 333 41.9 instead of 39.8).
+template <int D, bool FEW, bool LATER>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_constant__ CUtensorMap qmap_o,
                  const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -434,24 +456,34 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
     auto pv_issued = [&](int i) { return bars_s + 8u * (2 * NS + 12 + i); };
     // the same rows' warps of both streams are at the end of a narrow item
     auto met = [&](int q) { return bars_s + 8u * (2 * NS + 14 + q); };
-    const uint32_t met_all = bars_s + 8u * (2 * NS + 18);  // all softmax warps are at the end of an item of few rows
-    // and done with a query buffer that they have used for its results
-    auto few_free = [&](int i) { return bars_s + 8u * (2 * NS + 19 + i); };
-    auto item_full = [&](int i) { return bars_s + 8u * (2 * NS + 21 + i); };
-    auto item_empty = [&](int i) { return bars_s + 8u * (2 * NS + 21 + kItems + i); };
-    // A stream's result is in the ring: a barrier for each place of an item.
-    // The softmax warps never wait for the walking warp, which may be items
+    constexpr int kFewBars = 2 * NS + 18, kItemBars = kFewBars + (FEW ? 3 : 2 * kItems);
+    // of items of few rows: all softmax warps are at the end, and done with a
+    // query buffer that they have used for its results
+    const uint32_t met_all = bars_s + 8u * kFewBars;
+    auto few_free = [&](int i) { return bars_s + 8u * (kFewBars + 1 + i); };
+    // of others: a stream's result is in the ring, a barrier for each place of an
+    // item.  The softmax warps never wait for the walking warp, which may be items
     // behind while there are free places for K, V and results.  But the walking
-    // warp hands an item's place out again only after it has waited here for
-    // what was in it, so that no phase can pass unseen.
-    auto staged_full = [&](int st, uint32_t i) { return bars_s + 8u * (2 * NS + 21 + (2 + st) * kItems + i); };
-    const uint32_t done_bar = bars_s + 8u * (2 * NS + 21 + 4 * kItems);
-    constexpr int kBars = 2 * NS + 22 + 4 * kItems;
+    // warp hands an item's place out again only after it has waited here for what
+    // was in it, so that no phase can pass unseen.
+    auto staged_full = [&](int st, uint32_t i) { return bars_s + 8u * (kFewBars + st * kItems + i); };
+    auto item_full = [&](int i) { return bars_s + 8u * (kItemBars + i); };
+    auto item_empty = [&](int i) { return bars_s + 8u * (kItemBars + kItems + i); };
+    const uint32_t done_bar = bars_s + 8u * (kItemBars + 2 * kItems);
+    // V has arrived that the walking warp looks through before it is full
+    auto v_raw = [&](int s) { return bars_s + 8u * (kItemBars + 2 * kItems + 1 + s); };
+    constexpr int kBars = kItemBars + 2 * kItems + 1 + NS;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     Share &share = *reinterpret_cast<Share *>(tmem_slot + 2);
     Item *const ring = reinterpret_cast<Item *>(&share + 1);
-    static_assert(8 * kBars + 8 + sizeof(Share) + kItems * sizeof(Item) <= C::kBarBytes);
+    // Values that are not finite among keys that some rows of an item do not see:
+    // the first such key of each column of V, counted from seen_by_all; the item
+    // (by its number among those with such keys), and how many warps have used it.
+    uint8_t *const bad_key = reinterpret_cast<uint8_t *>(ring + kItems);
+    volatile uint32_t *const bad_item = reinterpret_cast<volatile uint32_t *>(bad_key + D);
+    volatile uint32_t *const bad_used = bad_item + 1;
+    static_assert(8 * kBars + 8 + sizeof(Share) + kItems * sizeof(Item) + D + 8 <= C::kBarBytes);
     float2 *const xml = reinterpret_cast<float2 *>(smem + (2 + NS) * C::kTileBytes + C::kBarBytes);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // uniform for the compiler too
@@ -464,11 +496,12 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
         for (int s = 0; s < NS; ++s) {
             mbar_init(kv_full(s), 1);
             mbar_init(kv_empty(s), 1);
+            mbar_init(v_raw(s), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full(i), 1);
             mbar_init(q_empty(i), 1);
-            mbar_init(few_free(i), 8);
+            if (FEW) mbar_init(few_free(i), 8);
             mbar_init(s_full(i), 1);
             mbar_init(p_full(i, 0), 4);
             mbar_init(p_full(i, 1), 4);
@@ -476,15 +509,18 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             mbar_init(pv_issued(i), 1);
         }
         for (int q = 0; q < 4; ++q) mbar_init(met(q), 2);
-        mbar_init(met_all, 8);
+        if (FEW) mbar_init(met_all, 8);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(item_full(i), 1);
             mbar_init(item_empty(i), kReaders);
-            mbar_init(staged_full(0, i), 4);
-            mbar_init(staged_full(1, i), 4);
+            if (!FEW) {
+                mbar_init(staged_full(0, i), 4);
+                mbar_init(staged_full(1, i), 4);
+            }
         }
         mbar_init(done_bar, 2);
         *abort_flag = 0;
+        *bad_item = *bad_used = 0;
         fence_mbar_init();
     }
     if (warp == kQkWarp) {
@@ -527,6 +563,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             Item it;
             uint32_t qpar = 0, qused = 0;  // bit i: parity of query buffer i's next use, used at all
             uint32_t fpar = 0, qfew = 0;   // bit i: parity of its next use for a few rows' results, if its last was one
+            uint32_t raw = 0, rpar = 0;    // bit s: v_raw counts place s's last fill; parity of its next use
             bool ok = true;
             if (elect_one()) {
                 tma_prefetch_desc(&qmap_p);
@@ -561,15 +598,23 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                         ok = __all_sync(0xffffffffu, mbar_wait_spin(kv_empty(s), ((seq / NS) & 1) ^ 1, ctl));
                         if (!ok) break;
                         const CUtensorMap *map = kv == 0 ? &kmap : &vmap;
+                        uint32_t full = kv_full(s);
+                        if (LATER) {
+                            raw &= ~(1u << s);
+                            if (kv == 1 && seen_by_all(it) < j * kKeys + valid) {
+                                full = v_raw(s);
+                                raw |= 1u << s, rpar ^= 1u << s;
+                            }
+                        }
                         if (w.page_size > 0) {
                             if (elect_one())
-                                mbar_arrive_expect_tx(kv_full(s), npages * w.page_size * 128 * C::kHalves);
+                                mbar_arrive_expect_tx(full, npages * w.page_size * 128 * C::kHalves);
                             __syncwarp();
                             if (lane < npages) {
 #pragma unroll 1
                             for (int hf = 0; hf < C::kHalves; ++hf)
-                                    tma_load_2d(sKV(s) + hf * C::kHalfBytes + lane * w.page_size * 128, map, kv_full(s),
-                                                hf * 64, row);
+                                    tma_load_2d(sKV(s) + hf * C::kHalfBytes + lane * w.page_size * 128, map, full, hf * 64,
+                                                row);
                             }
                             __syncwarp();
                         } else if (elect_one()) {
@@ -621,6 +666,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                         const int s = seq % NS;
                         ok = __all_sync(0xffffffffu, mbar_wait_spin(kv_empty(s), ((seq / NS) & 1) ^ 1, ctl));
                         if (!ok) break;
+                        if (LATER) raw &= ~(1u << s);
                         if (lane == 0) mbar_arrive(kv_full(s));
                         __syncwarp();
                     }
@@ -630,8 +676,13 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             if (elect_one()) {
                 // The last copies have landed before the CTA exits, also where a
                 // wait of another warp runs out after this one is through.
-                for (uint32_t q = seq > NS ? seq - NS : 0; q < seq; ++q)
-                    mbar_wait_drain(kv_full(q % NS), (q / NS) & 1, w.timeout_ns, w.status);
+                for (uint32_t q = seq > NS ? seq - NS : 0; q < seq; ++q) {
+                    const int s = q % NS;
+                    if (LATER && ((raw >> s) & 1))
+                        mbar_wait_drain(v_raw(s), ((rpar >> s) & 1) ^ 1, w.timeout_ns, w.status);
+                    else
+                        mbar_wait_drain(kv_full(s), (q / NS) & 1, w.timeout_ns, w.status);
+                }
                 for (int i = 0; i < 2; ++i)
                     if ((qused >> i) & 1) mbar_wait_drain(q_full(i), ((qpar >> i) & 1) ^ 1, w.timeout_ns, w.status);
             }
@@ -674,13 +725,91 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                 spar ^= 1u << place;
                 return true;
             };
+            // Keys that only later query tokens see: P is 0 in the rows of the others,
+            // but 0 x NaN is not.  So those rows of V come by way of this warp: what
+            // is not finite in them is set to 0, and its first key noted for each
+            // column, for the softmax to mark the rows that do see it.  (A prompt of
+            // 8192 x 32 / 8 heads of 128 takes 408 us, as without; 421 where the
+            // issuer of P V looks.  Four of 1024, few tiles an item: 50, 45.5 without.)
+            uint32_t partly = 0, bad_uses = 0;  // items with such keys, warps that have used notes or will
+            uint32_t rpar = 0;                  // bit s: parity of v_raw(s)'s next use
+            auto notes_free = [&] {
+                const uint64_t t0 = globaltimer_ns();
+                while (static_cast<int>(*bad_used - bad_uses) < 0) {
+                    if (*abort_flag) break;
+                    if (globaltimer_ns() - t0 > item_ctl.timeout_ns) {
+                        *abort_flag = 1;
+                        atomicOr(w.status, kDeviceStatusTimeout);
+                    }
+                    __nanosleep(200);
+                }
+                __threadfence_block();
+                return __all_sync(0xffffffffu, *abort_flag == 0) != 0;
+            };
+            auto set_aside = [&](uint8_t *v, int lo, int hi, int key) {
+#pragma unroll 1
+                for (int d = lane; d < D; d += 32) {
+#pragma unroll 1
+                    for (int r = lo; r < hi; ++r) {
+                        uint16_t *x = reinterpret_cast<uint16_t *>(v + d / 64 * C::kHalfBytes + r * 128 +
+                                                                   ((d % 64 / 8) ^ (r & 7)) * 16 + d % 8 * 2);
+                        if (!not_finite(*x)) continue;
+                        *x = 0;
+                        if (bad_key[d] == kNoneBad) bad_key[d] = static_cast<uint8_t>(key + r);
+                    }
+                }
+                fence_proxy_async_smem();
+            };
+            auto look = [&](uint32_t place) {
+                const Item &it = ring[place];
+                const int all_see = seen_by_all(it), ntiles = tiles_of(it.nkeys);
+                if (all_see >= it.nkeys) return true;
+                ++partly;
+#pragma unroll 1
+                for (int j = max(all_see, 0) / kKeys; j < ntiles; ++j) {
+                    const int s = (fills + 2 * j + 1) % NS;
+                    if (!__all_sync(0xffffffffu, mbar_wait_spin(v_raw(s), (rpar >> s) & 1, item_ctl))) return false;
+                    rpar ^= 1u << s;
+                    uint8_t *const v = smem + (2 + s) * C::kTileBytes;
+                    const int lo = max(all_see - j * kKeys, 0), hi = min(kKeys, it.nkeys - j * kKeys);
+                    uint32_t top[4] = {0, 0, 0, 0};
+#pragma unroll 1
+                    for (int hf = 0; hf < C::kHalves; ++hf) {
+#pragma unroll 4
+                        for (int i = lane; i < (hi - lo) * 8; i += 32) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(v + hf * C::kHalfBytes + lo * 128 + i * 16);
+                            top[0] = abs_max(top[0], x.x), top[1] = abs_max(top[1], x.y);
+                            top[2] = abs_max(top[2], x.z), top[3] = abs_max(top[3], x.w);
+                        }
+                    }
+                    const bool bad = not_finite(top[0]) | not_finite(top[1]) | not_finite(top[2]) | not_finite(top[3]);
+                    if (__any_sync(0xffffffffu, bad)) {
+                        if (*bad_item != partly) {
+                            if (!notes_free()) return false;
+                            for (int d = lane; d < D; d += 32) bad_key[d] = kNoneBad;
+                            const bool alone = !(it.flags & kWide) && ntiles == 1 && !(FEW && (it.flags & kFew));
+                            bad_uses += alone ? 4 : 8;
+                            __syncwarp();
+                            if (lane == 0) *bad_item = partly;
+                        }
+                        set_aside(v, lo, hi, j * kKeys - all_see);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(kv_full(s));
+                }
+                return true;
+            };
             bool more = true, ok = true;
-            uint32_t n = 0, sent = 0;  // items in the ring so far, looked after by store()
+            uint32_t n = 0, sent = 0;  // items in the ring so far, looked after by look() and store()
+            auto look_after = [&] {
+                const uint32_t place = sent++ % kItems;
+                return (!LATER || look(place)) && store(place);
+            };
 #pragma unroll 1
             for (; more; ++n) {
                 Item it;
                 more = w.chunk_o > 0 ? walk.next_fixed(w, it) : walk.next_share(w, share, it);
-                if (!more) it.nkeys = kEnd;
+                if (!more) it = Item{}, it.nkeys = kEnd;
                 const uint32_t i = n % kItems;
                 ok = __all_sync(0xffffffffu, mbar_wait_spin(item_empty(i), ((n / kItems) & 1) ^ 1, item_ctl));
                 if (!ok) break;
@@ -689,11 +818,11 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                     mbar_arrive(item_full(i));
                 }
                 __syncwarp();
-                if (!FEW && n - sent == kItems - 1) ok = store(sent++ % kItems);  // the oldest in the ring
+                if ((!FEW || LATER) && n - sent == kItems - 1) ok = look_after();  // the oldest in the ring
                 if (!ok) break;
             }
-            if (!FEW) {
-                while (ok && sent < n) ok = store(sent++ % kItems);
+            if (!FEW || LATER) {
+                while (ok && sent < n) ok = look_after();
                 if (lane == 0) bulk_wait();
             }
             __syncwarp();
@@ -877,6 +1006,34 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             __syncwarp();
             if (lane == 0) mbar_arrive(p_full(st, half));
         };
+        uint32_t partly = 0;
+        // Has the item keys that not all rows see?  Then what was noted of them
+        // before the stream's last product becomes visible here.
+        auto notes = [&](const Item &i, int tiles) {
+            if (!LATER || seen_by_all(i) >= i.nkeys || tiles == 0) return true;
+            return __all_sync(0xffffffffu, mbar_wait_spin(pv_issued(st), (cnt - 1) & 1, ctl)) != 0;
+        };
+        auto any_bad = [&](const Item &i) { return LATER && seen_by_all(i) < i.nkeys && *bad_item == partly; };
+        // NaN in O where the row sees a noted key; it sees as many as it has tokens
+        // of the item before it
+        auto mark = [&](int sees, bool has) {
+            if (has) {
+#pragma unroll 1
+                for (int q = 0; q < D / 16; ++q) {
+                    uint32_t o[16];
+                    tmem_ld_32x32b_x16(to + 16u * q, o);
+                    tmem_wait_ld16(o);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (sees > bad_key[16 * q + i]) o[i] = 0x7fffffffu;
+                    tmem_st_32x32b_x16(to + 16u * q, o);
+                }
+                tmem_wait_st();
+            }
+            __threadfence_block();
+            __syncwarp();
+            if (lane == 0) atomicAdd(const_cast<uint32_t *>(bad_used), 1u);
+        };
         const int quarter = warp & 3;
         // of an item of few rows (lanes from kFewRows on help at its end only)
         const int few_row = lane % kFewRows, few_tok = few_row / w.G, few_g = few_row - few_tok * w.G;
@@ -887,6 +1044,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             const bool wide = it.flags & kWide;
             const int buf = nar & 1;
             if (!wide && ntiles > 0) ++nar;
+            if (LATER && seen_by_all(it) < it.nkeys) ++partly;
             if (FEW && (it.flags & kFew) && ntiles > 0) {
                 // A few rows would leave all but one of a stream's warps idle: they
                 // are in the tile four times, 32 rows apart, and each warp takes a
@@ -896,7 +1054,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                 const int tok = it.tok0 + few_tok;
                 const bool row_live = few_tok < it.tok && tok < it.tok_end;
                 const bool live = row_live && lane < kFewRows;
-                const int limit = it.lim0 + it.lim_step * tok - it.key0 - 32 * quarter;
+                const int limit = limit_of(it, tok) - it.key0 - 32 * quarter;
                 float mref = -INFINITY, l = 0.f;
                 int done = 0;
 #pragma unroll 1
@@ -946,7 +1104,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                 }
                 if (!ok) break;
                 if (done > 0) {
-                    ok = __all_sync(0xffffffffu, mbar_wait_spin(o_full(st), (cnt - 1) & 1, ctl));
+                    ok = __all_sync(0xffffffffu, mbar_wait_spin(o_full(st), (cnt - 1) & 1, ctl)) && notes(it, done);
                     if (!ok) break;
                 }
                 // The result: eight parts of a row, by stream and quarter.  Each
@@ -959,6 +1117,13 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                 ok = meet_all();
                 if (!ok) break;
                 tc_fence_after_sync();
+                if (__builtin_expect(any_bad(it), 0)) {
+                    mark(tok - it.tok0, done > 0);
+                    tc_fence_before_sync();
+                    ok = meet_all();
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                }
                 const bool part = !(it.flags & kWhole);
                 float *const scratch = reinterpret_cast<float *>(smem + buf * C::kTileBytes);
                 float m = -INFINITY;
@@ -1042,7 +1207,7 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             const int tok = it.tok0 + (wide ? st * it.tok : 0) + row_tok;
             const bool live = row_tok < it.tok && tok < it.tok_end;
             const bool warp_live = __any_sync(0xffffffffu, live);
-            const int limit = it.lim0 + it.lim_step * tok;
+            const int limit = limit_of(it, tok);
             float mref = -INFINITY, l = 0.f;
             int done = 0;  // tiles of this stream
             for (int j = 0; j < ntiles; ++j) {
@@ -1115,8 +1280,12 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
             // narrow one's are both streams': each adds up one half of the
             // columns of the two accumulators, as a join of two parts would.
             if (done > 0) {
-                ok = __all_sync(0xffffffffu, mbar_wait_spin(o_full(st), (cnt - 1) & 1, ctl));
+                ok = __all_sync(0xffffffffu, mbar_wait_spin(o_full(st), (cnt - 1) & 1, ctl)) && notes(it, done);
                 if (!ok) break;
+                if (__builtin_expect((wide || ntiles == 1) && any_bad(it), 0)) {
+                    tc_fence_after_sync();
+                    mark(tok - it.tok0, warp_live);
+                }
             }
             if (it.own_parts > 0 && !w.direct && threadIdx.x == 0)
                 w.parts[1 + (it.b * w.Hkv + it.h) * w.rt_o + (it.tok0 - it.b * w.Lq) / (it.tok * (wide ? 2 : 1))] =
@@ -1168,6 +1337,13 @@ attention_kernel(const __grid_constant__ CUtensorMap qmap_p, const __grid_consta
                 xml[st * kRows + row] = make_float2(m, l);
                 ok = meet();
                 if (!ok) break;
+                if (__builtin_expect(any_bad(it), 0)) {
+                    tc_fence_after_sync();
+                    mark(tok - it.tok0, warp_live);
+                    tc_fence_before_sync();
+                    ok = meet();
+                    if (!ok) break;
+                }
                 const float2 o = xml[(1 - st) * kRows + row];
                 const float top = fmaxf(l != 0.f ? m : -INFINITY, o.y != 0.f ? o.x : -INFINITY);
                 f_mine = l != 0.f ? ex2(m - top) : 0.f;
@@ -1522,7 +1698,9 @@ cudaError_t launch(const AttentionArgs &a, Work &w, const LaunchCtx &ctx) {
         return cudaErrorInvalidValue;
     // few rows against each sequence's own keys, and no wide items besides
     const bool few = !w.wide_o && w.tok_o * w.G <= kFewRows && (w.tiles_p == 0 || !w.wide_p);
-    auto kern = few ? attention_kernel<D, true> : attention_kernel<D, false>;
+    const bool later = w.causal && w.Lq > 1;
+    auto kern = few ? (later ? attention_kernel<D, true, true> : attention_kernel<D, true, false>)
+                    : (later ? attention_kernel<D, false, true> : attention_kernel<D, false, false>);
     constexpr size_t smem = Cfg<D>::kSmemBytes;
     if (cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), static_cast<int>(smem));
         e != cudaSuccess)
