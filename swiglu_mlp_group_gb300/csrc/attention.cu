@@ -76,7 +76,7 @@ static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs == kThreads * kLaunchRegs &&
 // all 128 at once 472).
 constexpr int kFirstKeys = 96;
 // Query rows up to which a narrow item is one of few rows.  The call's kernel has
-// // their code where that is so of own items and none is wide: 16 x 1 x 1500 x 16
+// their code where that is so of own items and none is wide: 16 x 1 x 1500 x 16
 // heads of 64 take 22.4 us without it and 17.2 with it; with wide items besides
 // (128 x 1 x 4096 behind 32768, 64 heads over 8 of 128) it is 223 and 246: a wide
 // tile, bound by its softmax, takes longer in the kernel that has both.

@@ -66,7 +66,6 @@ struct AttentionArgs {
     bool causal;          // own key j is seen by query i when j <= len - Lq + i
     float scale;
     void *ws;
-    unsigned int *status;
 };
 // kAttentionTooLarge: more key tiles over all heads and sequences than a call
 // can count (2^30 of 128 keys).

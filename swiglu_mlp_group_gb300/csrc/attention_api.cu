@@ -87,7 +87,7 @@ ck_status run_attention(ck::AttentionArgs &a, const void *q, int64_t ldq, void *
     unsigned int *status = nullptr;
     if (ck_status st = device(&status); st != CK_OK) return st;
     a.q = bits(q), a.ldq = ldq, a.out = bits(out), a.ldo = ldo;
-    a.scale = scale, a.ws = ws, a.status = status;
+    a.scale = scale, a.ws = ws;
     return ck::launch_attention(a, context(stream, status)) == cudaSuccess ? CK_OK : CK_ERR_CUDA;
 }
 
