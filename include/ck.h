@@ -90,7 +90,8 @@ typedef enum {
     CK_ERR_UNSUPPORTED_DEVICE = 7, /* current device is not compute capability 10.3 */
     CK_ERR_CUDA = 8,               /* a CUDA runtime call or launch failed */
     CK_ERR_TIMEOUT = 9,            /* a device-side wait ran out (ck_poll_device_status) */
-    CK_ERR_INVALID = 10,           /* an enum argument has an unknown value (attention: a scale or eps too) */
+    CK_ERR_INVALID = 10,           /* an enum argument has an unknown value (attention: a scale or
+                                    * eps too) */
     CK_ERR_INDEX = 11              /* a position, slot, page or length on the device was out of range
                                     * (ck_poll_device_status) */
 } ck_status;
@@ -427,7 +428,9 @@ CK_API ck_status ck_packed_gemv_dequant(const int8_t *xq, const float *sx, int64
  * next to each other (D elements each) and tokens are a leading dimension ld*
  * apart (elements, a multiple of 8, at least heads * D), so the pieces of a
  * packed qkv projection are passed as pointers into its rows.  Every sum, norm
- * and softmax statistic is f32.
+ * and softmax statistic is f32; the softmax's weights enter the product with the
+ * values as bf16 (their sum is taken before that rounding).  An attention call's
+ * out may not overlap what the call reads.
  *
  * Indexes that live on the device (positions, slots, pages, lengths) are
  * checked where they are used: one out of range is never followed; it records
@@ -507,9 +510,9 @@ CK_API ck_status ck_kv_append(const void *k, int64_t ldk, const void *v, int64_t
  * consequence to its result, whatever it holds (rows past a length, tokens
  * behind its own); a value that it sees and that is not finite makes its result
  * NaN or infinite, in the value's column or, a key, in all (unless its weight
- * vanishes beside another part's of the row).  A length out of [0, max_seq_len] is taken as the nearer
- * end, a page out of [0, pages) as rows of zeros, and either records
- * CK_ERR_INDEX.  Errors: CK_ERR_NULL, CK_ERR_SHAPE, CK_ERR_INVALID (scale),
+ * vanishes beside another part's of the row).  A length out of [0, max_seq_len]
+ * is taken as the nearer end, a page out of [0, pages) as rows of zeros, and
+ * either records CK_ERR_INDEX.  Errors: CK_ERR_NULL, CK_ERR_SHAPE, CK_ERR_INVALID (scale),
  * CK_ERR_ALIGN, CK_ERR_WORKSPACE, CK_ERR_UNSUPPORTED_DEVICE, CK_ERR_CUDA.
  */
 CK_API ck_status ck_prefix_attention(const void *q, int64_t ldq, int64_t B, int64_t Lq, int64_t Hq,
@@ -534,8 +537,8 @@ CK_API size_t ck_prefix_attention_workspace_bytes(int64_t B, int64_t Lq, int64_t
  *   k, v      : bf16, B * Lk tokens of Hkv heads (ldk, ldv); Lk may be 0.
  *   kv_lens   : int32 [B], NULL: Lk for all.  A length out of [0, Lk] is taken
  *               as the nearer end and records CK_ERR_INDEX.
- * D is 64 or 128; Lk at most 2^30 and B * Lk below 2^31.  What padded states hold is of no consequence.  Errors as
- * ck_prefix_attention.
+ * D is 64 or 128; Lk at most 2^30 and B * Lk below 2^31.  What padded states hold
+ * is of no consequence.  Errors as ck_prefix_attention.
  */
 CK_API ck_status ck_cross_attention(const void *q, int64_t ldq, const void *k, int64_t ldk,
                                     const void *v, int64_t ldv, int64_t B, int64_t Lq, int64_t Lk,

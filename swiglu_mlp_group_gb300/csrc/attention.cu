@@ -33,7 +33,8 @@
 //   warps 9, 10      : MMA issue: S = Q K^T, O += P V.  Their steps alternate
 //                      between the streams.
 //   warp 11          : works the CTA's items out, ahead of the others, and hands
-//                      them round in a ring; sends finished rows out by TMA.
+//                      them round in a ring; sends finished rows out by TMA; looks
+//                      through V that only an item's later tokens see (LATER).
 // In an item of few rows (FEW) the four warps of a stream share them: each has a
 // copy of the rows in its 32 of the tile and a quarter of the tile's keys.
 // P is rounded to bf16 for the second product, the operand type of V; its sum
@@ -41,9 +42,10 @@
 //
 // What bounds it (measured on GB300).  Wide items: the chain of a stream's tile,
 // S -> softmax (1440 cycles) -> P V -> Q K^T, some 2460 cycles for two row tiles
-// whose products take 2048; 2 x 8192 x 4093 x 32 heads of 128 in 415-430 us, 1600
-// to 1655 TFLOP/s, the rate at which a library's plain product runs under the
-// power limit (1706).  Short wide items: their starts and ends besides.  Narrow
+// whose products take 2048 (4096 x 4096, nothing beside it); 2 x 8192 x 4093 x 32
+// heads of 128 in 412 to 447 us, over several boxes and ways of calling, 1540 to
+// 1670 TFLOP/s, against 1706 of a library's plain product under the power limit.
+// Short wide items: their starts and ends besides.  Narrow
 // items: the K and V in flight, three of the ring's five 32 KB places an SM (the
 // others hold what is being used): 5.5 to 6 TB/s.  Few rows: K and V, 1600 cycles
 // for a key tile of 64 KB, and their items' ends, about 4000 cycles from the last P
@@ -141,10 +143,12 @@ struct Work {
 };
 
 // Cost units: a sixteenth of a narrow key tile's time (cost_o of one).  A wide
-// tile is bound by its products and exponentials (2620 cycles for two row tiles),
-// a narrow one by the K and V it streams (64 KB, 2200 cycles with the SMs shared
-// between both); 21:16 divided a mixed call best of 19, 21 and 24.  An item's
-// query loads and result cost about a narrow tile.
+// tile is bound by its products and exponentials, a narrow one by the K and V it
+// streams (64 KB).  In a call that has both (128 sequences x 64 / 8 heads of 128
+// behind 32768, own lengths to 4096) they took 2620 cycles for two row tiles and
+// 2200, items' ends among them: 19:16.  The 21 is what divided that call best,
+// 225 us against 234 at 19 and 238 at 24; other mixed calls were not swept.  An
+// item's query loads and result cost about a narrow tile.
 constexpr int kTileCost = 16, kWideTileCost = 21, kItemCost = 16;
 constexpr int64_t kMostCost = int64_t{1} << 30;
 
@@ -1577,7 +1581,10 @@ Work plan(const AttentionArgs &a) {
     // heads 60 / 62, to 2000 97 / 92, to 4000 183 / 167, one 4000 among 250s 50 /
     // 35; 8 x 1024 x 8 heads to 2000 40 / 58, to 4000 71 / 85, one 4000 among
     // 250s 52 / 45.  Many wide groups level their lengths out, and a join passes
-    // over all their rows.
+    // over all their rows.  The rule knows the longest length alone: at its bounds
+    // (16 tiles narrow, 32 wide) it takes whole groups, which need no workspace,
+    // also where shares were faster, by 5 % at the 97 / 92 and by 15 % with one
+    // long sequence among short ones.
     const int64_t most = w.wide_o ? (base_o >= 4 * kPlanSms ? w.tiles_o : 32) : 16;
     w.direct = w.tiles_p == 0 && (w.tiles_o <= 2 || (base_o > kPlanSms && (!a.ragged || w.tiles_o <= most)));
     if (w.direct) {

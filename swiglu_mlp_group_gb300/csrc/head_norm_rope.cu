@@ -13,7 +13,8 @@ namespace {
 // Rows of a group of lanes in one unit of work, and blocks that share an SM (by
 // their registers): of 2, 4 and 8 rows with 512 to 1280 threads an SM, 8 rows
 // with 640 were best at long calls (30011 tokens x 48 heads x 128: 131 us; 4 rows
-// with 768 139, 2 with 1024 170; 8 rows with 768 spill: 160).
+// with 768 139, 2 with 1024 170, 8 with 768, which spill, 160).  At 640 the norm's
+// kernels spill nothing, the append's 4 (halves) and 36 bytes (pairs side by side).
 constexpr int kRows = 8;
 constexpr int kThreads = 128;
 constexpr int kBlocksPerSm = 5;
