@@ -1694,7 +1694,7 @@ cudaError_t launch(const AttentionArgs &a, Work &w, const LaunchCtx &ctx) {
         qp = qo;
     else if (!row_map(&qp, a, w.tok_p))
         return cudaErrorInvalidValue;
-    if (a.k) {
+    if (a.k && (a.pages > 0 || a.max_len > 0)) {
         if (!key_map(&km, a, a.k, a.ldk) || !key_map(&vm, a, a.v, a.ldv)) return cudaErrorInvalidValue;
     } else {
         km = vm = qo;  // no key at all
