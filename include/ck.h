@@ -501,9 +501,9 @@ CK_API ck_status ck_kv_append(const void *k, int64_t ldk, const void *v, int64_t
  *   prefix_pages : int32 [ceil(prefix_len / page_size)], NULL when prefix_len
  *               is 0; rows past prefix_len in its last page are not read as keys.
  *   block_table : int32 [B, table_stride], row b the pages of sequence b's own
- *               tokens (entries past its length are not read); NULL when
+ *               tokens (entries past its length are not read); may be NULL when
  *               max_seq_len is 0.
- *   seq_lens  : int32 [B], each at most max_seq_len; NULL when that is 0.
+ *   seq_lens  : int32 [B], each at most max_seq_len; may be NULL when that is 0.
  *   scale     : > 0 and finite.
  *   ws        : ck_prefix_attention_workspace_bytes(...) bytes.
  * D is 64 or 128; lengths at most 2^30.  What a query does not see is of no

@@ -185,7 +185,7 @@ CK_API ck_status ck_prefix_attention(const void *q, int64_t ldq, int64_t B, int6
     ck::AttentionArgs a = prefix_sizes(B, Lq, Hq, Hkv, D, prefix_len, max_seq_len);
     a.k = bits(k_cache), a.v = bits(v_cache), a.pages = pages, a.page_size = static_cast<int>(page_size);
     a.prefix_pages = prefix_pages, a.block_table = block_table, a.table_stride = table_stride;
-    a.lens = max_seq_len > 0 ? seq_lens : nullptr;
+    a.lens = seq_lens;
     return run_attention(a, q, ldq, out, ldo, scale, ws, ws_bytes, stream);
 }
 
@@ -210,7 +210,7 @@ CK_API ck_status ck_cross_attention(const void *q, int64_t ldq, const void *k, i
     if (!aligned16(q) || !aligned16(out) || !aligned16(k) || !aligned16(v)) return CK_ERR_ALIGN;
     ck::AttentionArgs a = cross_sizes(B, Lq, Lk, Hq, Hkv, D);
     a.k = bits(k), a.v = bits(v), a.ldk = ldk, a.ldv = ldv;
-    a.lens = Lk > 0 ? kv_lens : nullptr;
+    a.lens = kv_lens;
     a.ragged = a.lens != nullptr;
     return run_attention(a, q, ldq, out, ldo, scale, ws, ws_bytes, stream);
 }

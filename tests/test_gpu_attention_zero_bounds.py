@@ -22,3 +22,25 @@ def test_no_states_behind_real_pointers(Lq, ld):
     assert st == ck.CK_OK
     poll_ok()
     assert (out == 0).all()
+
+
+@pytest.mark.parametrize("prefix", [0, 70])
+@pytest.mark.parametrize("Lq", [1, 3, 300])
+def test_lengths_above_a_bound_of_zero(Lq, prefix):
+    """As above any other bound: taken as the bound, and reported."""
+    dev = device()
+    c = ref.Paged(2, 2, 2, 64, 16, prefix, [0, 0]).to(dev)
+    q = ref.randn(ref.gen(3), 2, Lq, 4, 64).to(dev)
+
+    def run(seq_lens):
+        return ck.prefix_attention(q, c.k_cache, c.v_cache, c.prefix_pages, prefix, c.block_table, seq_lens, 0)
+
+    good = run(torch.zeros(2, dtype=torch.int32, device=dev))
+    poll_ok()
+    out = run(torch.tensor([0, 1], dtype=torch.int32, device=dev))
+    assert ck.poll_device_status() == ck.CK_ERR_INDEX
+    assert torch.equal(out, good) and torch.equal(run(None), good)
+    poll_ok()
+    none = torch.empty(2, 0, 2, 64, dtype=torch.bfloat16, device=dev)
+    assert (ck.cross_attention(q, none, none, kv_lens=torch.tensor([0, 5], dtype=torch.int32, device=dev)) == 0).all()
+    assert ck.poll_device_status() == ck.CK_ERR_INDEX
