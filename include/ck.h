@@ -139,6 +139,19 @@ typedef enum {
     CK_ROPE_INTERLEAVED = 1 /* (x[2i], x[2i + 1]), i < r/2 */
 } ck_rope_mode;
 
+/* Microscaled 4-bit floats: E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign) with
+ * a scale for each block of consecutive columns. */
+typedef enum {
+    CK_FP4_MX = 0, /* 32 codes share a power of two (E8M0, 255: NaN) */
+    CK_FP4_NV = 1  /* 16 codes share an E4M3 number (0x7F: NaN), a tensor one f32 scale */
+} ck_fp4_format;
+
+/* The norm of a row. */
+typedef enum {
+    CK_NORM_RMS = 0,  /* x rsqrt(mean(x^2) + eps) */
+    CK_NORM_LAYER = 1 /* the same of x - mean(x) */
+} ck_norm;
+
 /* Operations whose workspace size ck_workspace_bytes reports. */
 typedef enum {
     CK_OP_INT8_LINEAR = 0,  /* (M, K, N, wlayout) */
@@ -548,6 +561,142 @@ CK_API ck_status ck_cross_attention(const void *q, int64_t ldq, const void *k, i
 /* Workspace bytes of that call, whatever the lengths (0 where it needs none). */
 CK_API size_t ck_cross_attention_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq,
                                                  int64_t Hkv, int64_t D);
+
+/*
+ * Linears on microscaled 4-bit floats, the operand format that this GPU's tensor
+ * cores multiply with the block scales applied by the instruction.  A value is
+ * code * block scale (* the tensor's scale, NV).
+ *
+ * Codes: [rows, K / 2] bytes, column 2j in the low half of byte j.  K is a
+ * multiple of 32 up to 32768.
+ * Scales: by row, one byte a block ([rows, K / 32] MX, [rows, K / 16] NV), is how
+ * checkpoints hold them; the operators read and write them tiled: words of four
+ * consecutive blocks of a row (64 columns NV, 128 MX; missing blocks 0), in tiles
+ * of 128 rows x one word, the ceil(K / 64 or 128) tiles of 128 rows one after
+ * another; row r's word lies at byte 16 (r % 32) + 4 (r % 128 / 32) of its tile.
+ * ck_fp4_scale_bytes(format, rows, K) bytes, 0 for sizes that are refused.  Words of
+ * rows past the last in its tile need not be set and are not written.
+ */
+CK_API size_t ck_fp4_scale_bytes(ck_fp4_format format, int64_t rows, int64_t K);
+
+/*
+ * Quantize M rows.  With amax the largest magnitude of a block and t the tensor's
+ * scale:
+ *   MX: s = 2^e, e = max(floor(log2(amax)) - 2, -127);
+ *   NV: s = E4M3(amax / (6 t)) to nearest even, at most 448;
+ *   code = E2M1(x / s) (NV: x / f32(s t)) to nearest, ties to the even code, at most 6
+ *   in magnitude, with x's sign; all codes of a block 0 where its s is 0.
+ * Divisions and products in f32, each correctly rounded.  A block with a NaN or an
+ * infinity gets the NaN scale.
+ *   x   : [M, ldx] of type xdt (act NONE: bf16 or f32; act SWIGLU: bf16 [gate | up],
+ *         2K columns, silu(gate) * up formed in f32 first); ldx a multiple of 8 (f32: 4).
+ *   tensor_scale : t, 2^-60 .. 2^60; MX: 1.
+ *   codes, scales : out, as above.
+ * Errors: CK_ERR_NULL, CK_ERR_INVALID (format, act, tensor_scale), CK_ERR_DTYPE,
+ * CK_ERR_SHAPE, CK_ERR_ALIGN, CK_ERR_UNSUPPORTED_DEVICE, CK_ERR_CUDA.
+ */
+CK_API ck_status ck_fp4_quantize(const void *x, ck_dtype xdt, int64_t M, int64_t K, int64_t ldx,
+                                 ck_input_act act, ck_fp4_format format, float tensor_scale,
+                                 void *codes, void *scales, ck_stream_t stream);
+
+/* Scales by row (a checkpoint's, one byte a block) into tiles, once, ahead of the
+ * forward passes.  Errors: CK_ERR_NULL, CK_ERR_INVALID (format), CK_ERR_SHAPE,
+ * CK_ERR_ALIGN (tiled), CK_ERR_UNSUPPORTED_DEVICE, CK_ERR_CUDA. */
+CK_API ck_status ck_fp4_tile_scales(const void *scales, int64_t rows, int64_t K,
+                                    ck_fp4_format format, void *tiled, ck_stream_t stream);
+
+/*
+ * The product of quantized activations and a quantized weight of one format:
+ *   y[m, n] = bf16( alpha * sum_k X[m, k] W[n, k] + bias[n] + residual[m, n] ),
+ * X and W code * block scale, the sum in f32, rounded once.  alpha carries both
+ * tensors' scales (finite).
+ *   codes, scales : of X [M, K], tiled;  W, w_scales : of W [N, K], tiled.
+ *   bias : bf16 [N] or NULL;  residual : bf16 [M, N] or NULL, may be y;
+ *   y    : out, bf16 [M, N];  N a multiple of 8.
+ * A NaN scale makes its row of X, or its row of W, NaN in y.  Errors: CK_ERR_NULL,
+ * CK_ERR_INVALID, CK_ERR_SHAPE, CK_ERR_ALIGN, CK_ERR_UNSUPPORTED_DEVICE, CK_ERR_CUDA.
+ */
+CK_API ck_status ck_fp4_gemm(const void *codes, const void *scales, int64_t M, int64_t K,
+                             ck_fp4_format format, const void *W, const void *w_scales, int64_t N,
+                             float alpha, const void *bias, const void *residual, void *y,
+                             ck_stream_t stream);
+
+/*
+ * A linear on 4-bit weights: ck_fp4_quantize of x (tensor scale x_scale), then
+ * ck_fp4_gemm with alpha = f32(x_scale * w_scale).
+ *   x, act, ldx : bf16, as ck_fp4_quantize; x may be y.
+ *   ws          : ck_fp4_linear_workspace_bytes(M, K, format) bytes.
+ * Errors: those of both, and CK_ERR_WORKSPACE.
+ */
+CK_API ck_status ck_fp4_linear(const void *x, int64_t M, int64_t K, int64_t ldx, ck_input_act act,
+                               ck_fp4_format format, float x_scale, const void *W,
+                               const void *w_scales, float w_scale, int64_t N, const void *bias,
+                               const void *residual, void *y, void *ws, size_t ws_bytes,
+                               ck_stream_t stream);
+/* Workspace bytes of that call (0 for sizes that it refuses). */
+CK_API size_t ck_fp4_linear_workspace_bytes(int64_t M, int64_t K, ck_fp4_format format);
+
+/*
+ * SwiGLU MLP of two such linears: h = linear(x, Wgu) in bf16 [M, 2I], then
+ * y = linear(silu(gate) * up, Wd) (+ residual), the product formed in f32 by the
+ * second one's quantizer.
+ *   x : bf16 [M, H], contiguous;  Wgu : [2I, H] (gate rows, then up rows);  Wd : [H, I];
+ *   x_scale, a_scale : tensor scales of x and of silu(gate) * up; gu_scale, d_scale
+ *       of the weights;  bgu bf16 [2I], bd bf16 [H], residual bf16 [M, H]: or NULL;
+ *   residual may be x or y, x may be y;
+ *   ws : ck_fp4_swiglu_mlp_workspace_bytes(M, H, I, format) bytes.
+ * Errors: as ck_fp4_linear.
+ */
+CK_API ck_status ck_fp4_swiglu_mlp(const void *x, int64_t M, int64_t H, int64_t I,
+                                   ck_fp4_format format, float x_scale, const void *Wgu,
+                                   const void *gu_scales, float gu_scale, const void *bgu,
+                                   float a_scale, const void *Wd, const void *d_scales,
+                                   float d_scale, const void *bd, const void *residual, void *y,
+                                   void *ws, size_t ws_bytes, ck_stream_t stream);
+/* Workspace bytes of that call (0 for sizes that it refuses). */
+CK_API size_t ck_fp4_swiglu_mlp_workspace_bytes(int64_t M, int64_t H, int64_t I,
+                                                ck_fp4_format format);
+
+/*
+ * What stands between a block's branch and the next linear, in one pass over the
+ * residual stream of T tokens x H channels (bf16):
+ *   b = branch                                  (post_weight NULL)
+ *   b = branch rsqrt(mean(branch^2) + eps) post_weight
+ *   h = x_factor x + branch_factor gate b       (gate NULL: 1; branch NULL: x_factor x)
+ *   n = norm(h) weight + bias                   (NULL: 1, 0)
+ *   n = n (1 + scale) + shift                   (NULL: 0)
+ * f32 throughout: n is formed from h before its rounding; both are rounded once.
+ *   x, branch, h_out, n_out : rows ld* elements apart (a multiple of 8, at least H);
+ *         h_out may be NULL; an output may be x or branch itself (with its leading
+ *         dimension), else outputs overlap neither inputs nor each other.
+ *   post_weight, weight, bias : [H] of type wdt (f32 or bf16).
+ *   gate, scale, shift : bf16, a row of H for every tokens_per_group tokens (the last
+ *         group may be short), rows ldm apart; tokens_per_group 0: one row for all.
+ * H is a multiple of 8 up to 16384.  Errors: CK_ERR_NULL (a gate or post_weight
+ * without a branch, too), CK_ERR_SHAPE, CK_ERR_DTYPE, CK_ERR_INVALID (norm; a factor
+ * that is not finite; eps negative or not finite), CK_ERR_ALIGN,
+ * CK_ERR_UNSUPPORTED_DEVICE, CK_ERR_CUDA.
+ */
+CK_API ck_status ck_block_norm(const void *x, int64_t ldx, const void *branch, int64_t ldb,
+                               int64_t T, int64_t H, const void *post_weight, const void *gate,
+                               const void *scale, const void *shift, int64_t ldm,
+                               int64_t tokens_per_group, float x_factor, float branch_factor,
+                               ck_norm norm, const void *weight, const void *bias, ck_dtype wdt,
+                               float eps, void *h_out, int64_t ldh, void *n_out, int64_t ldn,
+                               ck_stream_t stream);
+
+/*
+ * ck_block_norm whose n goes straight to the codes and tiled scales that ck_fp4_gemm
+ * reads, quantized from f32 as ck_fp4_quantize does (tensor scale n_scale); H a
+ * multiple of 32.  Errors: those of both.
+ */
+CK_API ck_status ck_block_norm_fp4(const void *x, int64_t ldx, const void *branch, int64_t ldb,
+                                   int64_t T, int64_t H, const void *post_weight, const void *gate,
+                                   const void *scale, const void *shift, int64_t ldm,
+                                   int64_t tokens_per_group, float x_factor, float branch_factor,
+                                   ck_norm norm, const void *weight, const void *bias, ck_dtype wdt,
+                                   float eps, void *h_out, int64_t ldh, ck_fp4_format format,
+                                   float n_scale, void *codes, void *scales, ck_stream_t stream);
 
 /*
  * Synchronizes `stream`, then reads and clears the device status word that

@@ -35,6 +35,9 @@ __all__ = [
     "set_launch_overlap", "debug_stalled_wait", "workspace_bytes",
     "qk_norm_rope", "kv_append", "prefix_attention", "prefix_attention_workspace", "cross_attention",
     "cross_attention_workspace",
+    "CK_FP4_MX", "CK_FP4_NV", "CK_NORM_RMS", "CK_NORM_LAYER",
+    "fp4_quantize", "fp4_tile_scales", "fp4_gemm", "fp4_linear", "fp4_linear_workspace", "fp4_swiglu_mlp",
+    "fp4_swiglu_mlp_workspace", "block_norm", "block_norm_fp4",
 ]
 
 # ck_status
@@ -54,8 +57,14 @@ GEMV_LAYOUT_OF_BITS = {8: CK_WLAYOUT_GEMV_PACKED, 6: CK_WLAYOUT_GEMV_PACKED_W6,
                        4: CK_WLAYOUT_GEMV_PACKED_W4}
 CK_OP_INT8_LINEAR, CK_OP_SWIGLU_MLP, CK_OP_GEMV_SMALLM, CK_OP_DEBUG_GEMM_S32 = 0, 1, 2, 3
 
+# ck_fp4_format, ck_norm
+CK_FP4_MX, CK_FP4_NV = 0, 1
+CK_NORM_RMS, CK_NORM_LAYER = 0, 1
+
 _ROPES = {"half": CK_ROPE_HALF, "interleaved": CK_ROPE_INTERLEAVED}
 _ACTS = {"none": CK_ACT_NONE, "swiglu": CK_ACT_SWIGLU}
+_FP4S = {"mx": CK_FP4_MX, "nv": CK_FP4_NV}
+_NORMS = {"rms": CK_NORM_RMS, "layer": CK_NORM_LAYER}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lock = threading.Lock()
@@ -98,6 +107,20 @@ _SIGNATURES = {
     "ck_cross_attention": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _i64, _i64, _i64,
                                   _vp, _f32, _vp, _i64, _vp, _sz, _vp]),
     "ck_cross_attention_workspace_bytes": (_sz, [_i64] * 6),
+    "ck_fp4_scale_bytes": (_sz, [_int, _i64, _i64]),
+    "ck_fp4_quantize": (_int, [_vp, _int, _i64, _i64, _i64, _int, _int, _f32, _vp, _vp, _vp]),
+    "ck_fp4_tile_scales": (_int, [_vp, _i64, _i64, _int, _vp, _vp]),
+    "ck_fp4_gemm": (_int, [_vp, _vp, _i64, _i64, _int, _vp, _vp, _i64, _f32, _vp, _vp, _vp, _vp]),
+    "ck_fp4_linear": (_int, [_vp, _i64, _i64, _i64, _int, _int, _f32, _vp, _vp, _f32, _i64, _vp, _vp, _vp,
+                             _vp, _sz, _vp]),
+    "ck_fp4_linear_workspace_bytes": (_sz, [_i64, _i64, _int]),
+    "ck_fp4_swiglu_mlp": (_int, [_vp, _i64, _i64, _i64, _int, _f32, _vp, _vp, _f32, _vp, _f32, _vp, _vp,
+                                 _f32, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "ck_fp4_swiglu_mlp_workspace_bytes": (_sz, [_i64, _i64, _i64, _int]),
+    "ck_block_norm": (_int, [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _f32, _f32,
+                             _int, _vp, _vp, _int, _f32, _vp, _i64, _vp, _i64, _vp]),
+    "ck_block_norm_fp4": (_int, [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _f32,
+                                 _f32, _int, _vp, _vp, _int, _f32, _vp, _i64, _int, _f32, _vp, _vp, _vp]),
     "ck_poll_device_status": (_int, [_vp]),
     "ck_set_wait_timeout_ns": (None, [ctypes.c_uint64]),
     "ck_set_launch_overlap": (None, [_int]),
@@ -433,7 +456,7 @@ def _call_device(x, what: str) -> int:
     """Index of the device of a call: x's.  The library launches on the current one, so it has to be that."""
     dev = x.get_device()
     if dev < 0:
-        raise ValueError(f"{what} must be a bf16 CUDA tensor")
+        raise ValueError(f"{what} must be a CUDA tensor")
     if dev != _torch().cuda.current_device():
         raise ValueError(f"{what} is on cuda:{dev}, which is not the current device")
     return dev
@@ -504,6 +527,15 @@ def _new(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _new_on(shape, device, stream):
+    """_new of bytes on a device."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=torch.uint8, device=device)
 
 
 def _rotation(cos_sin, positions, T: int, mode: str, dev: int):
@@ -692,6 +724,274 @@ def cross_attention(q, k, v, kv_lens=None, scale: float | None = None, out=None,
     if st != CK_OK:
         raise CkError(st, "ck_cross_attention")
     return out
+
+
+# ---------------------------------------------------------------------------
+# microscaled 4-bit floats, block norms
+# ---------------------------------------------------------------------------
+
+def _row_stride(x, dtype, what: str, dev: int, shape=None) -> int:
+    """Elements from one row of x (2-D, of this type and shape, on the call's device) to the next."""
+    if x.dtype is not dtype or x.get_device() != dev:
+        raise ValueError(f"{what} must be a tensor of {dtype} on cuda:{dev}")
+    if x.dim() != 2 or (shape is not None and x.shape != shape):
+        raise ValueError(f"{what} must have shape {tuple(shape) if shape is not None else '[rows, columns]'}")
+    st = x.stride()
+    if st[1] != 1 and x.shape[1] > 1:
+        raise ValueError(f"{what}: the elements of a row must lie next to each other")
+    return st[0] if x.shape[0] > 1 else x.shape[1]
+
+
+def _fp4_format(fmt: str) -> int:
+    f = _FP4S.get(fmt)
+    if f is None:
+        raise ValueError("fmt must be 'mx' or 'nv'")
+    return f
+
+
+def _act(act: str) -> int:
+    a = _ACTS.get(act)
+    if a is None:
+        raise ValueError("act must be 'none' or 'swiglu'")
+    return a
+
+
+def _tiled_bytes(f: int, rows: int, K: int, where: str) -> int:
+    n = int(lib().ck_fp4_scale_bytes(f, rows, K))
+    if n == 0:
+        raise CkError(CK_ERR_SHAPE, where)
+    return n
+
+
+def _fp4_operand(codes, scales, f: int, what: str, dev: int):
+    """(rows, K, pointers) of codes [rows, K / 2] and their tiled scales."""
+    u8 = _torch().uint8
+    if codes.dim() != 2:
+        raise ValueError(f"{what} must be codes [rows, K / 2]")
+    p, ps = _typed(codes, u8, what, dev), _typed(scales, u8, f"{what}'s scales", dev)
+    rows, K = codes.shape[0], 2 * codes.shape[1]
+    if scales.numel() < _tiled_bytes(f, rows, K, what):
+        raise ValueError(f"{what}'s scales must be tiled scales of these codes")
+    return rows, K, p, ps
+
+
+def _out_rows(out, M: int, N: int, dev: int, like, stream):
+    """A linear's output: the one given (contiguous bf16 [M, N]) or a new one."""
+    bf16 = _torch().bfloat16
+    if out is None:
+        return _new((M, N), bf16, like, stream)
+    _typed(out, bf16, "out", dev, (M, N))
+    return out
+
+
+def fp4_quantize(x, fmt: str, scale: float = 1.0, act: str = "none", codes=None, scales=None, stream=None):
+    """Quantize x [M, K] (bf16 or f32; act "swiglu": bf16 [gate | up] of 2K columns; rows may lie apart) to
+    microscaled 4-bit floats -> (codes uint8 [M, K / 2], tiled scales uint8).
+
+    fmt "mx": 32 codes share a power of two; "nv": 16 codes share an E4M3 number, the tensor `scale`."""
+    torch = _torch()
+    f, a = _fp4_format(fmt), _act(act)
+    dev = _call_device(x, "x")
+    f32 = x.dtype is torch.float32
+    ldx = _row_stride(x, torch.float32 if f32 else torch.bfloat16, "x", dev)
+    M, K = x.shape
+    if a == CK_ACT_SWIGLU:
+        K //= 2
+    n = _tiled_bytes(f, M, K, "ck_fp4_quantize")
+    if codes is None:
+        codes = _new((M, K // 2), torch.uint8, x, stream)
+    if scales is None:
+        scales = _new((n,), torch.uint8, x, stream)
+    elif scales.numel() < n:
+        raise ValueError(f"scales must hold {n} bytes")
+    st = lib().ck_fp4_quantize(x.data_ptr(), CK_F32 if f32 else CK_BF16, M, K, ldx, a, f, scale,
+                               _typed(codes, torch.uint8, "codes", dev, (M, K // 2)),
+                               _typed(scales, torch.uint8, "scales", dev), _run_stream(stream, dev))
+    if st != CK_OK:
+        raise CkError(st, "ck_fp4_quantize")
+    return codes, scales
+
+
+def fp4_tile_scales(scales, fmt: str, stream=None):
+    """Block scales by row (a checkpoint's: uint8 [rows, K / 32] "mx", [rows, K / 16] "nv") -> tiled."""
+    torch = _torch()
+    f = _fp4_format(fmt)
+    dev = _call_device(scales, "scales")
+    p = _typed(scales, torch.uint8, "scales", dev)
+    if scales.dim() != 2:
+        raise ValueError("scales must be [rows, blocks]")
+    rows, K = scales.shape[0], scales.shape[1] * (32 if f == CK_FP4_MX else 16)
+    out = _new((_tiled_bytes(f, rows, K, "ck_fp4_tile_scales"),), torch.uint8, scales, stream)
+    st = lib().ck_fp4_tile_scales(p, rows, K, f, out.data_ptr(), _run_stream(stream, dev))
+    if st != CK_OK:
+        raise CkError(st, "ck_fp4_tile_scales")
+    return out
+
+
+def fp4_gemm(codes, scales, W, w_scales, fmt: str, alpha: float = 1.0, bias=None, residual=None, out=None,
+             stream=None):
+    """y = bf16(alpha X W^T + bias + residual) -> bf16 [M, N], X of codes [M, K / 2] and W of [N, K / 2] with
+    tiled scales (fp4_quantize, block_norm_fp4, fp4_tile_scales).  residual may be out."""
+    f = _fp4_format(fmt)
+    bf16 = _torch().bfloat16
+    dev = _call_device(codes, "codes")
+    M, K, px, pxs = _fp4_operand(codes, scales, f, "codes", dev)
+    N, Kw, pw, pws = _fp4_operand(W, w_scales, f, "W", dev)
+    if Kw != K:
+        raise ValueError("codes and W must have the same columns")
+    y = _out_rows(out, M, N, dev, codes, stream)
+    st = lib().ck_fp4_gemm(px, pxs, M, K, f, pw, pws, N, alpha, _typed(bias, bf16, "bias", dev, (N,)),
+                           _typed(residual, bf16, "residual", dev, (M, N)), y.data_ptr(), _run_stream(stream, dev))
+    if st != CK_OK:
+        raise CkError(st, "ck_fp4_gemm")
+    return y
+
+
+def fp4_linear_workspace(M: int, K: int, fmt: str, device="cuda", stream=None):
+    """A workspace for fp4_linear calls of M tokens and K columns."""
+    n = int(lib().ck_fp4_linear_workspace_bytes(M, K, _fp4_format(fmt)))
+    return _new_on((max(n, 16),), device, stream)
+
+
+def fp4_linear(x, W, w_scales, fmt: str, x_scale: float = 1.0, w_scale: float = 1.0, bias=None, act: str = "none",
+               out=None, workspace=None, residual=None, stream=None):
+    """Linear on 4-bit weights -> bf16 [M, N]: x [M, K] bf16 (act "swiglu": [gate | up]; rows may lie apart) is
+    quantized on the way (tensor scale x_scale); W codes [N, K / 2] with tiled scales, tensor scale w_scale.
+    residual [M, N] may be out."""
+    bf16 = _torch().bfloat16
+    f, a = _fp4_format(fmt), _act(act)
+    dev = _call_device(x, "x")
+    ldx = _row_stride(x, bf16, "x", dev)
+    M, K = x.shape
+    if a == CK_ACT_SWIGLU:
+        K //= 2
+    N, Kw, pw, pws = _fp4_operand(W, w_scales, f, "W", dev)
+    if Kw != K:
+        raise ValueError("x and W must have the same columns")
+    y = _out_rows(out, M, N, dev, x, stream)
+    ws = (_given_workspace(workspace, dev) if workspace is not None else
+          fp4_linear_workspace(M, K, fmt, x.device, stream))
+    st = lib().ck_fp4_linear(x.data_ptr(), M, K, ldx, a, f, x_scale, pw, pws, w_scale, N,
+                             _typed(bias, bf16, "bias", dev, (N,)), _typed(residual, bf16, "residual", dev, (M, N)),
+                             y.data_ptr(), ws.data_ptr(), ws.nbytes, _run_stream(stream, dev))
+    if st != CK_OK:
+        raise CkError(st, "ck_fp4_linear")
+    return y
+
+
+def fp4_swiglu_mlp_workspace(M: int, H: int, I: int, fmt: str, device="cuda", stream=None):
+    """A workspace for fp4_swiglu_mlp calls of these sizes."""
+    n = int(lib().ck_fp4_swiglu_mlp_workspace_bytes(M, H, I, _fp4_format(fmt)))
+    return _new_on((max(n, 16),), device, stream)
+
+
+def fp4_swiglu_mlp(x, Wgu, gu_scales, Wd, d_scales, fmt: str, x_scale: float = 1.0, gate_up_scale: float = 1.0,
+                   act_scale: float = 1.0, down_scale: float = 1.0, bgu=None, bd=None, residual=None, out=None,
+                   workspace=None, stream=None):
+    """SwiGLU MLP on 4-bit weights -> bf16 [M, H]: h = linear(x, Wgu [2I, H / 2]), y = linear(silu(gate) * up,
+    Wd [H, I / 2]) + residual.  Tensor scales: x_scale of x, act_scale of silu(gate) * up, the others of the
+    weights.  residual may be x or out."""
+    bf16 = _torch().bfloat16
+    f = _fp4_format(fmt)
+    dev = _call_device(x, "x")
+    M, H = x.shape
+    px = _typed(x, bf16, "x", dev)
+    N, Kw, pgu, pgus = _fp4_operand(Wgu, gu_scales, f, "Wgu", dev)
+    Nd, I, pd, pds = _fp4_operand(Wd, d_scales, f, "Wd", dev)
+    if Kw != H or Nd != H or N != 2 * I:
+        raise ValueError("Wgu must be [2I, H / 2] and Wd [H, I / 2] of x's H columns")
+    y = _out_rows(out, M, H, dev, x, stream)
+    ws = (_given_workspace(workspace, dev) if workspace is not None else
+          fp4_swiglu_mlp_workspace(M, H, I, fmt, x.device, stream))
+    st = lib().ck_fp4_swiglu_mlp(px, M, H, I, f, x_scale, pgu, pgus, gate_up_scale, _typed(bgu, bf16, "bgu", dev, (N,)),
+                                 act_scale, pd, pds, down_scale, _typed(bd, bf16, "bd", dev, (H,)),
+                                 _typed(residual, bf16, "residual", dev, (M, H)), y.data_ptr(), ws.data_ptr(),
+                                 ws.nbytes, _run_stream(stream, dev))
+    if st != CK_OK:
+        raise CkError(st, "ck_fp4_swiglu_mlp")
+    return y
+
+
+def _norm_call(x, branch, post_weight, gate, scale, shift, tokens_per_group, x_factor, branch_factor, norm, weight,
+               bias, eps, h_out, stream):
+    """What block_norm and block_norm_fp4 share -> (C arguments up to h_out's, h, device)."""
+    bf16 = _torch().bfloat16
+    dev = _call_device(x, "x")
+    shape = x.shape
+    ldx = _row_stride(x, bf16, "x", dev)
+    T, H = shape
+    ldb = 0 if branch is None else _row_stride(branch, bf16, "branch", dev, shape)
+    kind = _NORMS.get(norm)
+    if kind is None:
+        raise ValueError("norm must be 'rms' or 'layer'")
+    groups = -(-T // tokens_per_group) if tokens_per_group > 0 else 1
+    ldm = None
+    for t, what in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
+        if t is None:
+            continue
+        if t.dim() != 2 or t.shape[0] < groups or t.shape[1] != H:
+            raise ValueError(f"{what} must have a row of {H} for each of {groups} groups")
+        ld = _row_stride(t, bf16, what, dev)
+        if groups > 1:
+            if ldm is not None and ld != ldm:
+                raise ValueError("gate, scale and shift must have their rows at one stride")
+            ldm = ld
+    dt, wdt = _weight_type(post_weight, weight, bias)
+    if h_out is None:
+        # without a branch and a factor the stream itself is h
+        h_out, ldh = (_new((T, H), bf16, x, stream), H) if branch is not None or x_factor != 1.0 else (None, 0)
+    else:
+        ldh = _row_stride(h_out, bf16, "h_out", dev, shape)
+    args = (x.data_ptr(), ldx, _ptr(branch), ldb, T, H, _norm_weight(post_weight, H, "post_weight", dt, dev),
+            _ptr(gate), _ptr(scale), _ptr(shift), ldm or H, tokens_per_group, x_factor, branch_factor, kind,
+            _norm_weight(weight, H, "weight", dt, dev), _norm_weight(bias, H, "bias", dt, dev), wdt, eps,
+            _ptr(h_out), ldh)
+    return args, x if h_out is None else h_out, dev
+
+
+def block_norm(x, branch=None, post_weight=None, gate=None, x_factor: float = 1.0, branch_factor: float = 1.0,
+               norm: str = "rms", weight=None, bias=None, scale=None, shift=None, tokens_per_group: int = 0,
+               eps: float = 1e-6, h_out=None, n_out=None, stream=None):
+    """The residual sum behind a block and the norm in front of the next, in one pass -> (h, n), bf16 [T, H].
+
+    h = x_factor x + branch_factor gate b, b the branch (RMS-normed times post_weight, where that is given);
+    n = norm(h) weight + bias, then n (1 + scale) + shift.  x, branch [T, H] bf16, rows may lie apart; weights
+    [H], f32 or bf16 alike; gate, scale, shift bf16 [groups, H], a row for every tokens_per_group tokens (0: one
+    row for all).  h_out=x and n_out=branch work in place.  Without a branch and a factor h is x."""
+    args, h, dev = _norm_call(x, branch, post_weight, gate, scale, shift, tokens_per_group, x_factor, branch_factor,
+                              norm, weight, bias, eps, h_out, stream)
+    if n_out is None:
+        n_out, ldn = _new(x.shape, x.dtype, x, stream), x.shape[1]
+    else:
+        ldn = _row_stride(n_out, x.dtype, "n_out", dev, x.shape)
+    st = lib().ck_block_norm(*args, n_out.data_ptr(), ldn, _run_stream(stream, dev))
+    if st != CK_OK:
+        raise CkError(st, "ck_block_norm")
+    return h, n_out
+
+
+def block_norm_fp4(x, branch=None, fmt: str = "nv", n_scale: float = 1.0, post_weight=None, gate=None,
+                   x_factor: float = 1.0, branch_factor: float = 1.0, norm: str = "rms", weight=None, bias=None,
+                   scale=None, shift=None, tokens_per_group: int = 0, eps: float = 1e-6, h_out=None, codes=None,
+                   scales=None, stream=None):
+    """block_norm whose n is quantized as by fp4_quantize (tensor scale n_scale) -> (h, codes, tiled scales)."""
+    u8 = _torch().uint8
+    f = _fp4_format(fmt)
+    T, H = x.shape
+    nbytes = _tiled_bytes(f, T, H, "ck_block_norm_fp4")
+    args, h, dev = _norm_call(x, branch, post_weight, gate, scale, shift, tokens_per_group, x_factor, branch_factor,
+                              norm, weight, bias, eps, h_out, stream)
+    if codes is None:
+        codes = _new((T, H // 2), u8, x, stream)
+    if scales is None:
+        scales = _new((nbytes,), u8, x, stream)
+    elif scales.numel() < nbytes:
+        raise ValueError(f"scales must hold {nbytes} bytes")
+    st = lib().ck_block_norm_fp4(*args, f, n_scale, _typed(codes, u8, "codes", dev, (T, H // 2)),
+                                 _typed(scales, u8, "scales", dev), _run_stream(stream, dev))
+    if st != CK_OK:
+        raise CkError(st, "ck_block_norm_fp4")
+    return h, codes, scales
 
 
 def debug_int8_gemm_s32(xq, Wq, stream=None):

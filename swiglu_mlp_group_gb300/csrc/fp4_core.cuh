@@ -1,0 +1,136 @@
+// fp4_core.cuh -- quantization to microscaled 4-bit floats, the part that the
+// quantizer and the block norm share.
+//
+// A code is an E2M1 number: 0, 0.5, 1, 1.5, 2, 3, 4 or 6 and a sign.  With
+// amax the largest magnitude of a block,
+//   MX (32 codes):  s = 2^e, e = max(floor(log2 amax) - 2, -127)   (E8M0)
+//   NV (16 codes):  s = E4M3(amax / (6 t)), at most 448, t the tensor's scale
+//   code = E2M1(x / d), to nearest, ties to the even code, at most 6;
+//   d = s (MX) or f32(s t) (NV); all codes 0 where s is 0.
+// A block with a NaN or an infinity gets a NaN scale (0xFF, 0x7F).
+//
+// Values on the border of two codes are common (the inputs are bf16 and d has
+// few bits), so the quotient has to be the correctly rounded one: a product with
+// 1 / d alone would land to either side of the border.  MX: 1 / d is a power of
+// two and the product exact.  NV: Markstein's correction, q + r (x - q d) with r
+// the correctly rounded 1 / d, on two elements at a time (three operations for
+// two elements; IEEE division of each element would be some ten each).
+//
+// Layout.  Codes: [rows, K / 2] bytes, the even column in the low half.  Scales:
+// tiles of 128 rows x one 32-bit word (four scales, 64 (NV) or 128 (MX)
+// columns), the words of a tile of rows one after another; in a tile of 512
+// bytes row r's word lies at 16 (r % 32) + 4 (r / 32): what tcgen05.cp copies to
+// TMEM as it stands.  Scales past K in a row's last word are 0.
+#pragma once
+
+#include <cuda_fp8.h>
+#include <stdint.h>
+
+#include "fp4.h"
+#include "ptx.cuh"
+
+namespace ck {
+namespace fp4 {
+
+constexpr unsigned kFull = 0xffffffffu;
+
+// Byte offset of row's word `word` of `words` a row.
+__device__ __forceinline__ int64_t scale_word_at(int64_t row, int word, int words) {
+    const int r = static_cast<int>(row & 127);
+    return ((row >> 7) * words + word) * 512 + (r & 31) * 16 + (r >> 5) * 4;
+}
+
+// Largest magnitude of three, a NaN if one of them is.
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// Eight codes of f32 pairs, the first in the lowest bits.
+__device__ __forceinline__ uint32_t pack8(const uint64_t (&q)[4]) {
+    float a[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f32x2_split(q[i], a[2 * i], a[2 * i + 1]);
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(r)
+        : "f"(a[0]), "f"(a[1]), "f"(a[2]), "f"(a[3]), "f"(a[4]), "f"(a[5]), "f"(a[6]), "f"(a[7]));
+    return r;
+}
+
+// Eight consecutive values of a row in each lane (two lanes hold an NV block,
+// four an MX block; lane 0's first value begins one) -> the lane's codes and the
+// block's scale byte.  Every lane of the warp takes part.
+struct Scale {
+    float tensor, six_tensor;  // t and 6 t
+};
+template <bool NV>
+__device__ __forceinline__ uint32_t quantize8(const uint64_t (&v)[4], const Scale &t, uint32_t &scale) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a, b;
+        f32x2_split(v[i], a, b);
+        m = max3_abs_nan(m, a, b);
+    }
+    m = max_nan(m, __shfl_xor_sync(kFull, m, 1));
+    if constexpr (!NV) m = max_nan(m, __shfl_xor_sync(kFull, m, 2));
+    const bool finite = m < __int_as_float(0x7f800000);
+    uint64_t q[4];
+    if constexpr (NV) {
+        const float s = __fdiv_rn(m, t.six_tensor);
+        const __nv_fp8_storage_t s8 = __nv_cvt_float_to_fp8(s, __NV_SATFINITE, __NV_E4M3);
+        scale = finite ? s8 : 0x7fu;
+        const float d = __fmul_rn(__half2float(__nv_cvt_fp8_to_halfraw(s8, __NV_E4M3)), t.tensor);
+        const float r = s8 != 0 && finite ? __frcp_rn(d) : 0.f;
+        const uint64_t r2 = f32x2(r, r), nd = f32x2(-d, -d);
+        // past what the largest scale reaches a quotient can overflow, and the
+        // correction would make it NaN
+        const bool clamp = !(s <= 448.f);
+        const float top = 8.f * d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint64_t x = v[i];
+            if (clamp) {
+                float a, b;
+                f32x2_split(x, a, b);
+                x = f32x2(fminf(fmaxf(a, -top), top), fminf(fmaxf(b, -top), top));
+            }
+            const uint64_t q0 = mul_f32x2(x, r2);
+            // (the correction turns -0 into 0: the sign is x's)
+            q[i] = fma_f32x2(fma_f32x2(q0, nd, x), r2, q0) | (x & 0x8000000080000000ull);
+        }
+    } else {
+        const uint32_t e = __float_as_uint(m) >> 23;
+        scale = finite ? (e > 2 ? e - 2 : 0u) : 0xffu;
+        const float r = finite ? __uint_as_float((254u - scale) << 23) : 0.f;
+        const uint64_t r2 = f32x2(r, r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = mul_f32x2(v[i], r2);
+    }
+    return pack8(q);
+}
+
+// The word of four scales that a group of lanes holds (8 lanes, NV; 16, MX).
+template <bool NV>
+__device__ __forceinline__ uint32_t scale_word(uint32_t scale, int lane) {
+    constexpr int kStep = NV ? 2 : 4;  // lanes of a block
+    uint32_t w = scale << (8 * ((lane / kStep) & 3));
+    w |= __shfl_xor_sync(kFull, w, kStep);
+    w |= __shfl_xor_sync(kFull, w, 2 * kStep);
+    return w;
+}
+
+}  // namespace fp4
+}  // namespace ck

@@ -1,0 +1,308 @@
+// fp4_gemm_few.cu -- the 4-bit product for few tokens:
+//
+//   y[m, n] = bf16( alpha * sum_k X[m, k] W[n, k] + bias[n] + residual[m, n] )
+//
+// X, W: E2M1 codes times the scales of their blocks (fp4_core.cuh).  The weight's
+// bytes are the floor, so the weight is the operand that the tensor cores walk:
+// a CTA has 128 rows of W as tcgen05.mma's A and TN tokens as its B, D[n, m] in
+// TMEM, and the scales' multiplication is the instruction's own -- nothing is
+// decoded.  K is split over the S CTAs of a cluster so that every SM has weight to
+// fetch; each CTA sends the columns of its partial sums to the CTA that finishes
+// them through distributed shared memory, which adds them in the order of the
+// CTAs' ranks (f32: the result does not depend on timing).
+//
+// Roles (6 warps): warp 0 TMA producer, warp 1 TMEM and MMA issue, warps 2..5 the
+// epilogue (one 32-lane quarter of TMEM each).
+#include <cuda_bf16.h>
+
+#include "fp4_core.cuh"
+#include "launch_util.h"
+
+namespace ck {
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kRows = 128;               // rows of W a CTA
+constexpr int kStageK = 256;             // 128 bytes of codes a row
+constexpr int kABytes = kRows * kStageK / 2;
+
+template <int TN, bool NV>
+struct Cfg {
+    static constexpr int kWords = kStageK / fp4_word(NV);  // scale words of a stage
+    static constexpr int kSfBytes = kWords * 512;
+    static constexpr int kBBytes = TN * kStageK / 2;
+    static constexpr int kStageBytes = kABytes + kBBytes + 2 * kSfBytes;
+    static constexpr int kRedBytes = TN * kRows * 4;
+    // two CTAs an SM up to 16 tokens, else one
+    static constexpr int kStages = ((TN <= 16 ? 110 : 220) * 1024 - kRedBytes) / kStageBytes;
+    static constexpr int kTmemSf = TN < 32 ? 32 : TN;  // first column of the scales
+    static constexpr int kTmemCols = kTmemSf + 32 <= 64 ? 64 : (kTmemSf + 32 <= 128 ? 128 : 256);
+    static constexpr size_t kSmemBytes = static_cast<size_t>(kStages) * kStageBytes + kRedBytes + 256 + 1024;
+    static_assert(kStageBytes % 1024 == 0 && kStages >= 3, "stage");
+};
+
+struct Args {
+    const uint8_t *xs, *ws;
+    int M, N, K, words;  // words: scale words a row
+    float alpha;
+    const __nv_bfloat16 *bias, *residual;
+    __nv_bfloat16 *y;
+    bool weights_settled;
+    unsigned int *status;
+    unsigned long long timeout_ns;
+};
+
+template <int TN, bool NV>
+__global__ void __launch_bounds__(kThreads)
+fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                    const __grid_constant__ Args a) {
+    using C = Cfg<TN, NV>;
+    constexpr int kStages = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_s = smem_u32(smem_raw);
+    const uint32_t smem_s = (raw_s + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (smem_s - raw_s);
+    const uint32_t red_s = smem_s + kStages * C::kStageBytes;
+    const float *red = reinterpret_cast<const float *>(smem + kStages * C::kStageBytes);
+    const uint32_t bars_s = red_s + C::kRedBytes;
+    uint8_t *bars = smem + kStages * C::kStageBytes + C::kRedBytes;
+    auto full = [&](int s) { return bars_s + 8u * s; };
+    auto empty = [&](int s) { return bars_s + 8u * (kStages + s); };
+    const uint32_t done = bars_s + 8u * (2 * kStages);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 8 * (2 * kStages + 1));
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    // a stage: W codes, X codes, W scales, X scales
+    auto stage = [&](int s) { return smem_s + s * C::kStageBytes; };
+    constexpr int kOffB = kABytes, kOffSfa = kABytes + C::kBBytes, kOffSfb = kOffSfa + C::kSfBytes;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int splits = static_cast<int>(gridDim.x / ((a.N + kRows - 1) / kRows));
+    const int n_tile = blockIdx.x / splits;
+    const int n0 = n_tile * kRows, m0 = blockIdx.y * TN;
+    const int num_kb = (a.K + kStageK - 1) / kStageK;
+    const int kb0 = num_kb * rank / splits, kb1 = num_kb * (rank + 1) / splits;
+    const WaitCtl ctl{abort_flag, a.status, a.timeout_ns};
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    pdl_launch_dependents();
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        int issued = 0;
+        if (elect_one()) {
+            tma_prefetch_desc(&tm_w);
+            tma_prefetch_desc(&tm_x);
+            const uint8_t *ws = a.ws + (static_cast<int64_t>(n_tile) * a.words) * 512;
+            const uint8_t *xs = a.xs + (static_cast<int64_t>(m0 >> 7) * a.words) * 512;
+            auto sf_bytes = [&](int kb) {
+                const int left = a.words - kb * C::kWords;
+                return static_cast<uint32_t>((left < C::kWords ? left : C::kWords) * 512);
+            };
+            auto load_w = [&](int s, int kb) {
+                const uint32_t sf = sf_bytes(kb);
+                mbar_arrive_expect_tx(full(s), kABytes + C::kBBytes + 2 * sf);
+                tma_load_2d(stage(s), &tm_w, full(s), kb * (kStageK / 2), n0);
+                bulk_load_1d(stage(s) + kOffSfa, ws + static_cast<int64_t>(kb) * C::kSfBytes, sf, full(s));
+            };
+            auto load_x = [&](int s, int kb) {
+                tma_load_2d(stage(s) + kOffB, &tm_x, full(s), kb * (kStageK / 2), m0);
+                bulk_load_1d(stage(s) + kOffSfb, xs + static_cast<int64_t>(kb) * C::kSfBytes, sf_bytes(kb), full(s));
+            };
+            if (!a.weights_settled) pdl_wait();
+            const int pre = kb1 - kb0 < kStages ? kb1 - kb0 : kStages;
+            for (int i = 0; i < pre; ++i) load_w(i, kb0 + i);
+            if (a.weights_settled) pdl_wait();
+            for (int i = 0; i < pre; ++i) load_x(i, kb0 + i);
+            issued = pre;
+            for (int i = pre; i < kb1 - kb0; ++i) {
+                const int s = i % kStages;
+                if (!mbar_wait(empty(s), ((i / kStages) & 1) ^ 1, ctl)) break;
+                load_w(s, kb0 + i);
+                load_x(s, kb0 + i);
+                issued = i + 1;
+            }
+            if (*abort_flag) {
+                const int first = issued > kStages ? issued - kStages : 0;
+                for (int i = first; i < issued; ++i)
+                    mbar_wait_drain(full(i % kStages), (i / kStages) & 1, a.timeout_ns, a.status);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issue
+        const uint32_t sfa = tmem + C::kTmemSf, sfb = sfa + 16;
+        const uint32_t sfb_tile = sfb + ((m0 & 127) >> 5);  // this tile's tokens within their 128 rows of scales
+        if (elect_one()) {
+            bool ok = true;
+            for (int kb = kb0; kb < kb1 && ok; ++kb) {
+                const int i = kb - kb0, s = i % kStages;
+                ok = mbar_wait(full(s), (i / kStages) & 1, ctl);
+                if (!ok) break;
+                tc_fence_after_sync();
+                const uint64_t ad = sdesc_kmajor_sw128(stage(s)), bd = sdesc_kmajor_sw128(stage(s) + kOffB);
+                const int words = a.words - kb * C::kWords;
+#pragma unroll
+                for (int w = 0; w < C::kWords; ++w)
+                    if (w < words) {
+                        tmem_copy_scales(sfa + 4 * w, sdesc_scales(stage(s) + kOffSfa + 512 * w));
+                        tmem_copy_scales(sfb + 4 * w, sdesc_scales(stage(s) + kOffSfb + 512 * w));
+                    }
+                const int left = a.K - kb * kStageK;  // columns of K from here on
+#pragma unroll
+                for (int k = 0; k < kStageK / 64; ++k)
+                    if (64 * k < left) {
+                        const int w = NV ? k : k / 2;
+                        mma_fp4<NV>(tmem, ad + 2 * k, bd + 2 * k, idesc_fp4(kRows, TN, NV, NV ? 0 : k & 1),
+                                    sfa + 4 * w, sfb_tile + 4 * w, i > 0 || k > 0 ? 1u : 0u);
+                    }
+                mma_commit(empty(s));
+            }
+            mma_commit(done);
+            if (!ok) mbar_wait_drain(done, 0, a.timeout_ns, a.status);
+        }
+        __syncwarp();
+    }
+    // ---------------------------------------------------------------- epilogue
+    // Column c of the tile is finished by the CTA of rank c / own.
+    const int own = TN / splits;
+    cluster_sync();  // every CTA of the cluster has begun: its shared memory may be written
+    if (warp >= 2) {
+        const int q = warp & 3;
+        bool ok = mbar_wait(done, 0, ctl);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after_sync();
+        if (ok) {
+            const int r = q * 32 + lane;
+#pragma unroll
+            for (int c0 = 0; c0 < TN; c0 += (TN < 16 ? 8 : 16)) {
+                uint32_t v[16];
+                tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(q * 32) << 16) + c0, v);
+                tmem_wait_ld16(v);
+#pragma unroll
+                for (int j = 0; j < (TN < 16 ? 8 : 16); ++j) {
+                    const int c = c0 + j, owner = c / own;
+                    const uint32_t at = red_s + 4u * ((rank * own + c - owner * own) * kRows + r);
+                    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(mapa_shared(at, owner)), "r"(v[j]) : "memory");
+                }
+            }
+        }
+        tc_fence_before_sync();
+    }
+    cluster_sync();
+    if (warp >= 2 && !*abort_flag) {
+        const int t = threadIdx.x - 64;
+        const int n = n0 + 2 * (t & 63);
+        float b0 = 0.f, b1 = 0.f;
+        if (a.bias != nullptr && n < a.N) {
+            const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162 *>(a.bias + n);
+            b0 = __low2float(b), b1 = __high2float(b);
+        }
+        if (n < a.N) {
+            pdl_wait();  // the residual may come from the kernel ahead
+            for (int c = t >> 6; c < own; c += 2) {
+                const int m = m0 + rank * own + c;
+                if (m >= a.M) break;
+                float s0 = 0.f, s1 = 0.f;
+                for (int src = 0; src < splits; ++src) {
+                    const float2 p = *reinterpret_cast<const float2 *>(red + (src * own + c) * kRows + 2 * (t & 63));
+                    s0 += p.x, s1 += p.y;
+                }
+                const int64_t at = static_cast<int64_t>(m) * a.N + n;
+                float r0 = 0.f, r1 = 0.f;
+                if (a.residual != nullptr) {
+                    const __nv_bfloat162 r = *reinterpret_cast<const __nv_bfloat162 *>(a.residual + at);
+                    r0 = __low2float(r), r1 = __high2float(r);
+                }
+                *reinterpret_cast<__nv_bfloat162 *>(a.y + at) =
+                    __floats2bfloat162_rn(a.alpha * s0 + b0 + r0, a.alpha * s1 + b1 + r1);
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+template <int TN, bool NV>
+cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx) {
+    using C = Cfg<TN, NV>;
+    CUtensorMap mw, mx;
+    const int row_bytes = static_cast<int>(g.K / 2);
+    if (!tensor_map_2d(&mw, g.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.N, row_bytes, kStageK / 2, kRows,
+                       CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !tensor_map_2d(&mx, g.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.M, row_bytes, kStageK / 2, TN,
+                       CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    auto kern = fp4_gemm_few_kernel<TN, NV>;
+    if (cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), static_cast<int>(C::kSmemBytes));
+        e != cudaSuccess)
+        return e;
+    const int sms = sm_count();
+    if (sms < 1) return cudaErrorInvalidDevice;
+    const int64_t n_tiles = (g.N + kRows - 1) / kRows, m_tiles = (g.M + TN - 1) / TN;
+    const int64_t num_kb = (g.K + kStageK - 1) / kStageK;
+    if (m_tiles > 65535) return cudaErrorInvalidValue;
+    int splits = 1;
+    while (splits < 8 && n_tiles * m_tiles * splits * 2 <= 2 * sms && splits * 2 <= num_kb) splits *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(n_tiles * splits), static_cast<unsigned>(m_tiles));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = ctx.stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ctx.pdl ? 2 : 1;
+    Args a = {};
+    a.xs = g.xs, a.ws = g.ws;
+    a.M = static_cast<int>(g.M), a.N = static_cast<int>(g.N), a.K = static_cast<int>(g.K);
+    a.words = static_cast<int>(fp4_words(g.K, g.nv));
+    a.alpha = g.alpha;
+    a.bias = static_cast<const __nv_bfloat16 *>(g.bias), a.residual = static_cast<const __nv_bfloat16 *>(g.residual);
+    a.y = static_cast<__nv_bfloat16 *>(g.y);
+    a.weights_settled = g.weights_settled;
+    a.status = ctx.status, a.timeout_ns = ctx.timeout_ns;
+    return cudaLaunchKernelEx(&cfg, kern, mw, mx, a);
+}
+
+template <bool NV>
+cudaError_t launch_n(const Fp4Gemm &g, const LaunchCtx &ctx) {
+    if (g.M <= 8) return launch_t<8, NV>(g, ctx);
+    if (g.M <= 16) return launch_t<16, NV>(g, ctx);
+    if (g.M <= 32) return launch_t<32, NV>(g, ctx);
+    return launch_t<64, NV>(g, ctx);
+}
+
+}  // namespace
+
+cudaError_t launch_fp4_gemm_few(const Fp4Gemm &g, const LaunchCtx &ctx) {
+    return g.nv ? launch_n<true>(g, ctx) : launch_n<false>(g, ctx);
+}
+
+cudaError_t launch_fp4_gemm(const Fp4Gemm &g, const LaunchCtx &ctx) { return launch_fp4_gemm_few(g, ctx); }
+
+}  // namespace ck

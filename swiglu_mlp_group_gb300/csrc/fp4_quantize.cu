@@ -1,0 +1,137 @@
+// fp4_quantize.cu -- bf16 (or f32) rows to microscaled 4-bit floats, and the
+// block scales of a checkpoint into the tiles that the tensor cores read.
+#include <cuda_bf16.h>
+
+#include "fp4_core.cuh"
+#include "launch_util.h"
+#include "quant_core.cuh"
+
+namespace ck {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRowsPerWarp = 4;
+
+// Read once, written once: 2 bytes in and 0.56 (NV) or 0.53 (MX) out an element.
+// A lane has 8 columns, 16 bytes to load and 4 to store, so that a warp's load is
+// 512 bytes in a row; a warp takes 256 columns of 4 rows, whose loads are on
+// their way together and whose scale words lie next to each other.
+enum class In : int { kBf16, kF32, kSwiglu };
+
+template <bool NV, In IN>
+__global__ void __launch_bounds__(kThreads)
+fp4_quantize_kernel(const void *__restrict__ x, int64_t M, int K, int64_t ldx, fp4::Scale t,
+                    uint8_t *__restrict__ codes, uint8_t *__restrict__ scales, bool early_trigger) {
+    if (early_trigger) pdl_launch_dependents();
+    pdl_wait();
+    if (!early_trigger) pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int segs = (K + 255) / 256;
+    const int words = static_cast<int>(fp4_words(K, NV));
+    const int64_t task = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t row0 = task / segs * kRowsPerWarp;
+    const int col = static_cast<int>(task % segs) * 256 + lane * 8;
+    if (row0 >= M) return;
+    const bool in = col < K;
+    uint4 a[kRowsPerWarp], b[kRowsPerWarp];
+#pragma unroll
+    for (int i = 0; i < kRowsPerWarp; ++i) {
+        a[i] = b[i] = make_uint4(0, 0, 0, 0);
+        if (!in || row0 + i >= M) continue;
+        if constexpr (IN == In::kF32) {
+            const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(x) + (row0 + i) * ldx + col);
+            a[i] = __ldg(p), b[i] = __ldg(p + 1);
+        } else {
+            const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(x) + (row0 + i) * ldx + col;
+            a[i] = __ldg(reinterpret_cast<const uint4 *>(p));
+            if constexpr (IN == In::kSwiglu) b[i] = __ldg(reinterpret_cast<const uint4 *>(p + K));
+        }
+    }
+    const int group = NV ? 8 : 16;  // lanes of a word
+#pragma unroll
+    for (int i = 0; i < kRowsPerWarp; ++i) {
+        if (row0 + i >= M) break;
+        const uint32_t ra[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, rb[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+        uint64_t v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (IN == In::kF32) {
+                const uint32_t *r = j < 2 ? ra : rb;
+                v[j] = f32x2(__uint_as_float(r[2 * (j & 1)]), __uint_as_float(r[2 * (j & 1) + 1]));
+            } else {
+                const float lo = __uint_as_float(ra[j] << 16), hi = __uint_as_float(ra[j] & 0xffff0000u);
+                if constexpr (IN == In::kSwiglu)
+                    v[j] = f32x2(qc::silu_mul(lo, __uint_as_float(rb[j] << 16)),
+                                 qc::silu_mul(hi, __uint_as_float(rb[j] & 0xffff0000u)));
+                else
+                    v[j] = f32x2(lo, hi);
+            }
+        }
+        uint32_t scale;
+        const uint32_t q = fp4::quantize8<NV>(v, t, scale);
+        const uint32_t word = fp4::scale_word<NV>(in ? scale : 0u, lane);
+        if (in) {
+            *reinterpret_cast<uint32_t *>(codes + (row0 + i) * (K / 2) + col / 2) = q;
+            if (lane % group == 0)
+                *reinterpret_cast<uint32_t *>(scales + fp4::scale_word_at(row0 + i, col / (8 * group), words)) = word;
+        }
+    }
+}
+
+// One word a thread.
+__global__ void __launch_bounds__(kThreads)
+fp4_tile_scales_kernel(const uint8_t *__restrict__ in, int64_t rows, int words, int blocks, uint8_t *__restrict__ out) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    const int64_t row = i / words;
+    if (row >= rows) return;
+    const int word = static_cast<int>(i - row * words);
+    uint32_t w = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (4 * word + j < blocks) w |= static_cast<uint32_t>(in[row * blocks + 4 * word + j]) << (8 * j);
+    *reinterpret_cast<uint32_t *>(out + fp4::scale_word_at(row, word, words)) = w;
+}
+
+template <typename... A, typename... B>
+cudaError_t launch(void (*kernel)(A...), int64_t blocks, const LaunchCtx &ctx, B... args) {
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = ctx.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ctx.pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace
+
+cudaError_t launch_fp4_quantize(const void *x, bool x_f32, Act act, int64_t M, int64_t K, int64_t ldx, bool nv,
+                                float tensor_scale, uint8_t *codes, uint8_t *scales, const LaunchCtx &ctx) {
+    using Kernel = void (*)(const void *, int64_t, int, int64_t, fp4::Scale, uint8_t *, uint8_t *, bool);
+    static const Kernel kernels[2][3] = {
+        {fp4_quantize_kernel<false, In::kBf16>, fp4_quantize_kernel<false, In::kF32>,
+         fp4_quantize_kernel<false, In::kSwiglu>},
+        {fp4_quantize_kernel<true, In::kBf16>, fp4_quantize_kernel<true, In::kF32>,
+         fp4_quantize_kernel<true, In::kSwiglu>}};
+    const In in = x_f32 ? In::kF32 : act == Act::kSwiglu ? In::kSwiglu : In::kBf16;
+    const int64_t tasks = (M + kRowsPerWarp - 1) / kRowsPerWarp * ((K + 255) / 256);
+    constexpr int kWarps = kThreads / 32;
+    return launch(kernels[nv ? 1 : 0][static_cast<int>(in)], (tasks + kWarps - 1) / kWarps, ctx, x, M,
+                  static_cast<int>(K), ldx, fp4::Scale{tensor_scale, 6.f * tensor_scale}, codes, scales,
+                  ctx.early_trigger);
+}
+
+cudaError_t launch_fp4_tile_scales(const uint8_t *scales, int64_t rows, int64_t K, bool nv, uint8_t *tiled,
+                                   const LaunchCtx &ctx) {
+    const int words = static_cast<int>(fp4_words(K, nv));
+    return launch(fp4_tile_scales_kernel, (rows * words + kThreads - 1) / kThreads, ctx, scales, rows, words,
+                  static_cast<int>(K / fp4_block(nv)), tiled);
+}
+
+}  // namespace ck

@@ -389,6 +389,55 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
         : "memory");
 }
 
+// ---------------------------------------------------------------------------
+// tcgen05 on microscaled 4-bit floats (E2M1 codes, a scale for each block of K)
+// ---------------------------------------------------------------------------
+// Shared-memory matrix descriptor of a 512-byte tile of block scales (32 rows
+// of 16 bytes, no swizzle): 8-row core matrices of 128 bytes one after another.
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(128 >> 4) << 32 |
+           static_cast<uint64_t>(1) << 46;
+}
+
+// Such a tile into four TMEM columns, the same in each quarter of the lanes.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t sdesc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+// Instruction descriptor of the block-scaled kinds with E2M1 A and B (both
+// K-major), shape M x N (x K = 64): NV takes four E4M3 scales a row (one word),
+// MX two E8M0 ones, the lower (half 0) or upper (half 1) two of a word.
+__host__ __device__ constexpr uint32_t idesc_fp4(int M, int N, bool nv, int half) {
+    return (1u << 7) | (1u << 10)                    // A, B format: E2M1
+           | (static_cast<uint32_t>(2 * half) << 4)  // which scale of a word is B's first
+           | (static_cast<uint32_t>(N >> 3) << 17)   // N / 8
+           | (nv ? 0u : 1u << 23)                    // scales: E4M3 or E8M0
+           | (static_cast<uint32_t>(M >> 7) << 27)   // M / 128
+           | (static_cast<uint32_t>(2 * half) << 29);  // which is A's first
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T with the block scales of both in TMEM.
+template <bool NV>
+__device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    if constexpr (NV)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+                d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+                d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+}
+
 // CTA-pair variants: the allocation spans both CTAs of the pair (one warp of
 // each CTA issues it), the MMA is issued by one thread of the even CTA and
 // reads A and B halves from both CTAs' shared memory, and the commit arrives
