@@ -42,8 +42,9 @@ struct Fp4Gemm {
     bool weights_settled;
 };
 cudaError_t launch_fp4_gemm(const Fp4Gemm &g, const LaunchCtx &ctx);
-// its kernel for few tokens
+// its kernels for few tokens and for many
 cudaError_t launch_fp4_gemm_few(const Fp4Gemm &g, const LaunchCtx &ctx);
+cudaError_t launch_fp4_gemm_pair(const Fp4Gemm &g, const LaunchCtx &ctx);
 
 enum class Norm : int { kRms = 0, kLayer = 1 };
 

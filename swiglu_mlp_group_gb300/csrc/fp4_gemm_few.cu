@@ -169,7 +169,7 @@ fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
                 for (int k = 0; k < kStageK / 64; ++k)
                     if (64 * k < left) {
                         const int w = NV ? k : k / 2;
-                        mma_fp4<NV>(tmem, ad + 2 * k, bd + 2 * k, idesc_fp4(kRows, TN, NV, NV ? 0 : k & 1),
+                        mma_fp4<NV, false>(tmem, ad + 2 * k, bd + 2 * k, idesc_fp4(kRows, TN, NV, NV ? 0 : k & 1),
                                     sfa + 4 * w, sfb_tile + 4 * w, i > 0 || k > 0 ? 1u : 0u);
                     }
                 mma_commit(empty(s));
@@ -303,6 +303,8 @@ cudaError_t launch_fp4_gemm_few(const Fp4Gemm &g, const LaunchCtx &ctx) {
     return g.nv ? launch_n<true>(g, ctx) : launch_n<false>(g, ctx);
 }
 
-cudaError_t launch_fp4_gemm(const Fp4Gemm &g, const LaunchCtx &ctx) { return launch_fp4_gemm_few(g, ctx); }
+cudaError_t launch_fp4_gemm(const Fp4Gemm &g, const LaunchCtx &ctx) {
+    return g.M > 128 ? launch_fp4_gemm_pair(g, ctx) : launch_fp4_gemm_few(g, ctx);
+}
 
 }  // namespace ck

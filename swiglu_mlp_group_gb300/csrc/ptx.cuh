@@ -399,9 +399,13 @@ __device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
            static_cast<uint64_t>(1) << 46;
 }
 
-// Such a tile into four TMEM columns, the same in each quarter of the lanes.
+// Such a tile into four TMEM columns, the same in each quarter of the lanes (of a
+// pair: in each CTA its own tile).
 __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t sdesc) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint64_t sdesc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 
 // Instruction descriptor of the block-scaled kinds with E2M1 A and B (both
@@ -416,26 +420,26 @@ __host__ __device__ constexpr uint32_t idesc_fp4(int M, int N, bool nv, int half
            | (static_cast<uint32_t>(2 * half) << 29);  // which is A's first
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T with the block scales of both in TMEM.
-template <bool NV>
+// D[tmem] (+)= A[smem] * B[smem]^T with the block scales of both in TMEM; PAIR:
+// by a CTA pair, each CTA holding the scales of its rows of A and of all of B.
+template <bool NV, bool PAIR>
 __device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                         uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-    if constexpr (NV)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-                d_tmem),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-            : "memory");
+#define CK_MMA_FP4(FORM)                                                                                   \
+    asm volatile("{\n\t.reg .pred p;\n\t"                                                                 \
+                 "setp.ne.b32 p, %6, 0;\n\t"                                                               \
+                 "tcgen05.mma." FORM " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),               \
+                 "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)                   \
+                 : "memory")
+    if constexpr (NV && PAIR)
+        CK_MMA_FP4("cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X");
+    else if constexpr (NV)
+        CK_MMA_FP4("cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X");
+    else if constexpr (PAIR)
+        CK_MMA_FP4("cta_group::2.kind::mxf4.block_scale.scale_vec::2X");
     else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-                d_tmem),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-            : "memory");
+        CK_MMA_FP4("cta_group::1.kind::mxf4.block_scale.scale_vec::2X");
+#undef CK_MMA_FP4
 }
 
 // CTA-pair variants: the allocation spans both CTAs of the pair (one warp of
