@@ -529,13 +529,13 @@ def _new(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _new_on(shape, device, stream):
-    """_new of bytes on a device."""
+def _new_on(shape, dtype, device, stream):
+    """_new on a device (its index will do)."""
     torch = _torch()
     if stream is None:
-        return torch.empty(shape, dtype=torch.uint8, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=torch.uint8, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _rotation(cos_sin, positions, T: int, mode: str, dev: int):
@@ -734,12 +734,13 @@ def _row_stride(x, dtype, what: str, dev: int, shape=None) -> int:
     """Elements from one row of x (2-D, of this type and shape, on the call's device) to the next."""
     if x.dtype is not dtype or x.get_device() != dev:
         raise ValueError(f"{what} must be a tensor of {dtype} on cuda:{dev}")
-    if x.dim() != 2 or (shape is not None and x.shape != shape):
+    xs = x.shape
+    if len(xs) != 2 or (shape is not None and xs != shape):
         raise ValueError(f"{what} must have shape {tuple(shape) if shape is not None else '[rows, columns]'}")
-    st = x.stride()
-    if st[1] != 1 and x.shape[1] > 1:
+    ld, inner = x.stride()
+    if inner != 1 and xs[1] > 1:
         raise ValueError(f"{what}: the elements of a row must lie next to each other")
-    return st[0] if x.shape[0] > 1 else x.shape[1]
+    return ld if xs[0] > 1 else xs[1]
 
 
 def _fp4_format(fmt: str) -> int:
@@ -756,32 +757,42 @@ def _act(act: str) -> int:
     return a
 
 
-def _tiled_bytes(f: int, rows: int, K: int, where: str) -> int:
-    n = int(lib().ck_fp4_scale_bytes(f, rows, K))
-    if n == 0:
-        raise CkError(CK_ERR_SHAPE, where)
-    return n
+def _tiled_bytes(f: int, rows: int, K: int) -> int:
+    """ck_fp4_scale_bytes, without its refusals (a call's own come before a tensor is used)."""
+    return (rows + 127) // 128 * ((K + 63) // 64 if f == CK_FP4_NV else (K + 127) // 128) * 512
 
 
 def _fp4_operand(codes, scales, f: int, what: str, dev: int):
     """(rows, K, pointers) of codes [rows, K / 2] and their tiled scales."""
     u8 = _torch().uint8
-    if codes.dim() != 2:
-        raise ValueError(f"{what} must be codes [rows, K / 2]")
     p, ps = _typed(codes, u8, what, dev), _typed(scales, u8, f"{what}'s scales", dev)
-    rows, K = codes.shape[0], 2 * codes.shape[1]
-    if scales.numel() < _tiled_bytes(f, rows, K, what):
+    shape = codes.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what} must be codes [rows, K / 2]")
+    rows, K = shape[0], 2 * shape[1]
+    if scales.nbytes < _tiled_bytes(f, rows, K):
         raise ValueError(f"{what}'s scales must be tiled scales of these codes")
     return rows, K, p, ps
 
 
-def _out_rows(out, M: int, N: int, dev: int, like, stream):
+def _out_rows(out, M: int, N: int, dev: int, stream):
     """A linear's output: the one given (contiguous bf16 [M, N]) or a new one."""
-    bf16 = _torch().bfloat16
+    torch = _torch()
     if out is None:
-        return _new((M, N), bf16, like, stream)
-    _typed(out, bf16, "out", dev, (M, N))
+        return _new_on((M, N), torch.bfloat16, dev, stream)
+    _typed(out, torch.bfloat16, "out", dev, (M, N))
     return out
+
+
+def _scales_out(scales, n: int, dev: int, stream):
+    """Tiled scales to write: the tensor given, if it is large enough, or a new one."""
+    u8 = _torch().uint8
+    if scales is None:
+        return _new_on((n,), u8, dev, stream)
+    _typed(scales, u8, "scales", dev)
+    if scales.nbytes < n:
+        raise ValueError(f"scales must hold {n} bytes")
+    return scales
 
 
 def fp4_quantize(x, fmt: str, scale: float = 1.0, act: str = "none", codes=None, scales=None, stream=None):
@@ -797,16 +808,15 @@ def fp4_quantize(x, fmt: str, scale: float = 1.0, act: str = "none", codes=None,
     M, K = x.shape
     if a == CK_ACT_SWIGLU:
         K //= 2
-    n = _tiled_bytes(f, M, K, "ck_fp4_quantize")
+    n = int(lib().ck_fp4_scale_bytes(f, M, K))
+    if n == 0:
+        raise CkError(CK_ERR_SHAPE, "ck_fp4_quantize")
     if codes is None:
-        codes = _new((M, K // 2), torch.uint8, x, stream)
-    if scales is None:
-        scales = _new((n,), torch.uint8, x, stream)
-    elif scales.numel() < n:
-        raise ValueError(f"scales must hold {n} bytes")
+        codes = _new_on((M, K // 2), torch.uint8, dev, stream)
+    scales = _scales_out(scales, n, dev, stream)
     st = lib().ck_fp4_quantize(x.data_ptr(), CK_F32 if f32 else CK_BF16, M, K, ldx, a, f, scale,
-                               _typed(codes, torch.uint8, "codes", dev, (M, K // 2)),
-                               _typed(scales, torch.uint8, "scales", dev), _run_stream(stream, dev))
+                               _typed(codes, torch.uint8, "codes", dev, (M, K // 2)), scales.data_ptr(),
+                               _run_stream(stream, dev))
     if st != CK_OK:
         raise CkError(st, "ck_fp4_quantize")
     return codes, scales
@@ -821,7 +831,10 @@ def fp4_tile_scales(scales, fmt: str, stream=None):
     if scales.dim() != 2:
         raise ValueError("scales must be [rows, blocks]")
     rows, K = scales.shape[0], scales.shape[1] * (32 if f == CK_FP4_MX else 16)
-    out = _new((_tiled_bytes(f, rows, K, "ck_fp4_tile_scales"),), torch.uint8, scales, stream)
+    n = int(lib().ck_fp4_scale_bytes(f, rows, K))
+    if n == 0:
+        raise CkError(CK_ERR_SHAPE, "ck_fp4_tile_scales")
+    out = _new_on((n,), torch.uint8, dev, stream)
     st = lib().ck_fp4_tile_scales(p, rows, K, f, out.data_ptr(), _run_stream(stream, dev))
     if st != CK_OK:
         raise CkError(st, "ck_fp4_tile_scales")
@@ -833,15 +846,15 @@ def fp4_gemm(codes, scales, W, w_scales, fmt: str, alpha: float = 1.0, bias=None
     """y = bf16(alpha X W^T + bias + residual) -> bf16 [M, N], X of codes [M, K / 2] and W of [N, K / 2] with
     tiled scales (fp4_quantize, block_norm_fp4, fp4_tile_scales).  residual may be out."""
     f = _fp4_format(fmt)
-    bf16 = _torch().bfloat16
     dev = _call_device(codes, "codes")
     M, K, px, pxs = _fp4_operand(codes, scales, f, "codes", dev)
     N, Kw, pw, pws = _fp4_operand(W, w_scales, f, "W", dev)
     if Kw != K:
         raise ValueError("codes and W must have the same columns")
-    y = _out_rows(out, M, N, dev, codes, stream)
-    st = lib().ck_fp4_gemm(px, pxs, M, K, f, pw, pws, N, alpha, _typed(bias, bf16, "bias", dev, (N,)),
-                           _typed(residual, bf16, "residual", dev, (M, N)), y.data_ptr(), _run_stream(stream, dev))
+    bf16 = _torch().bfloat16
+    pb, pr = _typed(bias, bf16, "bias", dev, (N,)), _typed(residual, bf16, "residual", dev, (M, N))
+    y = _out_rows(out, M, N, dev, stream)
+    st = lib().ck_fp4_gemm(px, pxs, M, K, f, pw, pws, N, alpha, pb, pr, y.data_ptr(), _run_stream(stream, dev))
     if st != CK_OK:
         raise CkError(st, "ck_fp4_gemm")
     return y
@@ -850,7 +863,7 @@ def fp4_gemm(codes, scales, W, w_scales, fmt: str, alpha: float = 1.0, bias=None
 def fp4_linear_workspace(M: int, K: int, fmt: str, device="cuda", stream=None):
     """A workspace for fp4_linear calls of M tokens and K columns."""
     n = int(lib().ck_fp4_linear_workspace_bytes(M, K, _fp4_format(fmt)))
-    return _new_on((max(n, 16),), device, stream)
+    return _new_on((max(n, 16),), _torch().uint8, device, stream)
 
 
 def fp4_linear(x, W, w_scales, fmt: str, x_scale: float = 1.0, w_scale: float = 1.0, bias=None, act: str = "none",
@@ -868,12 +881,11 @@ def fp4_linear(x, W, w_scales, fmt: str, x_scale: float = 1.0, w_scale: float = 
     N, Kw, pw, pws = _fp4_operand(W, w_scales, f, "W", dev)
     if Kw != K:
         raise ValueError("x and W must have the same columns")
-    y = _out_rows(out, M, N, dev, x, stream)
-    ws = (_given_workspace(workspace, dev) if workspace is not None else
-          fp4_linear_workspace(M, K, fmt, x.device, stream))
-    st = lib().ck_fp4_linear(x.data_ptr(), M, K, ldx, a, f, x_scale, pw, pws, w_scale, N,
-                             _typed(bias, bf16, "bias", dev, (N,)), _typed(residual, bf16, "residual", dev, (M, N)),
-                             y.data_ptr(), ws.data_ptr(), ws.nbytes, _run_stream(stream, dev))
+    pb, pr = _typed(bias, bf16, "bias", dev, (N,)), _typed(residual, bf16, "residual", dev, (M, N))
+    y = _out_rows(out, M, N, dev, stream)
+    ws = (_given_workspace(workspace, dev) if workspace is not None else fp4_linear_workspace(M, K, fmt, dev, stream))
+    st = lib().ck_fp4_linear(x.data_ptr(), M, K, ldx, a, f, x_scale, pw, pws, w_scale, N, pb, pr, y.data_ptr(),
+                             ws.data_ptr(), ws.nbytes, _run_stream(stream, dev))
     if st != CK_OK:
         raise CkError(st, "ck_fp4_linear")
     return y
@@ -882,7 +894,7 @@ def fp4_linear(x, W, w_scales, fmt: str, x_scale: float = 1.0, w_scale: float = 
 def fp4_swiglu_mlp_workspace(M: int, H: int, I: int, fmt: str, device="cuda", stream=None):
     """A workspace for fp4_swiglu_mlp calls of these sizes."""
     n = int(lib().ck_fp4_swiglu_mlp_workspace_bytes(M, H, I, _fp4_format(fmt)))
-    return _new_on((max(n, 16),), device, stream)
+    return _new_on((max(n, 16),), _torch().uint8, device, stream)
 
 
 def fp4_swiglu_mlp(x, Wgu, gu_scales, Wd, d_scales, fmt: str, x_scale: float = 1.0, gate_up_scale: float = 1.0,
@@ -894,19 +906,19 @@ def fp4_swiglu_mlp(x, Wgu, gu_scales, Wd, d_scales, fmt: str, x_scale: float = 1
     bf16 = _torch().bfloat16
     f = _fp4_format(fmt)
     dev = _call_device(x, "x")
-    M, H = x.shape
     px = _typed(x, bf16, "x", dev)
+    M, H = x.shape
     N, Kw, pgu, pgus = _fp4_operand(Wgu, gu_scales, f, "Wgu", dev)
     Nd, I, pd, pds = _fp4_operand(Wd, d_scales, f, "Wd", dev)
     if Kw != H or Nd != H or N != 2 * I:
         raise ValueError("Wgu must be [2I, H / 2] and Wd [H, I / 2] of x's H columns")
-    y = _out_rows(out, M, H, dev, x, stream)
+    pbgu, pbd = _typed(bgu, bf16, "bgu", dev, (N,)), _typed(bd, bf16, "bd", dev, (H,))
+    pr = _typed(residual, bf16, "residual", dev, (M, H))
+    y = _out_rows(out, M, H, dev, stream)
     ws = (_given_workspace(workspace, dev) if workspace is not None else
-          fp4_swiglu_mlp_workspace(M, H, I, fmt, x.device, stream))
-    st = lib().ck_fp4_swiglu_mlp(px, M, H, I, f, x_scale, pgu, pgus, gate_up_scale, _typed(bgu, bf16, "bgu", dev, (N,)),
-                                 act_scale, pd, pds, down_scale, _typed(bd, bf16, "bd", dev, (H,)),
-                                 _typed(residual, bf16, "residual", dev, (M, H)), y.data_ptr(), ws.data_ptr(),
-                                 ws.nbytes, _run_stream(stream, dev))
+          fp4_swiglu_mlp_workspace(M, H, I, fmt, dev, stream))
+    st = lib().ck_fp4_swiglu_mlp(px, M, H, I, f, x_scale, pgu, pgus, gate_up_scale, pbgu, act_scale, pd, pds,
+                                 down_scale, pbd, pr, y.data_ptr(), ws.data_ptr(), ws.nbytes, _run_stream(stream, dev))
     if st != CK_OK:
         raise CkError(st, "ck_fp4_swiglu_mlp")
     return y
@@ -915,38 +927,46 @@ def fp4_swiglu_mlp(x, Wgu, gu_scales, Wd, d_scales, fmt: str, x_scale: float = 1
 def _norm_call(x, branch, post_weight, gate, scale, shift, tokens_per_group, x_factor, branch_factor, norm, weight,
                bias, eps, h_out, stream):
     """What block_norm and block_norm_fp4 share -> (C arguments up to h_out's, h, device)."""
-    bf16 = _torch().bfloat16
+    torch = _torch()
+    bf16 = torch.bfloat16
     dev = _call_device(x, "x")
-    shape = x.shape
     ldx = _row_stride(x, bf16, "x", dev)
+    shape = x.shape
     T, H = shape
-    ldb = 0 if branch is None else _row_stride(branch, bf16, "branch", dev, shape)
     kind = _NORMS.get(norm)
     if kind is None:
         raise ValueError("norm must be 'rms' or 'layer'")
-    groups = -(-T // tokens_per_group) if tokens_per_group > 0 else 1
-    ldm = None
-    for t, what in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
-        if t is None:
-            continue
-        if t.dim() != 2 or t.shape[0] < groups or t.shape[1] != H:
-            raise ValueError(f"{what} must have a row of {H} for each of {groups} groups")
-        ld = _row_stride(t, bf16, what, dev)
-        if groups > 1:
-            if ldm is not None and ld != ldm:
-                raise ValueError("gate, scale and shift must have their rows at one stride")
-            ldm = ld
+    pb = pg = psc = psh = ph = None
+    ldb = ldh = 0
+    ldm = H
+    if branch is not None:
+        pb, ldb = branch.data_ptr(), _row_stride(branch, bf16, "branch", dev, shape)
+    if gate is not None or scale is not None or shift is not None:
+        groups = -(-T // tokens_per_group) if tokens_per_group > 0 else 1
+        rows = set()
+        for t, what in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
+            if t is None:
+                continue
+            ld = _row_stride(t, bf16, what, dev)
+            if t.shape[0] < groups or t.shape[1] != H:
+                raise ValueError(f"{what} must have a row of {H} for each of {groups} groups")
+            rows.add(ld if groups > 1 else H)
+        if len(rows) > 1:
+            raise ValueError("gate, scale and shift must have their rows at one stride")
+        ldm = rows.pop()
+        pg, psc, psh = _ptr(gate), _ptr(scale), _ptr(shift)
     dt, wdt = _weight_type(post_weight, weight, bias)
-    if h_out is None:
-        # without a branch and a factor the stream itself is h
-        h_out, ldh = (_new((T, H), bf16, x, stream), H) if branch is not None or x_factor != 1.0 else (None, 0)
+    pp, pw, pbias = (None if w is None else _typed(w, dt, what, dev, (H,))
+                     for w, what in ((post_weight, "post_weight"), (weight, "weight"), (bias, "bias")))
+    if h_out is not None:
+        ph, ldh = h_out.data_ptr(), _row_stride(h_out, bf16, "h_out", dev, shape)
+    elif branch is not None or x_factor != 1.0:
+        h_out, ldh = _new_on(shape, bf16, dev, stream), H
+        ph = h_out.data_ptr()
     else:
-        ldh = _row_stride(h_out, bf16, "h_out", dev, shape)
-    args = (x.data_ptr(), ldx, _ptr(branch), ldb, T, H, _norm_weight(post_weight, H, "post_weight", dt, dev),
-            _ptr(gate), _ptr(scale), _ptr(shift), ldm or H, tokens_per_group, x_factor, branch_factor, kind,
-            _norm_weight(weight, H, "weight", dt, dev), _norm_weight(bias, H, "bias", dt, dev), wdt, eps,
-            _ptr(h_out), ldh)
-    return args, x if h_out is None else h_out, dev
+        h_out = x  # without a branch and a factor the stream itself is h
+    return (x.data_ptr(), ldx, pb, ldb, T, H, pp, pg, psc, psh, ldm, tokens_per_group, x_factor, branch_factor, kind,
+            pw, pbias, wdt, eps, ph, ldh), h_out, dev
 
 
 def block_norm(x, branch=None, post_weight=None, gate=None, x_factor: float = 1.0, branch_factor: float = 1.0,
@@ -961,7 +981,8 @@ def block_norm(x, branch=None, post_weight=None, gate=None, x_factor: float = 1.
     args, h, dev = _norm_call(x, branch, post_weight, gate, scale, shift, tokens_per_group, x_factor, branch_factor,
                               norm, weight, bias, eps, h_out, stream)
     if n_out is None:
-        n_out, ldn = _new(x.shape, x.dtype, x, stream), x.shape[1]
+        shape = x.shape
+        n_out, ldn = _new_on(shape, x.dtype, dev, stream), shape[1]
     else:
         ldn = _row_stride(n_out, x.dtype, "n_out", dev, x.shape)
     st = lib().ck_block_norm(*args, n_out.data_ptr(), ldn, _run_stream(stream, dev))
@@ -977,18 +998,16 @@ def block_norm_fp4(x, branch=None, fmt: str = "nv", n_scale: float = 1.0, post_w
     """block_norm whose n is quantized as by fp4_quantize (tensor scale n_scale) -> (h, codes, tiled scales)."""
     u8 = _torch().uint8
     f = _fp4_format(fmt)
-    T, H = x.shape
-    nbytes = _tiled_bytes(f, T, H, "ck_block_norm_fp4")
     args, h, dev = _norm_call(x, branch, post_weight, gate, scale, shift, tokens_per_group, x_factor, branch_factor,
                               norm, weight, bias, eps, h_out, stream)
+    T, H = args[4], args[5]
+    if H % 32 != 0:
+        raise CkError(CK_ERR_SHAPE, "ck_block_norm_fp4")
     if codes is None:
-        codes = _new((T, H // 2), u8, x, stream)
-    if scales is None:
-        scales = _new((nbytes,), u8, x, stream)
-    elif scales.numel() < nbytes:
-        raise ValueError(f"scales must hold {nbytes} bytes")
-    st = lib().ck_block_norm_fp4(*args, f, n_scale, _typed(codes, u8, "codes", dev, (T, H // 2)),
-                                 _typed(scales, u8, "scales", dev), _run_stream(stream, dev))
+        codes = _new_on((T, H // 2), u8, dev, stream)
+    scales = _scales_out(scales, _tiled_bytes(f, T, H), dev, stream)
+    st = lib().ck_block_norm_fp4(*args, f, n_scale, _typed(codes, u8, "codes", dev, (T, H // 2)), scales.data_ptr(),
+                                 _run_stream(stream, dev))
     if st != CK_OK:
         raise CkError(st, "ck_block_norm_fp4")
     return h, codes, scales

@@ -30,10 +30,17 @@ cudaError_t launch_fp4_tile_scales(const uint8_t *scales, int64_t rows, int64_t 
                                    const LaunchCtx &ctx);
 
 // y bf16 [M, N] = bf16(alpha * X W^T + bias[n] + residual[m, n]).  X: codes [M, K / 2]
-// and tiled scales, W: [N, K / 2] likewise.  weights_settled: nothing in flight
-// writes W or its scales once the kernel has been let in.
+// and tiled scales; or (few tokens) bf16 x [M, ldx] that the kernel quantizes with
+// tensor scale x_scale (swiglu: of [gate | up]).  W: [N, K / 2] codes and tiled
+// scales.  weights_settled: nothing in flight writes W or its scales once the kernel
+// has been let in.
 struct Fp4Gemm {
-    const uint8_t *x, *xs, *w, *ws;
+    const uint8_t *x, *xs;
+    const void *x_bf16;
+    int64_t ldx;
+    bool swiglu;
+    float x_scale;
+    const uint8_t *w, *ws;
     int64_t M, N, K;
     bool nv;
     float alpha;
@@ -42,6 +49,8 @@ struct Fp4Gemm {
     bool weights_settled;
 };
 cudaError_t launch_fp4_gemm(const Fp4Gemm &g, const LaunchCtx &ctx);
+// Most tokens that a product quantizes itself.
+constexpr int64_t kFp4QuantizeInside = 16;
 // its kernels for few tokens and for many
 cudaError_t launch_fp4_gemm_few(const Fp4Gemm &g, const LaunchCtx &ctx);
 cudaError_t launch_fp4_gemm_pair(const Fp4Gemm &g, const LaunchCtx &ctx);

@@ -77,7 +77,7 @@ ck_status check_rows(const void *x, int64_t M, int64_t K, int64_t ldx, ck_input_
 
 ck::Fp4Gemm gemm(const uint8_t *x, const uint8_t *xs, int64_t M, int64_t K, bool nv, const void *W, const void *ws,
                  int64_t N, float alpha, const void *bias, const void *residual, void *y, bool settled) {
-    ck::Fp4Gemm g;
+    ck::Fp4Gemm g = {};
     g.x = x, g.xs = xs, g.w = static_cast<const uint8_t *>(W), g.ws = static_cast<const uint8_t *>(ws);
     g.M = M, g.N = N, g.K = K, g.nv = nv, g.alpha = alpha;
     g.bias = bias, g.residual = residual, g.y = y;
@@ -85,11 +85,25 @@ ck::Fp4Gemm gemm(const uint8_t *x, const uint8_t *xs, int64_t M, int64_t K, bool
     return g;
 }
 
-// The quantizer and the product of one linear.
+// Whether [p, p + n) and [q, q + m) share a byte.
+bool overlap(const void *p, size_t n, const void *q, size_t m) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b + m && b < a + n;
+}
+
+// One linear: with few tokens a single kernel, which quantizes x in every CTA (and so
+// while others write y), else the quantizer and the product.
 ck_status run_linear(const void *x, int64_t M, int64_t K, int64_t ldx, ck_input_act act, bool nv, float x_scale,
                      const void *W, const void *w_scales, float w_scale, int64_t N, const void *bias,
                      const void *residual, void *y, void *ws, const Codes &c, unsigned int *status,
                      ck_stream_t stream) {
+    const size_t x_bytes = (static_cast<size_t>(M - 1) * ldx + (act == CK_ACT_SWIGLU ? 2 * K : K)) * 2;
+    if (M <= ck::kFp4QuantizeInside && !overlap(x, x_bytes, y, static_cast<size_t>(M) * N * 2)) {
+        ck::Fp4Gemm g = gemm(nullptr, nullptr, M, K, nv, W, w_scales, N, x_scale * w_scale, bias, residual, y,
+                             ck::launch_overlap());
+        g.x_bf16 = x, g.ldx = ldx, g.swiglu = act == CK_ACT_SWIGLU, g.x_scale = x_scale;
+        return from_cuda(ck::launch_fp4_gemm_few(g, quantizer_context(stream, status)));
+    }
     if (ck::launch_fp4_quantize(x, false, act == CK_ACT_SWIGLU ? ck::Act::kSwiglu : ck::Act::kNone, M, K, ldx, nv,
                                 x_scale, at(ws, c.codes), at(ws, c.scales),
                                 quantizer_context(stream, status)) != cudaSuccess)

@@ -12,11 +12,15 @@
 // CTAs' ranks (f32: the result does not depend on timing).
 //
 // Roles (6 warps): warp 0 TMA producer, warp 1 TMEM and MMA issue, warps 2..5 the
-// epilogue (one 32-lane quarter of TMEM each).
+// epilogue (one 32-lane quarter of TMEM each).  With up to 16 tokens these four also
+// quantize: x comes as bf16 and every CTA quantizes its own columns of it into the
+// stages, while the weight is on its way, instead of a kernel ahead (blocks need
+// nothing beyond themselves, so a CTA does with its share of K).
 #include <cuda_bf16.h>
 
 #include "fp4_core.cuh"
 #include "launch_util.h"
+#include "quant_core.cuh"
 
 namespace ck {
 namespace {
@@ -25,6 +29,10 @@ constexpr int kThreads = 192;
 constexpr int kRows = 128;               // rows of W a CTA
 constexpr int kStageK = 256;             // 128 bytes of codes a row
 constexpr int kABytes = kRows * kStageK / 2;
+constexpr int kCtaBytes = 112 * 1024 + 256;  // two CTAs an SM
+
+// Where X comes from: codes, or bf16 x (or [gate | up]) to quantize.
+enum class From : int { kCodes, kBf16, kSwiglu };
 
 template <int TN, bool NV>
 struct Cfg {
@@ -32,40 +40,47 @@ struct Cfg {
     static constexpr int kSfBytes = kWords * 512;
     static constexpr int kBBytes = TN * kStageK / 2;
     static constexpr int kStageBytes = kABytes + kBBytes + 2 * kSfBytes;
+    // partial sums: beside the stages, so that a CTA may send its own while another
+    // still multiplies; in their place where the stages need the room
     static constexpr int kRedBytes = TN * kRows * 4;
-    // two CTAs an SM up to 16 tokens, else one
-    static constexpr int kStages = ((TN <= 16 ? 110 : 220) * 1024 - kRedBytes) / kStageBytes;
+    static constexpr bool kOwnRed = TN <= 16;
+    static constexpr int kStages = (kCtaBytes - 1024 - 256 - (kOwnRed ? kRedBytes : 0)) / kStageBytes;
     static constexpr int kTmemSf = TN < 32 ? 32 : TN;  // first column of the scales
     static constexpr int kTmemCols = kTmemSf + 32 <= 64 ? 64 : (kTmemSf + 32 <= 128 ? 128 : 256);
-    static constexpr size_t kSmemBytes = static_cast<size_t>(kStages) * kStageBytes + kRedBytes + 256 + 1024;
-    static_assert(kStageBytes % 1024 == 0 && kStages >= 3, "stage");
+    static constexpr size_t kSmemBytes =
+        static_cast<size_t>(kStages) * kStageBytes + (kOwnRed ? kRedBytes : 0) + 256 + 1024;
+    static_assert(kStageBytes % 1024 == 0 && kStages >= 3 && 8 * (2 * kStages + 1) + 8 <= 256, "stage");
+    static_assert(kOwnRed || kRedBytes <= kStages * kStageBytes, "partial sums");
 };
 
 struct Args {
     const uint8_t *xs, *ws;
-    int M, N, K, words;  // words: scale words a row
+    const __nv_bfloat16 *x;  // to quantize
+    int64_t ldx;
+    fp4::Scale t;
+    int M, N, K, words, splits;  // words: scale words a row
     float alpha;
     const __nv_bfloat16 *bias, *residual;
     __nv_bfloat16 *y;
-    bool weights_settled;
+    bool weights_settled, early_trigger;
     unsigned int *status;
     unsigned long long timeout_ns;
 };
 
-template <int TN, bool NV>
-__global__ void __launch_bounds__(kThreads)
+template <int TN, bool NV, From FROM>
+__global__ void __launch_bounds__(kThreads, 2)
 fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                     const __grid_constant__ Args a) {
     using C = Cfg<TN, NV>;
     constexpr int kStages = C::kStages;
+    constexpr bool kQuant = FROM != From::kCodes;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_s = smem_u32(smem_raw);
     const uint32_t smem_s = (raw_s + 1023u) & ~1023u;
-    uint8_t *smem = smem_raw + (smem_s - raw_s);
-    const uint32_t red_s = smem_s + kStages * C::kStageBytes;
-    const float *red = reinterpret_cast<const float *>(smem + kStages * C::kStageBytes);
-    const uint32_t bars_s = red_s + C::kRedBytes;
-    uint8_t *bars = smem + kStages * C::kStageBytes + C::kRedBytes;
+    const uint32_t red_s = C::kOwnRed ? smem_s + kStages * C::kStageBytes : smem_s;
+    const float *red = reinterpret_cast<const float *>(smem_raw + (red_s - raw_s));
+    const uint32_t bars_s = smem_s + kStages * C::kStageBytes + (C::kOwnRed ? C::kRedBytes : 0);
+    uint8_t *bars = smem_raw + (bars_s - raw_s);
     auto full = [&](int s) { return bars_s + 8u * s; };
     auto empty = [&](int s) { return bars_s + 8u * (kStages + s); };
     const uint32_t done = bars_s + 8u * (2 * kStages);
@@ -77,16 +92,15 @@ fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());
-    const int splits = static_cast<int>(gridDim.x / ((a.N + kRows - 1) / kRows));
-    const int n_tile = blockIdx.x / splits;
+    const int n_tile = blockIdx.x / a.splits;
     const int n0 = n_tile * kRows, m0 = blockIdx.y * TN;
     const int num_kb = (a.K + kStageK - 1) / kStageK;
-    const int kb0 = num_kb * rank / splits, kb1 = num_kb * (rank + 1) / splits;
+    const int kb0 = num_kb * rank / a.splits, kbs = num_kb * (rank + 1) / a.splits - kb0;
     const WaitCtl ctl{abort_flag, a.status, a.timeout_ns};
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(full(s), 1);
+            mbar_init(full(s), kQuant ? 5 : 1);  // the copies, and the quantizers' warps
             mbar_init(empty(s), 1);
         }
         mbar_init(done, 1);
@@ -100,43 +114,50 @@ fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
+    if constexpr (C::kOwnRed) cluster_arrive();  // waited for before another CTA's shared memory is written
     const uint32_t tmem = *tmem_slot;
-    pdl_launch_dependents();
+    // A kernel behind this one that reads what settles before it (a weight) may do so
+    // once let in: with x quantized here, no kernel ahead has waited for it.
+    if (!kQuant || a.early_trigger) pdl_launch_dependents();
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         int issued = 0;
         if (elect_one()) {
             tma_prefetch_desc(&tm_w);
-            tma_prefetch_desc(&tm_x);
+            if constexpr (!kQuant) tma_prefetch_desc(&tm_x);
             const uint8_t *ws = a.ws + (static_cast<int64_t>(n_tile) * a.words) * 512;
-            const uint8_t *xs = a.xs + (static_cast<int64_t>(m0 >> 7) * a.words) * 512;
+            const uint8_t *xs = kQuant ? nullptr : a.xs + (static_cast<int64_t>(m0 >> 7) * a.words) * 512;
             auto sf_bytes = [&](int kb) {
                 const int left = a.words - kb * C::kWords;
                 return static_cast<uint32_t>((left < C::kWords ? left : C::kWords) * 512);
             };
             auto load_w = [&](int s, int kb) {
                 const uint32_t sf = sf_bytes(kb);
-                mbar_arrive_expect_tx(full(s), kABytes + C::kBBytes + 2 * sf);
+                mbar_arrive_expect_tx(full(s), kABytes + sf + (kQuant ? 0 : C::kBBytes + sf));
                 tma_load_2d(stage(s), &tm_w, full(s), kb * (kStageK / 2), n0);
                 bulk_load_1d(stage(s) + kOffSfa, ws + static_cast<int64_t>(kb) * C::kSfBytes, sf, full(s));
             };
             auto load_x = [&](int s, int kb) {
-                tma_load_2d(stage(s) + kOffB, &tm_x, full(s), kb * (kStageK / 2), m0);
-                bulk_load_1d(stage(s) + kOffSfb, xs + static_cast<int64_t>(kb) * C::kSfBytes, sf_bytes(kb), full(s));
+                if constexpr (!kQuant) {
+                    tma_load_2d(stage(s) + kOffB, &tm_x, full(s), kb * (kStageK / 2), m0);
+                    bulk_load_1d(stage(s) + kOffSfb, xs + static_cast<int64_t>(kb) * C::kSfBytes, sf_bytes(kb), full(s));
+                }
             };
             if (!a.weights_settled) pdl_wait();
-            const int pre = kb1 - kb0 < kStages ? kb1 - kb0 : kStages;
+            const int pre = kbs < kStages ? kbs : kStages;
             for (int i = 0; i < pre; ++i) load_w(i, kb0 + i);
             if (a.weights_settled) pdl_wait();
             for (int i = 0; i < pre; ++i) load_x(i, kb0 + i);
             issued = pre;
-            for (int i = pre; i < kb1 - kb0; ++i) {
-                const int s = i % kStages;
-                if (!mbar_wait(empty(s), ((i / kStages) & 1) ^ 1, ctl)) break;
+            int s = 0;
+            uint32_t ph = 0;
+            for (int i = pre; i < kbs; ++i) {
+                if (!mbar_wait_spin(empty(s), ph, ctl)) break;
                 load_w(s, kb0 + i);
                 load_x(s, kb0 + i);
                 issued = i + 1;
+                if (++s == kStages) s = 0, ph ^= 1u;
             }
             if (*abort_flag) {
                 const int first = issued > kStages ? issued - kStages : 0;
@@ -151,53 +172,133 @@ fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
         const uint32_t sfb_tile = sfb + ((m0 & 127) >> 5);  // this tile's tokens within their 128 rows of scales
         if (elect_one()) {
             bool ok = true;
-            for (int kb = kb0; kb < kb1 && ok; ++kb) {
-                const int i = kb - kb0, s = i % kStages;
-                ok = mbar_wait(full(s), (i / kStages) & 1, ctl);
+            int s = 0;
+            uint32_t ph = 0;
+            for (int i = 0; i < kbs; ++i) {
+                ok = mbar_wait_spin(full(s), ph, ctl);
                 if (!ok) break;
                 tc_fence_after_sync();
                 const uint64_t ad = sdesc_kmajor_sw128(stage(s)), bd = sdesc_kmajor_sw128(stage(s) + kOffB);
-                const int words = a.words - kb * C::kWords;
+                const int words = a.words - (kb0 + i) * C::kWords;
 #pragma unroll
                 for (int w = 0; w < C::kWords; ++w)
                     if (w < words) {
                         tmem_copy_scales(sfa + 4 * w, sdesc_scales(stage(s) + kOffSfa + 512 * w));
                         tmem_copy_scales(sfb + 4 * w, sdesc_scales(stage(s) + kOffSfb + 512 * w));
                     }
-                const int left = a.K - kb * kStageK;  // columns of K from here on
+                const int left = a.K - (kb0 + i) * kStageK;  // columns of K from here on
 #pragma unroll
                 for (int k = 0; k < kStageK / 64; ++k)
                     if (64 * k < left) {
                         const int w = NV ? k : k / 2;
                         mma_fp4<NV, false>(tmem, ad + 2 * k, bd + 2 * k, idesc_fp4(kRows, TN, NV, NV ? 0 : k & 1),
-                                    sfa + 4 * w, sfb_tile + 4 * w, i > 0 || k > 0 ? 1u : 0u);
+                                           sfa + 4 * w, sfb_tile + 4 * w, i > 0 || k > 0 ? 1u : 0u);
                     }
                 mma_commit(empty(s));
+                if (++s == kStages) s = 0, ph ^= 1u;
             }
             mma_commit(done);
             if (!ok) mbar_wait_drain(done, 0, a.timeout_ns, a.status);
         }
         __syncwarp();
+    } else if constexpr (kQuant) {
+        // ------------------------------------------------------------ quantizers
+        // A warp has a token's 256 columns of a stage, 8 a lane; the tokens go round
+        // the four warps, and the next stage's values are on their way.
+        constexpr int kMine = TN / 4;
+        const int t0 = warp - 2;
+        constexpr int kGroup = NV ? 8 : 16;  // lanes of a word
+        pdl_wait();
+        if (!a.early_trigger) pdl_launch_dependents();
+        uint4 u[kMine], v[kMine];
+        auto fetch = [&](int i) {
+            const int col = (kb0 + i) * kStageK + lane * 8;
+#pragma unroll
+            for (int j = 0; j < kMine; ++j) {
+                u[j] = v[j] = make_uint4(0, 0, 0, 0);
+                if (t0 + 4 * j < a.M && i < kbs && col < a.K) {
+                    const __nv_bfloat16 *p = a.x + (t0 + 4 * j) * a.ldx + col;
+                    u[j] = *reinterpret_cast<const uint4 *>(p);
+                    if constexpr (FROM == From::kSwiglu) v[j] = *reinterpret_cast<const uint4 *>(p + a.K);
+                }
+            }
+        };
+        fetch(0);
+        int s = 0;
+        uint32_t ph = 1;
+        bool ok = true;
+        for (int i = 0; i < kbs; ++i) {
+            uint32_t codes[kMine], word[kMine];
+#pragma unroll
+            for (int j = 0; j < kMine; ++j) {
+                codes[j] = word[j] = 0;
+                if (t0 + 4 * j >= a.M) continue;  // (uniform over the warp)
+                const uint32_t ru[4] = {u[j].x, u[j].y, u[j].z, u[j].w}, rv[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+                uint64_t q[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float lo = __uint_as_float(ru[e] << 16), hi = __uint_as_float(ru[e] & 0xffff0000u);
+                    q[e] = FROM == From::kSwiglu ? f32x2(qc::silu_mul(lo, __uint_as_float(rv[e] << 16)),
+                                                         qc::silu_mul(hi, __uint_as_float(rv[e] & 0xffff0000u)))
+                                                 : f32x2(lo, hi);
+                }
+                uint32_t scale;
+                codes[j] = fp4::quantize8<NV>(q, a.t, scale);
+                word[j] = fp4::scale_word<NV>(scale, lane);
+            }
+            fetch(i + 1);
+            int got = 0;
+            if (lane == 0) got = mbar_wait_spin(empty(s), ph, ctl) ? 1 : 0;  // (the first round's is over at once)
+            ok = __shfl_sync(0xffffffffu, got, 0) != 0;
+            if (!ok) break;
+#pragma unroll
+            for (int j = 0; j < kMine; ++j) {
+                const int t = t0 + 4 * j;
+                if (t >= a.M) continue;
+                // 128-byte rows, their 16-byte pieces swizzled by the row
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage(s) + kOffB + t * 128 + (((lane >> 2) ^ (t & 7)) << 4) + (lane & 3) * 4),
+                             "r"(codes[j])
+                             : "memory");
+                if (lane % kGroup == 0)
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage(s) + kOffSfb + lane / kGroup * 512 + t * 16), "r"(word[j])
+                                 : "memory");
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full(s));
+            if (++s == kStages) s = 0, ph ^= 1u;
+        }
     }
     // ---------------------------------------------------------------- epilogue
     // Column c of the tile is finished by the CTA of rank c / own.
-    const int own = TN / splits;
-    cluster_sync();  // every CTA of the cluster has begun: its shared memory may be written
+    const int own = TN / a.splits;
+    bool ok = true;
+    if (warp >= 2) {
+        int got = 0;
+        if (lane == 0) got = mbar_wait(done, 0, ctl) ? 1 : 0;
+        ok = __shfl_sync(0xffffffffu, got, 0) != 0;
+        tc_fence_after_sync();
+    }
+    __syncwarp();
+    if constexpr (C::kOwnRed)
+        cluster_wait();  // every CTA of the cluster has begun
+    else
+        cluster_sync();  // every CTA's products are done with its stages
     if (warp >= 2) {
         const int q = warp & 3;
-        bool ok = mbar_wait(done, 0, ctl);
-        ok = __all_sync(0xffffffffu, ok);
-        tc_fence_after_sync();
         if (ok) {
             const int r = q * 32 + lane;
+            constexpr int kStep = TN < 16 ? 8 : 16;
 #pragma unroll
-            for (int c0 = 0; c0 < TN; c0 += (TN < 16 ? 8 : 16)) {
+            for (int c0 = 0; c0 < TN; c0 += kStep) {
+                if (m0 + c0 >= a.M) break;
                 uint32_t v[16];
                 tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(q * 32) << 16) + c0, v);
                 tmem_wait_ld16(v);
 #pragma unroll
-                for (int j = 0; j < (TN < 16 ? 8 : 16); ++j) {
+                for (int j = 0; j < kStep; ++j) {
                     const int c = c0 + j, owner = c / own;
+                    if (m0 + c >= a.M) break;
                     const uint32_t at = red_s + 4u * ((rank * own + c - owner * own) * kRows + r);
                     asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(mapa_shared(at, owner)), "r"(v[j]) : "memory");
                 }
@@ -209,26 +310,26 @@ fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
     if (warp >= 2 && !*abort_flag) {
         const int t = threadIdx.x - 64;
         const int n = n0 + 2 * (t & 63);
-        float b0 = 0.f, b1 = 0.f;
-        if (a.bias != nullptr && n < a.N) {
-            const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162 *>(a.bias + n);
-            b0 = __low2float(b), b1 = __high2float(b);
-        }
         if (n < a.N) {
-            pdl_wait();  // the residual may come from the kernel ahead
+            float b0 = 0.f, b1 = 0.f;
+            if (a.bias != nullptr) {
+                const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162 *>(a.bias + n);
+                b0 = __low2float(b), b1 = __high2float(b);
+            }
+            if constexpr (!kQuant) pdl_wait();  // the residual may come from the kernel ahead
             for (int c = t >> 6; c < own; c += 2) {
                 const int m = m0 + rank * own + c;
                 if (m >= a.M) break;
-                float s0 = 0.f, s1 = 0.f;
-                for (int src = 0; src < splits; ++src) {
-                    const float2 p = *reinterpret_cast<const float2 *>(red + (src * own + c) * kRows + 2 * (t & 63));
-                    s0 += p.x, s1 += p.y;
-                }
                 const int64_t at = static_cast<int64_t>(m) * a.N + n;
                 float r0 = 0.f, r1 = 0.f;
                 if (a.residual != nullptr) {
                     const __nv_bfloat162 r = *reinterpret_cast<const __nv_bfloat162 *>(a.residual + at);
                     r0 = __low2float(r), r1 = __high2float(r);
+                }
+                float s0 = 0.f, s1 = 0.f;
+                for (int src = 0; src < a.splits; ++src) {
+                    const float2 p = *reinterpret_cast<const float2 *>(red + (src * own + c) * kRows + 2 * (t & 63));
+                    s0 += p.x, s1 += p.y;
                 }
                 *reinterpret_cast<__nv_bfloat162 *>(a.y + at) =
                     __floats2bfloat162_rn(a.alpha * s0 + b0 + r0, a.alpha * s1 + b1 + r1);
@@ -242,17 +343,22 @@ fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
     }
 }
 
-template <int TN, bool NV>
+template <int TN, bool NV, From FROM>
 cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx) {
     using C = Cfg<TN, NV>;
     CUtensorMap mw, mx;
     const int row_bytes = static_cast<int>(g.K / 2);
     if (!tensor_map_2d(&mw, g.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.N, row_bytes, kStageK / 2, kRows,
-                       CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !tensor_map_2d(&mx, g.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.M, row_bytes, kStageK / 2, TN,
                        CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    auto kern = fp4_gemm_few_kernel<TN, NV>;
+    if constexpr (FROM == From::kCodes) {
+        if (!tensor_map_2d(&mx, g.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.M, row_bytes, kStageK / 2, TN,
+                           CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+    } else {
+        mx = mw;  // not used
+    }
+    auto kern = fp4_gemm_few_kernel<TN, NV, FROM>;
     if (cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), static_cast<int>(C::kSmemBytes));
         e != cudaSuccess)
         return e;
@@ -261,6 +367,7 @@ cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx) {
     const int64_t n_tiles = (g.N + kRows - 1) / kRows, m_tiles = (g.M + TN - 1) / TN;
     const int64_t num_kb = (g.K + kStageK - 1) / kStageK;
     if (m_tiles > 65535) return cudaErrorInvalidValue;
+    // as many parts of K as leave all CTAs resident at once
     int splits = 1;
     while (splits < 8 && n_tiles * m_tiles * splits * 2 <= 2 * sms && splits * 2 <= num_kb) splits *= 2;
     cudaLaunchConfig_t cfg = {};
@@ -279,22 +386,31 @@ cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx) {
     cfg.numAttrs = ctx.pdl ? 2 : 1;
     Args a = {};
     a.xs = g.xs, a.ws = g.ws;
+    a.x = static_cast<const __nv_bfloat16 *>(g.x_bf16), a.ldx = g.ldx;
+    a.t = fp4::Scale{g.x_scale, 6.f * g.x_scale};
     a.M = static_cast<int>(g.M), a.N = static_cast<int>(g.N), a.K = static_cast<int>(g.K);
     a.words = static_cast<int>(fp4_words(g.K, g.nv));
+    a.splits = splits;
     a.alpha = g.alpha;
     a.bias = static_cast<const __nv_bfloat16 *>(g.bias), a.residual = static_cast<const __nv_bfloat16 *>(g.residual);
     a.y = static_cast<__nv_bfloat16 *>(g.y);
-    a.weights_settled = g.weights_settled;
+    a.weights_settled = g.weights_settled, a.early_trigger = ctx.early_trigger;
     a.status = ctx.status, a.timeout_ns = ctx.timeout_ns;
     return cudaLaunchKernelEx(&cfg, kern, mw, mx, a);
 }
 
 template <bool NV>
 cudaError_t launch_n(const Fp4Gemm &g, const LaunchCtx &ctx) {
-    if (g.M <= 8) return launch_t<8, NV>(g, ctx);
-    if (g.M <= 16) return launch_t<16, NV>(g, ctx);
-    if (g.M <= 32) return launch_t<32, NV>(g, ctx);
-    return launch_t<64, NV>(g, ctx);
+    if (g.x_bf16 != nullptr) {
+        if (g.swiglu)
+            return g.M <= 8 ? launch_t<8, NV, From::kSwiglu>(g, ctx) : launch_t<16, NV, From::kSwiglu>(g, ctx);
+        return g.M <= 8 ? launch_t<8, NV, From::kBf16>(g, ctx) : launch_t<16, NV, From::kBf16>(g, ctx);
+    }
+    if (g.M <= 8) return launch_t<8, NV, From::kCodes>(g, ctx);
+    if (g.M <= 16) return launch_t<16, NV, From::kCodes>(g, ctx);
+    if (g.M <= 32) return launch_t<32, NV, From::kCodes>(g, ctx);
+    if (g.M <= 64) return launch_t<64, NV, From::kCodes>(g, ctx);
+    return launch_t<128, NV, From::kCodes>(g, ctx);
 }
 
 }  // namespace

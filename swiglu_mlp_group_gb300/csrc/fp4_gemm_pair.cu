@@ -3,82 +3,112 @@
 //   y[m, n] = bf16( alpha * sum_k X[m, k] W[n, k] + bias[n] + residual[m, n] )
 //
 // X, W: E2M1 codes times the scales of their blocks (fp4_core.cuh).  CTA pairs
-// (tcgen05.mma.cta_group::2): a tile of 256 tokens x PN rows of W on two SMs, each
-// holding its 128 tokens, half of W's rows, and the scales of its tokens and of all
-// of W's rows; f32 accumulators in TMEM, two of them, so that a tile's epilogue runs
-// under the next one's products.  PN is at most 192: two accumulators of 256 columns
-// would leave TMEM no room for scales.
+// (tcgen05.mma.cta_group::2): a tile of 256 tokens x 192 rows of W on two SMs, each
+// holding its 128 tokens, half of W's rows, and the scales of its tokens and of all of
+// W's rows; two f32 accumulators in TMEM, so that a tile's epilogue runs under the next
+// one's products (two of 256 columns would leave no room for the scales).
 //
-// Roles (each CTA, 10 warps): warp 0 TMA producer, warp 1 TMEM and, in the leader,
-// the issue of the scales' copies to TMEM and of the MMAs (both run in the order of
-// their issue), warps 2..9 the epilogue on this CTA's 128 tokens.
+// Roles (each CTA, 12 warps): warps 0 and 2 TMA producers of the tokens' and of the
+// weight's codes and scales, warp 1 TMEM and, in the leader, the issue of the scales'
+// copies to TMEM and of the MMAs (both run in the order of their issue), warps 4..11
+// the epilogue.
+//
+// What bounds it.  The MMAs of a stage (256 columns of K) take 384 clocks, 9.5 PFLOP/s
+// in all, with or without the scales' copies between them (timed alone, from shared
+// memory).  On zeros, which draw little power, the kernel runs at 7.3 (MX) and 6.9 (NV)
+// PFLOP/s at 16384 x 4096 -> 12288, without its stores at 8.3 and 7.7, without its
+// epilogue at 9.1 and 8.2: operands come in at some 77 bytes a clock and SM of the 81 and
+// 89 that the MMAs would take, and y's bytes go the same way.  On random codes power takes
+// another tenth.  What it took: one lane that polls and issues, of a warp of its own (32
+// lanes polling a barrier cost the issuer a third of its time), a producer for each
+// operand (one for both took longer to issue than the MMAs to run), y through shared
+// memory and TMA (exchanged between lanes and stored by them: 252 us against 240, NV).
+// Tried and slower: tiles of 512 tokens on both accumulators (22 % less operand traffic,
+// but no accumulator to spare: 252 us against 240), the stages unrolled in the issuer
+// (no gain), tiles in bands of 8 and 16 rows of tiles (no gain), y in pieces of 64
+// columns (250).
 #include <cuda_bf16.h>
 
 #include "fp4_core.cuh"
-#include "gemm_epilogue.cuh"
 #include "launch_util.h"
 
 namespace ck {
 namespace {
 
-constexpr int kThreads = 320;
-constexpr int kRows = 128;     // tokens a CTA
+constexpr int kThreads = 384;
+constexpr int kRows = 128;     // tokens of an accumulator
 constexpr int kStageK = 256;   // 128 bytes of codes a row
-constexpr int kABytes = kRows * kStageK / 2;
+constexpr int kPN = 192;       // rows of W a tile
 
-template <int PN, bool NV>
+template <bool NV>
 struct Cfg {
     static constexpr int kWords = kStageK / fp4_word(NV);  // scale words of a stage
     static constexpr int kSfaBytes = kWords * 512;
-    static constexpr int kBTiles = (PN + 127) / 128;       // 128-row tiles of W's scales
-    static constexpr int kSfBytes = kSfaBytes * (1 + kBTiles);
-    static constexpr int kBBytes = PN / 2 * kStageK / 2;
-    static constexpr int kStageBytes = kABytes + kBBytes + kSfBytes;
+    static constexpr int kBTiles = 2;                      // 128-row tiles of W's scales
+    static constexpr int kABytes = kRows * kStageK / 2;
+    static constexpr int kBBytes = kPN / 2 * kStageK / 2;
+    static constexpr int kXBytes = kABytes + kSfaBytes, kWBytes = kBBytes + kBTiles * kSfaBytes;
+    static constexpr int kStageBytes = kXBytes + kWBytes;
     static constexpr int kBarBytes = 256;
-    static constexpr int kStages = (225 * 1024 - kBarBytes) / kStageBytes;
-    static constexpr int kTmemSf = 2 * PN;                 // the scales' first column
+    static constexpr int kOutBytes = 8 * 2048;             // a 32 x 32 piece of y a warp of the epilogue
+    static constexpr int kStages = (226 * 1024 - kBarBytes - kOutBytes - 1024) / kStageBytes;
+    static constexpr int kTmemSf = 2 * kPN;                // the scales' first column
     static constexpr int kSfCols = 4 * kWords * (1 + kBTiles);
     static constexpr int kTmemCols = 512;
-    static constexpr size_t kSmemBytes = static_cast<size_t>(kStages) * kStageBytes + kBarBytes + 1024;
+    static constexpr size_t kSmemBytes = static_cast<size_t>(kStages) * kStageBytes + kOutBytes + kBarBytes + 1024;
     static_assert(kStageBytes % 1024 == 0 && kTmemSf + 2 * kSfCols <= kTmemCols, "layout");
     static_assert(8 * (2 * kStages + 5) + 8 <= kBarBytes && kSmemBytes <= 227 * 1024, "shared memory");
 };
 
 struct Args {
-    int M, N, K, words, m_pairs;
+    int M, N, K, m_tiles;
     float alpha;
     const __nv_bfloat16 *bias, *residual;
-    __nv_bfloat16 *y;
     bool weights_settled;
     unsigned int *status;
     unsigned long long timeout_ns;
 };
 
 // Eight columns of a row, packed to bf16: alpha * acc + bias + residual.
-__device__ __forceinline__ void finish8(const uint32_t *acc, float alpha, const uint4 &b, const uint4 &r, uint32_t *pk) {
-    const uint32_t bw[4] = {b.x, b.y, b.z, b.w}, rw[4] = {r.x, r.y, r.z, r.w};
+__device__ __forceinline__ uint4 finish8(const uint32_t *acc, uint64_t alpha, const __nv_bfloat16 *bias,
+                                         const __nv_bfloat16 *residual) {
+    uint64_t v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        v[e] = mul_f32x2(f32x2(__uint_as_float(acc[2 * e]), __uint_as_float(acc[2 * e + 1])), alpha);
+    auto add = [&](const uint4 &u) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            v[e] = add_f32x2(v[e], f32x2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u)));
+    };
+    if (bias != nullptr) add(__ldg(reinterpret_cast<const uint4 *>(bias)));
+    if (residual != nullptr) add(*reinterpret_cast<const uint4 *>(residual));
+    uint32_t p[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const float y0 = __uint_as_float(acc[2 * e]) * alpha + __uint_as_float(bw[e] << 16) + __uint_as_float(rw[e] << 16);
-        const float y1 = __uint_as_float(acc[2 * e + 1]) * alpha + __uint_as_float(bw[e] & 0xffff0000u) +
-                         __uint_as_float(rw[e] & 0xffff0000u);
-        const __nv_bfloat162 v = __floats2bfloat162_rn(y0, y1);
-        pk[e] = *reinterpret_cast<const uint32_t *>(&v);
+        float lo, hi;
+        f32x2_split(v[e], lo, hi);
+        const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+        p[e] = *reinterpret_cast<const uint32_t *>(&t);
     }
+    return make_uint4(p[0], p[1], p[2], p[3]);
 }
 
-template <int PN, bool NV>
+template <bool NV>
 __global__ void __launch_bounds__(kThreads, 1)
 fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                      const __grid_constant__ CUtensorMap tm_xs, const __grid_constant__ CUtensorMap tm_ws,
+                     const __grid_constant__ CUtensorMap tm_y,
                      const __grid_constant__ Args a) {
-    using C = Cfg<PN, NV>;
+    using C = Cfg<NV>;
     constexpr int kStages = C::kStages;
-    constexpr int kOffB = kABytes, kOffSfa = kABytes + C::kBBytes, kOffSfb = kOffSfa + C::kSfaBytes;
+    constexpr int kOffB = C::kABytes, kOffSfa = kOffB + C::kBBytes, kOffSfb = kOffSfa + C::kSfaBytes;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_s = smem_u32(smem_raw);
     const uint32_t smem_s = (raw_s + 1023u) & ~1023u;
-    const uint32_t bars_s = smem_s + kStages * C::kStageBytes;
+    const uint32_t out_s = smem_s + kStages * C::kStageBytes;
+    const uint32_t bars_s = out_s + C::kOutBytes;
     uint8_t *bars = smem_raw + (bars_s - raw_s);
     auto full = [&](int s) { return bars_s + 8u * s; };
     auto empty = [&](int s) { return bars_s + 8u * (kStages + s); };
@@ -92,15 +122,13 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());  // 0: leader (issues), 1: peer
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-    const int total = a.m_pairs * ((a.N + PN - 1) / PN);
-    const int my_tiles = pair < total ? (total - 1 - pair) / npairs + 1 : 0;
+    const int total = a.m_tiles * ((a.N + kPN - 1) / kPN);
     const int num_kb = (a.K + kStageK - 1) / kStageK;
-    const int total_kb = my_tiles * num_kb;
     const WaitCtl ctl{abort_flag, a.status, a.timeout_ns};
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(full(s), 1);
+            mbar_init(full(s), 2);  // the leader's two producers
             mbar_init(empty(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -122,46 +150,36 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     const uint32_t tmem = *tmem_slot;
     pdl_launch_dependents();
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ producer
+    if (warp == 0 || warp == 2) {
+        // ------------------------------------------------------------ producers
+        // Both CTAs' copies complete on the leader's barrier of the stage, where
+        // the leader's producers announce the pair's bytes.
+        const bool weight = warp == 2;
         int issued = 0;
         if (elect_one()) {
-            tma_prefetch_desc(&tm_x);
-            tma_prefetch_desc(&tm_w);
-            tma_prefetch_desc(&tm_xs);
-            tma_prefetch_desc(&tm_ws);
-            // both CTAs' copies complete on the leader's barrier, which counts the pair's bytes
-            auto load_w = [&](int s, int kb, int tile) {
-                if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * C::kStageBytes);
-                const uint32_t bar = mapa_shared(full(s), 0);
-                const int n0 = tile / a.m_pairs * PN;
-                tma_load_2d_pair(stage(s) + kOffB, &tm_w, bar, kb * (kStageK / 2), n0 + rank * (PN / 2));
-#pragma unroll
-                for (int i = 0; i < C::kBTiles; ++i)
-                    tma_load_2d_pair(stage(s) + kOffSfb + i * C::kSfaBytes, &tm_ws, bar, 0,
-                                     (((n0 >> 7) + i) * a.words + kb * C::kWords) * 4);
-            };
-            auto load_x = [&](int s, int kb, int tile) {
-                const uint32_t bar = mapa_shared(full(s), 0);
-                const int m0 = tile % a.m_pairs * (2 * kRows) + rank * kRows;
-                tma_load_2d_pair(stage(s), &tm_x, bar, kb * (kStageK / 2), m0);
-                tma_load_2d_pair(stage(s) + kOffSfa, &tm_xs, bar, 0, ((m0 >> 7) * a.words + kb * C::kWords) * 4);
-            };
-            if (!a.weights_settled) pdl_wait();
-            const int pre = total_kb > 0 ? min(kStages, num_kb) : 0;
-            for (int i = 0; i < pre; ++i) load_w(i, i, pair);
-            if (a.weights_settled) pdl_wait();
-            for (int i = 0; i < pre; ++i) load_x(i, i, pair);
-            issued = pre;
-            int s = pre % kStages, kb = pre == num_kb ? 0 : pre, tile = pre == num_kb ? pair + npairs : pair;
-            uint32_t ph = pre / kStages;
-            for (int i = pre; i < total_kb; ++i) {
-                if (!mbar_wait_spin(empty(s), (ph & 1) ^ 1, ctl)) break;
-                load_w(s, kb, tile);
-                load_x(s, kb, tile);
-                issued = i + 1;
-                if (++s == kStages) s = 0, ++ph;
-                if (++kb == num_kb) kb = 0, tile += npairs;
+            const CUtensorMap *codes = weight ? &tm_w : &tm_x, *scales = weight ? &tm_ws : &tm_xs;
+            tma_prefetch_desc(codes);
+            tma_prefetch_desc(scales);
+            if (!weight || !a.weights_settled) pdl_wait();
+            const uint32_t to_codes = stage(0) + (weight ? kOffB : 0), to_scales = stage(0) + (weight ? kOffSfb : kOffSfa);
+            const uint32_t bytes = 2 * (weight ? C::kWBytes : C::kXBytes);
+            const uint32_t lead = mapa_shared(full(0), 0);
+            int s = 0;
+            uint32_t ph = 1;
+            for (int tile = pair; tile < total; tile += npairs) {
+                const int n0 = tile / a.m_tiles * kPN, m0 = tile % a.m_tiles * (2 * kRows) + rank * kRows;
+                const int row = weight ? n0 + rank * (kPN / 2) : m0, sf_tile = (weight ? n0 : m0) >> 7;
+                bool ok = true;
+                for (int kb = 0; kb < num_kb; ++kb) {
+                    ok = mbar_wait_spin(empty(s), ph, ctl);  // (the first round's wait is over at once)
+                    if (!ok) break;
+                    if (rank == 0) mbar_arrive_expect_tx(full(s), bytes);
+                    tma_load_2d_pair(to_codes + s * C::kStageBytes, codes, lead + 8 * s, kb * (kStageK / 2), row);
+                    tma_load_2d_pair(to_scales + s * C::kStageBytes, scales, lead + 8 * s, kb * (C::kWords * 64), sf_tile);
+                    ++issued;
+                    if (++s == kStages) s = 0, ph ^= 1;
+                }
+                if (!ok) break;
             }
             if (*abort_flag) {
                 if (rank == 0) {
@@ -182,106 +200,110 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
         if (rank == 0) {
             const uint64_t ad0 = sdesc_kmajor_sw128(stage(0)), bd0 = sdesc_kmajor_sw128(stage(0) + kOffB);
             const uint64_t sa0 = sdesc_scales(stage(0) + kOffSfa), sb0 = sdesc_scales(stage(0) + kOffSfb);
-            int kb = 0, tile = pair, gc = 0, s = 0, parity = 0;
+            const int tail = (a.K - (num_kb - 1) * kStageK + 63) / 64;  // MMAs of a tile's last k-block
+            if (elect_one()) {
+            int gc = 0, s = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (int i = 0; i < total_kb; ++i) {
-                const int buf = gc & 1;
-                if (kb == 0 && gc >= 2) {
-                    // the epilogue has read what this accumulator held two tiles ago
-                    ok = __all_sync(0xffffffffu, mbar_wait_spin(acce(buf), ((gc >> 1) - 1) & 1, ctl));
+            for (int tile = pair; tile < total && ok; tile += npairs, ++gc) {
+                const int acc = gc & 1;
+                const uint32_t d = tmem + acc * kPN;
+                // where W's rows of this tile begin in their scales' 128-row tile
+                const uint32_t sfb_off = (tile / a.m_tiles * kPN & 127) >> 5;
+                // the epilogue has read what this accumulator held two tiles ago
+                if (gc >= 2) ok = mbar_wait_spin(acce(acc), ((gc >> 1) - 1) & 1, ctl);
+                if (!ok) break;
+                for (int kb = 0; kb < num_kb; ++kb) {
+                    ok = mbar_wait_spin(full(s), ph, ctl);
                     if (!ok) break;
                     tc_fence_after_sync();
-                }
-                ok = __all_sync(0xffffffffu, mbar_wait_spin(full(s), ph, ctl));
-                if (!ok) break;
-                tc_fence_after_sync();
-                const bool last = kb + 1 == num_kb;
-                if (elect_one()) {
                     const uint64_t step = static_cast<uint64_t>(s) * (C::kStageBytes / 16);
-                    const uint32_t sfa = tmem + C::kTmemSf + parity * C::kSfCols, sfb = sfa + 4 * C::kWords;
-                    // where W's rows of this tile begin in their scales' 128-row tile
-                    const uint32_t sfb_tile = sfb + ((tile / a.m_pairs * PN & 127) >> 5);
+                    const uint64_t ad = ad0 + step, bd = bd0 + step, sa = sa0 + step, sb = sb0 + step;
+                    const uint32_t sfa = tmem + C::kTmemSf + (s & 1) * C::kSfCols, sfb = sfa + 4 * C::kWords;
+                    const bool last = kb + 1 == num_kb;
+                    const int n = last ? tail : 4;
 #pragma unroll
                     for (int w = 0; w < C::kWords; ++w) {
-                        tmem_copy_scales_pair(sfa + 4 * w, sa0 + step + 32 * w);
+                        tmem_copy_scales_pair(sfa + 4 * w, sa + 32 * w);
 #pragma unroll
                         for (int t = 0; t < C::kBTiles; ++t)
-                            tmem_copy_scales_pair(sfb + 4 * (C::kBTiles * w + t), sb0 + step + t * (C::kSfaBytes / 16) + 32 * w);
+                            tmem_copy_scales_pair(sfb + 4 * (C::kBTiles * w + t), sb + t * (C::kSfaBytes / 16) + 32 * w);
                     }
-                    const int left = a.K - kb * kStageK;
 #pragma unroll
-                    for (int k = 0; k < kStageK / 64; ++k)
-                        if (64 * k < left) {
+                    for (int k = 0; k < 4; ++k)
+                        if (k < n) {
                             const int w = NV ? k : k / 2;
-                            mma_fp4<NV, true>(tmem + buf * PN, ad0 + step + 2 * k, bd0 + step + 2 * k,
-                                              idesc_fp4(2 * kRows, PN, NV, NV ? 0 : k & 1), sfa + 4 * w,
-                                              sfb_tile + 4 * C::kBTiles * w, kb > 0 || k > 0 ? 1u : 0u);
+                            mma_fp4<NV, true>(d, ad + 2 * k, bd + 2 * k, idesc_fp4(2 * kRows, kPN, NV, NV ? 0 : k & 1),
+                                              sfa + 4 * w, sfb + sfb_off + 4 * C::kBTiles * w, kb > 0 || k > 0 ? 1u : 0u);
                         }
                     mma_commit_pair(empty(s), 0x3);
-                    if (last) mma_commit_pair(accf(buf), 0x3);
+                    if (last) mma_commit_pair(accf(acc), 0x3);
+                    if (++s == kStages) s = 0, ph ^= 1;
                 }
-                __syncwarp();
-                parity ^= 1;
-                if (++s == kStages) s = 0, ph ^= 1;
-                if (++kb == num_kb) kb = 0, ++gc, tile += npairs;
             }
-            if (elect_one()) {
                 mma_commit_pair(done, 0x1);
                 mbar_wait_drain(done, 0, a.timeout_ns, a.status);
             }
         }
         __syncwarp();
-    } else {
+    } else if (warp >= 4) {
         // ------------------------------------------------------------ epilogue
-        constexpr int kCols = PN / 2;
-        const int q = warp & 3, h = (warp - 2) >> 2;
-        const int qi = lane & 3;
+        constexpr int kCols = kPN / 2, kGroups = kCols / 32;
+        const int q = warp & 3, c0 = (warp - 4) / 4 * kCols;
+        const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + c0;
         pdl_wait();  // the residual may come from the kernel ahead
+        // This thread's row of an accumulator into registers; the accumulator is free.
+        auto read = [&](int acc, int use, uint32_t (&r)[kGroups][32]) {
+            int got = 0;
+            if (lane == 0) got = mbar_wait(accf(acc), use & 1, ctl) ? 1 : 0;
+            if (!__shfl_sync(0xffffffffu, got, 0)) return false;
+            tc_fence_after_sync();
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) tmem_ld_32x32b_x32(tbase + acc * kPN + 32 * g, r[g]);
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) tmem_wait_ld(r[g]);
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(acce(acc), 0));
+            return true;
+        };
+        const uint64_t alpha = f32x2(a.alpha, a.alpha);
+        // 32 rows x 32 columns at a time through shared memory (64-byte rows, swizzled as
+        // the map has it) and out by TMA.
+        const uint32_t piece = out_s + (warp - 4) * 2048;
+        const uint32_t mine = piece + lane * 64, turn = (lane >> 1) & 3;
         int gc = 0;
         for (int tile = pair; tile < total; tile += npairs, ++gc) {
-            const int buf = gc & 1;
-            int got = 0;
-            if (lane == 0) got = mbar_wait(accf(buf), (gc >> 1) & 1, ctl) ? 1 : 0;
-            got = __shfl_sync(0xffffffffu, got, 0);
-            if (!got) break;
-            tc_fence_after_sync();
-            const int row0 = tile % a.m_pairs * (2 * kRows) + rank * kRows + q * 32;
-            const int m = row0 + lane;
-            const int n0 = tile / a.m_pairs * PN + h * kCols;
-            const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * PN + h * kCols;
+            const int n0 = tile / a.m_tiles * kPN + c0;
+            const int row0 = tile % a.m_tiles * (2 * kRows) + rank * kRows + q * 32;
+            const bool in = row0 + lane < a.M;
+            uint32_t r[kGroups][32];
+            if (!read(gc & 1, gc >> 1, r)) break;
 #pragma unroll
-            for (int grp = 0; grp < kCols / 32; ++grp) {
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(tbase + 32 * grp, r);
-                tmem_wait_ld(r);
-                if (grp == kCols / 32 - 1) {
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(acce(buf), 0));
-                }
-                const int n1 = n0 + 32 * grp;
-                uint32_t P[16];
+            for (int g = 0; g < kGroups; ++g) {
+                const int n1 = n0 + 32 * g;
+                if (n1 >= a.N || row0 >= a.M) break;
+                if (lane == 0) bulk_wait_read();  // the piece before has left
+                __syncwarp();
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
                     const int n = n1 + 8 * p;
-                    uint4 b = make_uint4(0, 0, 0, 0), res = b;
-                    if (a.bias != nullptr && n < a.N) b = __ldg(reinterpret_cast<const uint4 *>(a.bias + n));
-                    if (a.residual != nullptr && n < a.N && m < a.M)
-                        res = *reinterpret_cast<const uint4 *>(a.residual + static_cast<int64_t>(m) * a.N + n);
-                    finish8(r + 8 * p, a.alpha, b, res, P + 4 * p);
+                    const uint4 v = finish8(r[g] + 8 * p, alpha, a.bias != nullptr && n < a.N ? a.bias + n : nullptr,
+                                            a.residual != nullptr && n < a.N && in
+                                                ? a.residual + static_cast<int64_t>(row0 + lane) * a.N + n : nullptr);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + ((p ^ turn) << 4)), "r"(v.x),
+                                 "r"(v.y), "r"(v.z), "r"(v.w)
+                                 : "memory");
                 }
-                ep::quad_transpose(P, qi);
-                const int n = n1 + 8 * qi;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int mr = row0 + (lane & ~3) + k;
-                    if (mr < a.M && n < a.N)
-                        *reinterpret_cast<uint4 *>(a.y + static_cast<int64_t>(mr) * a.N + n) =
-                            make_uint4(P[4 * k], P[4 * k + 1], P[4 * k + 2], P[4 * k + 3]);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_2d(&tm_y, piece, n1, row0);
+                    bulk_commit();
                 }
             }
         }
+        if (lane == 0) bulk_wait();
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -292,32 +314,28 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     }
 }
 
-// The scales of `rows` rows as a tensor of 128-byte rows, four of them a word tile.
-bool scale_map(CUtensorMap *map, const uint8_t *scales, int64_t rows, int64_t words, int box_words) {
-    return tensor_map_2d(map, scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (rows + 127) / 128 * words * 4, 128, 128,
-                         4 * box_words, CU_TENSOR_MAP_SWIZZLE_NONE);
-}
-
-template <int PN, bool NV>
+template <bool NV>
 cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx) {
-    using C = Cfg<PN, NV>;
-    CUtensorMap mx, mw, mxs, mws;
+    using C = Cfg<NV>;
+    CUtensorMap mx, mw, mxs, mws, my;
     const int row_bytes = static_cast<int>(g.K / 2);
     const int64_t words = fp4_words(g.K, NV);
     if (!tensor_map_2d(&mx, g.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.M, row_bytes, kStageK / 2, kRows,
                        CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !tensor_map_2d(&mw, g.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.N, row_bytes, kStageK / 2, PN / 2,
+        !tensor_map_2d(&mw, g.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.N, row_bytes, kStageK / 2, kPN / 2,
                        CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !scale_map(&mxs, g.xs, g.M, words, C::kWords) || !scale_map(&mws, g.ws, g.N, words, C::kWords))
+        !tensor_map_scales(&mxs, g.xs, (g.M + 127) / 128, words, C::kWords, 1) ||
+        !tensor_map_scales(&mws, g.ws, (g.N + 127) / 128, words, C::kWords, C::kBTiles) ||
+        !tensor_map_2d(&my, g.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.M, g.N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
         return cudaErrorInvalidValue;
-    auto kern = fp4_gemm_pair_kernel<PN, NV>;
+    auto kern = fp4_gemm_pair_kernel<NV>;
     if (cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), static_cast<int>(C::kSmemBytes));
         e != cudaSuccess)
         return e;
     const int sms = sm_count();
     if (sms < 2) return cudaErrorInvalidDevice;
-    const int64_t m_pairs = (g.M + 2 * kRows - 1) / (2 * kRows);
-    const int64_t tiles = m_pairs * ((g.N + PN - 1) / PN);
+    const int64_t m_tiles = (g.M + 2 * kRows - 1) / (2 * kRows);
+    const int64_t tiles = m_tiles * ((g.N + kPN - 1) / kPN);
     if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
     const int pairs = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
     cudaLaunchConfig_t cfg = {};
@@ -336,19 +354,18 @@ cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx) {
     cfg.numAttrs = ctx.pdl ? 2 : 1;
     Args a = {};
     a.M = static_cast<int>(g.M), a.N = static_cast<int>(g.N), a.K = static_cast<int>(g.K);
-    a.words = static_cast<int>(words), a.m_pairs = static_cast<int>(m_pairs);
+    a.m_tiles = static_cast<int>(m_tiles);
     a.alpha = g.alpha;
     a.bias = static_cast<const __nv_bfloat16 *>(g.bias), a.residual = static_cast<const __nv_bfloat16 *>(g.residual);
-    a.y = static_cast<__nv_bfloat16 *>(g.y);
     a.weights_settled = g.weights_settled;
     a.status = ctx.status, a.timeout_ns = ctx.timeout_ns;
-    return cudaLaunchKernelEx(&cfg, kern, mx, mw, mxs, mws, a);
+    return cudaLaunchKernelEx(&cfg, kern, mx, mw, mxs, mws, my, a);
 }
 
 }  // namespace
 
 cudaError_t launch_fp4_gemm_pair(const Fp4Gemm &g, const LaunchCtx &ctx) {
-    return g.nv ? launch_t<192, true>(g, ctx) : launch_t<192, false>(g, ctx);
+    return g.nv ? launch_t<true>(g, ctx) : launch_t<false>(g, ctx);
 }
 
 }  // namespace ck

@@ -169,11 +169,10 @@ int max_active_clusters(const void *kernel, int threads, size_t smem, int cluste
         [](int n) { return n > 0; });
 }
 
-bool tensor_map_2d(CUtensorMap *map, const void *ptr, CUtensorMapDataType dtype, int elem_bytes,
-                   int64_t rows, int64_t cols, int box_cols, int box_rows,
-                   CUtensorMapSwizzle swizzle) {
-    const MapKey key{ptr, rows, cols, static_cast<int>(dtype), elem_bytes, box_cols, box_rows,
-                     static_cast<int>(swizzle)};
+namespace {
+// The map of a request, encoded by `make` where the cache does not have it.
+template <typename Make>
+bool cached_map(CUtensorMap *map, const MapKey &key, Make make) {
     const size_t slot = slot_of(key);
     {
         std::lock_guard<std::mutex> lock(g_map_mu);
@@ -183,17 +182,8 @@ bool tensor_map_2d(CUtensorMap *map, const void *ptr, CUtensorMapDataType dtype,
             return true;
         }
     }
-    auto encode = encode_fn();
-    if (!encode) return false;
-    cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * static_cast<cuuint64_t>(elem_bytes)};
-    cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
-    cuuint32_t estr[2] = {1, 1};
     CUtensorMap m;
-    if (encode(&m, dtype, 2, const_cast<void *>(ptr), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return false;
+    if (!make(&m)) return false;
     std::lock_guard<std::mutex> lock(g_map_mu);
     g_maps[slot].used = true;
     g_maps[slot].key = key;
@@ -201,6 +191,43 @@ bool tensor_map_2d(CUtensorMap *map, const void *ptr, CUtensorMapDataType dtype,
     ++g_map_misses;
     memcpy(map, &m, sizeof(CUtensorMap));
     return true;
+}
+}  // namespace
+
+bool tensor_map_2d(CUtensorMap *map, const void *ptr, CUtensorMapDataType dtype, int elem_bytes,
+                   int64_t rows, int64_t cols, int box_cols, int box_rows,
+                   CUtensorMapSwizzle swizzle) {
+    const MapKey key{ptr, rows, cols, static_cast<int>(dtype), elem_bytes, box_cols, box_rows,
+                     static_cast<int>(swizzle)};
+    return cached_map(map, key, [&](CUtensorMap *m) {
+        auto encode = encode_fn();
+        if (!encode) return false;
+        cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+        cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * static_cast<cuuint64_t>(elem_bytes)};
+        cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
+        cuuint32_t estr[2] = {1, 1};
+        return encode(m, dtype, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    });
+}
+
+bool tensor_map_scales(CUtensorMap *map, const void *ptr, int64_t tiles, int64_t words, int box_words,
+                       int box_tiles) {
+    // told from a 2-D map by its element size, which no such map has
+    const MapKey key{ptr, tiles, words, static_cast<int>(CU_TENSOR_MAP_DATA_TYPE_FLOAT64), 0, box_words, box_tiles,
+                     static_cast<int>(CU_TENSOR_MAP_SWIZZLE_NONE)};
+    return cached_map(map, key, [&](CUtensorMap *m) {
+        auto encode = encode_fn();
+        if (!encode) return false;
+        cuuint64_t dims[2] = {static_cast<cuuint64_t>(words) * 64, static_cast<cuuint64_t>(tiles)};
+        cuuint64_t strides[1] = {static_cast<cuuint64_t>(words) * 512};
+        cuuint32_t box[2] = {static_cast<cuuint32_t>(64 * box_words), static_cast<cuuint32_t>(box_tiles)};
+        cuuint32_t estr[2] = {1, 1};
+        return encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    });
 }
 
 bool tensor_map_bf16(CUtensorMap *map, const void *ptr, int rank, const uint64_t *dims,

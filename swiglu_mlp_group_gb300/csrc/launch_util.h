@@ -40,6 +40,12 @@ bool tensor_map_2d(CUtensorMap *map, const void *ptr, CUtensorMapDataType dtype,
                    int64_t rows, int64_t cols, int box_cols, int box_rows,
                    CUtensorMapSwizzle swizzle);
 
+// The tiled scales of 4-bit rows (tiles of 128 rows, `words` 512-byte words each) as
+// a tensor [tiles][words x 64] of 8-byte elements (a box's row is up to 256 of
+// them), box of box_tiles x 64 box_words, no swizzle; cached alike.
+bool tensor_map_scales(CUtensorMap *map, const void *ptr, int64_t tiles, int64_t words, int box_words,
+                       int box_tiles);
+
 // A bf16 tensor map of rank 2 to 4, 128-byte swizzle, out-of-range elements
 // read as zero: dims and box innermost first, strides in bytes of dims 1 ...
 // Encoded on the spot, never cached.
