@@ -244,7 +244,7 @@ cudaError_t launch_block_norm(const BlockNorm &b, const LaunchCtx &ctx) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = ctx.pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, b, warps, rows, fp4::Scale{b.n_scale, 6.f * b.n_scale});
+    return cudaLaunchKernelEx(&cfg, kernel, b, warps, rows, fp4::scale_of(b.n_scale));
 }
 
 }  // namespace ck

@@ -13,8 +13,13 @@
 // few bits), so the quotient has to be the correctly rounded one: a product with
 // 1 / d alone would land to either side of the border.  MX: 1 / d is a power of
 // two and the product exact.  NV: Markstein's correction, q + r (x - q d) with r
-// the correctly rounded 1 / d, on two elements at a time (three operations for
-// two elements; IEEE division of each element would be some ten each).
+// = 1 / d, on two elements at a time (three operations for two elements); r by a
+// Newton step on the hardware's approximation, within 2^-23 of itself, which
+// leaves the corrected quotient within 2^-43 of x / d before its rounding: exact
+// where x / d is an f32 number, as on a border, and nearest elsewhere but for
+// quotients that close to the middle of two f32 numbers.  amax / (6 t) likewise,
+// its reciprocal from the host.  (IEEE divisions in their place: the quantizer of
+// 16384 x 4096 49 us instead of 37.)
 //
 // Layout.  Codes: [rows, K / 2] bytes, the even column in the low half.  Scales:
 // tiles of 128 rows x one 32-bit word (four scales, 64 (NV) or 128 (MX)
@@ -73,8 +78,9 @@ __device__ __forceinline__ uint32_t pack8(const uint64_t (&q)[4]) {
 // four an MX block; lane 0's first value begins one) -> the lane's codes and the
 // block's scale byte.  Every lane of the warp takes part.
 struct Scale {
-    float tensor, six_tensor;  // t and 6 t
+    float tensor, six_tensor, inv_six;  // t, 6 t and 1 / (6 t)
 };
+inline Scale scale_of(float tensor) { return Scale{tensor, 6.f * tensor, 1.f / (6.f * tensor)}; }
 template <bool NV>
 __device__ __forceinline__ uint32_t quantize8(const uint64_t (&v)[4], const Scale &t, uint32_t &scale) {
     float m = 0.f;
@@ -89,11 +95,16 @@ __device__ __forceinline__ uint32_t quantize8(const uint64_t (&v)[4], const Scal
     const bool finite = m < __int_as_float(0x7f800000);
     uint64_t q[4];
     if constexpr (NV) {
-        const float s = __fdiv_rn(m, t.six_tensor);
+        // past 448 the scale is cut off; so far past it the quotient might overflow
+        const float m_cut = fminf(m, 1024.f * t.six_tensor);
+        const float s0 = __fmul_rn(m_cut, t.inv_six);
+        const float s = __fmaf_rn(__fmaf_rn(-s0, t.six_tensor, m_cut), t.inv_six, s0);
         const __nv_fp8_storage_t s8 = __nv_cvt_float_to_fp8(s, __NV_SATFINITE, __NV_E4M3);
         scale = finite ? s8 : 0x7fu;
         const float d = __fmul_rn(__half2float(__nv_cvt_fp8_to_halfraw(s8, __NV_E4M3)), t.tensor);
-        const float r = s8 != 0 && finite ? __frcp_rn(d) : 0.f;
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+        r = s8 != 0 && finite ? __fmaf_rn(__fmaf_rn(-d, r, 1.f), r, r) : 0.f;
         const uint64_t r2 = f32x2(r, r), nd = f32x2(-d, -d);
         // past what the largest scale reaches a quotient can overflow, and the
         // correction would make it NaN

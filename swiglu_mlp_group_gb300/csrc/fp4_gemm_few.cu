@@ -203,71 +203,107 @@ fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
         __syncwarp();
     } else if constexpr (kQuant) {
         // ------------------------------------------------------------ quantizers
-        // A warp has a token's 256 columns of a stage, 8 a lane; the tokens go round
-        // the four warps, and the next stage's values are on their way.
-        constexpr int kMine = TN / 4;
-        const int t0 = warp - 2;
+        // Items (a token's 256 columns of a stage, 8 a lane) go round the four warps, stage
+        // after stage; a warp quantizes four at a time, the next four on their way: one
+        // alone is some 500 clocks from its load to its codes, most of them latency.
+        constexpr int kBatch = 4;
         constexpr int kGroup = NV ? 8 : 16;  // lanes of a word
+        const int step_kb = 4 / a.M, step_t = 4 - step_kb * a.M;
         pdl_wait();
         if (!a.early_trigger) pdl_launch_dependents();
-        uint4 u[kMine], v[kMine];
-        auto fetch = [&](int i) {
-            const int col = (kb0 + i) * kStageK + lane * 8;
+        struct Item {
+            int kb, t;
+        };
+        auto forward = [&](Item &it) {
+            it.kb += step_kb, it.t += step_t;
+            if (it.t >= a.M) it.t -= a.M, ++it.kb;
+        };
+        uint4 u[kBatch], v[FROM == From::kSwiglu ? kBatch : 1];
+        Item ahead{(warp - 2) / a.M, (warp - 2) % a.M}, now = ahead;
+        auto fetch = [&] {
 #pragma unroll
-            for (int j = 0; j < kMine; ++j) {
-                u[j] = v[j] = make_uint4(0, 0, 0, 0);
-                if (t0 + 4 * j < a.M && i < kbs && col < a.K) {
-                    const __nv_bfloat16 *p = a.x + (t0 + 4 * j) * a.ldx + col;
+            for (int j = 0; j < kBatch; ++j) {
+                const int col = (kb0 + ahead.kb) * kStageK + lane * 8;
+                u[j] = make_uint4(0, 0, 0, 0);
+                if constexpr (FROM == From::kSwiglu) v[j] = u[j];
+                if (ahead.kb < kbs && col < a.K) {
+                    const __nv_bfloat16 *p = a.x + ahead.t * a.ldx + col;
                     u[j] = *reinterpret_cast<const uint4 *>(p);
                     if constexpr (FROM == From::kSwiglu) v[j] = *reinterpret_cast<const uint4 *>(p + a.K);
                 }
+                forward(ahead);
             }
         };
-        fetch(0);
-        int s = 0;
+        fetch();
+        int kb = 0, s = 0;  // the stage that is being filled
         uint32_t ph = 1;
-        bool ok = true;
-        for (int i = 0; i < kbs; ++i) {
-            uint32_t codes[kMine], word[kMine];
+        bool waited = false, ok = true;
+        auto wait = [&] {  // (the first round's is over at once)
+            if (!waited) {
+                int got = 0;
+                if (lane == 0) got = mbar_wait_spin(empty(s), ph, ctl) ? 1 : 0;
+                ok = __shfl_sync(0xffffffffu, got, 0) != 0;
+                waited = true;
+            }
+            return ok;
+        };
+        // Hands the stages before `to` over.
+        auto hand_over = [&](int to) {
+            for (; kb < to; ++kb) {
+                if (!wait()) return;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full(s));
+                waited = false;
+                if (++s == kStages) s = 0, ph ^= 1u;
+            }
+        };
+        while (now.kb < kbs && ok) {
+            uint32_t codes[kBatch], word[kBatch];
+            uint64_t q[kBatch][4];
 #pragma unroll
-            for (int j = 0; j < kMine; ++j) {
-                codes[j] = word[j] = 0;
-                if (t0 + 4 * j >= a.M) continue;  // (uniform over the warp)
-                const uint32_t ru[4] = {u[j].x, u[j].y, u[j].z, u[j].w}, rv[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-                uint64_t q[4];
+            for (int j = 0; j < kBatch; ++j) {
+                const uint32_t ru[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float lo = __uint_as_float(ru[e] << 16), hi = __uint_as_float(ru[e] & 0xffff0000u);
-                    q[e] = FROM == From::kSwiglu ? f32x2(qc::silu_mul(lo, __uint_as_float(rv[e] << 16)),
-                                                         qc::silu_mul(hi, __uint_as_float(rv[e] & 0xffff0000u)))
-                                                 : f32x2(lo, hi);
+                    if constexpr (FROM == From::kSwiglu) {
+                        const uint32_t rv[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+                        q[j][e] = f32x2(qc::silu_mul(lo, __uint_as_float(rv[e] << 16)),
+                                        qc::silu_mul(hi, __uint_as_float(rv[e] & 0xffff0000u)));
+                    } else {
+                        q[j][e] = f32x2(lo, hi);
+                    }
                 }
+            }
+            fetch();
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
                 uint32_t scale;
-                codes[j] = fp4::quantize8<NV>(q, a.t, scale);
+                codes[j] = fp4::quantize8<NV>(q[j], a.t, scale);
                 word[j] = fp4::scale_word<NV>(scale, lane);
             }
-            fetch(i + 1);
-            int got = 0;
-            if (lane == 0) got = mbar_wait_spin(empty(s), ph, ctl) ? 1 : 0;  // (the first round's is over at once)
-            ok = __shfl_sync(0xffffffffu, got, 0) != 0;
-            if (!ok) break;
 #pragma unroll
-            for (int j = 0; j < kMine; ++j) {
-                const int t = t0 + 4 * j;
-                if (t >= a.M) continue;
-                // 128-byte rows, their 16-byte pieces swizzled by the row
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage(s) + kOffB + t * 128 + (((lane >> 2) ^ (t & 7)) << 4) + (lane & 3) * 4),
-                             "r"(codes[j])
-                             : "memory");
-                if (lane % kGroup == 0)
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage(s) + kOffSfb + lane / kGroup * 512 + t * 16), "r"(word[j])
-                                 : "memory");
+            for (int j = 0; j < kBatch; ++j) {
+                if (now.kb < kbs && ok) {
+                    hand_over(now.kb);
+                    if (ok && wait()) {
+                        // 128-byte rows, their 16-byte pieces swizzled by the row
+                        const int t = now.t;
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage(s) + kOffB + t * 128 + (((lane >> 2) ^ (t & 7)) << 4) +
+                                                                     (lane & 3) * 4),
+                                     "r"(codes[j])
+                                     : "memory");
+                        if (lane % kGroup == 0)
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage(s) + kOffSfb + lane / kGroup * 512 + t * 16),
+                                         "r"(word[j])
+                                         : "memory");
+                    }
+                }
+                forward(now);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(full(s));
-            if (++s == kStages) s = 0, ph ^= 1u;
         }
+        if (ok) hand_over(kbs);
     }
     // ---------------------------------------------------------------- epilogue
     // Column c of the tile is finished by the CTA of rank c / own.
@@ -387,7 +423,7 @@ cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx) {
     Args a = {};
     a.xs = g.xs, a.ws = g.ws;
     a.x = static_cast<const __nv_bfloat16 *>(g.x_bf16), a.ldx = g.ldx;
-    a.t = fp4::Scale{g.x_scale, 6.f * g.x_scale};
+    a.t = fp4::scale_of(g.x_scale);
     a.M = static_cast<int>(g.M), a.N = static_cast<int>(g.N), a.K = static_cast<int>(g.K);
     a.words = static_cast<int>(fp4_words(g.K, g.nv));
     a.splits = splits;

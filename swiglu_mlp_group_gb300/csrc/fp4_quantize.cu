@@ -123,7 +123,7 @@ cudaError_t launch_fp4_quantize(const void *x, bool x_f32, Act act, int64_t M, i
     const int64_t tasks = (M + kRowsPerWarp - 1) / kRowsPerWarp * ((K + 255) / 256);
     constexpr int kWarps = kThreads / 32;
     return launch(kernels[nv ? 1 : 0][static_cast<int>(in)], (tasks + kWarps - 1) / kWarps, ctx, x, M,
-                  static_cast<int>(K), ldx, fp4::Scale{tensor_scale, 6.f * tensor_scale}, codes, scales,
+                  static_cast<int>(K), ldx, fp4::scale_of(tensor_scale), codes, scales,
                   ctx.early_trigger);
 }
 
