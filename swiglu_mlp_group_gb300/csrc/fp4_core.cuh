@@ -45,6 +45,14 @@ __device__ __forceinline__ int64_t scale_word_at(int64_t row, int word, int word
     return ((row >> 7) * words + word) * 512 + (r & 31) * 16 + (r >> 5) * 4;
 }
 
+// A pair of bf16 as f32, and as f32 with the signs turned (one operation each).
+__device__ __forceinline__ uint64_t unpack2(uint32_t w) {
+    return f32x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint64_t unpack2_neg(uint32_t w) {
+    return f32x2(__uint_as_float(w * 65536u + 0x80000000u), __uint_as_float((w & 0xffff0000u) ^ 0x80000000u));
+}
+
 // Largest magnitude of three, a NaN if one of them is.
 __device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
     float d;
@@ -75,19 +83,22 @@ __device__ __forceinline__ uint32_t pack8(const uint64_t (&q)[4]) {
 }
 
 // Eight consecutive values of a row in each lane (two lanes hold an NV block,
-// four an MX block; lane 0's first value begins one) -> the lane's codes and the
-// block's scale byte.  Every lane of the warp takes part.
+// four an MX block; lane 0's first value begins one), their signs turned, -> the
+// lane's codes and the block's scale byte.  Every lane of the warp takes part.
+//
+// NV: with n = -x, q0 = n (-r), the remainder q0 d + n and q0 + remainder (-r): in
+// this form a zero keeps its sign.
 struct Scale {
     float tensor, six_tensor, inv_six;  // t, 6 t and 1 / (6 t)
 };
 inline Scale scale_of(float tensor) { return Scale{tensor, 6.f * tensor, 1.f / (6.f * tensor)}; }
 template <bool NV>
-__device__ __forceinline__ uint32_t quantize8(const uint64_t (&v)[4], const Scale &t, uint32_t &scale) {
+__device__ __forceinline__ uint32_t quantize8(const uint64_t (&n)[4], const Scale &t, uint32_t &scale) {
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float a, b;
-        f32x2_split(v[i], a, b);
+        f32x2_split(n[i], a, b);
         m = max3_abs_nan(m, a, b);
     }
     m = max_nan(m, __shfl_xor_sync(kFull, m, 1));
@@ -104,44 +115,40 @@ __device__ __forceinline__ uint32_t quantize8(const uint64_t (&v)[4], const Scal
         const float d = __fmul_rn(__half2float(__nv_cvt_fp8_to_halfraw(s8, __NV_E4M3)), t.tensor);
         float r;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
-        r = s8 != 0 && finite ? __fmaf_rn(__fmaf_rn(-d, r, 1.f), r, r) : 0.f;
-        const uint64_t r2 = f32x2(r, r), nd = f32x2(-d, -d);
-        // past what the largest scale reaches a quotient can overflow, and the
-        // correction would make it NaN
-        const bool clamp = !(s <= 448.f);
-        const float top = 8.f * d;
+        r = s8 != 0 ? __fmaf_rn(__fmaf_rn(d, -r, 1.f), -r, -r) : -0.f;  // -1 / d
+        const uint64_t r2 = f32x2(r, r), d2 = f32x2(d, d);
+        if (s <= 448.f) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint64_t x = v[i];
-            if (clamp) {
-                float a, b;
-                f32x2_split(x, a, b);
-                x = f32x2(fminf(fmaxf(a, -top), top), fminf(fmaxf(b, -top), top));
+            for (int i = 0; i < 4; ++i) {
+                const uint64_t q0 = mul_f32x2(n[i], r2);
+                q[i] = fma_f32x2(fma_f32x2(q0, d2, n[i]), r2, q0);
             }
-            const uint64_t q0 = mul_f32x2(x, r2);
-            // (the correction turns -0 into 0: the sign is x's)
-            q[i] = fma_f32x2(fma_f32x2(q0, nd, x), r2, q0) | (x & 0x8000000080000000ull);
+        } else {
+            // a quotient could overflow, and the correction would make it NaN
+            const float top = 8.f * d;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float a, b;
+                f32x2_split(n[i], a, b);
+                const uint64_t x = f32x2(fminf(fmaxf(a, -top), top), fminf(fmaxf(b, -top), top));
+                const uint64_t q0 = mul_f32x2(x, r2);
+                q[i] = fma_f32x2(fma_f32x2(q0, d2, x), r2, q0);
+            }
         }
     } else {
         const uint32_t e = __float_as_uint(m) >> 23;
         scale = finite ? (e > 2 ? e - 2 : 0u) : 0xffu;
-        const float r = finite ? __uint_as_float((254u - scale) << 23) : 0.f;
+        const float r = __uint_as_float(((254u - scale) << 23) | 0x80000000u);  // -2^-e (of a NaN scale: not a number)
         const uint64_t r2 = f32x2(r, r);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = mul_f32x2(v[i], r2);
+        for (int i = 0; i < 4; ++i) q[i] = mul_f32x2(n[i], r2);
     }
     return pack8(q);
 }
 
-// The word of four scales that a group of lanes holds (8 lanes, NV; 16, MX).
-template <bool NV>
-__device__ __forceinline__ uint32_t scale_word(uint32_t scale, int lane) {
-    constexpr int kStep = NV ? 2 : 4;  // lanes of a block
-    uint32_t w = scale << (8 * ((lane / kStep) & 3));
-    w |= __shfl_xor_sync(kFull, w, kStep);
-    w |= __shfl_xor_sync(kFull, w, 2 * kStep);
-    return w;
-}
+// Lanes of a block and of a word of four.
+constexpr int block_lanes(bool nv) { return nv ? 2 : 4; }
+constexpr int word_lanes(bool nv) { return nv ? 8 : 16; }
 
 }  // namespace fp4
 }  // namespace ck

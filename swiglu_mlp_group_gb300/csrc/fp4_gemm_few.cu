@@ -207,7 +207,7 @@ fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
         // after stage; a warp quantizes four at a time, the next four on their way: one
         // alone is some 500 clocks from its load to its codes, most of them latency.
         constexpr int kBatch = 4;
-        constexpr int kGroup = NV ? 8 : 16;  // lanes of a word
+        constexpr int kBlock = fp4::block_lanes(NV);
         const int step_kb = 4 / a.M, step_t = 4 - step_kb * a.M;
         pdl_wait();
         if (!a.early_trigger) pdl_launch_dependents();
@@ -259,29 +259,26 @@ fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
             }
         };
         while (now.kb < kbs && ok) {
-            uint32_t codes[kBatch], word[kBatch];
+            uint32_t codes[kBatch], scale[kBatch];
             uint64_t q[kBatch][4];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
                 const uint32_t ru[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float lo = __uint_as_float(ru[e] << 16), hi = __uint_as_float(ru[e] & 0xffff0000u);
                     if constexpr (FROM == From::kSwiglu) {
                         const uint32_t rv[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-                        q[j][e] = f32x2(qc::silu_mul(lo, __uint_as_float(rv[e] << 16)),
-                                        qc::silu_mul(hi, __uint_as_float(rv[e] & 0xffff0000u)));
+                        q[j][e] = f32x2(-qc::silu_mul(__uint_as_float(ru[e] << 16), __uint_as_float(rv[e] << 16)),
+                                        -qc::silu_mul(__uint_as_float(ru[e] & 0xffff0000u), __uint_as_float(rv[e] & 0xffff0000u)));
                     } else {
-                        q[j][e] = f32x2(lo, hi);
+                        q[j][e] = fp4::unpack2_neg(ru[e]);
                     }
                 }
             }
             fetch();
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-                uint32_t scale;
-                codes[j] = fp4::quantize8<NV>(q[j], a.t, scale);
-                word[j] = fp4::scale_word<NV>(scale, lane);
+                codes[j] = fp4::quantize8<NV>(q[j], a.t, scale[j]);
             }
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
@@ -294,9 +291,10 @@ fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
                                                                      (lane & 3) * 4),
                                      "r"(codes[j])
                                      : "memory");
-                        if (lane % kGroup == 0)
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage(s) + kOffSfb + lane / kGroup * 512 + t * 16),
-                                         "r"(word[j])
+                        if (lane % kBlock == 0)
+                            asm volatile("st.shared.u8 [%0], %1;" ::"r"(stage(s) + kOffSfb + lane / (4 * kBlock) * 512 + t * 16 +
+                                                                      (lane / kBlock & 3)),
+                                         "r"(scale[j])
                                          : "memory");
                     }
                 }

@@ -15,7 +15,9 @@ constexpr int kRowsPerWarp = 4;
 // Read once, written once: 2 bytes in and 0.56 (NV) or 0.53 (MX) out an element.
 // A lane has 8 columns, 16 bytes to load and 4 to store, so that a warp's load is
 // 512 bytes in a row; a warp takes 256 columns of 4 rows, whose loads are on
-// their way together and whose scale words lie next to each other.
+// their way together and whose scales lie next to each other.  What counts then is
+// instructions, of the ALU above all: addresses are worked out once for the four
+// rows, and each block's first lane stores its scale byte itself.
 enum class In : int { kBf16, kF32, kSwiglu };
 
 template <bool NV, In IN>
@@ -25,56 +27,58 @@ fp4_quantize_kernel(const void *__restrict__ x, int64_t M, int K, int64_t ldx, f
     if (early_trigger) pdl_launch_dependents();
     pdl_wait();
     if (!early_trigger) pdl_launch_dependents();
+    constexpr int kBlock = fp4::block_lanes(NV), kWord = fp4::word_lanes(NV);
     const int lane = threadIdx.x & 31;
-    const int segs = (K + 255) / 256;
+    const uint32_t segs = (static_cast<uint32_t>(K) + 255) / 256;
     const int words = static_cast<int>(fp4_words(K, NV));
     const int64_t task = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t row0 = task / segs * kRowsPerWarp;
-    const int col = static_cast<int>(task % segs) * 256 + lane * 8;
+    // (tasks are fewer than 2^35 and segs at most 128: 32 bits for calls of a usual size)
+    const int64_t quad = task <= 0xffffffffll ? static_cast<uint32_t>(task) / segs : task / segs;
+    const int64_t row0 = quad * kRowsPerWarp;
+    const int col = static_cast<int>(task - quad * segs) * 256 + lane * 8;
     if (row0 >= M) return;
+    const int rows = M - row0 < kRowsPerWarp ? static_cast<int>(M - row0) : kRowsPerWarp;
     const bool in = col < K;
     uint4 a[kRowsPerWarp], b[kRowsPerWarp];
+    const char *src = static_cast<const char *>(x) + (row0 * ldx + col) * (IN == In::kF32 ? 4 : 2);
+    const int64_t src_step = ldx * (IN == In::kF32 ? 4 : 2);
 #pragma unroll
     for (int i = 0; i < kRowsPerWarp; ++i) {
         a[i] = b[i] = make_uint4(0, 0, 0, 0);
-        if (!in || row0 + i >= M) continue;
-        if constexpr (IN == In::kF32) {
-            const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(x) + (row0 + i) * ldx + col);
-            a[i] = __ldg(p), b[i] = __ldg(p + 1);
-        } else {
-            const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(x) + (row0 + i) * ldx + col;
-            a[i] = __ldg(reinterpret_cast<const uint4 *>(p));
-            if constexpr (IN == In::kSwiglu) b[i] = __ldg(reinterpret_cast<const uint4 *>(p + K));
+        if (in && i < rows) {
+            a[i] = __ldg(reinterpret_cast<const uint4 *>(src));
+            if constexpr (IN == In::kF32) b[i] = __ldg(reinterpret_cast<const uint4 *>(src) + 1);
+            if constexpr (IN == In::kSwiglu) b[i] = __ldg(reinterpret_cast<const uint4 *>(src + 2 * K));
         }
+        src += src_step;
     }
-    const int group = NV ? 8 : 16;  // lanes of a word
+    uint8_t *code = codes + row0 * (K / 2) + col / 2;
+    // four rows from a multiple of four on: their words 16 bytes apart
+    const int word = col / (8 * kWord);
+    uint8_t *scale_at = scales + fp4::scale_word_at(row0, word, words) + (lane / kBlock & 3);
+    const bool has_scale = word < words && lane % kBlock == 0;
 #pragma unroll
     for (int i = 0; i < kRowsPerWarp; ++i) {
-        if (row0 + i >= M) break;
+        if (i >= rows) break;
         const uint32_t ra[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, rb[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
-        uint64_t v[4];
+        uint64_t n[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if constexpr (IN == In::kF32) {
                 const uint32_t *r = j < 2 ? ra : rb;
-                v[j] = f32x2(__uint_as_float(r[2 * (j & 1)]), __uint_as_float(r[2 * (j & 1) + 1]));
+                n[j] = f32x2(-__uint_as_float(r[2 * (j & 1)]), -__uint_as_float(r[2 * (j & 1) + 1]));
+            } else if constexpr (IN == In::kSwiglu) {
+                n[j] = f32x2(-qc::silu_mul(__uint_as_float(ra[j] << 16), __uint_as_float(rb[j] << 16)),
+                             -qc::silu_mul(__uint_as_float(ra[j] & 0xffff0000u), __uint_as_float(rb[j] & 0xffff0000u)));
             } else {
-                const float lo = __uint_as_float(ra[j] << 16), hi = __uint_as_float(ra[j] & 0xffff0000u);
-                if constexpr (IN == In::kSwiglu)
-                    v[j] = f32x2(qc::silu_mul(lo, __uint_as_float(rb[j] << 16)),
-                                 qc::silu_mul(hi, __uint_as_float(rb[j] & 0xffff0000u)));
-                else
-                    v[j] = f32x2(lo, hi);
+                n[j] = fp4::unpack2_neg(ra[j]);
             }
         }
         uint32_t scale;
-        const uint32_t q = fp4::quantize8<NV>(v, t, scale);
-        const uint32_t word = fp4::scale_word<NV>(in ? scale : 0u, lane);
-        if (in) {
-            *reinterpret_cast<uint32_t *>(codes + (row0 + i) * (K / 2) + col / 2) = q;
-            if (lane % group == 0)
-                *reinterpret_cast<uint32_t *>(scales + fp4::scale_word_at(row0 + i, col / (8 * group), words)) = word;
-        }
+        const uint32_t q = fp4::quantize8<NV>(n, t, scale);
+        if (in) *reinterpret_cast<uint32_t *>(code) = q;
+        if (has_scale) scale_at[16 * i] = static_cast<uint8_t>(scale);
+        code += K / 2;
     }
 }
 
