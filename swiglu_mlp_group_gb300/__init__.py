@@ -457,7 +457,7 @@ def _call_device(x, what: str) -> int:
     dev = x.get_device()
     if dev < 0:
         raise ValueError(f"{what} must be a CUDA tensor")
-    if dev != _torch().cuda.current_device():
+    if dev != _torch()._C._cuda_getDevice():
         raise ValueError(f"{what} is on cuda:{dev}, which is not the current device")
     return dev
 
@@ -735,12 +735,13 @@ def _row_stride(x, dtype, what: str, dev: int, shape=None) -> int:
     if x.dtype is not dtype or x.get_device() != dev:
         raise ValueError(f"{what} must be a tensor of {dtype} on cuda:{dev}")
     xs = x.shape
-    if len(xs) != 2 or (shape is not None and xs != shape):
-        raise ValueError(f"{what} must have shape {tuple(shape) if shape is not None else '[rows, columns]'}")
+    if (len(xs) != 2) if shape is None else (xs != shape):
+        raise ValueError(f"{what} must have shape {'[rows, columns]' if shape is None else tuple(shape)}")
+    rows, columns = xs
     ld, inner = x.stride()
-    if inner != 1 and xs[1] > 1:
+    if inner != 1 and columns > 1:
         raise ValueError(f"{what}: the elements of a row must lie next to each other")
-    return ld if xs[0] > 1 else xs[1]
+    return ld if rows > 1 else columns
 
 
 def _fp4_format(fmt: str) -> int:
@@ -881,9 +882,10 @@ def fp4_linear(x, W, w_scales, fmt: str, x_scale: float = 1.0, w_scale: float = 
     N, Kw, pw, pws = _fp4_operand(W, w_scales, f, "W", dev)
     if Kw != K:
         raise ValueError("x and W must have the same columns")
-    pb, pr = _typed(bias, bf16, "bias", dev, (N,)), _typed(residual, bf16, "residual", dev, (M, N))
+    pb = None if bias is None else _typed(bias, bf16, "bias", dev, (N,))
+    pr = None if residual is None else _typed(residual, bf16, "residual", dev, (M, N))
     y = _out_rows(out, M, N, dev, stream)
-    ws = (_given_workspace(workspace, dev) if workspace is not None else fp4_linear_workspace(M, K, fmt, dev, stream))
+    ws = _given_workspace(workspace, dev) if workspace is not None else fp4_linear_workspace(M, K, fmt, dev, stream)
     st = lib().ck_fp4_linear(x.data_ptr(), M, K, ldx, a, f, x_scale, pw, pws, w_scale, N, pb, pr, y.data_ptr(),
                              ws.data_ptr(), ws.nbytes, _run_stream(stream, dev))
     if st != CK_OK:
@@ -927,8 +929,7 @@ def fp4_swiglu_mlp(x, Wgu, gu_scales, Wd, d_scales, fmt: str, x_scale: float = 1
 def _norm_call(x, branch, post_weight, gate, scale, shift, tokens_per_group, x_factor, branch_factor, norm, weight,
                bias, eps, h_out, stream):
     """What block_norm and block_norm_fp4 share -> (C arguments up to h_out's, h, device)."""
-    torch = _torch()
-    bf16 = torch.bfloat16
+    bf16 = _torch().bfloat16
     dev = _call_device(x, "x")
     ldx = _row_stride(x, bf16, "x", dev)
     shape = x.shape
@@ -936,7 +937,7 @@ def _norm_call(x, branch, post_weight, gate, scale, shift, tokens_per_group, x_f
     kind = _NORMS.get(norm)
     if kind is None:
         raise ValueError("norm must be 'rms' or 'layer'")
-    pb = pg = psc = psh = ph = None
+    pb = pg = psc = psh = pp = pw = pbias = ph = None
     ldb = ldh = 0
     ldm = H
     if branch is not None:
@@ -955,13 +956,20 @@ def _norm_call(x, branch, post_weight, gate, scale, shift, tokens_per_group, x_f
             raise ValueError("gate, scale and shift must have their rows at one stride")
         ldm = rows.pop()
         pg, psc, psh = _ptr(gate), _ptr(scale), _ptr(shift)
-    dt, wdt = _weight_type(post_weight, weight, bias)
-    pp, pw, pbias = (None if w is None else _typed(w, dt, what, dev, (H,))
-                     for w, what in ((post_weight, "post_weight"), (weight, "weight"), (bias, "bias")))
+    wdt = CK_BF16
+    if weight is not None or bias is not None or post_weight is not None:
+        dt, wdt = _weight_type(weight, bias, post_weight)
+        vector = (H,)
+        if weight is not None:
+            pw = _typed(weight, dt, "weight", dev, vector)
+        if bias is not None:
+            pbias = _typed(bias, dt, "bias", dev, vector)
+        if post_weight is not None:
+            pp = _typed(post_weight, dt, "post_weight", dev, vector)
     if h_out is not None:
         ph, ldh = h_out.data_ptr(), _row_stride(h_out, bf16, "h_out", dev, shape)
     elif branch is not None or x_factor != 1.0:
-        h_out, ldh = _new_on(shape, bf16, dev, stream), H
+        h_out, ldh = _new_like(x, stream), H
         ph = h_out.data_ptr()
     else:
         h_out = x  # without a branch and a factor the stream itself is h
@@ -981,8 +989,7 @@ def block_norm(x, branch=None, post_weight=None, gate=None, x_factor: float = 1.
     args, h, dev = _norm_call(x, branch, post_weight, gate, scale, shift, tokens_per_group, x_factor, branch_factor,
                               norm, weight, bias, eps, h_out, stream)
     if n_out is None:
-        shape = x.shape
-        n_out, ldn = _new_on(shape, x.dtype, dev, stream), shape[1]
+        n_out, ldn = _new_like(x, stream), args[5]
     else:
         ldn = _row_stride(n_out, x.dtype, "n_out", dev, x.shape)
     st = lib().ck_block_norm(*args, n_out.data_ptr(), ldn, _run_stream(stream, dev))

@@ -35,22 +35,22 @@ cudaError_t launch_fp4_tile_scales(const uint8_t *scales, int64_t rows, int64_t 
 // scales.  weights_settled: nothing in flight writes W or its scales once the kernel
 // has been let in.
 struct Fp4Gemm {
-    const uint8_t *x, *xs;
-    const void *x_bf16;
-    int64_t ldx;
-    bool swiglu;
-    float x_scale;
-    const uint8_t *w, *ws;
-    int64_t M, N, K;
-    bool nv;
-    float alpha;
-    const void *bias, *residual;
-    void *y;
-    bool weights_settled;
+    const uint8_t *x = nullptr, *xs = nullptr;
+    const void *x_bf16 = nullptr;
+    int64_t ldx = 0;
+    bool swiglu = false;
+    float x_scale = 1.f;
+    const uint8_t *w = nullptr, *ws = nullptr;
+    int64_t M = 0, N = 0, K = 0;
+    bool nv = false;
+    float alpha = 1.f;
+    const void *bias = nullptr, *residual = nullptr;
+    void *y = nullptr;
+    bool weights_settled = false;
 };
 cudaError_t launch_fp4_gemm(const Fp4Gemm &g, const LaunchCtx &ctx);
 // Most tokens that a product quantizes itself.
-constexpr int64_t kFp4QuantizeInside = 16;
+constexpr int64_t kFp4QuantizeInside = 8;
 // its kernels for few tokens and for many
 cudaError_t launch_fp4_gemm_few(const Fp4Gemm &g, const LaunchCtx &ctx);
 cudaError_t launch_fp4_gemm_pair(const Fp4Gemm &g, const LaunchCtx &ctx);

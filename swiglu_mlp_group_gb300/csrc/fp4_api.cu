@@ -77,7 +77,7 @@ ck_status check_rows(const void *x, int64_t M, int64_t K, int64_t ldx, ck_input_
 
 ck::Fp4Gemm gemm(const uint8_t *x, const uint8_t *xs, int64_t M, int64_t K, bool nv, const void *W, const void *ws,
                  int64_t N, float alpha, const void *bias, const void *residual, void *y, bool settled) {
-    ck::Fp4Gemm g = {};
+    ck::Fp4Gemm g;
     g.x = x, g.xs = xs, g.w = static_cast<const uint8_t *>(W), g.ws = static_cast<const uint8_t *>(ws);
     g.M = M, g.N = N, g.K = K, g.nv = nv, g.alpha = alpha;
     g.bias = bias, g.residual = residual, g.y = y;

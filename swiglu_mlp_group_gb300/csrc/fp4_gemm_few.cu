@@ -12,10 +12,10 @@
 // CTAs' ranks (f32: the result does not depend on timing).
 //
 // Roles (6 warps): warp 0 TMA producer, warp 1 TMEM and MMA issue, warps 2..5 the
-// epilogue (one 32-lane quarter of TMEM each).  With up to 16 tokens these four also
-// quantize: x comes as bf16 and every CTA quantizes its own columns of it into the
-// stages, while the weight is on its way, instead of a kernel ahead (blocks need
-// nothing beyond themselves, so a CTA does with its share of K).
+// epilogue (one 32-lane quarter of TMEM each).  Up to 8 tokens can come as bf16: these
+// four and four more then quantize, every CTA its own columns of x into the stages
+// while the weight is on its way, instead of a kernel ahead (a block needs nothing
+// beyond itself, so a CTA does with its share of K).
 #include <cuda_bf16.h>
 
 #include "fp4_core.cuh"
@@ -25,7 +25,8 @@
 namespace ck {
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 192;            // without the four more
+constexpr int kQuantWarps = 8;
 constexpr int kRows = 128;               // rows of W a CTA
 constexpr int kStageK = 256;             // 128 bytes of codes a row
 constexpr int kABytes = kRows * kStageK / 2;
@@ -40,17 +41,14 @@ struct Cfg {
     static constexpr int kSfBytes = kWords * 512;
     static constexpr int kBBytes = TN * kStageK / 2;
     static constexpr int kStageBytes = kABytes + kBBytes + 2 * kSfBytes;
-    // partial sums: beside the stages, so that a CTA may send its own while another
-    // still multiplies; in their place where the stages need the room
+    // partial sums, beside the stages: a CTA may send its own while another multiplies
     static constexpr int kRedBytes = TN * kRows * 4;
-    static constexpr bool kOwnRed = TN <= 16;
-    static constexpr int kStages = (kCtaBytes - 1024 - 256 - (kOwnRed ? kRedBytes : 0)) / kStageBytes;
-    static constexpr int kTmemSf = TN < 32 ? 32 : TN;  // first column of the scales
-    static constexpr int kTmemCols = kTmemSf + 32 <= 64 ? 64 : (kTmemSf + 32 <= 128 ? 128 : 256);
-    static constexpr size_t kSmemBytes =
-        static_cast<size_t>(kStages) * kStageBytes + (kOwnRed ? kRedBytes : 0) + 256 + 1024;
+    static constexpr int kStages = (kCtaBytes - 1024 - 256 - kRedBytes) / kStageBytes;
+    static constexpr int kTmemSf = 32;  // first column of the scales
+    static constexpr int kTmemCols = 64;
+    static constexpr size_t kSmemBytes = static_cast<size_t>(kStages) * kStageBytes + kRedBytes + 256 + 1024;
+    static_assert(kTmemSf + 32 <= kTmemCols, "TMEM");
     static_assert(kStageBytes % 1024 == 0 && kStages >= 3 && 8 * (2 * kStages + 1) + 8 <= 256, "stage");
-    static_assert(kOwnRed || kRedBytes <= kStages * kStageBytes, "partial sums");
 };
 
 struct Args {
@@ -68,7 +66,7 @@ struct Args {
 };
 
 template <int TN, bool NV, From FROM>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(FROM == From::kCodes ? kThreads : kThreads + 128, 2)
 fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                     const __grid_constant__ Args a) {
     using C = Cfg<TN, NV>;
@@ -77,9 +75,9 @@ fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_s = smem_u32(smem_raw);
     const uint32_t smem_s = (raw_s + 1023u) & ~1023u;
-    const uint32_t red_s = C::kOwnRed ? smem_s + kStages * C::kStageBytes : smem_s;
+    const uint32_t red_s = smem_s + kStages * C::kStageBytes;
     const float *red = reinterpret_cast<const float *>(smem_raw + (red_s - raw_s));
-    const uint32_t bars_s = smem_s + kStages * C::kStageBytes + (C::kOwnRed ? C::kRedBytes : 0);
+    const uint32_t bars_s = red_s + C::kRedBytes;
     uint8_t *bars = smem_raw + (bars_s - raw_s);
     auto full = [&](int s) { return bars_s + 8u * s; };
     auto empty = [&](int s) { return bars_s + 8u * (kStages + s); };
@@ -100,7 +98,7 @@ fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(full(s), kQuant ? 5 : 1);  // the copies, and the quantizers' warps
+            mbar_init(full(s), kQuant ? 1 + kQuantWarps : 1);  // the copies, and the quantizers' warps
             mbar_init(empty(s), 1);
         }
         mbar_init(done, 1);
@@ -114,7 +112,7 @@ fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if constexpr (C::kOwnRed) cluster_arrive();  // waited for before another CTA's shared memory is written
+    cluster_arrive();  // waited for before another CTA's shared memory is written
     const uint32_t tmem = *tmem_slot;
     // A kernel behind this one that reads what settles before it (a weight) may do so
     // once let in: with x quantized here, no kernel ahead has waited for it.
@@ -203,12 +201,12 @@ fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
         __syncwarp();
     } else if constexpr (kQuant) {
         // ------------------------------------------------------------ quantizers
-        // Items (a token's 256 columns of a stage, 8 a lane) go round the four warps, stage
+        // Items (a token's 256 columns of a stage, 8 a lane) go round the warps, stage
         // after stage; a warp quantizes four at a time, the next four on their way: one
         // alone is some 500 clocks from its load to its codes, most of them latency.
         constexpr int kBatch = 4;
         constexpr int kBlock = fp4::block_lanes(NV);
-        const int step_kb = 4 / a.M, step_t = 4 - step_kb * a.M;
+        const int step_kb = kQuantWarps / a.M, step_t = kQuantWarps - step_kb * a.M;
         pdl_wait();
         if (!a.early_trigger) pdl_launch_dependents();
         struct Item {
@@ -307,18 +305,16 @@ fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
     // Column c of the tile is finished by the CTA of rank c / own.
     const int own = TN / a.splits;
     bool ok = true;
-    if (warp >= 2) {
+    const bool finishes = warp >= 2 && warp < 6;
+    if (finishes) {
         int got = 0;
         if (lane == 0) got = mbar_wait(done, 0, ctl) ? 1 : 0;
         ok = __shfl_sync(0xffffffffu, got, 0) != 0;
         tc_fence_after_sync();
     }
     __syncwarp();
-    if constexpr (C::kOwnRed)
-        cluster_wait();  // every CTA of the cluster has begun
-    else
-        cluster_sync();  // every CTA's products are done with its stages
-    if (warp >= 2) {
+    cluster_wait();  // every CTA of the cluster has begun
+    if (finishes) {
         const int q = warp & 3;
         if (ok) {
             const int r = q * 32 + lane;
@@ -341,7 +337,7 @@ fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
         tc_fence_before_sync();
     }
     cluster_sync();
-    if (warp >= 2 && !*abort_flag) {
+    if (finishes && !*abort_flag) {
         const int t = threadIdx.x - 64;
         const int n = n0 + 2 * (t & 63);
         if (n < a.N) {
@@ -406,7 +402,7 @@ cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx) {
     while (splits < 8 && n_tiles * m_tiles * splits * 2 <= 2 * sms && splits * 2 <= num_kb) splits *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(n_tiles * splits), static_cast<unsigned>(m_tiles));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(FROM == From::kCodes ? kThreads : kThreads + 128);
     cfg.dynamicSmemBytes = C::kSmemBytes;
     cfg.stream = ctx.stream;
     cudaLaunchAttribute attr[2];
@@ -436,15 +432,12 @@ cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx) {
 template <bool NV>
 cudaError_t launch_n(const Fp4Gemm &g, const LaunchCtx &ctx) {
     if (g.x_bf16 != nullptr) {
-        if (g.swiglu)
-            return g.M <= 8 ? launch_t<8, NV, From::kSwiglu>(g, ctx) : launch_t<16, NV, From::kSwiglu>(g, ctx);
-        return g.M <= 8 ? launch_t<8, NV, From::kBf16>(g, ctx) : launch_t<16, NV, From::kBf16>(g, ctx);
+        if (g.M > kFp4QuantizeInside) return cudaErrorInvalidValue;
+        return g.swiglu ? launch_t<8, NV, From::kSwiglu>(g, ctx) : launch_t<8, NV, From::kBf16>(g, ctx);
     }
     if (g.M <= 8) return launch_t<8, NV, From::kCodes>(g, ctx);
     if (g.M <= 16) return launch_t<16, NV, From::kCodes>(g, ctx);
-    if (g.M <= 32) return launch_t<32, NV, From::kCodes>(g, ctx);
-    if (g.M <= 64) return launch_t<64, NV, From::kCodes>(g, ctx);
-    return launch_t<128, NV, From::kCodes>(g, ctx);
+    return launch_t<32, NV, From::kCodes>(g, ctx);
 }
 
 }  // namespace
@@ -453,8 +446,12 @@ cudaError_t launch_fp4_gemm_few(const Fp4Gemm &g, const LaunchCtx &ctx) {
     return g.nv ? launch_n<true>(g, ctx) : launch_n<false>(g, ctx);
 }
 
+// Up to 32 tokens the weight's bytes count, and a tile of 256 tokens leaves most SMs
+// without any (32 x 4096 -> 4096: 6.5 us against 8.1); from 33 on a second tile of
+// tokens costs the few-token kernel more than that (33: 7.4 against 8.2, but 8.6 of
+// the other's at -> 12288 against 12.4).
 cudaError_t launch_fp4_gemm(const Fp4Gemm &g, const LaunchCtx &ctx) {
-    return g.M > 128 ? launch_fp4_gemm_pair(g, ctx) : launch_fp4_gemm_few(g, ctx);
+    return g.M > 32 ? launch_fp4_gemm_pair(g, ctx) : launch_fp4_gemm_few(g, ctx);
 }
 
 }  // namespace ck
