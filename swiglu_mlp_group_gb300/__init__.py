@@ -732,16 +732,15 @@ def cross_attention(q, k, v, kv_lens=None, scale: float | None = None, out=None,
 
 def _row_stride(x, dtype, what: str, dev: int, shape=None) -> int:
     """Elements from one row of x (2-D, of this type and shape, on the call's device) to the next."""
-    if x.dtype is not dtype or x.get_device() != dev:
-        raise ValueError(f"{what} must be a tensor of {dtype} on cuda:{dev}")
     xs = x.shape
-    if (len(xs) != 2) if shape is None else (xs != shape):
-        raise ValueError(f"{what} must have shape {'[rows, columns]' if shape is None else tuple(shape)}")
-    rows, columns = xs
-    ld, inner = x.stride()
-    if inner != 1 and columns > 1:
+    if x.dtype is dtype and x.get_device() == dev and (xs == shape if shape is not None else len(xs) == 2):
+        ld, inner = x.stride()
+        if inner == 1 or xs[1] <= 1:
+            return ld if xs[0] > 1 else xs[1]
         raise ValueError(f"{what}: the elements of a row must lie next to each other")
-    return ld if rows > 1 else columns
+    if len(xs) != 2 or (shape is not None and xs != shape):
+        raise ValueError(f"{what} must have shape {'[rows, columns]' if shape is None else tuple(shape)}")
+    raise ValueError(f"{what} must be a tensor of {dtype} on cuda:{dev}")
 
 
 def _fp4_format(fmt: str) -> int:
@@ -766,23 +765,25 @@ def _tiled_bytes(f: int, rows: int, K: int) -> int:
 def _fp4_operand(codes, scales, f: int, what: str, dev: int):
     """(rows, K, pointers) of codes [rows, K / 2] and their tiled scales."""
     u8 = _torch().uint8
-    p, ps = _typed(codes, u8, what, dev), _typed(scales, u8, f"{what}'s scales", dev)
     shape = codes.shape
     if len(shape) != 2:
         raise ValueError(f"{what} must be codes [rows, K / 2]")
-    rows, K = shape[0], 2 * shape[1]
-    if scales.nbytes < _tiled_bytes(f, rows, K):
+    rows, half = shape
+    p, ps = _typed(codes, u8, what, dev), _typed(scales, u8, "scales", dev)
+    if scales.numel() < (rows + 127) // 128 * (half + 31 >> 5 if f else half + 63 >> 6) * 512:
         raise ValueError(f"{what}'s scales must be tiled scales of these codes")
-    return rows, K, p, ps
+    return rows, 2 * half, p, ps
 
 
 def _out_rows(out, M: int, N: int, dev: int, stream):
-    """A linear's output: the one given (contiguous bf16 [M, N]) or a new one."""
+    """A linear's output (contiguous bf16 [M, N]): the one given, checked, or a new one."""
     torch = _torch()
-    if out is None:
-        return _new_on((M, N), torch.bfloat16, dev, stream)
-    _typed(out, torch.bfloat16, "out", dev, (M, N))
-    return out
+    if out is not None:
+        _typed(out, torch.bfloat16, "out", dev, (M, N))
+        return out
+    if stream is None:
+        return torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    return _new_on((M, N), torch.bfloat16, dev, stream)
 
 
 def _scales_out(scales, n: int, dev: int, stream):

@@ -47,13 +47,23 @@ struct Fp4Gemm {
     const void *bias = nullptr, *residual = nullptr;
     void *y = nullptr;
     bool weights_settled = false;
+    // launch_fp4_gemm_glu's result
+    uint8_t *a_codes = nullptr, *a_scales = nullptr;
+    float a_scale = 1.f;
 };
 cudaError_t launch_fp4_gemm(const Fp4Gemm &g, const LaunchCtx &ctx);
 // Most tokens that a product quantizes itself.
 constexpr int64_t kFp4QuantizeInside = 8;
+// Most tokens of its kernel for few.
+constexpr int64_t kFp4Few = 32;
 // its kernels for few tokens and for many
 cudaError_t launch_fp4_gemm_few(const Fp4Gemm &g, const LaunchCtx &ctx);
 cudaError_t launch_fp4_gemm_pair(const Fp4Gemm &g, const LaunchCtx &ctx);
+// The product with W = [gate | up] of 2 N rows, N a multiple of 64, and from the bf16
+// gate and up (with bias; no residual) silu(gate) * up, quantized with tensor scale
+// a_scale: a_codes [M, N / 2] and tiled a_scales, the same as a linear, then the
+// quantizer, would leave.
+cudaError_t launch_fp4_gemm_glu(const Fp4Gemm &g, const LaunchCtx &ctx);
 
 enum class Norm : int { kRms = 0, kLayer = 1 };
 

@@ -257,6 +257,21 @@ CK_API ck_status ck_fp4_swiglu_mlp(const void *x, int64_t M, int64_t H, int64_t 
     if (!aligned16(ws)) return CK_ERR_ALIGN;
     unsigned int *status = nullptr;
     if (int st = ck::device_ready_status(&status); st != CK_OK) return static_cast<ck_status>(st);
+    if (M > ck::kFp4Few && I % 64 == 0) {
+        // gate and up never leave the chip as such: the first product's epilogue
+        // quantizes silu(gate) * up (up's rows of a tile begin at a half or a whole of
+        // 128 rows of scales for such I)
+        if (ck::launch_fp4_quantize(x, false, ck::Act::kNone, M, H, H, nv, x_scale, at(ws, w.x.codes), at(ws, w.x.scales),
+                                    quantizer_context(stream, status)) != cudaSuccess)
+            return CK_ERR_CUDA;
+        ck::Fp4Gemm g = gemm(at(ws, w.x.codes), at(ws, w.x.scales), M, H, nv, Wgu, gu_scales, I, x_scale * gu_scale, bgu,
+                             nullptr, nullptr, true);
+        g.a_codes = at(ws, w.a.codes), g.a_scales = at(ws, w.a.scales), g.a_scale = a_scale;
+        if (ck::launch_fp4_gemm_glu(g, context(stream, status)) != cudaSuccess) return CK_ERR_CUDA;
+        return from_cuda(ck::launch_fp4_gemm(gemm(at(ws, w.a.codes), at(ws, w.a.scales), M, I, nv, Wd, d_scales, H,
+                                                  a_scale * d_scale, bd, residual, y, true),
+                                             context(stream, status)));
+    }
     if (ck_status st = run_linear(x, M, H, H, CK_ACT_NONE, nv, x_scale, Wgu, gu_scales, gu_scale, 2 * I, bgu, nullptr,
                                   at(ws, w.h), ws, w.x, status, stream);
         st != CK_OK)

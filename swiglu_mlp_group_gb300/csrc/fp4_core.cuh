@@ -82,31 +82,25 @@ __device__ __forceinline__ uint32_t pack8(const uint64_t (&q)[4]) {
     return r;
 }
 
-// Eight consecutive values of a row in each lane (two lanes hold an NV block,
-// four an MX block; lane 0's first value begins one), their signs turned, -> the
-// lane's codes and the block's scale byte.  Every lane of the warp takes part.
-//
-// NV: with n = -x, q0 = n (-r), the remainder q0 d + n and q0 + remainder (-r): in
-// this form a zero keeps its sign.
+// A tensor's scale.
 struct Scale {
     float tensor, six_tensor, inv_six;  // t, 6 t and 1 / (6 t)
 };
 inline Scale scale_of(float tensor) { return Scale{tensor, 6.f * tensor, 1.f / (6.f * tensor)}; }
+
+// What a block's values are divided by, from its largest magnitude (a NaN if it has
+// one), and its scale byte.
+struct Divisor {
+    uint64_t r2;   // -1 / d twice (MX: of a NaN scale not a number)
+    uint64_t d2;   // d twice (NV)
+    bool cut;      // NV: the scale is cut off, and a quotient could overflow
+};
 template <bool NV>
-__device__ __forceinline__ uint32_t quantize8(const uint64_t (&n)[4], const Scale &t, uint32_t &scale) {
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float a, b;
-        f32x2_split(n[i], a, b);
-        m = max3_abs_nan(m, a, b);
-    }
-    m = max_nan(m, __shfl_xor_sync(kFull, m, 1));
-    if constexpr (!NV) m = max_nan(m, __shfl_xor_sync(kFull, m, 2));
+__device__ __forceinline__ Divisor divisor(float m, const Scale &t, uint32_t &scale) {
+    Divisor v;
     const bool finite = m < __int_as_float(0x7f800000);
-    uint64_t q[4];
     if constexpr (NV) {
-        // past 448 the scale is cut off; so far past it the quotient might overflow
+        // past 448 the scale is cut off; so far past it this quotient might overflow, too
         const float m_cut = fminf(m, 1024.f * t.six_tensor);
         const float s0 = __fmul_rn(m_cut, t.inv_six);
         const float s = __fmaf_rn(__fmaf_rn(-s0, t.six_tensor, m_cut), t.inv_six, s0);
@@ -115,35 +109,68 @@ __device__ __forceinline__ uint32_t quantize8(const uint64_t (&n)[4], const Scal
         const float d = __fmul_rn(__half2float(__nv_cvt_fp8_to_halfraw(s8, __NV_E4M3)), t.tensor);
         float r;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
-        r = s8 != 0 ? __fmaf_rn(__fmaf_rn(d, -r, 1.f), -r, -r) : -0.f;  // -1 / d
-        const uint64_t r2 = f32x2(r, r), d2 = f32x2(d, d);
-        if (s <= 448.f) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint64_t q0 = mul_f32x2(n[i], r2);
-                q[i] = fma_f32x2(fma_f32x2(q0, d2, n[i]), r2, q0);
-            }
-        } else {
-            // a quotient could overflow, and the correction would make it NaN
-            const float top = 8.f * d;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float a, b;
-                f32x2_split(n[i], a, b);
-                const uint64_t x = f32x2(fminf(fmaxf(a, -top), top), fminf(fmaxf(b, -top), top));
-                const uint64_t q0 = mul_f32x2(x, r2);
-                q[i] = fma_f32x2(fma_f32x2(q0, d2, x), r2, q0);
-            }
-        }
+        r = s8 != 0 ? __fmaf_rn(__fmaf_rn(d, -r, 1.f), -r, -r) : -0.f;
+        v.r2 = f32x2(r, r), v.d2 = f32x2(d, d);
+        v.cut = !(s <= 448.f);
     } else {
         const uint32_t e = __float_as_uint(m) >> 23;
         scale = finite ? (e > 2 ? e - 2 : 0u) : 0xffu;
-        const float r = __uint_as_float(((254u - scale) << 23) | 0x80000000u);  // -2^-e (of a NaN scale: not a number)
-        const uint64_t r2 = f32x2(r, r);
+        const float r = __uint_as_float(((254u - scale) << 23) | 0x80000000u);
+        v.r2 = f32x2(r, r), v.d2 = 0, v.cut = false;
+    }
+    return v;
+}
+
+// Codes of eight values, their signs turned.  NV: with n = -x, q0 = n (-r), the
+// remainder q0 d + n and q0 + remainder (-r): in this form a zero keeps its sign.
+template <bool NV>
+__device__ __forceinline__ uint32_t codes8(const uint64_t (&n)[4], const Divisor &v) {
+    uint64_t q[4];
+    if constexpr (!NV) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = mul_f32x2(n[i], r2);
+        for (int i = 0; i < 4; ++i) q[i] = mul_f32x2(n[i], v.r2);
+    } else if (!v.cut) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint64_t q0 = mul_f32x2(n[i], v.r2);
+            q[i] = fma_f32x2(fma_f32x2(q0, v.d2, n[i]), v.r2, q0);
+        }
+    } else {
+        // an infinite quotient's correction would be NaN
+        float d, unused;
+        f32x2_split(v.d2, d, unused);
+        const float top = 8.f * d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float a, b;
+            f32x2_split(n[i], a, b);
+            const uint64_t x = f32x2(fminf(fmaxf(a, -top), top), fminf(fmaxf(b, -top), top));
+            const uint64_t q0 = mul_f32x2(x, v.r2);
+            q[i] = fma_f32x2(fma_f32x2(q0, v.d2, x), v.r2, q0);
+        }
     }
     return pack8(q);
+}
+
+__device__ __forceinline__ float amax8(const uint64_t (&n)[4], float m) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a, b;
+        f32x2_split(n[i], a, b);
+        m = max3_abs_nan(m, a, b);
+    }
+    return m;
+}
+
+// Eight consecutive values of a row in each lane (two lanes hold an NV block,
+// four an MX block; lane 0's first value begins one), their signs turned, -> the
+// lane's codes and the block's scale byte.  Every lane of the warp takes part.
+template <bool NV>
+__device__ __forceinline__ uint32_t quantize8(const uint64_t (&n)[4], const Scale &t, uint32_t &scale) {
+    float m = amax8(n, 0.f);
+    m = max_nan(m, __shfl_xor_sync(kFull, m, 1));
+    if constexpr (!NV) m = max_nan(m, __shfl_xor_sync(kFull, m, 2));
+    return codes8<NV>(n, divisor<NV>(m, t, scale));
 }
 
 // Lanes of a block and of a word of four.

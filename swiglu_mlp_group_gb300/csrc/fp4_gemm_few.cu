@@ -451,7 +451,7 @@ cudaError_t launch_fp4_gemm_few(const Fp4Gemm &g, const LaunchCtx &ctx) {
 // tokens costs the few-token kernel more than that (33: 7.4 against 8.2, but 8.6 of
 // the other's at -> 12288 against 12.4).
 cudaError_t launch_fp4_gemm(const Fp4Gemm &g, const LaunchCtx &ctx) {
-    return g.M > 32 ? launch_fp4_gemm_pair(g, ctx) : launch_fp4_gemm_few(g, ctx);
+    return g.M > kFp4Few ? launch_fp4_gemm_pair(g, ctx) : launch_fp4_gemm_few(g, ctx);
 }
 
 }  // namespace ck

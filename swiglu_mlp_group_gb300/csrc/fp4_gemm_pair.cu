@@ -31,6 +31,7 @@
 
 #include "fp4_core.cuh"
 #include "launch_util.h"
+#include "quant_core.cuh"
 
 namespace ck {
 namespace {
@@ -40,30 +41,35 @@ constexpr int kRows = 128;     // tokens of an accumulator
 constexpr int kStageK = 256;   // 128 bytes of codes a row
 constexpr int kPN = 192;       // rows of W a tile
 
-template <bool NV>
+// GLU: a tile is 192 rows of gate and the 192 rows of up that go with them.
+template <bool NV, bool GLU>
 struct Cfg {
     static constexpr int kWords = kStageK / fp4_word(NV);  // scale words of a stage
     static constexpr int kSfaBytes = kWords * 512;
     static constexpr int kBTiles = 2;                      // 128-row tiles of W's scales
     static constexpr int kABytes = kRows * kStageK / 2;
     static constexpr int kBBytes = kPN / 2 * kStageK / 2;
-    static constexpr int kXBytes = kABytes + kSfaBytes, kWBytes = kBBytes + kBTiles * kSfaBytes;
+    static constexpr int kParts = GLU ? 2 : 1;             // accumulators of a tile
+    static constexpr int kXBytes = kABytes + kSfaBytes, kWBytes = kParts * (kBBytes + kBTiles * kSfaBytes);
     static constexpr int kStageBytes = kXBytes + kWBytes;
     static constexpr int kBarBytes = 256;
-    static constexpr int kOutBytes = 8 * 2048;             // a 32 x 32 piece of y a warp of the epilogue
-    static constexpr int kStages = (226 * 1024 - kBarBytes - kOutBytes - 1024) / kStageBytes;
+    static constexpr int kOutBytes = GLU ? 0 : 8 * 2048;   // a 32 x 32 piece of y a warp of the epilogue
+    static constexpr int kStages = (227 * 1024 - kBarBytes - kOutBytes - 1024) / kStageBytes;
     static constexpr int kTmemSf = 2 * kPN;                // the scales' first column
-    static constexpr int kSfCols = 4 * kWords * (1 + kBTiles);
+    static constexpr int kSfCols = 4 * kWords * (1 + kParts * kBTiles);
     static constexpr int kTmemCols = 512;
+    static constexpr int kSets = kTmemSf + 2 * kSfCols <= kTmemCols ? 2 : 1;  // of scales, taken in turn
     static constexpr size_t kSmemBytes = static_cast<size_t>(kStages) * kStageBytes + kOutBytes + kBarBytes + 1024;
-    static_assert(kStageBytes % 1024 == 0 && kTmemSf + 2 * kSfCols <= kTmemCols, "layout");
+    static_assert(kStageBytes % 1024 == 0 && kTmemSf + kSets * kSfCols <= kTmemCols, "layout");
     static_assert(8 * (2 * kStages + 5) + 8 <= kBarBytes && kSmemBytes <= 227 * 1024, "shared memory");
 };
 
 struct Args {
-    int M, N, K, m_tiles;
+    int M, N, K, m_tiles;  // N: rows of W (GLU: of gate, and of up)
     float alpha;
     const __nv_bfloat16 *bias, *residual;
+    uint8_t *codes, *scales;  // GLU: out
+    fp4::Scale t;
     bool weights_settled;
     unsigned int *status;
     unsigned long long timeout_ns;
@@ -95,15 +101,15 @@ __device__ __forceinline__ uint4 finish8(const uint32_t *acc, uint64_t alpha, co
     return make_uint4(p[0], p[1], p[2], p[3]);
 }
 
-template <bool NV>
+template <bool NV, bool GLU>
 __global__ void __launch_bounds__(kThreads, 1)
 fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                      const __grid_constant__ CUtensorMap tm_xs, const __grid_constant__ CUtensorMap tm_ws,
                      const __grid_constant__ CUtensorMap tm_y,
                      const __grid_constant__ Args a) {
-    using C = Cfg<NV>;
+    using C = Cfg<NV, GLU>;
     constexpr int kStages = C::kStages;
-    constexpr int kOffB = C::kABytes, kOffSfa = kOffB + C::kBBytes, kOffSfb = kOffSfa + C::kSfaBytes;
+    constexpr int kOffB = C::kABytes, kOffSfa = kOffB + C::kParts * C::kBBytes, kOffSfb = kOffSfa + C::kSfaBytes;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_s = smem_u32(smem_raw);
     const uint32_t smem_s = (raw_s + 1023u) & ~1023u;
@@ -174,8 +180,14 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
                     ok = mbar_wait_spin(empty(s), ph, ctl);  // (the first round's wait is over at once)
                     if (!ok) break;
                     if (rank == 0) mbar_arrive_expect_tx(full(s), bytes);
-                    tma_load_2d_pair(to_codes + s * C::kStageBytes, codes, lead + 8 * s, kb * (kStageK / 2), row);
-                    tma_load_2d_pair(to_scales + s * C::kStageBytes, scales, lead + 8 * s, kb * (C::kWords * 64), sf_tile);
+                    const uint32_t dst = to_codes + s * C::kStageBytes, sf_dst = to_scales + s * C::kStageBytes;
+                    tma_load_2d_pair(dst, codes, lead + 8 * s, kb * (kStageK / 2), row);
+                    tma_load_2d_pair(sf_dst, scales, lead + 8 * s, kb * (C::kWords * 64), sf_tile);
+                    if (GLU && weight) {
+                        tma_load_2d_pair(dst + C::kBBytes, codes, lead + 8 * s, kb * (kStageK / 2), a.N + row);
+                        tma_load_2d_pair(sf_dst + C::kBTiles * C::kSfaBytes, scales, lead + 8 * s, kb * (C::kWords * 64),
+                                         (a.N + n0) >> 7);
+                    }
                     ++issued;
                     if (++s == kStages) s = 0, ph ^= 1;
                 }
@@ -206,38 +218,51 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
             uint32_t ph = 0;
             bool ok = true;
             for (int tile = pair; tile < total && ok; tile += npairs, ++gc) {
-                const int acc = gc & 1;
-                const uint32_t d = tmem + acc * kPN;
                 // where W's rows of this tile begin in their scales' 128-row tile
-                const uint32_t sfb_off = (tile / a.m_tiles * kPN & 127) >> 5;
-                // the epilogue has read what this accumulator held two tiles ago
-                if (gc >= 2) ok = mbar_wait_spin(acce(acc), ((gc >> 1) - 1) & 1, ctl);
-                if (!ok) break;
+                const int n0 = tile / a.m_tiles * kPN;
+                const uint32_t sfb_off[2] = {static_cast<uint32_t>((n0 & 127) >> 5), static_cast<uint32_t>(((a.N + n0) & 127) >> 5)};
                 for (int kb = 0; kb < num_kb; ++kb) {
                     ok = mbar_wait_spin(full(s), ph, ctl);
                     if (!ok) break;
                     tc_fence_after_sync();
                     const uint64_t step = static_cast<uint64_t>(s) * (C::kStageBytes / 16);
                     const uint64_t ad = ad0 + step, bd = bd0 + step, sa = sa0 + step, sb = sb0 + step;
-                    const uint32_t sfa = tmem + C::kTmemSf + (s & 1) * C::kSfCols, sfb = sfa + 4 * C::kWords;
+                    const uint32_t sfa = tmem + C::kTmemSf + s % C::kSets * C::kSfCols, sfb = sfa + 4 * C::kWords;
+                    constexpr int kPartCols = 4 * C::kWords * C::kBTiles;
                     const bool last = kb + 1 == num_kb;
                     const int n = last ? tail : 4;
 #pragma unroll
                     for (int w = 0; w < C::kWords; ++w) {
                         tmem_copy_scales_pair(sfa + 4 * w, sa + 32 * w);
 #pragma unroll
-                        for (int t = 0; t < C::kBTiles; ++t)
-                            tmem_copy_scales_pair(sfb + 4 * (C::kBTiles * w + t), sb + t * (C::kSfaBytes / 16) + 32 * w);
+                        for (int p = 0; p < C::kParts; ++p)
+#pragma unroll
+                            for (int t = 0; t < C::kBTiles; ++t)
+                                tmem_copy_scales_pair(sfb + p * kPartCols + 4 * (C::kBTiles * w + t),
+                                                      sb + (p * C::kBTiles + t) * (C::kSfaBytes / 16) + 32 * w);
                     }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (k < n) {
-                            const int w = NV ? k : k / 2;
-                            mma_fp4<NV, true>(d, ad + 2 * k, bd + 2 * k, idesc_fp4(2 * kRows, kPN, NV, NV ? 0 : k & 1),
-                                              sfa + 4 * w, sfb + sfb_off + 4 * C::kBTiles * w, kb > 0 || k > 0 ? 1u : 0u);
+                    for (int p = 0; p < C::kParts; ++p) {
+                        const int acc = GLU ? p : gc & 1, use = GLU ? gc : gc >> 1;
+                        // the epilogue has read what this accumulator held before
+                        if (kb == 0 && use > 0) {
+                            ok = mbar_wait_spin(acce(acc), (use - 1) & 1, ctl);
+                            if (!ok) break;
+                            tc_fence_after_sync();
                         }
-                    mma_commit_pair(empty(s), 0x3);
-                    if (last) mma_commit_pair(accf(acc), 0x3);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (k < n) {
+                                const int w = NV ? k : k / 2;
+                                mma_fp4<NV, true>(tmem + acc * kPN, ad + 2 * k, bd + p * (C::kBBytes / 16) + 2 * k,
+                                                  idesc_fp4(2 * kRows, kPN, NV, NV ? 0 : k & 1), sfa + 4 * w,
+                                                  sfb + p * kPartCols + sfb_off[p] + 4 * C::kBTiles * w,
+                                                  kb > 0 || k > 0 ? 1u : 0u);
+                            }
+                        if (p == C::kParts - 1) mma_commit_pair(empty(s), 0x3);
+                        if (last) mma_commit_pair(accf(acc), 0x3);
+                    }
+                    if (!ok) break;
                     if (++s == kStages) s = 0, ph ^= 1;
                 }
             }
@@ -268,42 +293,106 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
             return true;
         };
         const uint64_t alpha = f32x2(a.alpha, a.alpha);
-        // 32 rows x 32 columns at a time through shared memory (64-byte rows, swizzled as
-        // the map has it) and out by TMA.
-        const uint32_t piece = out_s + (warp - 4) * 2048;
-        const uint32_t mine = piece + lane * 64, turn = (lane >> 1) & 3;
-        int gc = 0;
-        for (int tile = pair; tile < total; tile += npairs, ++gc) {
-            const int n0 = tile / a.m_tiles * kPN + c0;
-            const int row0 = tile % a.m_tiles * (2 * kRows) + rank * kRows + q * 32;
-            const bool in = row0 + lane < a.M;
-            uint32_t r[kGroups][32];
-            if (!read(gc & 1, gc >> 1, r)) break;
+        if constexpr (GLU) {
+            // gate and up, as bf16 as a linear of its own would leave them, and from
+            // them silu(gate) * up in f32, quantized: a thread has 96 columns of a row,
+            // whole blocks.  Both accumulators go back before that.
+            constexpr int kBlock = fp4_block(NV);
+            const int words = static_cast<int>(fp4_words(a.N, NV));
+            int gc = 0;
+            for (int tile = pair; tile < total; tile += npairs, ++gc) {
+                const int n0 = tile / a.m_tiles * kPN + c0;
+                const int m = tile % a.m_tiles * (2 * kRows) + rank * kRows + q * 32 + lane;
+                uint32_t r[kGroups][32];
+                uint4 gate[4 * kGroups], up[4 * kGroups];
+                auto take = [&](int part, uint4 (&v)[4 * kGroups]) {
+                    if (!read(part, gc, r)) return false;
+                    const __nv_bfloat16 *bias = a.bias != nullptr ? a.bias + part * a.N + n0 : nullptr;
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                const int n1 = n0 + 32 * g;
-                if (n1 >= a.N || row0 >= a.M) break;
-                if (lane == 0) bulk_wait_read();  // the piece before has left
-                __syncwarp();
+                    for (int p = 0; p < 4 * kGroups; ++p)
+                        v[p] = finish8(r[p / 4] + 8 * (p % 4), alpha, bias != nullptr && n0 + 8 * p < a.N ? bias + 8 * p : nullptr,
+                                       nullptr);
+                    return true;
+                };
+                if (!take(0, gate) || !take(1, up)) break;
+                if (m < a.M) {
+                    uint8_t *code = a.codes + static_cast<int64_t>(m) * (a.N / 2) + n0 / 2;
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const int n = n1 + 8 * p;
-                    const uint4 v = finish8(r[g] + 8 * p, alpha, a.bias != nullptr && n < a.N ? a.bias + n : nullptr,
-                                            a.residual != nullptr && n < a.N && in
-                                                ? a.residual + static_cast<int64_t>(row0 + lane) * a.N + n : nullptr);
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + ((p ^ turn) << 4)), "r"(v.x),
-                                 "r"(v.y), "r"(v.z), "r"(v.w)
-                                 : "memory");
+                    for (int b = 0; b < kCols / kBlock; ++b) {
+                        const int col = n0 + b * kBlock;
+                        uint32_t scale = 0;
+                        if (col < a.N) {  // (a.N is a multiple of both blocks)
+                            uint64_t n[kBlock / 8][4];
+                            float top = 0.f;
+#pragma unroll
+                            for (int i = 0; i < kBlock / 8; ++i) {
+                                const uint4 g = gate[b * (kBlock / 8) + i], u = up[b * (kBlock / 8) + i];
+                                const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    n[i][e] = f32x2(-qc::silu_mul(__uint_as_float(gw[e] << 16), __uint_as_float(uw[e] << 16)),
+                                                    -qc::silu_mul(__uint_as_float(gw[e] & 0xffff0000u),
+                                                                  __uint_as_float(uw[e] & 0xffff0000u)));
+                                top = fp4::amax8(n[i], top);
+                            }
+                            const fp4::Divisor d = fp4::divisor<NV>(top, a.t, scale);
+                            uint32_t c[kBlock / 8];
+#pragma unroll
+                            for (int i = 0; i < kBlock / 8; ++i) c[i] = fp4::codes8<NV>(n[i], d);
+                            if constexpr (NV)
+                                *reinterpret_cast<uint2 *>(code + b * 8) = make_uint2(c[0], c[1]);
+                            else
+                                *reinterpret_cast<uint4 *>(code + b * 16) = make_uint4(c[0], c[1], c[2], c[3]);
+                        }
+                        const int block = col / kBlock;
+                        if (block < 4 * words)
+                            a.scales[fp4::scale_word_at(m, block / 4, words) + (block & 3)] = static_cast<uint8_t>(scale);
+                    }
+                    // the last word's blocks past the last tile
+                    if (n0 + kCols >= (a.N + kPN - 1) / kPN * kPN)
+                        for (int block = (n0 + kCols) / kBlock; block < 4 * words; ++block)
+                            a.scales[fp4::scale_word_at(m, block / 4, words) + (block & 3)] = 0;
                 }
-                fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) {
-                    tma_store_2d(&tm_y, piece, n1, row0);
-                    bulk_commit();
+            }
+        } else {
+            // 32 rows x 32 columns at a time through shared memory (64-byte rows, swizzled as
+            // the map has it) and out by TMA.
+            const uint32_t piece = out_s + (warp - 4) * 2048;
+            const uint32_t mine = piece + lane * 64, turn = (lane >> 1) & 3;
+            int gc = 0;
+            for (int tile = pair; tile < total; tile += npairs, ++gc) {
+                const int n0 = tile / a.m_tiles * kPN + c0;
+                const int row0 = tile % a.m_tiles * (2 * kRows) + rank * kRows + q * 32;
+                const bool in = row0 + lane < a.M;
+                uint32_t r[kGroups][32];
+                if (!read(gc & 1, gc >> 1, r)) break;
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    const int n1 = n0 + 32 * g;
+                    if (n1 >= a.N || row0 >= a.M) break;
+                    if (lane == 0) bulk_wait_read();  // the piece before has left
+                    __syncwarp();
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const int n = n1 + 8 * p;
+                        const uint4 v = finish8(r[g] + 8 * p, alpha, a.bias != nullptr && n < a.N ? a.bias + n : nullptr,
+                                                a.residual != nullptr && n < a.N && in
+                                                    ? a.residual + static_cast<int64_t>(row0 + lane) * a.N + n : nullptr);
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + ((p ^ turn) << 4)), "r"(v.x),
+                                     "r"(v.y), "r"(v.z), "r"(v.w)
+                                     : "memory");
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&tm_y, piece, n1, row0);
+                        bulk_commit();
+                    }
                 }
             }
+            if (lane == 0) bulk_wait();
         }
-        if (lane == 0) bulk_wait();
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -314,21 +403,24 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     }
 }
 
-template <bool NV>
+template <bool NV, bool GLU>
 cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx) {
-    using C = Cfg<NV>;
+    using C = Cfg<NV, GLU>;
     CUtensorMap mx, mw, mxs, mws, my;
     const int row_bytes = static_cast<int>(g.K / 2);
-    const int64_t words = fp4_words(g.K, NV);
+    const int64_t words = fp4_words(g.K, NV), w_rows = GLU ? 2 * g.N : g.N;
     if (!tensor_map_2d(&mx, g.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.M, row_bytes, kStageK / 2, kRows,
                        CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !tensor_map_2d(&mw, g.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.N, row_bytes, kStageK / 2, kPN / 2,
+        !tensor_map_2d(&mw, g.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w_rows, row_bytes, kStageK / 2, kPN / 2,
                        CU_TENSOR_MAP_SWIZZLE_128B) ||
         !tensor_map_scales(&mxs, g.xs, (g.M + 127) / 128, words, C::kWords, 1) ||
-        !tensor_map_scales(&mws, g.ws, (g.N + 127) / 128, words, C::kWords, C::kBTiles) ||
-        !tensor_map_2d(&my, g.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.M, g.N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+        !tensor_map_scales(&mws, g.ws, (w_rows + 127) / 128, words, C::kWords, C::kBTiles))
         return cudaErrorInvalidValue;
-    auto kern = fp4_gemm_pair_kernel<NV>;
+    if constexpr (GLU)
+        my = mx;  // not used
+    else if (!tensor_map_2d(&my, g.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.M, g.N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+        return cudaErrorInvalidValue;
+    auto kern = fp4_gemm_pair_kernel<NV, GLU>;
     if (cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), static_cast<int>(C::kSmemBytes));
         e != cudaSuccess)
         return e;
@@ -357,6 +449,7 @@ cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx) {
     a.m_tiles = static_cast<int>(m_tiles);
     a.alpha = g.alpha;
     a.bias = static_cast<const __nv_bfloat16 *>(g.bias), a.residual = static_cast<const __nv_bfloat16 *>(g.residual);
+    a.codes = g.a_codes, a.scales = g.a_scales, a.t = fp4::scale_of(g.a_scale);
     a.weights_settled = g.weights_settled;
     a.status = ctx.status, a.timeout_ns = ctx.timeout_ns;
     return cudaLaunchKernelEx(&cfg, kern, mx, mw, mxs, mws, my, a);
@@ -365,7 +458,11 @@ cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx) {
 }  // namespace
 
 cudaError_t launch_fp4_gemm_pair(const Fp4Gemm &g, const LaunchCtx &ctx) {
-    return g.nv ? launch_t<true>(g, ctx) : launch_t<false>(g, ctx);
+    return g.nv ? launch_t<true, false>(g, ctx) : launch_t<false, false>(g, ctx);
+}
+
+cudaError_t launch_fp4_gemm_glu(const Fp4Gemm &g, const LaunchCtx &ctx) {
+    return g.nv ? launch_t<true, true>(g, ctx) : launch_t<false, true>(g, ctx);
 }
 
 }  // namespace ck

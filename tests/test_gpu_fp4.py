@@ -295,6 +295,34 @@ def test_mlp_is_two_linears(M, H, I, fmt):
     poll_ok()
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,H,I", [(33, 96, 64), (129, 544, 192), (257, 256, 576), (300, 1056, 320), (600, 512, 1088), (1000, 256, 3008)])
+def test_mlp_gate_and_up_on_chip(M, H, I, fmt):
+    """Where I is a multiple of 64 the first product quantizes silu(gate) * up itself: the same bits as two linears, its
+    scales' missing blocks too (the second product would show them)."""
+    test_mlp_is_two_linears(M, H, I, fmt)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_mlp_not_finite(fmt):
+    """A token with a NaN, and a gate row with one, stay with their rows; an infinite gate's silu is its own block's."""
+    dev = device()
+    g = ref.gen(8)
+    M, H, I = 70, 256, 192
+    x = ref.randn(g, M, H)
+    x[5, 7] = float("nan")
+    t = T[fmt]
+    gu = ck.fp4_quantize(ref.randn(g, 2 * I, H, std=H ** -0.5).to(dev), fmt, scale=t)
+    d = ck.fp4_quantize(ref.randn(g, H, I, std=I ** -0.5).to(dev), fmt, scale=t)
+    kw = dict(x_scale=t, gate_up_scale=t, act_scale=t, down_scale=t)
+    y = ck.fp4_swiglu_mlp(x.to(dev), *gu, *d, fmt, **kw)
+    h = ck.fp4_linear(x.to(dev), *gu, fmt, x_scale=t, w_scale=t)
+    want = ck.fp4_linear(h, *d, fmt, x_scale=t, w_scale=t, act="swiglu")
+    poll_ok()
+    assert torch.equal(torch.isnan(y), torch.isnan(want)) and torch.isnan(y[5]).all() and not torch.isnan(y[:5]).any()
+    assert torch.equal(torch.nan_to_num(y), torch.nan_to_num(want))
+
+
 @pytest.mark.parametrize("M", [2, 300])
 def test_graph_and_streams(M):
     """Captured and replayed on changed inputs; another stream; two graphs that share a workspace, replayed in turn."""
