@@ -3,31 +3,27 @@
 //   y[m, n] = bf16( alpha * sum_k X[m, k] W[n, k] + bias[n] + residual[m, n] )
 //
 // X, W: E2M1 codes times the scales of their blocks (fp4_core.cuh).  CTA pairs
-// (tcgen05.mma.cta_group::2): a tile of 256 tokens x 192 rows of W on two SMs, each
-// holding its 128 tokens, half of W's rows, and the scales of its tokens and of all of
-// W's rows; two f32 accumulators in TMEM, so that a tile's epilogue runs under the next
-// one's products (two of 256 columns would leave no room for the scales).
+// (tcgen05.mma.cta_group::2): a tile of 256 tokens x one or two parts of 192 rows of W
+// on two SMs, each holding its 128 tokens, half of W's rows, and the scales of its
+// tokens and of all of W's rows; an f32 accumulator in TMEM for each part, two of them
+// in all (of 256 columns they would leave no room for the scales).
+//
+// One part a tile: the accumulators in turn, so that a tile's epilogue runs under the
+// next one's products.  Two: X's bytes once for both, and the epilogue first reads both
+// accumulators into registers as packed bf16, the first while the second's last products
+// run, and hands them back before it does anything else.
+//
+// GLU: the parts are rows of gate and the rows of up that go with them, and the
+// epilogue makes silu(gate) * up of them and quantizes it: what the next linear of a
+// SwiGLU MLP reads, without gate and up ever leaving the chip.
 //
 // Roles (each CTA, 12 warps): warps 0 and 2 TMA producers of the tokens' and of the
 // weight's codes and scales, warp 1 TMEM and, in the leader, the issue of the scales'
 // copies to TMEM and of the MMAs (both run in the order of their issue), warps 4..11
 // the epilogue.
-//
-// What bounds it.  The MMAs of a stage (256 columns of K) take 384 clocks, 9.5 PFLOP/s
-// in all, with or without the scales' copies between them (timed alone, from shared
-// memory).  On zeros, which draw little power, the kernel runs at 7.3 (MX) and 6.9 (NV)
-// PFLOP/s at 16384 x 4096 -> 12288, without its stores at 8.3 and 7.7, without its
-// epilogue at 9.1 and 8.2: operands come in at some 77 bytes a clock and SM of the 81 and
-// 89 that the MMAs would take, and y's bytes go the same way.  On random codes power takes
-// another tenth.  What it took: one lane that polls and issues, of a warp of its own (32
-// lanes polling a barrier cost the issuer a third of its time), a producer for each
-// operand (one for both took longer to issue than the MMAs to run), y through shared
-// memory and TMA (exchanged between lanes and stored by them: 252 us against 240, NV).
-// Tried and slower: tiles of 512 tokens on both accumulators (22 % less operand traffic,
-// but no accumulator to spare: 252 us against 240), the stages unrolled in the issuer
-// (no gain), tiles in bands of 8 and 16 rows of tiles (no gain), y in pieces of 64
-// columns (250).
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "fp4_core.cuh"
 #include "launch_util.h"
@@ -37,26 +33,28 @@ namespace ck {
 namespace {
 
 constexpr int kThreads = 384;
+// Registers of a thread of warps 0..3 and of the epilogue's; together what the block is
+// launched with (168 a thread).
+constexpr int kOtherRegs = 56, kEpilogueRegs = 224;
+static_assert(128 * kOtherRegs + 256 * kEpilogueRegs <= kThreads * 168, "registers");
 constexpr int kRows = 128;     // tokens of an accumulator
 constexpr int kStageK = 256;   // 128 bytes of codes a row
-constexpr int kPN = 192;       // rows of W a tile
+constexpr int kPN = 192;       // rows of W a part
 
-// GLU: a tile is 192 rows of gate and the 192 rows of up that go with them.
-template <bool NV, bool GLU>
+template <bool NV, int PARTS, bool GLU>
 struct Cfg {
     static constexpr int kWords = kStageK / fp4_word(NV);  // scale words of a stage
     static constexpr int kSfaBytes = kWords * 512;
-    static constexpr int kBTiles = 2;                      // 128-row tiles of W's scales
+    static constexpr int kBTiles = 2;                      // 128-row tiles of a part's scales
     static constexpr int kABytes = kRows * kStageK / 2;
     static constexpr int kBBytes = kPN / 2 * kStageK / 2;
-    static constexpr int kParts = GLU ? 2 : 1;             // accumulators of a tile
-    static constexpr int kXBytes = kABytes + kSfaBytes, kWBytes = kParts * (kBBytes + kBTiles * kSfaBytes);
+    static constexpr int kXBytes = kABytes + kSfaBytes, kWBytes = PARTS * (kBBytes + kBTiles * kSfaBytes);
     static constexpr int kStageBytes = kXBytes + kWBytes;
-    static constexpr int kBarBytes = 256;
     static constexpr int kOutBytes = GLU ? 0 : 8 * 2048;   // a 32 x 32 piece of y a warp of the epilogue
+    static constexpr int kBarBytes = 256;
     static constexpr int kStages = (227 * 1024 - kBarBytes - kOutBytes - 1024) / kStageBytes;
     static constexpr int kTmemSf = 2 * kPN;                // the scales' first column
-    static constexpr int kSfCols = 4 * kWords * (1 + kParts * kBTiles);
+    static constexpr int kSfCols = 4 * kWords * (1 + PARTS * kBTiles);
     static constexpr int kTmemCols = 512;
     static constexpr int kSets = kTmemSf + 2 * kSfCols <= kTmemCols ? 2 : 1;  // of scales, taken in turn
     static constexpr size_t kSmemBytes = static_cast<size_t>(kStages) * kStageBytes + kOutBytes + kBarBytes + 1024;
@@ -65,7 +63,7 @@ struct Cfg {
 };
 
 struct Args {
-    int M, N, K, m_tiles;  // N: rows of W (GLU: of gate, and of up)
+    int M, N, K, m_tiles, n_tiles;  // N: rows of W (GLU: of gate, and of up)
     float alpha;
     const __nv_bfloat16 *bias, *residual;
     uint8_t *codes, *scales;  // GLU: out
@@ -75,41 +73,102 @@ struct Args {
     unsigned long long timeout_ns;
 };
 
-// Eight columns of a row, packed to bf16: alpha * acc + bias + residual.
-__device__ __forceinline__ uint4 finish8(const uint32_t *acc, uint64_t alpha, const __nv_bfloat16 *bias,
-                                         const __nv_bfloat16 *residual) {
-    uint64_t v[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        v[e] = mul_f32x2(f32x2(__uint_as_float(acc[2 * e]), __uint_as_float(acc[2 * e + 1])), alpha);
-    auto add = [&](const uint4 &u) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            v[e] = add_f32x2(v[e], f32x2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u)));
-    };
-    if (bias != nullptr) add(__ldg(reinterpret_cast<const uint4 *>(bias)));
-    if (residual != nullptr) add(*reinterpret_cast<const uint4 *>(residual));
+// Eight columns of a row, packed to bf16: alpha * acc (+ bias) (+ residual).
+template <bool BIAS, bool RESIDUAL>
+__device__ __forceinline__ uint4 finish8(const uint32_t *acc, uint64_t alpha, const uint4 &bias, const uint4 &residual) {
+    const uint32_t b[4] = {bias.x, bias.y, bias.z, bias.w}, r[4] = {residual.x, residual.y, residual.z, residual.w};
     uint32_t p[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
+        uint64_t v = mul_f32x2(f32x2(__uint_as_float(acc[2 * e]), __uint_as_float(acc[2 * e + 1])), alpha);
+        if constexpr (BIAS) v = add_f32x2(v, fp4::unpack2(b[e]));
+        if constexpr (RESIDUAL) v = add_f32x2(v, fp4::unpack2(r[e]));
         float lo, hi;
-        f32x2_split(v[e], lo, hi);
+        f32x2_split(v, lo, hi);
         const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
         p[e] = *reinterpret_cast<const uint32_t *>(&t);
     }
     return make_uint4(p[0], p[1], p[2], p[3]);
 }
 
-template <bool NV, bool GLU>
+__device__ __forceinline__ void st_shared_v4(uint32_t at, const uint4 &v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
+// silu(gate) * up of whole blocks of a row, quantized: codes from `code` on (a
+// thread's 96 columns from `col` on), scale bytes to row m of `scales`.
+template <bool NV, int COLS>
+__device__ __forceinline__ void quantize_glu(const uint4 (&gate)[COLS / 8], const uint4 (&up)[COLS / 8], int col, int N,
+                                             const fp4::Scale &t, uint8_t *code, uint8_t *scales, int64_t m, int words) {
+    constexpr int kBlock = fp4_block(NV);
+#pragma unroll
+    for (int b = 0; b < COLS / kBlock; ++b) {
+        uint32_t scale = 0;
+        if (col + b * kBlock < N) {  // (N is a multiple of both blocks)
+            uint64_t n[kBlock / 8][4];
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < kBlock / 8; ++i) {
+                const uint4 g = gate[b * (kBlock / 8) + i], u = up[b * (kBlock / 8) + i];
+                const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    n[i][e] = f32x2(-qc::silu_mul(__uint_as_float(gw[e] << 16), __uint_as_float(uw[e] << 16)),
+                                    -qc::silu_mul(__uint_as_float(gw[e] & 0xffff0000u), __uint_as_float(uw[e] & 0xffff0000u)));
+                top = fp4::amax8(n[i], top);
+            }
+            const fp4::Divisor d = fp4::divisor<NV>(top, t, scale);
+            uint32_t c[kBlock / 8];
+#pragma unroll
+            for (int i = 0; i < kBlock / 8; ++i) c[i] = fp4::codes8<NV>(n[i], d);
+            if constexpr (NV)
+                *reinterpret_cast<uint2 *>(code + b * 8) = make_uint2(c[0], c[1]);
+            else
+                *reinterpret_cast<uint4 *>(code + b * 16) = make_uint4(c[0], c[1], c[2], c[3]);
+        }
+        const int block = col / kBlock + b;
+        if (block < 4 * words)
+            scales[fp4::scale_word_at(m, block / 4, words) + (block & 3)] = static_cast<uint8_t>(scale);
+    }
+}
+
+// What bounds it.  The MMAs of a part's stage (256 columns of K) take 384 clocks, 9.5
+// PFLOP/s in all, with or without the scales' copies between them (timed alone, from
+// shared memory).  Their operands: 81 (MX) and 89 (NV) bytes a clock and SM with one
+// part, of which some 77 come in, 59 and 65 with two, whose k-blocks run at 97 % of the
+// MMAs' rate; there the rest is between tiles (the first k-block's data, the
+// accumulators' reading).  Random codes draw so much power that the clock gives another
+// tenth: 227 us (NV) and 216 (MX) for 16384 x 4096 -> 12288, 218 on zeros, or 7.3 and 7.6
+// PFLOP/s; gate and up of as many tokens with 6144 rows each 215 and 206.
+//
+// What it took: one lane that polls and issues, of a warp of its own (32 lanes polling a
+// barrier cost the issuer a third of its time), a producer for each operand (one for both
+// took longer to issue than the MMAs to run), y through shared memory and TMA (exchanged
+// between lanes and stored by them: 252 us against 240), no branches between the columns
+// of an accumulator's reading (1450 clocks for 96 columns with them, 650 without), the
+// residual read in whole sectors, four lanes a row, and turned to rows in shared memory
+// (a lane its own row: 300 us against 265, 8192 x 1024 -> 8192 77 against 71; read a tile
+// ahead: 330), with two parts more registers for the epilogue than for the rest (222 us
+// without, and a tenth more with a residual; one part does not need them: 247 against 242).
+// Tried and slower (one part): 512 tokens x 192 rows (252 us against 240), the issuer's stages
+// unrolled, tiles in bands of 8 and 16 rows of tiles, y in pieces of 64 columns (250),
+// the next tile's first k-blocks prefetched to L2 (264 against 249).
+template <bool NV, int PARTS, bool GLU>
 __global__ void __launch_bounds__(kThreads, 1)
 fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                      const __grid_constant__ CUtensorMap tm_xs, const __grid_constant__ CUtensorMap tm_ws,
-                     const __grid_constant__ CUtensorMap tm_y,
-                     const __grid_constant__ Args a) {
-    using C = Cfg<NV, GLU>;
+                     const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ Args a) {
+    static_assert(PARTS == 2 || !GLU, "gate and up");
+    using C = Cfg<NV, PARTS, GLU>;
     constexpr int kStages = C::kStages;
-    constexpr int kOffB = C::kABytes, kOffSfa = kOffB + C::kParts * C::kBBytes, kOffSfb = kOffSfa + C::kSfaBytes;
+    constexpr int kOffB = C::kABytes, kOffSfa = kOffB + PARTS * C::kBBytes, kOffSfb = kOffSfa + C::kSfaBytes;
+    constexpr int kTileN = GLU ? kPN : PARTS * kPN;  // columns of y, or of the product, a tile
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_s = smem_u32(smem_raw);
     const uint32_t smem_s = (raw_s + 1023u) & ~1023u;
@@ -128,9 +187,11 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());  // 0: leader (issues), 1: peer
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-    const int total = a.m_tiles * ((a.N + kPN - 1) / kPN);
+    const int total = a.m_tiles * a.n_tiles;
     const int num_kb = (a.K + kStageK - 1) / kStageK;
     const WaitCtl ctl{abort_flag, a.status, a.timeout_ns};
+    // first row of W of a tile's part (GLU: up's rows follow gate's N)
+    auto part_row = [&](int tile, int p) { return tile / a.m_tiles * kTileN + p * (GLU ? a.N : kPN); };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -156,126 +217,133 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     const uint32_t tmem = *tmem_slot;
     pdl_launch_dependents();
 
-    if (warp == 0 || warp == 2) {
-        // ------------------------------------------------------------ producers
-        // Both CTAs' copies complete on the leader's barrier of the stage, where
-        // the leader's producers announce the pair's bytes.
-        const bool weight = warp == 2;
-        int issued = 0;
-        if (elect_one()) {
-            const CUtensorMap *codes = weight ? &tm_w : &tm_x, *scales = weight ? &tm_ws : &tm_xs;
-            tma_prefetch_desc(codes);
-            tma_prefetch_desc(scales);
-            if (!weight || !a.weights_settled) pdl_wait();
-            const uint32_t to_codes = stage(0) + (weight ? kOffB : 0), to_scales = stage(0) + (weight ? kOffSfb : kOffSfa);
-            const uint32_t bytes = 2 * (weight ? C::kWBytes : C::kXBytes);
-            const uint32_t lead = mapa_shared(full(0), 0);
-            int s = 0;
-            uint32_t ph = 1;
-            for (int tile = pair; tile < total; tile += npairs) {
-                const int n0 = tile / a.m_tiles * kPN, m0 = tile % a.m_tiles * (2 * kRows) + rank * kRows;
-                const int row = weight ? n0 + rank * (kPN / 2) : m0, sf_tile = (weight ? n0 : m0) >> 7;
-                bool ok = true;
-                for (int kb = 0; kb < num_kb; ++kb) {
-                    ok = mbar_wait_spin(empty(s), ph, ctl);  // (the first round's wait is over at once)
-                    if (!ok) break;
-                    if (rank == 0) mbar_arrive_expect_tx(full(s), bytes);
-                    const uint32_t dst = to_codes + s * C::kStageBytes, sf_dst = to_scales + s * C::kStageBytes;
-                    tma_load_2d_pair(dst, codes, lead + 8 * s, kb * (kStageK / 2), row);
-                    tma_load_2d_pair(sf_dst, scales, lead + 8 * s, kb * (C::kWords * 64), sf_tile);
-                    if (GLU && weight) {
-                        tma_load_2d_pair(dst + C::kBBytes, codes, lead + 8 * s, kb * (kStageK / 2), a.N + row);
-                        tma_load_2d_pair(sf_dst + C::kBTiles * C::kSfaBytes, scales, lead + 8 * s, kb * (C::kWords * 64),
-                                         (a.N + n0) >> 7);
-                    }
-                    ++issued;
-                    if (++s == kStages) s = 0, ph ^= 1;
-                }
-                if (!ok) break;
-            }
-            if (*abort_flag) {
-                if (rank == 0) {
-                    const int first = issued > kStages ? issued - kStages : 0;
-                    for (int i = first; i < issued; ++i)
-                        mbar_wait_drain(full(i % kStages), (i / kStages) & 1, a.timeout_ns, a.status);
-                } else {
-                    // copies in flight into this CTA land within microseconds
-                    const uint64_t t0 = globaltimer_ns();
-                    while (globaltimer_ns() - t0 < 50000ull) {
-                    }
-                }
-            }
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issue
-        if (rank == 0) {
-            const uint64_t ad0 = sdesc_kmajor_sw128(stage(0)), bd0 = sdesc_kmajor_sw128(stage(0) + kOffB);
-            const uint64_t sa0 = sdesc_scales(stage(0) + kOffSfa), sb0 = sdesc_scales(stage(0) + kOffSfb);
-            const int tail = (a.K - (num_kb - 1) * kStageK + 63) / 64;  // MMAs of a tile's last k-block
+    if (warp < 4) {
+        if constexpr (PARTS == 2) setmaxnreg_dec<kOtherRegs>();  // by all four warps at once
+        if (warp == 0 || warp == 2) {
+            // -------------------------------------------------------- producers
+            // Both CTAs' copies complete on the leader's barrier of the stage, where
+            // the leader's producers announce the pair's bytes.
+            const bool weight = warp == 2;
+            int issued = 0;
             if (elect_one()) {
-            int gc = 0, s = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            for (int tile = pair; tile < total && ok; tile += npairs, ++gc) {
-                // where W's rows of this tile begin in their scales' 128-row tile
-                const int n0 = tile / a.m_tiles * kPN;
-                const uint32_t sfb_off[2] = {static_cast<uint32_t>((n0 & 127) >> 5), static_cast<uint32_t>(((a.N + n0) & 127) >> 5)};
-                for (int kb = 0; kb < num_kb; ++kb) {
-                    ok = mbar_wait_spin(full(s), ph, ctl);
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    const uint64_t step = static_cast<uint64_t>(s) * (C::kStageBytes / 16);
-                    const uint64_t ad = ad0 + step, bd = bd0 + step, sa = sa0 + step, sb = sb0 + step;
-                    const uint32_t sfa = tmem + C::kTmemSf + s % C::kSets * C::kSfCols, sfb = sfa + 4 * C::kWords;
-                    constexpr int kPartCols = 4 * C::kWords * C::kBTiles;
-                    const bool last = kb + 1 == num_kb;
-                    const int n = last ? tail : 4;
-#pragma unroll
-                    for (int w = 0; w < C::kWords; ++w) {
-                        tmem_copy_scales_pair(sfa + 4 * w, sa + 32 * w);
-#pragma unroll
-                        for (int p = 0; p < C::kParts; ++p)
-#pragma unroll
-                            for (int t = 0; t < C::kBTiles; ++t)
-                                tmem_copy_scales_pair(sfb + p * kPartCols + 4 * (C::kBTiles * w + t),
-                                                      sb + (p * C::kBTiles + t) * (C::kSfaBytes / 16) + 32 * w);
+                const CUtensorMap *codes = weight ? &tm_w : &tm_x, *scales = weight ? &tm_ws : &tm_xs;
+                tma_prefetch_desc(codes);
+                tma_prefetch_desc(scales);
+                if (!weight || !a.weights_settled) pdl_wait();
+                const uint32_t to_codes = stage(0) + (weight ? kOffB : 0), to_scales = stage(0) + (weight ? kOffSfb : kOffSfa);
+                const uint32_t bytes = 2 * (weight ? C::kWBytes : C::kXBytes);
+                const uint32_t lead = mapa_shared(full(0), 0);
+                int s = 0;
+                uint32_t ph = 1;
+                for (int tile = pair; tile < total; tile += npairs) {
+                    const int m0 = tile % a.m_tiles * (2 * kRows) + rank * kRows;
+                    const int w0 = part_row(tile, 0), w1 = part_row(tile, PARTS - 1);
+                    const int row = weight ? w0 + rank * (kPN / 2) : m0, sf_tile = (weight ? w0 : m0) >> 7;
+                    bool ok = true;
+                    for (int kb = 0; kb < num_kb; ++kb) {
+                        ok = mbar_wait_spin(empty(s), ph, ctl);  // (the first round's wait is over at once)
+                        if (!ok) break;
+                        if (rank == 0) mbar_arrive_expect_tx(full(s), bytes);
+                        const uint32_t dst = to_codes + s * C::kStageBytes, sf_dst = to_scales + s * C::kStageBytes;
+                        const int x = kb * (kStageK / 2), sf_x = kb * (C::kWords * 64);
+                        tma_load_2d_pair(dst, codes, lead + 8 * s, x, row);
+                        tma_load_2d_pair(sf_dst, scales, lead + 8 * s, sf_x, sf_tile);
+                        if (PARTS == 2 && weight) {
+                            tma_load_2d_pair(dst + C::kBBytes, codes, lead + 8 * s, x, w1 + rank * (kPN / 2));
+                            tma_load_2d_pair(sf_dst + C::kBTiles * C::kSfaBytes, scales, lead + 8 * s, sf_x, w1 >> 7);
+                        }
+                        ++issued;
+                        if (++s == kStages) s = 0, ph ^= 1;
                     }
-#pragma unroll
-                    for (int p = 0; p < C::kParts; ++p) {
-                        const int acc = GLU ? p : gc & 1, use = GLU ? gc : gc >> 1;
-                        // the epilogue has read what this accumulator held before
-                        if (kb == 0 && use > 0) {
-                            ok = mbar_wait_spin(acce(acc), (use - 1) & 1, ctl);
+                    if (!ok) break;
+                }
+                if (*abort_flag) {
+                    if (rank == 0) {
+                        const int first = issued > kStages ? issued - kStages : 0;
+                        for (int i = first; i < issued; ++i)
+                            mbar_wait_drain(full(i % kStages), (i / kStages) & 1, a.timeout_ns, a.status);
+                    } else {
+                        // copies in flight into this CTA land within microseconds
+                        const uint64_t t0 = globaltimer_ns();
+                        while (globaltimer_ns() - t0 < 50000ull) {
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // (rank == 0 in this branch's own condition made the issuer a tenth slower)
+            if (rank == 0) {
+                // -------------------------------------------------------- MMA issue
+                const uint64_t ad0 = sdesc_kmajor_sw128(stage(0)), bd0 = sdesc_kmajor_sw128(stage(0) + kOffB);
+                const uint64_t sa0 = sdesc_scales(stage(0) + kOffSfa), sb0 = sdesc_scales(stage(0) + kOffSfb);
+                const int tail = (a.K - (num_kb - 1) * kStageK + 63) / 64;  // MMAs of a tile's last k-block
+                if (elect_one()) {
+                    int gc = 0, s = 0;
+                    uint32_t ph = 0;
+                    bool ok = true;
+                    for (int tile = pair; tile < total && ok; tile += npairs, ++gc) {
+                        // where a part's rows begin in their scales' 128-row tile
+                        const uint32_t sfb_off[2] = {static_cast<uint32_t>(part_row(tile, 0) & 127) >> 5,
+                                                     static_cast<uint32_t>(part_row(tile, 1) & 127) >> 5};
+                        for (int kb = 0; kb < num_kb; ++kb) {
+                            ok = mbar_wait_spin(full(s), ph, ctl);
                             if (!ok) break;
                             tc_fence_after_sync();
-                        }
+                            const uint64_t step = static_cast<uint64_t>(s) * (C::kStageBytes / 16);
+                            const uint64_t ad = ad0 + step, bd = bd0 + step, sa = sa0 + step, sb = sb0 + step;
+                            const uint32_t sfa = tmem + C::kTmemSf + s % C::kSets * C::kSfCols, sfb = sfa + 4 * C::kWords;
+                            constexpr int kPartCols = 4 * C::kWords * C::kBTiles;
+                            const bool last = kb + 1 == num_kb;
+                            const int n = last ? tail : 4;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (k < n) {
-                                const int w = NV ? k : k / 2;
-                                mma_fp4<NV, true>(tmem + acc * kPN, ad + 2 * k, bd + p * (C::kBBytes / 16) + 2 * k,
-                                                  idesc_fp4(2 * kRows, kPN, NV, NV ? 0 : k & 1), sfa + 4 * w,
-                                                  sfb + p * kPartCols + sfb_off[p] + 4 * C::kBTiles * w,
-                                                  kb > 0 || k > 0 ? 1u : 0u);
+                            for (int w = 0; w < C::kWords; ++w) {
+                                tmem_copy_scales_pair(sfa + 4 * w, sa + 32 * w);
+#pragma unroll
+                                for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+                                    for (int t = 0; t < C::kBTiles; ++t)
+                                        tmem_copy_scales_pair(sfb + p * kPartCols + 4 * (C::kBTiles * w + t),
+                                                              sb + (p * C::kBTiles + t) * (C::kSfaBytes / 16) + 32 * w);
                             }
-                        if (p == C::kParts - 1) mma_commit_pair(empty(s), 0x3);
-                        if (last) mma_commit_pair(accf(acc), 0x3);
+#pragma unroll
+                            for (int p = 0; p < PARTS; ++p) {
+                                const int acc = PARTS == 2 ? p : gc & 1, use = PARTS == 2 ? gc : gc >> 1;
+                                // the epilogue has read what this accumulator held before
+                                if (kb == 0 && use > 0) {
+                                    ok = mbar_wait_spin(acce(acc), (use - 1) & 1, ctl);
+                                    if (!ok) break;
+                                    tc_fence_after_sync();
+                                }
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    if (k < n) {
+                                        const int w = NV ? k : k / 2;
+                                        mma_fp4<NV, true>(tmem + acc * kPN, ad + 2 * k, bd + p * (C::kBBytes / 16) + 2 * k,
+                                                          idesc_fp4(2 * kRows, kPN, NV, NV ? 0 : k & 1), sfa + 4 * w,
+                                                          sfb + p * kPartCols + sfb_off[p] + 4 * C::kBTiles * w,
+                                                          kb > 0 || k > 0 ? 1u : 0u);
+                                    }
+                                if (p == PARTS - 1) mma_commit_pair(empty(s), 0x3);
+                                if (last) mma_commit_pair(accf(acc), 0x3);
+                            }
+                            if (!ok) break;
+                            if (++s == kStages) s = 0, ph ^= 1;
+                        }
                     }
-                    if (!ok) break;
-                    if (++s == kStages) s = 0, ph ^= 1;
+                    mma_commit_pair(done, 0x1);
+                    mbar_wait_drain(done, 0, a.timeout_ns, a.status);
                 }
             }
-                mma_commit_pair(done, 0x1);
-                mbar_wait_drain(done, 0, a.timeout_ns, a.status);
-            }
+            __syncwarp();
         }
-        __syncwarp();
-    } else if (warp >= 4) {
+    } else {
+        if constexpr (PARTS == 2) setmaxnreg_inc<kEpilogueRegs>();
         // ------------------------------------------------------------ epilogue
-        constexpr int kCols = kPN / 2, kGroups = kCols / 32;
+        constexpr int kCols = kPN / 2, kGroups = kCols / 32, kPieces = kCols / 8;
         const int q = warp & 3, c0 = (warp - 4) / 4 * kCols;
         const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + c0;
+        const uint64_t alpha = f32x2(a.alpha, a.alpha);
         pdl_wait();  // the residual may come from the kernel ahead
         // This thread's row of an accumulator into registers; the accumulator is free.
         auto read = [&](int acc, int use, uint32_t (&r)[kGroups][32]) {
@@ -292,105 +360,105 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
             if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(acce(acc), 0));
             return true;
         };
-        const uint64_t alpha = f32x2(a.alpha, a.alpha);
-        if constexpr (GLU) {
-            // gate and up, as bf16 as a linear of its own would leave them, and from
-            // them silu(gate) * up in f32, quantized: a thread has 96 columns of a row,
-            // whole blocks.  Both accumulators go back before that.
-            constexpr int kBlock = fp4_block(NV);
-            const int words = static_cast<int>(fp4_words(a.N, NV));
-            int gc = 0;
-            for (int tile = pair; tile < total; tile += npairs, ++gc) {
-                const int n0 = tile / a.m_tiles * kPN + c0;
-                const int m = tile % a.m_tiles * (2 * kRows) + rank * kRows + q * 32 + lane;
-                uint32_t r[kGroups][32];
-                uint4 gate[4 * kGroups], up[4 * kGroups];
-                auto take = [&](int part, uint4 (&v)[4 * kGroups]) {
-                    if (!read(part, gc, r)) return false;
-                    const __nv_bfloat16 *bias = a.bias != nullptr ? a.bias + part * a.N + n0 : nullptr;
+        // 32 rows x 32 columns of y at a time through shared memory (64-byte rows,
+        // swizzled as the map has it) and out by TMA.
+        const uint32_t piece = out_s + (warp - 4) * 2048;
+        const uint32_t mine = piece + lane * 64, turn = (lane >> 1) & 3;
+        const uint32_t turned = piece + lane / 4 * 64 + (((lane ^ (lane >> 3)) & 3) << 4);  // row lane / 4, its piece lane % 4
+        auto store = [&](int row0, int n0, const uint4 (&v)[kPieces]) {
 #pragma unroll
-                    for (int p = 0; p < 4 * kGroups; ++p)
-                        v[p] = finish8(r[p / 4] + 8 * (p % 4), alpha, bias != nullptr && n0 + 8 * p < a.N ? bias + 8 * p : nullptr,
-                                       nullptr);
-                    return true;
-                };
-                if (!take(0, gate) || !take(1, up)) break;
-                if (m < a.M) {
-                    uint8_t *code = a.codes + static_cast<int64_t>(m) * (a.N / 2) + n0 / 2;
-#pragma unroll
-                    for (int b = 0; b < kCols / kBlock; ++b) {
-                        const int col = n0 + b * kBlock;
-                        uint32_t scale = 0;
-                        if (col < a.N) {  // (a.N is a multiple of both blocks)
-                            uint64_t n[kBlock / 8][4];
-                            float top = 0.f;
-#pragma unroll
-                            for (int i = 0; i < kBlock / 8; ++i) {
-                                const uint4 g = gate[b * (kBlock / 8) + i], u = up[b * (kBlock / 8) + i];
-                                const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    n[i][e] = f32x2(-qc::silu_mul(__uint_as_float(gw[e] << 16), __uint_as_float(uw[e] << 16)),
-                                                    -qc::silu_mul(__uint_as_float(gw[e] & 0xffff0000u),
-                                                                  __uint_as_float(uw[e] & 0xffff0000u)));
-                                top = fp4::amax8(n[i], top);
-                            }
-                            const fp4::Divisor d = fp4::divisor<NV>(top, a.t, scale);
-                            uint32_t c[kBlock / 8];
-#pragma unroll
-                            for (int i = 0; i < kBlock / 8; ++i) c[i] = fp4::codes8<NV>(n[i], d);
-                            if constexpr (NV)
-                                *reinterpret_cast<uint2 *>(code + b * 8) = make_uint2(c[0], c[1]);
-                            else
-                                *reinterpret_cast<uint4 *>(code + b * 16) = make_uint4(c[0], c[1], c[2], c[3]);
-                        }
-                        const int block = col / kBlock;
-                        if (block < 4 * words)
-                            a.scales[fp4::scale_word_at(m, block / 4, words) + (block & 3)] = static_cast<uint8_t>(scale);
-                    }
-                    // the last word's blocks past the last tile
-                    if (n0 + kCols >= (a.N + kPN - 1) / kPN * kPN)
-                        for (int block = (n0 + kCols) / kBlock; block < 4 * words; ++block)
-                            a.scales[fp4::scale_word_at(m, block / 4, words) + (block & 3)] = 0;
-                }
+            for (int g = 0; g < kGroups; ++g) {
+                if (n0 + 32 * g >= a.N || row0 >= a.M) break;
+                if (lane == 0) bulk_wait_read();  // the piece before has left
                 __syncwarp();
-            }
-        } else {
-            // 32 rows x 32 columns at a time through shared memory (64-byte rows, swizzled as
-            // the map has it) and out by TMA.
-            const uint32_t piece = out_s + (warp - 4) * 2048;
-            const uint32_t mine = piece + lane * 64, turn = (lane >> 1) & 3;
-            int gc = 0;
-            for (int tile = pair; tile < total; tile += npairs, ++gc) {
-                const int n0 = tile / a.m_tiles * kPN + c0;
-                const int row0 = tile % a.m_tiles * (2 * kRows) + rank * kRows + q * 32;
-                const bool in = row0 + lane < a.M;
-                uint32_t r[kGroups][32];
-                if (!read(gc & 1, gc >> 1, r)) break;
 #pragma unroll
-                for (int g = 0; g < kGroups; ++g) {
-                    const int n1 = n0 + 32 * g;
-                    if (n1 >= a.N || row0 >= a.M) break;
-                    if (lane == 0) bulk_wait_read();  // the piece before has left
-                    __syncwarp();
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        const int n = n1 + 8 * p;
-                        const uint4 v = finish8(r[g] + 8 * p, alpha, a.bias != nullptr && n < a.N ? a.bias + n : nullptr,
-                                                a.residual != nullptr && n < a.N && in
-                                                    ? a.residual + static_cast<int64_t>(row0 + lane) * a.N + n : nullptr);
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + ((p ^ turn) << 4)), "r"(v.x),
-                                     "r"(v.y), "r"(v.z), "r"(v.w)
-                                     : "memory");
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tma_store_2d(&tm_y, piece, n1, row0);
-                        bulk_commit();
-                    }
+                for (int p = 0; p < 4; ++p) st_shared_v4(mine + ((p ^ turn) << 4), v[4 * g + p]);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_2d(&tm_y, piece, n0 + 32 * g, row0);
+                    bulk_commit();
                 }
             }
+        };
+        // All of this CTA's tiles.  Pieces past the last column or row read the bias and
+        // the residual of the last one there is, and are not stored.
+        auto run = [&](auto bias_tag, auto residual_tag) {
+            constexpr bool kBias = decltype(bias_tag)::value, kResidual = decltype(residual_tag)::value;
+            int gc = 0;
+            for (int tile = pair; tile < total; tile += npairs, ++gc) {
+                const int row0 = tile % a.m_tiles * (2 * kRows) + rank * kRows + q * 32, m = row0 + lane;
+                uint4 v[PARTS][kPieces], res[kResidual ? PARTS : 1][kPieces];
+                int n0[PARTS];
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p) {
+                    n0[p] = tile / a.m_tiles * kTileN + (GLU ? 0 : p * kPN) + c0;
+                    if constexpr (kResidual) {  // four lanes a row: its turn to rows comes below
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const __nv_bfloat16 *r = a.residual + static_cast<int64_t>(min(row0 + 8 * i + lane / 4, a.M - 1)) * a.N;
+#pragma unroll
+                            for (int g = 0; g < kGroups; ++g)
+                                res[p][4 * g + i] =
+                                    *reinterpret_cast<const uint4 *>(r + min(n0[p] + 32 * g + 8 * (lane % 4), a.N - 8));
+                        }
+                    }
+                }
+                bool ok = true;
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p) {
+                    uint32_t r[kGroups][32];
+                    ok = read(PARTS == 2 ? p : gc & 1, PARTS == 2 ? gc : gc >> 1, r);
+                    if (!ok) break;
+                    if constexpr (kResidual) {
+                        if (lane == 0) bulk_wait_read();
+#pragma unroll
+                        for (int g = 0; g < kGroups; ++g) {
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) st_shared_v4(turned + i * 512, res[p][4 * g + i]);
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) res[p][4 * g + i] = ld_shared_v4(mine + ((i ^ turn) << 4));
+                        }
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i) {
+                        uint4 b = make_uint4(0, 0, 0, 0);
+                        if constexpr (kBias)
+                            b = __ldg(reinterpret_cast<const uint4 *>(a.bias + (GLU ? p * a.N : 0) + min(n0[p] + 8 * i, a.N - 8)));
+                        v[p][i] = finish8<kBias, kResidual>(r[i / 4] + 8 * (i % 4), alpha, b, res[kResidual ? p : 0][i]);
+                    }
+                }
+                if (!ok) break;
+                if constexpr (GLU) {
+                    const int words = static_cast<int>(fp4_words(a.N, NV));
+                    if (m < a.M) {
+                        quantize_glu<NV, kCols>(v[0], v[PARTS - 1], n0[0], a.N, a.t,
+                                                a.codes + static_cast<int64_t>(m) * (a.N / 2) + n0[0] / 2, a.scales, m, words);
+                        // the last word's blocks past the last tile
+                        if (n0[0] + kCols >= a.n_tiles * kPN)
+                            for (int block = a.n_tiles * kPN / fp4_block(NV); block < 4 * words; ++block)
+                                a.scales[fp4::scale_word_at(m, block / 4, words) + (block & 3)] = 0;
+                    }
+                    __syncwarp();
+                } else {
+#pragma unroll
+                    for (int p = 0; p < PARTS; ++p) store(row0, n0[p], v[p]);
+                }
+            }
+        };
+        using std::false_type;
+        using std::true_type;
+        if constexpr (GLU) {
+            if (a.bias != nullptr) run(true_type(), false_type());
+            else run(false_type(), false_type());
+        } else {
+            if (a.bias != nullptr && a.residual != nullptr) run(true_type(), true_type());
+            else if (a.bias != nullptr) run(true_type(), false_type());
+            else if (a.residual != nullptr) run(false_type(), true_type());
+            else run(false_type(), false_type());
             if (lane == 0) bulk_wait();
         }
     }
@@ -403,9 +471,9 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     }
 }
 
-template <bool NV, bool GLU>
+template <bool NV, int PARTS, bool GLU>
 cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx) {
-    using C = Cfg<NV, GLU>;
+    using C = Cfg<NV, PARTS, GLU>;
     CUtensorMap mx, mw, mxs, mws, my;
     const int row_bytes = static_cast<int>(g.K / 2);
     const int64_t words = fp4_words(g.K, NV), w_rows = GLU ? 2 * g.N : g.N;
@@ -420,14 +488,15 @@ cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx) {
         my = mx;  // not used
     else if (!tensor_map_2d(&my, g.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.M, g.N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
         return cudaErrorInvalidValue;
-    auto kern = fp4_gemm_pair_kernel<NV, GLU>;
+    auto kern = fp4_gemm_pair_kernel<NV, PARTS, GLU>;
     if (cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), static_cast<int>(C::kSmemBytes));
         e != cudaSuccess)
         return e;
     const int sms = sm_count();
     if (sms < 2) return cudaErrorInvalidDevice;
-    const int64_t m_tiles = (g.M + 2 * kRows - 1) / (2 * kRows);
-    const int64_t tiles = m_tiles * ((g.N + kPN - 1) / kPN);
+    constexpr int kTileN = GLU ? kPN : PARTS * kPN;
+    const int64_t m_tiles = (g.M + 2 * kRows - 1) / (2 * kRows), n_tiles = (g.N + kTileN - 1) / kTileN;
+    const int64_t tiles = m_tiles * n_tiles;
     if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
     const int pairs = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
     cudaLaunchConfig_t cfg = {};
@@ -446,7 +515,7 @@ cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx) {
     cfg.numAttrs = ctx.pdl ? 2 : 1;
     Args a = {};
     a.M = static_cast<int>(g.M), a.N = static_cast<int>(g.N), a.K = static_cast<int>(g.K);
-    a.m_tiles = static_cast<int>(m_tiles);
+    a.m_tiles = static_cast<int>(m_tiles), a.n_tiles = static_cast<int>(n_tiles);
     a.alpha = g.alpha;
     a.bias = static_cast<const __nv_bfloat16 *>(g.bias), a.residual = static_cast<const __nv_bfloat16 *>(g.residual);
     a.codes = g.a_codes, a.scales = g.a_scales, a.t = fp4::scale_of(g.a_scale);
@@ -458,11 +527,22 @@ cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx) {
 }  // namespace
 
 cudaError_t launch_fp4_gemm_pair(const Fp4Gemm &g, const LaunchCtx &ctx) {
-    return g.nv ? launch_t<true, false>(g, ctx) : launch_t<false, false>(g, ctx);
+    const int64_t pairs = sm_count() / 2;
+    if (pairs < 1) return cudaErrorInvalidDevice;
+    // Two parts a tile take 1.8 times one part's time where K is long, and nearly twice
+    // it where the stores bound both, so they pay when they take half the rounds of tiles:
+    // 218 us against 243 for 16384 x 4096 -> 12288 (27 rounds against 54), 62 against 66
+    // for 4096 x 4096 -> 12288 (7, 14), but 34.5 against 33.6 for 8192 x 1024 -> 8192
+    // (10, 19), 70.5 against 61 for 4096 x 12288 -> 4096 (3, 5) and 19.5 against 15.9 for
+    // 2048 x 4096 -> 4096 (2, 3).
+    auto rounds = [&](int n) { return ((g.M + 2 * kRows - 1) / (2 * kRows) * ((g.N + n - 1) / n) + pairs - 1) / pairs; };
+    if (2 * rounds(2 * kPN) <= rounds(kPN))
+        return g.nv ? launch_t<true, 2, false>(g, ctx) : launch_t<false, 2, false>(g, ctx);
+    return g.nv ? launch_t<true, 1, false>(g, ctx) : launch_t<false, 1, false>(g, ctx);
 }
 
 cudaError_t launch_fp4_gemm_glu(const Fp4Gemm &g, const LaunchCtx &ctx) {
-    return g.nv ? launch_t<true, true>(g, ctx) : launch_t<false, true>(g, ctx);
+    return g.nv ? launch_t<true, 2, true>(g, ctx) : launch_t<false, 2, true>(g, ctx);
 }
 
 }  // namespace ck

@@ -196,6 +196,14 @@ def test_gemm_large(M, K, N, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,K,N,bias,residual", [(2048, 352, 3400, False, False), (1999, 256, 3256, True, False), (1801, 288, 3400, False, True),
+                                                 (2041, 96, 3272, True, True), (4100, 64, 3456, True, True)])
+def test_gemm_many_tiles(M, K, N, fmt, bias, residual):
+    """Enough tiles that each holds twice the rows of W, whose second half ends inside N, at it, or lies behind it."""
+    check_gemm(M, K, N, fmt, bias=bias, residual=residual)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("M", [4, 40, 400])
 def test_gemm_nan_scales(M, fmt):
     """A block with a NaN scale makes its row of X, or its row of W, NaN, and nothing else."""
