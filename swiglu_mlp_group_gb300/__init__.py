@@ -457,7 +457,7 @@ def _call_device(x, what: str) -> int:
     dev = x.get_device()
     if dev < 0:
         raise ValueError(f"{what} must be a CUDA tensor")
-    if dev != _torch()._C._cuda_getDevice():
+    if dev != _torch().cuda.current_device():
         raise ValueError(f"{what} is on cuda:{dev}, which is not the current device")
     return dev
 

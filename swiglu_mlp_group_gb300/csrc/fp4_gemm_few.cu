@@ -91,7 +91,7 @@ fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());
     const int n_tile = blockIdx.x / a.splits;
-    const int n0 = n_tile * kRows, m0 = blockIdx.y * TN;
+    const int n0 = n_tile * kRows;
     const int num_kb = (a.K + kStageK - 1) / kStageK;
     const int kb0 = num_kb * rank / a.splits, kbs = num_kb * (rank + 1) / a.splits - kb0;
     const WaitCtl ctl{abort_flag, a.status, a.timeout_ns};
@@ -125,7 +125,6 @@ fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
             tma_prefetch_desc(&tm_w);
             if constexpr (!kQuant) tma_prefetch_desc(&tm_x);
             const uint8_t *ws = a.ws + (static_cast<int64_t>(n_tile) * a.words) * 512;
-            const uint8_t *xs = kQuant ? nullptr : a.xs + (static_cast<int64_t>(m0 >> 7) * a.words) * 512;
             auto sf_bytes = [&](int kb) {
                 const int left = a.words - kb * C::kWords;
                 return static_cast<uint32_t>((left < C::kWords ? left : C::kWords) * 512);
@@ -138,8 +137,8 @@ fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
             };
             auto load_x = [&](int s, int kb) {
                 if constexpr (!kQuant) {
-                    tma_load_2d(stage(s) + kOffB, &tm_x, full(s), kb * (kStageK / 2), m0);
-                    bulk_load_1d(stage(s) + kOffSfb, xs + static_cast<int64_t>(kb) * C::kSfBytes, sf_bytes(kb), full(s));
+                    tma_load_2d(stage(s) + kOffB, &tm_x, full(s), kb * (kStageK / 2), 0);
+                    bulk_load_1d(stage(s) + kOffSfb, a.xs + static_cast<int64_t>(kb) * C::kSfBytes, sf_bytes(kb), full(s));
                 }
             };
             if (!a.weights_settled) pdl_wait();
@@ -167,7 +166,6 @@ fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issue
         const uint32_t sfa = tmem + C::kTmemSf, sfb = sfa + 16;
-        const uint32_t sfb_tile = sfb + ((m0 & 127) >> 5);  // this tile's tokens within their 128 rows of scales
         if (elect_one()) {
             bool ok = true;
             int s = 0;
@@ -190,7 +188,7 @@ fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
                     if (64 * k < left) {
                         const int w = NV ? k : k / 2;
                         mma_fp4<NV, false>(tmem, ad + 2 * k, bd + 2 * k, idesc_fp4(kRows, TN, NV, NV ? 0 : k & 1),
-                                           sfa + 4 * w, sfb_tile + 4 * w, i > 0 || k > 0 ? 1u : 0u);
+                                           sfa + 4 * w, sfb + 4 * w, i > 0 || k > 0 ? 1u : 0u);
                     }
                 mma_commit(empty(s));
                 if (++s == kStages) s = 0, ph ^= 1u;
@@ -321,14 +319,14 @@ fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
             constexpr int kStep = TN < 16 ? 8 : 16;
 #pragma unroll
             for (int c0 = 0; c0 < TN; c0 += kStep) {
-                if (m0 + c0 >= a.M) break;
+                if (c0 >= a.M) break;
                 uint32_t v[16];
                 tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(q * 32) << 16) + c0, v);
                 tmem_wait_ld16(v);
 #pragma unroll
                 for (int j = 0; j < kStep; ++j) {
                     const int c = c0 + j, owner = c / own;
-                    if (m0 + c >= a.M) break;
+                    if (c >= a.M) break;
                     const uint32_t at = red_s + 4u * ((rank * own + c - owner * own) * kRows + r);
                     asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(mapa_shared(at, owner)), "r"(v[j]) : "memory");
                 }
@@ -348,7 +346,7 @@ fp4_gemm_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
             }
             if constexpr (!kQuant) pdl_wait();  // the residual may come from the kernel ahead
             for (int c = t >> 6; c < own; c += 2) {
-                const int m = m0 + rank * own + c;
+                const int m = rank * own + c;
                 if (m >= a.M) break;
                 const int64_t at = static_cast<int64_t>(m) * a.N + n;
                 float r0 = 0.f, r1 = 0.f;
@@ -394,14 +392,14 @@ cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx) {
         return e;
     const int sms = sm_count();
     if (sms < 1) return cudaErrorInvalidDevice;
-    const int64_t n_tiles = (g.N + kRows - 1) / kRows, m_tiles = (g.M + TN - 1) / TN;
+    const int64_t n_tiles = (g.N + kRows - 1) / kRows;
     const int64_t num_kb = (g.K + kStageK - 1) / kStageK;
-    if (m_tiles > 65535) return cudaErrorInvalidValue;
+    if (g.M > TN) return cudaErrorInvalidValue;  // one tile of tokens
     // as many parts of K as leave all CTAs resident at once
     int splits = 1;
-    while (splits < 8 && n_tiles * m_tiles * splits * 2 <= 2 * sms && splits * 2 <= num_kb) splits *= 2;
+    while (splits < 8 && n_tiles * splits * 2 <= 2 * sms && splits * 2 <= num_kb) splits *= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(n_tiles * splits), static_cast<unsigned>(m_tiles));
+    cfg.gridDim = dim3(static_cast<unsigned>(n_tiles * splits));
     cfg.blockDim = dim3(FROM == From::kCodes ? kThreads : kThreads + 128);
     cfg.dynamicSmemBytes = C::kSmemBytes;
     cfg.stream = ctx.stream;
@@ -447,9 +445,8 @@ cudaError_t launch_fp4_gemm_few(const Fp4Gemm &g, const LaunchCtx &ctx) {
 }
 
 // Up to 32 tokens the weight's bytes count, and a tile of 256 tokens leaves most SMs
-// without any (32 x 4096 -> 4096: 6.5 us against 8.1); from 33 on a second tile of
-// tokens costs the few-token kernel more than that (33: 7.4 against 8.2, but 8.6 of
-// the other's at -> 12288 against 12.4).
+// without any (32 x 4096 -> 4096: 6.5 us against 8.1); with a second tile of tokens here,
+// 33 took 7.4 against 8.2, but 12.4 against the other's 8.6 at -> 12288.
 cudaError_t launch_fp4_gemm(const Fp4Gemm &g, const LaunchCtx &ctx) {
     return g.M > kFp4Few ? launch_fp4_gemm_pair(g, ctx) : launch_fp4_gemm_few(g, ctx);
 }

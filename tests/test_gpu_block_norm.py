@@ -88,6 +88,16 @@ def test_f32_weights_and_many_rows(norm):
     check(a, *ck.block_norm(**to(a, dev)))
 
 
+@pytest.mark.parametrize("parts", ["post", "all"])
+@pytest.mark.parametrize("norm", ["rms", "layer"])
+@pytest.mark.parametrize("T,H,per", [(1311, 1480, 100), (701, 2056, 0), (607, 4096, 33), (4103, 392, 0), (9001, 264, 1000), (40001, 40, 7)])
+def test_wide_threads(T, H, per, norm, parts):
+    """So many rows that threads take more columns each; H fills them, or does not."""
+    dev = device()
+    a = case(T + H, T, H, parts, norm, per)
+    check(a, *ck.block_norm(**to(a, dev)))
+
+
 def test_rows_far_from_zero():
     """A mean of a thousand deviations, a channel a thousand times the others, a row of zeros, rows of tiny and huge values."""
     dev = device()
@@ -144,7 +154,7 @@ def test_not_finite_stays_in_its_row():
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
 @pytest.mark.parametrize("norm", ["rms", "layer"])
 @pytest.mark.parametrize("T,H,per,parts", [(1, 32, 0, "norm"), (5, 96, 0, "sum"), (133, 1184, 9, "all"), (40, 2080, 3, "modulated"),
-                                           (6, 8224, 0, "post"), (3, 16384, 2, "gate")])
+                                           (1310, 1504, 9, "all"), (4103, 416, 0, "sum"), (1250, 1024, 3, "modulated"), (6, 8224, 0, "post"), (3, 16384, 2, "gate")])
 def test_block_norm_fp4(T, H, per, parts, norm, fmt):
     dev = device()
     t = 1.0 if fmt == "mx" else 0.0037
