@@ -10,8 +10,9 @@
 //
 // One part a tile: the accumulators in turn, so that a tile's epilogue runs under the
 // next one's products.  Two: X's bytes once for both, and the epilogue first reads both
-// accumulators into registers as packed bf16, the first while the second's last products
-// run, and hands them back before it does anything else.
+// accumulators into registers and hands them back before it does anything else; a
+// tile's first and last two k-blocks go to the first part together, then to the second,
+// so that the tensor cores have 768 clocks of work while an accumulator is read.
 //
 // GLU: the parts are rows of gate and the rows of up that go with them, and the
 // epilogue makes silu(gate) * up of them and quantizes it: what the next linear of a
@@ -54,11 +55,10 @@ struct Cfg {
     static constexpr int kBarBytes = 256;
     static constexpr int kStages = (227 * 1024 - kBarBytes - kOutBytes - 1024) / kStageBytes;
     static constexpr int kTmemSf = 2 * kPN;                // the scales' first column
-    static constexpr int kSfCols = 4 * kWords * (1 + PARTS * kBTiles);
+    static constexpr int kSfCols = 4 * kWords * (1 + kBTiles);
     static constexpr int kTmemCols = 512;
-    static constexpr int kSets = kTmemSf + 2 * kSfCols <= kTmemCols ? 2 : 1;  // of scales, taken in turn
     static constexpr size_t kSmemBytes = static_cast<size_t>(kStages) * kStageBytes + kOutBytes + kBarBytes + 1024;
-    static_assert(kStageBytes % 1024 == 0 && kTmemSf + kSets * kSfCols <= kTmemCols, "layout");
+    static_assert(kStageBytes % 1024 == 0 && kTmemSf + 2 * kSfCols <= kTmemCols, "layout");
     static_assert(8 * (2 * kStages + 5) + 8 <= kBarBytes && kSmemBytes <= 227 * 1024, "shared memory");
 };
 
@@ -141,24 +141,27 @@ __device__ __forceinline__ void quantize_glu(const uint4 (&gate)[COLS / 8], cons
 // What bounds it.  The MMAs of a part's stage (256 columns of K) take 384 clocks, 9.5
 // PFLOP/s in all, with or without the scales' copies between them (timed alone, from
 // shared memory).  Their operands: 81 (MX) and 89 (NV) bytes a clock and SM with one
-// part, of which some 77 come in, 59 and 65 with two, whose k-blocks run at 97 % of the
-// MMAs' rate; there the rest is between tiles (the first k-block's data, the
-// accumulators' reading).  Random codes draw so much power that the clock gives another
-// tenth: 227 us (NV) and 216 (MX) for 16384 x 4096 -> 12288, 218 on zeros, or 7.3 and 7.6
-// PFLOP/s; gate and up of as many tokens with 6144 rows each 215 and 206.
+// part, of which some 70 come in, 59 and 65 with two, which then wait for the issue
+// (28 instructions a k-block, NV, at some 30 clocks each, MX 18) and between tiles.
+// Random codes draw so much power that the clock gives another 5 %.  16384 x 4096 ->
+// 12288: 223 us (NV) and 217 (MX), on zeros 213 and 208 (7.7 and 7.9 PFLOP/s), with a
+// residual 272 and 264; gate and up of as many tokens with 6144 rows each, where no y is
+// stored, 209 and 200, on zeros 196 and 188 (8.4 and 8.8).
 //
 // What it took: one lane that polls and issues, of a warp of its own (32 lanes polling a
-// barrier cost the issuer a third of its time), a producer for each operand (one for both
-// took longer to issue than the MMAs to run), y through shared memory and TMA (exchanged
-// between lanes and stored by them: 252 us against 240), no branches between the columns
-// of an accumulator's reading (1450 clocks for 96 columns with them, 650 without), the
-// residual read in whole sectors, four lanes a row, and turned to rows in shared memory
-// (a lane its own row: 300 us against 265, 8192 x 1024 -> 8192 77 against 71; read a tile
-// ahead: 330), with two parts more registers for the epilogue than for the rest (222 us
-// without, and a tenth more with a residual; one part does not need them: 247 against 242).
-// Tried and slower (one part): 512 tokens x 192 rows (252 us against 240), the issuer's stages
-// unrolled, tiles in bands of 8 and 16 rows of tiles, y in pieces of 64 columns (250),
-// the next tile's first k-blocks prefetched to L2 (264 against 249).
+// barrier, or walking together and issuing by predicate, 259 us against 205), a producer
+// for each operand (one for both took longer to issue than the MMAs to run), y through
+// shared memory and TMA (exchanged between lanes and stored by them 252 us against 240,
+// from shared memory by coalesced stores 212 against 208), no branches between the
+// columns of an accumulator's reading (1450 clocks for 96 columns with them, 650
+// without), the residual read in whole sectors, four lanes a row, and turned to rows in
+// shared memory (a lane its own row: 300 us against 265), with two parts more registers
+// for the epilogue than for the rest (222 us against 218; one part does not need them:
+// 247 against 242), the k-blocks' order at a tile's ends (gate and up 206 us without, MX;
+// for every k-block NV 205 against 196), in a loop that is not unrolled (278).
+// Tried and slower, one part: 512 tokens x 192 rows (252 us against 240), the issuer's
+// stages unrolled, tiles in bands of 8 and 16 rows of tiles, y in pieces of 64 columns
+// (250), the next tile's first k-blocks prefetched to L2 (264 against 249).
 template <bool NV, int PARTS, bool GLU>
 __global__ void __launch_bounds__(kThreads, 1)
 fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
@@ -282,53 +285,62 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
                     int gc = 0, s = 0;
                     uint32_t ph = 0;
                     bool ok = true;
+                    // Stage st's share of a part: its scales' copies to set `set`, its MMAs.
+                    auto unit = [&](int st, int set, int acc, int p, uint32_t sfb_off, int n, bool first) {
+                        const uint64_t step = static_cast<uint64_t>(st) * (C::kStageBytes / 16);
+                        const uint64_t ad = ad0 + step, bd = bd0 + step + p * (C::kBBytes / 16);
+                        const uint64_t sa = sa0 + step, sb = sb0 + step + p * (C::kBTiles * C::kSfaBytes / 16);
+                        const uint32_t sfa = tmem + C::kTmemSf + set * C::kSfCols, sfb = sfa + 4 * C::kWords;
+#pragma unroll
+                        for (int w = 0; w < C::kWords; ++w) {
+                            if (p == 0) tmem_copy_scales_pair(sfa + 4 * w, sa + 32 * w);
+#pragma unroll
+                            for (int t = 0; t < C::kBTiles; ++t)
+                                tmem_copy_scales_pair(sfb + 4 * (C::kBTiles * w + t), sb + t * (C::kSfaBytes / 16) + 32 * w);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (k < n) {
+                                const int w = NV ? k : k / 2;
+                                mma_fp4<NV, true>(tmem + acc * kPN, ad + 2 * k, bd + 2 * k,
+                                                  idesc_fp4(2 * kRows, kPN, NV, NV ? 0 : k & 1), sfa + 4 * w,
+                                                  sfb + sfb_off + 4 * C::kBTiles * w, !first || k > 0 ? 1u : 0u);
+                            }
+                    };
                     for (int tile = pair; tile < total && ok; tile += npairs, ++gc) {
                         // where a part's rows begin in their scales' 128-row tile
                         const uint32_t sfb_off[2] = {static_cast<uint32_t>(part_row(tile, 0) & 127) >> 5,
                                                      static_cast<uint32_t>(part_row(tile, 1) & 127) >> 5};
-                        for (int kb = 0; kb < num_kb; ++kb) {
-                            ok = mbar_wait_spin(full(s), ph, ctl);
-                            if (!ok) break;
-                            tc_fence_after_sync();
-                            const uint64_t step = static_cast<uint64_t>(s) * (C::kStageBytes / 16);
-                            const uint64_t ad = ad0 + step, bd = bd0 + step, sa = sa0 + step, sb = sb0 + step;
-                            const uint32_t sfa = tmem + C::kTmemSf + s % C::kSets * C::kSfCols, sfb = sfa + 4 * C::kWords;
-                            constexpr int kPartCols = 4 * C::kWords * C::kBTiles;
-                            const bool last = kb + 1 == num_kb;
-                            const int n = last ? tail : 4;
-#pragma unroll
-                            for (int w = 0; w < C::kWords; ++w) {
-                                tmem_copy_scales_pair(sfa + 4 * w, sa + 32 * w);
-#pragma unroll
-                                for (int p = 0; p < PARTS; ++p)
-#pragma unroll
-                                    for (int t = 0; t < C::kBTiles; ++t)
-                                        tmem_copy_scales_pair(sfb + p * kPartCols + 4 * (C::kBTiles * w + t),
-                                                              sb + (p * C::kBTiles + t) * (C::kSfaBytes / 16) + 32 * w);
-                            }
+                        for (int kb = 0; kb < num_kb;) {
+                            const int group = PARTS == 2 && (kb == 0 || kb + 2 == num_kb) && kb + 1 < num_kb ? 2 : 1;
+                            int st = s;
+                            uint32_t sph = ph;
 #pragma unroll
                             for (int p = 0; p < PARTS; ++p) {
                                 const int acc = PARTS == 2 ? p : gc & 1, use = PARTS == 2 ? gc : gc >> 1;
-                                // the epilogue has read what this accumulator held before
-                                if (kb == 0 && use > 0) {
-                                    ok = mbar_wait_spin(acce(acc), (use - 1) & 1, ctl);
-                                    if (!ok) break;
-                                    tc_fence_after_sync();
-                                }
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    if (k < n) {
-                                        const int w = NV ? k : k / 2;
-                                        mma_fp4<NV, true>(tmem + acc * kPN, ad + 2 * k, bd + p * (C::kBBytes / 16) + 2 * k,
-                                                          idesc_fp4(2 * kRows, kPN, NV, NV ? 0 : k & 1), sfa + 4 * w,
-                                                          sfb + p * kPartCols + sfb_off[p] + 4 * C::kBTiles * w,
-                                                          kb > 0 || k > 0 ? 1u : 0u);
+                                st = s, sph = ph;
+#pragma unroll 1
+                                for (int j = 0; j < group; ++j) {
+                                    if (p == 0) {
+                                        ok = mbar_wait_spin(full(st), sph, ctl);
+                                        if (!ok) break;
                                     }
-                                if (p == PARTS - 1) mma_commit_pair(empty(s), 0x3);
-                                if (last) mma_commit_pair(accf(acc), 0x3);
+                                    // the epilogue has read what this accumulator held before
+                                    if (kb + j == 0 && use > 0) {
+                                        ok = mbar_wait_spin(acce(acc), (use - 1) & 1, ctl);
+                                        if (!ok) break;
+                                    }
+                                    tc_fence_after_sync();
+                                    const bool last = kb + j + 1 == num_kb;
+                                    unit(st, PARTS == 2 ? j : st & 1, acc, p, sfb_off[p], last ? tail : 4, kb + j == 0);
+                                    if (p == PARTS - 1) mma_commit_pair(empty(st), 0x3);
+                                    if (last) mma_commit_pair(accf(acc), 0x3);
+                                    if (++st == kStages) st = 0, sph ^= 1;
+                                }
+                                if (!ok) break;
                             }
                             if (!ok) break;
-                            if (++s == kStages) s = 0, ph ^= 1;
+                            kb += group, s = st, ph = sph;
                         }
                     }
                     mma_commit_pair(done, 0x1);
@@ -345,20 +357,23 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
         const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + c0;
         const uint64_t alpha = f32x2(a.alpha, a.alpha);
         pdl_wait();  // the residual may come from the kernel ahead
-        // This thread's row of an accumulator into registers; the accumulator is free.
-        auto read = [&](int acc, int use, uint32_t (&r)[kGroups][32]) {
+        // This thread's row of an accumulator into registers, in two steps: when both are
+        // done the accumulator is free.
+        auto begin_read = [&](int acc, int use, uint32_t (&r)[kGroups][32]) {
             int got = 0;
             if (lane == 0) got = mbar_wait(accf(acc), use & 1, ctl) ? 1 : 0;
             if (!__shfl_sync(0xffffffffu, got, 0)) return false;
             tc_fence_after_sync();
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) tmem_ld_32x32b_x32(tbase + acc * kPN + 32 * g, r[g]);
+            return true;
+        };
+        auto end_read = [&](int acc, uint32_t (&r)[kGroups][32]) {
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) tmem_wait_ld(r[g]);
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(acce(acc), 0));
-            return true;
         };
         // 32 rows x 32 columns of y at a time through shared memory (64-byte rows,
         // swizzled as the map has it) and out by TMA.
@@ -387,7 +402,7 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
             constexpr bool kBias = decltype(bias_tag)::value, kResidual = decltype(residual_tag)::value;
             int gc = 0;
             for (int tile = pair; tile < total; tile += npairs, ++gc) {
-                const int row0 = tile % a.m_tiles * (2 * kRows) + rank * kRows + q * 32, m = row0 + lane;
+                const int row0 = tile % a.m_tiles * (2 * kRows) + rank * kRows + q * 32;
                 uint4 v[PARTS][kPieces], res[kResidual ? PARTS : 1][kPieces];
                 int n0[PARTS];
 #pragma unroll
@@ -404,12 +419,7 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
                         }
                     }
                 }
-                bool ok = true;
-#pragma unroll
-                for (int p = 0; p < PARTS; ++p) {
-                    uint32_t r[kGroups][32];
-                    ok = read(PARTS == 2 ? p : gc & 1, PARTS == 2 ? gc : gc >> 1, r);
-                    if (!ok) break;
+                auto finish = [&](int p, const uint32_t (&r)[kGroups][32]) {
                     if constexpr (kResidual) {
                         if (lane == 0) bulk_wait_read();
 #pragma unroll
@@ -430,10 +440,21 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
                             b = __ldg(reinterpret_cast<const uint4 *>(a.bias + (GLU ? p * a.N : 0) + min(n0[p] + 8 * i, a.N - 8)));
                         v[p][i] = finish8<kBias, kResidual>(r[i / 4] + 8 * (i % 4), alpha, b, res[kResidual ? p : 0][i]);
                     }
+                };
+                uint32_t r[kGroups][32];
+                if (!begin_read(PARTS == 2 ? 0 : gc & 1, PARTS == 2 ? gc : gc >> 1, r)) break;
+                end_read(PARTS == 2 ? 0 : gc & 1, r);
+                if constexpr (PARTS == 1 || kResidual) finish(0, r);
+                if constexpr (PARTS == 2) {
+                    // (with a residual there are no registers for both)
+                    uint32_t r1[kGroups][32];
+                    if (!begin_read(1, gc, r1)) break;
+                    if constexpr (!kResidual) finish(0, r);
+                    end_read(1, r1);
+                    finish(1, r1);
                 }
-                if (!ok) break;
                 if constexpr (GLU) {
-                    const int words = static_cast<int>(fp4_words(a.N, NV));
+                    const int words = static_cast<int>(fp4_words(a.N, NV)), m = row0 + lane;
                     if (m < a.M) {
                         quantize_glu<NV, kCols>(v[0], v[PARTS - 1], n0[0], a.N, a.t,
                                                 a.codes + static_cast<int64_t>(m) * (a.N / 2) + n0[0] / 2, a.scales, m, words);
@@ -529,12 +550,12 @@ cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx) {
 cudaError_t launch_fp4_gemm_pair(const Fp4Gemm &g, const LaunchCtx &ctx) {
     const int64_t pairs = sm_count() / 2;
     if (pairs < 1) return cudaErrorInvalidDevice;
-    // Two parts a tile take 1.8 times one part's time where K is long, and nearly twice
-    // it where the stores bound both, so they pay when they take half the rounds of tiles:
-    // 218 us against 243 for 16384 x 4096 -> 12288 (27 rounds against 54), 62 against 66
-    // for 4096 x 4096 -> 12288 (7, 14), but 34.5 against 33.6 for 8192 x 1024 -> 8192
-    // (10, 19), 70.5 against 61 for 4096 x 12288 -> 4096 (3, 5) and 19.5 against 15.9 for
-    // 2048 x 4096 -> 4096 (2, 3).
+    // Two parts a tile take 1.75 times one part's time where K is long, and twice it where
+    // the stores bound both, so they pay when they take half the rounds of tiles: 213 us
+    // against 240 for 16384 x 4096 -> 12288 (27 rounds against 54; NV, zeros), 60.5
+    // against 65 for 4096 x 4096 -> 12288 (7, 14), but 34.3 against 33.5 for 8192 x 1024
+    // -> 8192 (10, 19), 67 against 60 for 4096 x 12288 -> 4096 (3, 5) and 19.5 against
+    // 15.7 for 2048 x 4096 -> 4096 (2, 3).
     auto rounds = [&](int n) { return ((g.M + 2 * kRows - 1) / (2 * kRows) * ((g.N + n - 1) / n) + pairs - 1) / pairs; };
     if (2 * rounds(2 * kPN) <= rounds(kPN))
         return g.nv ? launch_t<true, 2, false>(g, ctx) : launch_t<false, 2, false>(g, ctx);
