@@ -530,7 +530,7 @@ def _new(shape, dtype, like, stream):
 
 
 def _new_on(shape, dtype, device, stream):
-    """_new on a device (its index will do)."""
+    """A new tensor of the call's stream (device: a torch.device, x's; an index is 2 us of a small call's 10)."""
     torch = _torch()
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
@@ -775,22 +775,20 @@ def _fp4_operand(codes, scales, f: int, what: str, dev: int):
     return rows, 2 * half, p, ps
 
 
-def _out_rows(out, M: int, N: int, dev: int, stream):
+def _out_rows(out, M: int, N: int, dev: int, device, stream):
     """A linear's output (contiguous bf16 [M, N]): the one given, checked, or a new one."""
     torch = _torch()
     if out is not None:
         _typed(out, torch.bfloat16, "out", dev, (M, N))
         return out
-    if stream is None:
-        return torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    return _new_on((M, N), torch.bfloat16, dev, stream)
+    return _new_on((M, N), torch.bfloat16, device, stream)
 
 
-def _scales_out(scales, n: int, dev: int, stream):
+def _scales_out(scales, n: int, dev: int, device, stream):
     """Tiled scales to write: the tensor given, if it is large enough, or a new one."""
     u8 = _torch().uint8
     if scales is None:
-        return _new_on((n,), u8, dev, stream)
+        return _new_on((n,), u8, device, stream)
     _typed(scales, u8, "scales", dev)
     if scales.nbytes < n:
         raise ValueError(f"scales must hold {n} bytes")
@@ -814,8 +812,8 @@ def fp4_quantize(x, fmt: str, scale: float = 1.0, act: str = "none", codes=None,
     if n == 0:
         raise CkError(CK_ERR_SHAPE, "ck_fp4_quantize")
     if codes is None:
-        codes = _new_on((M, K // 2), torch.uint8, dev, stream)
-    scales = _scales_out(scales, n, dev, stream)
+        codes = _new_on((M, K // 2), torch.uint8, x.device, stream)
+    scales = _scales_out(scales, n, dev, x.device, stream)
     st = lib().ck_fp4_quantize(x.data_ptr(), CK_F32 if f32 else CK_BF16, M, K, ldx, a, f, scale,
                                _typed(codes, torch.uint8, "codes", dev, (M, K // 2)), scales.data_ptr(),
                                _run_stream(stream, dev))
@@ -836,7 +834,7 @@ def fp4_tile_scales(scales, fmt: str, stream=None):
     n = int(lib().ck_fp4_scale_bytes(f, rows, K))
     if n == 0:
         raise CkError(CK_ERR_SHAPE, "ck_fp4_tile_scales")
-    out = _new_on((n,), torch.uint8, dev, stream)
+    out = _new_on((n,), torch.uint8, scales.device, stream)
     st = lib().ck_fp4_tile_scales(p, rows, K, f, out.data_ptr(), _run_stream(stream, dev))
     if st != CK_OK:
         raise CkError(st, "ck_fp4_tile_scales")
@@ -855,7 +853,7 @@ def fp4_gemm(codes, scales, W, w_scales, fmt: str, alpha: float = 1.0, bias=None
         raise ValueError("codes and W must have the same columns")
     bf16 = _torch().bfloat16
     pb, pr = _typed(bias, bf16, "bias", dev, (N,)), _typed(residual, bf16, "residual", dev, (M, N))
-    y = _out_rows(out, M, N, dev, stream)
+    y = _out_rows(out, M, N, dev, codes.device, stream)
     st = lib().ck_fp4_gemm(px, pxs, M, K, f, pw, pws, N, alpha, pb, pr, y.data_ptr(), _run_stream(stream, dev))
     if st != CK_OK:
         raise CkError(st, "ck_fp4_gemm")
@@ -885,8 +883,8 @@ def fp4_linear(x, W, w_scales, fmt: str, x_scale: float = 1.0, w_scale: float = 
         raise ValueError("x and W must have the same columns")
     pb = None if bias is None else _typed(bias, bf16, "bias", dev, (N,))
     pr = None if residual is None else _typed(residual, bf16, "residual", dev, (M, N))
-    y = _out_rows(out, M, N, dev, stream)
-    ws = _given_workspace(workspace, dev) if workspace is not None else fp4_linear_workspace(M, K, fmt, dev, stream)
+    y = _out_rows(out, M, N, dev, x.device, stream)
+    ws = _given_workspace(workspace, dev) if workspace is not None else fp4_linear_workspace(M, K, fmt, x.device, stream)
     st = lib().ck_fp4_linear(x.data_ptr(), M, K, ldx, a, f, x_scale, pw, pws, w_scale, N, pb, pr, y.data_ptr(),
                              ws.data_ptr(), ws.nbytes, _run_stream(stream, dev))
     if st != CK_OK:
@@ -917,9 +915,9 @@ def fp4_swiglu_mlp(x, Wgu, gu_scales, Wd, d_scales, fmt: str, x_scale: float = 1
         raise ValueError("Wgu must be [2I, H / 2] and Wd [H, I / 2] of x's H columns")
     pbgu, pbd = _typed(bgu, bf16, "bgu", dev, (N,)), _typed(bd, bf16, "bd", dev, (H,))
     pr = _typed(residual, bf16, "residual", dev, (M, H))
-    y = _out_rows(out, M, H, dev, stream)
+    y = _out_rows(out, M, H, dev, x.device, stream)
     ws = (_given_workspace(workspace, dev) if workspace is not None else
-          fp4_swiglu_mlp_workspace(M, H, I, fmt, dev, stream))
+          fp4_swiglu_mlp_workspace(M, H, I, fmt, x.device, stream))
     st = lib().ck_fp4_swiglu_mlp(px, M, H, I, f, x_scale, pgu, pgus, gate_up_scale, pbgu, act_scale, pd, pds,
                                  down_scale, pbd, pr, y.data_ptr(), ws.data_ptr(), ws.nbytes, _run_stream(stream, dev))
     if st != CK_OK:
@@ -1012,8 +1010,8 @@ def block_norm_fp4(x, branch=None, fmt: str = "nv", n_scale: float = 1.0, post_w
     if H % 32 != 0:
         raise CkError(CK_ERR_SHAPE, "ck_block_norm_fp4")
     if codes is None:
-        codes = _new_on((T, H // 2), u8, dev, stream)
-    scales = _scales_out(scales, _tiled_bytes(f, T, H), dev, stream)
+        codes = _new_on((T, H // 2), u8, x.device, stream)
+    scales = _scales_out(scales, _tiled_bytes(f, T, H), dev, x.device, stream)
     st = lib().ck_block_norm_fp4(*args, f, n_scale, _typed(codes, u8, "codes", dev, (T, H // 2)), scales.data_ptr(),
                                  _run_stream(stream, dev))
     if st != CK_OK:
