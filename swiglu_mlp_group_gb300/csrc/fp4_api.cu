@@ -92,15 +92,16 @@ bool overlap(const void *p, size_t n, const void *q, size_t m) {
 }
 
 // One linear: with few tokens a single kernel, which quantizes x in every CTA (and so
-// while others write y), else the quantizer and the product.
+// while others write y), else the quantizer and the product.  settled: the kernel ahead
+// is this call's, let this one in behind its own wait, and does not write W.
 ck_status run_linear(const void *x, int64_t M, int64_t K, int64_t ldx, ck_input_act act, bool nv, float x_scale,
                      const void *W, const void *w_scales, float w_scale, int64_t N, const void *bias,
-                     const void *residual, void *y, void *ws, const Codes &c, unsigned int *status,
+                     const void *residual, void *y, void *ws, const Codes &c, bool settled, unsigned int *status,
                      ck_stream_t stream) {
     const size_t x_bytes = (static_cast<size_t>(M - 1) * ldx + (act == CK_ACT_SWIGLU ? 2 * K : K)) * 2;
     if (M <= ck::kFp4QuantizeInside && !overlap(x, x_bytes, y, static_cast<size_t>(M) * N * 2)) {
         ck::Fp4Gemm g = gemm(nullptr, nullptr, M, K, nv, W, w_scales, N, x_scale * w_scale, bias, residual, y,
-                             ck::launch_overlap());
+                             settled || ck::launch_overlap());
         g.x_bf16 = x, g.ldx = ldx, g.swiglu = act == CK_ACT_SWIGLU, g.x_scale = x_scale;
         return from_cuda(ck::launch_fp4_gemm_few(g, quantizer_context(stream, status)));
     }
@@ -229,7 +230,7 @@ CK_API ck_status ck_fp4_linear(const void *x, int64_t M, int64_t K, int64_t ldx,
     if (!aligned16(ws)) return CK_ERR_ALIGN;
     unsigned int *status = nullptr;
     if (int st = ck::device_ready_status(&status); st != CK_OK) return static_cast<ck_status>(st);
-    return run_linear(x, M, K, ldx, act, nv, x_scale, W, w_scales, w_scale, N, bias, residual, y, ws, c, status,
+    return run_linear(x, M, K, ldx, act, nv, x_scale, W, w_scales, w_scale, N, bias, residual, y, ws, c, false, status,
                       stream);
 }
 
@@ -273,11 +274,11 @@ CK_API ck_status ck_fp4_swiglu_mlp(const void *x, int64_t M, int64_t H, int64_t 
                                              context(stream, status)));
     }
     if (ck_status st = run_linear(x, M, H, H, CK_ACT_NONE, nv, x_scale, Wgu, gu_scales, gu_scale, 2 * I, bgu, nullptr,
-                                  at(ws, w.h), ws, w.x, status, stream);
+                                  at(ws, w.h), ws, w.x, false, status, stream);
         st != CK_OK)
         return st;
     return run_linear(at(ws, w.h), M, I, 2 * I, CK_ACT_SWIGLU, nv, a_scale, Wd, d_scales, d_scale, H, bd, residual, y,
-                      ws, w.a, status, stream);
+                      ws, w.a, true, status, stream);
 }
 
 CK_API ck_status ck_block_norm(const void *x, int64_t ldx, const void *branch, int64_t ldb, int64_t T, int64_t H,
