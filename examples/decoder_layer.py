@@ -6,8 +6,11 @@ shared prompt, each with its own generated tokens in a paged cache.
     the shared prompt and each sequence's own tokens -> output projection + x
     -> SwiGLU MLP + residual
 
-and, where encoder states are given, a cross attention between the two.  Every
-step runs in the library's CUDA kernels; torch holds the memory.
+and, where encoder states are given, a cross attention between the two.  The same
+layer with its norms, on 4-bit weights (Fp4DecoderLayer): each norm takes in the sum
+of the residual stream and the branch ahead, and goes straight to the codes that the
+next product reads.  Every step runs in the library's CUDA kernels; torch holds the
+memory.
 
     python examples/decoder_layer.py        # a few steps, checked against float64 attention
 """
@@ -39,6 +42,21 @@ class Linear:
         return ck.int8_linear(x, self.gemm, self.scale, G, wlayout=ck.CK_WLAYOUT_GEMM_F16, residual=residual)
 
 
+class Fp4Linear:
+    """A weight of microscaled 4-bit floats, its scales in the order that the tensor cores read."""
+
+    def __init__(self, W, fmt):
+        self.N, self.fmt = W.shape[0], fmt
+        # an NV tensor's scale lets its largest block scale reach E4M3's largest number
+        self.scale = float(W.abs().max()) / (6 * 448) if fmt == "nv" else 1.0
+        self.x_scale = 16 / (6 * 448) if fmt == "nv" else 1.0
+        self.W, self.scales = ck.fp4_quantize(W.float(), fmt, scale=self.scale)
+
+    def __call__(self, x, residual=None):
+        return ck.fp4_linear(x, self.W, self.scales, self.fmt, x_scale=self.x_scale, w_scale=self.scale,
+                             residual=residual)
+
+
 class DecoderLayer:
     def __init__(self, hidden=512, inner=1024, Hq=8, Hkv=2, D=64, page=16, pages=256, max_pos=4096, seed=0, device="cuda"):
         gen = torch.Generator(device="cpu").manual_seed(seed)
@@ -47,13 +65,10 @@ class DecoderLayer:
             return (torch.randn(n, k, generator=gen) / math.sqrt(k)).to(device)
 
         self.Hq, self.Hkv, self.D, self.page = Hq, Hkv, D, page
-        self.qkv = Linear(weight((Hq + 2 * Hkv) * D, hidden))
-        self.out = Linear(weight(hidden, Hq * D))
-        self.cross_q, self.cross_out = Linear(weight(Hq * D, hidden)), Linear(weight(hidden, Hq * D))
-        gate_up, self.gate_up_scale = ck.quantize_weight(weight(2 * inner, hidden), G)
-        down, self.down_scale = ck.quantize_weight(weight(hidden, inner), G)
-        self.gate_up = ck.prepare_weight(gate_up, self.gate_up_scale, ck.CK_WLAYOUT_GEMM_F16)
-        self.down = ck.prepare_weight(down, self.down_scale, ck.CK_WLAYOUT_GEMM_F16)
+        self.qkv = self._linear(weight((Hq + 2 * Hkv) * D, hidden))
+        self.out = self._linear(weight(hidden, Hq * D))
+        self.cross_q, self.cross_out = self._linear(weight(Hq * D, hidden)), self._linear(weight(hidden, Hq * D))
+        self._init_mlp(weight(2 * inner, hidden), weight(hidden, inner))
         self.q_norm = torch.ones(D, dtype=torch.bfloat16, device=device)
         self.k_norm = torch.ones(D, dtype=torch.bfloat16, device=device)
         inv = 10000.0 ** (-torch.arange(0, D, 2, dtype=torch.float64) / D)
@@ -62,10 +77,29 @@ class DecoderLayer:
         self.k_cache = torch.zeros(pages, Hkv, page, D, dtype=torch.bfloat16, device=device)
         self.v_cache = torch.zeros_like(self.k_cache)
 
+    def _linear(self, W):
+        return Linear(W)
+
+    def _init_mlp(self, gate_up, down):
+        gate_up, self.gate_up_scale = ck.quantize_weight(gate_up, G)
+        down, self.down_scale = ck.quantize_weight(down, G)
+        self.gate_up = ck.prepare_weight(gate_up, self.gate_up_scale, ck.CK_WLAYOUT_GEMM_F16)
+        self.down = ck.prepare_weight(down, self.down_scale, ck.CK_WLAYOUT_GEMM_F16)
+
+    def _project(self, x):
+        """The packed projection of tokens x to queries, keys and values."""
+        return self.qkv(x)
+
+    def _mlp(self, x, branch, projection):
+        """projection(branch) added to x, and the MLP behind it."""
+        x = projection(branch, residual=x)
+        return ck.swiglu_mlp(x, self.gate_up, self.gate_up_scale, self.down, self.down_scale, G,
+                             wlayout=ck.CK_WLAYOUT_GEMM_F16, residual=x)
+
     def _heads(self, x):
         """Queries, keys and values as views of the packed projection of tokens x."""
         T, Hq, H, D = x.shape[0], self.Hq, self.Hkv, self.D
-        p = self.qkv(x)
+        p = self._project(x)
         return (p[:, :Hq * D].view(T, Hq, D), p[:, Hq * D:(Hq + H) * D].view(T, H, D),
                 p[:, (Hq + H) * D:].view(T, H, D))
 
@@ -83,18 +117,45 @@ class DecoderLayer:
         q, _ = ck.qk_norm_rope(q, None, self.cos_sin, positions, wq=self.q_norm)
         a = ck.prefix_attention(q[:, None], self.k_cache, self.v_cache, prefix_pages, prefix_len, block_table,
                                 seq_lens, max_seq_len)
+        if states is None:
+            return self._mlp(x, a.view(B, -1), self.out)
         x = self.out(a.view(B, -1), residual=x)
-        if states is not None:
-            sk, sv = states
-            cq = self.cross_q(x).view(B, 1, self.Hq, self.D)
-            x = self.cross_out(ck.cross_attention(cq, sk, sv, kv_lens=state_lens).view(B, -1), residual=x)
-        return ck.swiglu_mlp(x, self.gate_up, self.gate_up_scale, self.down, self.down_scale, G,
-                             wlayout=ck.CK_WLAYOUT_GEMM_F16, residual=x)
+        sk, sv = states
+        cq = self.cross_q(x).view(B, 1, self.Hq, self.D)
+        c = ck.cross_attention(cq, sk, sv, kv_lens=state_lens)
+        return self._mlp(x, c.view(B, -1), self.cross_out)
 
 
-def run(B=4, prompt=150, steps=5, with_states=True, device="cuda"):
-    """A few steps of a batch behind a shared prompt -> (attention error of the last step, output)."""
-    layer = DecoderLayer(device=device)
+class Fp4DecoderLayer(DecoderLayer):
+    """The layer on 4-bit weights ("mx" or "nv"), with the norms in front of its projection and its MLP."""
+
+    def __init__(self, fmt, hidden=512, device="cuda", **sizes):
+        self.fmt = fmt
+        super().__init__(hidden=hidden, device=device, **sizes)
+        self.norm_in, self.norm_mlp = (torch.ones(hidden, dtype=torch.bfloat16, device=device) for _ in range(2))
+
+    def _linear(self, W):
+        return Fp4Linear(W, self.fmt)
+
+    def _init_mlp(self, gate_up, down):
+        self.gate_up, self.down = self._linear(gate_up), self._linear(down)
+
+    def _project(self, x):
+        w = self.qkv
+        _, codes, scales = ck.block_norm_fp4(x, fmt=self.fmt, n_scale=w.x_scale, weight=self.norm_in)
+        return ck.fp4_gemm(codes, scales, w.W, w.scales, self.fmt, alpha=w.x_scale * w.scale)
+
+    def _mlp(self, x, branch, projection):
+        gu, d = self.gate_up, self.down
+        h, n = ck.block_norm(x, projection(branch), weight=self.norm_mlp)
+        return ck.fp4_swiglu_mlp(n, gu.W, gu.scales, d.W, d.scales, self.fmt, x_scale=gu.x_scale,
+                                 gate_up_scale=gu.scale, act_scale=d.x_scale, down_scale=d.scale, residual=h)
+
+
+def run(B=4, prompt=150, steps=5, with_states=True, device="cuda", fmt=None):
+    """A few steps of a batch behind a shared prompt, on INT8 weights or 4-bit ones (fmt "mx", "nv") -> (attention
+    error of the last step, output)."""
+    layer = DecoderLayer(device=device) if fmt is None else Fp4DecoderLayer(fmt, device=device)
     gen = torch.Generator(device="cpu").manual_seed(1)
     hidden = layer.out.N
 
@@ -140,6 +201,7 @@ def run(B=4, prompt=150, steps=5, with_states=True, device="cuda"):
 
 if __name__ == "__main__":
     ck.build()
-    error, y = run()
-    print(f"attention of the last step: relative error {error:.2e} against float64; layer output {tuple(y.shape)}, "
-          f"finite: {bool(torch.isfinite(y.float()).all())}")
+    for fmt in (None, "mx", "nv"):
+        error, y = run(fmt=fmt)
+        print(f"{fmt or 'int8'} weights: attention of the last step: relative error {error:.2e} against float64; "
+              f"layer output {tuple(y.shape)}, finite: {bool(torch.isfinite(y.float()).all())}")

@@ -1,5 +1,6 @@
 /*
- * ck.h -- C ABI of the GB300 (sm_103a) ConvRot INT8 W8A8 linear library.
+ * ck.h -- C ABI of the GB300 (sm_103a) ConvRot INT8 W8A8 linear library, and of
+ * what stands around its linears: attention, linears on 4-bit floats, norms.
  *
  * The method (web pages, cited by title and section):
  *   [P1] sglang PR #44196, "comfy_kitchen SwiGLU MLP for Qwen-Image 2.1",
@@ -28,7 +29,7 @@
  * the residual fused into the dequant epilogue [P2: Commits, Description --
  * a residual fusion is named among the decode fusions, with no formula].
  * residual may be y itself (an in-place add): each element is read before it
- * is written, by the same thread.
+ * is written, by the same thread or warp.
  *
  * Names against the call list of the hot path: ck_convrot_quantize_weight
  * writes the row-major layout (the GEMV packing is ck_prepare_weight);
@@ -720,10 +721,11 @@ CK_API void ck_set_wait_timeout_ns(uint64_t ns);
  * for that kernel before touching memory, so an earlier kernel's tail hides
  * its launch.  With on != 0, additionally:
  *   - the GEMM / GEMV behind a quantizer may start before the quantizer's own
- *     wait, and ck_int8_gemm_dequant / ck_int8_gemv_dequant start before the
- *     work ahead of them has finished;
- *   - such a kernel reads its weight operands at once (the prepared weight,
- *     its scales, the bias), and everything else only after its wait.
+ *     wait, and ck_int8_gemm_dequant / ck_int8_gemv_dequant / ck_fp4_gemm start
+ *     before the work ahead of them has finished;
+ *   - such a kernel reads its weight operands at once (the prepared weight or
+ *     the codes, their scales, the bias), and everything else only after its
+ *     wait.
  * The caller guarantees that no work still in flight on the stream writes
  * those weight operands: prepare them, then synchronize, before their first
  * use in this mode.  Calls on CK_WLAYOUT_ROWMAJOR_I8 weights (widened into
