@@ -14,6 +14,9 @@
 // tile's first and last two k-blocks go to the first part together, then to the second,
 // so that the tensor cores have 768 clocks of work while an accumulator is read.
 //
+// SPLIT: few tiles and long K, so a tile has a cluster of up to four pairs, each with its
+// share of K; the pairs' sums meet through distributed shared memory.
+//
 // GLU: the parts are rows of gate and the rows of up that go with them, and the
 // epilogue makes silu(gate) * up of them and quantizes it: what the next linear of a
 // SwiGLU MLP reads, without gate and up ever leaving the chip.
@@ -42,7 +45,7 @@ constexpr int kRows = 128;     // tokens of an accumulator
 constexpr int kStageK = 256;   // 128 bytes of codes a row
 constexpr int kPN = 192;       // rows of W a part
 
-template <bool NV, int PARTS, bool GLU>
+template <bool NV, int PARTS, bool GLU, bool SPLIT = false>
 struct Cfg {
     static constexpr int kWords = kStageK / fp4_word(NV);  // scale words of a stage
     static constexpr int kSfaBytes = kWords * 512;
@@ -51,7 +54,9 @@ struct Cfg {
     static constexpr int kBBytes = kPN / 2 * kStageK / 2;
     static constexpr int kXBytes = kABytes + kSfaBytes, kWBytes = PARTS * (kBBytes + kBTiles * kSfaBytes);
     static constexpr int kStageBytes = kXBytes + kWBytes;
-    static constexpr int kOutBytes = GLU ? 0 : 8 * 2048;   // a 32 x 32 piece of y a warp of the epilogue
+    // a 32 x 32 piece of y a warp of the epilogue; SPLIT: the other pairs' sums, a CTA's rows
+    // of at most three quarters of the columns
+    static constexpr int kOutBytes = SPLIT ? kRows * kPN * 3 : (GLU ? 0 : 8 * 2048);
     static constexpr int kBarBytes = 256;
     static constexpr int kStages = (227 * 1024 - kBarBytes - kOutBytes - 1024) / kStageBytes;
     static constexpr int kTmemSf = 2 * kPN;                // the scales' first column
@@ -64,6 +69,8 @@ struct Cfg {
 
 struct Args {
     int M, N, K, m_tiles, n_tiles;  // N: rows of W (GLU: of gate, and of up)
+    int splits;                     // SPLIT: pairs of a tile
+    __nv_bfloat16 *y;               // SPLIT
     float alpha;
     const __nv_bfloat16 *bias, *residual;
     uint8_t *codes, *scales;  // GLU: out
@@ -99,6 +106,10 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t at) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
     return v;
+}
+
+__device__ __forceinline__ void st_cluster_v4(uint32_t at, const uint4 &v) {
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
 // silu(gate) * up of whole blocks of a row, quantized: codes from `code` on (a
@@ -164,13 +175,13 @@ __device__ __forceinline__ void quantize_glu(const uint4 (&gate)[COLS / 8], cons
 // (250), the next tile's first k-blocks prefetched to L2 (264 against 249); two parts, the
 // last round's tiles part by part where that is one round less (61 us against 59 of one
 // part for 4096 x 12288 -> 4096).
-template <bool NV, int PARTS, bool GLU>
+template <bool NV, int PARTS, bool GLU, bool SPLIT = false>
 __global__ void __launch_bounds__(kThreads, 1)
 fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                      const __grid_constant__ CUtensorMap tm_xs, const __grid_constant__ CUtensorMap tm_ws,
                      const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ Args a) {
-    static_assert(PARTS == 2 || !GLU, "gate and up");
-    using C = Cfg<NV, PARTS, GLU>;
+    static_assert(PARTS == 2 ? !SPLIT : !GLU, "gate and up in two parts, K split for one");
+    using C = Cfg<NV, PARTS, GLU, SPLIT>;
     constexpr int kStages = C::kStages;
     constexpr int kOffB = C::kABytes, kOffSfa = kOffB + PARTS * C::kBBytes, kOffSfb = kOffSfa + C::kSfaBytes;
     constexpr int kTileN = GLU ? kPN : PARTS * kPN;  // columns of y, or of the product, a tile
@@ -190,10 +201,15 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     auto stage = [&](int s) { return smem_s + s * C::kStageBytes; };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = static_cast<int>(cluster_ctarank());  // 0: leader (issues), 1: peer
-    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const int crank = static_cast<int>(cluster_ctarank()), rank = SPLIT ? crank & 1 : crank;  // 0: leader (issues), 1: peer
+    const int lead_rank = SPLIT ? crank & ~1 : 0;
+    const uint16_t both = static_cast<uint16_t>(0x3 << lead_rank);
+    // SPLIT: a cluster a tile, the pairs of which have a share of K each
+    const int share = crank >> 1;
+    const int pair = SPLIT ? blockIdx.x / (2 * a.splits) : blockIdx.x >> 1, npairs = SPLIT ? 1 << 30 : gridDim.x >> 1;
     const int total = a.m_tiles * a.n_tiles;
     const int num_kb = (a.K + kStageK - 1) / kStageK;
+    const int kb0 = SPLIT ? num_kb * share / a.splits : 0, kb1 = SPLIT ? num_kb * (share + 1) / a.splits : num_kb;
     const WaitCtl ctl{abort_flag, a.status, a.timeout_ns};
     // first row of W of a tile's part (GLU: up's rows follow gate's N)
     auto part_row = [&](int tile, int p) { return tile / a.m_tiles * kTileN + p * (GLU ? a.N : kPN); };
@@ -237,7 +253,7 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
                 if (!weight || !a.weights_settled) pdl_wait();
                 const uint32_t to_codes = stage(0) + (weight ? kOffB : 0), to_scales = stage(0) + (weight ? kOffSfb : kOffSfa);
                 const uint32_t bytes = 2 * (weight ? C::kWBytes : C::kXBytes);
-                const uint32_t lead = mapa_shared(full(0), 0);
+                const uint32_t lead = mapa_shared(full(0), lead_rank);
                 int s = 0;
                 uint32_t ph = 1;
                 for (int tile = pair; tile < total; tile += npairs) {
@@ -245,7 +261,7 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
                     const int w0 = part_row(tile, 0), w1 = part_row(tile, PARTS - 1);
                     const int row = weight ? w0 + rank * (kPN / 2) : m0, sf_tile = (weight ? w0 : m0) >> 7;
                     bool ok = true;
-                    for (int kb = 0; kb < num_kb; ++kb) {
+                    for (int kb = kb0; kb < kb1; ++kb) {
                         ok = mbar_wait_spin(empty(s), ph, ctl);  // (the first round's wait is over at once)
                         if (!ok) break;
                         if (rank == 0) mbar_arrive_expect_tx(full(s), bytes);
@@ -313,7 +329,7 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
                         // where a part's rows begin in their scales' 128-row tile
                         const uint32_t sfb_off[2] = {static_cast<uint32_t>(part_row(tile, 0) & 127) >> 5,
                                                      static_cast<uint32_t>(part_row(tile, 1) & 127) >> 5};
-                        for (int kb = 0; kb < num_kb;) {
+                        for (int kb = kb0; kb < kb1;) {
                             const int group = PARTS == 2 && (kb == 0 || kb + 2 == num_kb) && kb + 1 < num_kb ? 2 : 1;
                             int st = s;
                             uint32_t sph = ph;
@@ -328,15 +344,15 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
                                         if (!ok) break;
                                     }
                                     // the epilogue has read what this accumulator held before
-                                    if (kb + j == 0 && use > 0) {
+                                    if (kb + j == kb0 && use > 0) {
                                         ok = mbar_wait_spin(acce(acc), (use - 1) & 1, ctl);
                                         if (!ok) break;
                                     }
                                     tc_fence_after_sync();
-                                    const bool last = kb + j + 1 == num_kb;
-                                    unit(st, PARTS == 2 ? j : st & 1, acc, p, sfb_off[p], last ? tail : 4, kb + j == 0);
-                                    if (p == PARTS - 1) mma_commit_pair(empty(st), 0x3);
-                                    if (last) mma_commit_pair(accf(acc), 0x3);
+                                    const bool last = kb + j + 1 == kb1;
+                                    unit(st, PARTS == 2 ? j : st & 1, acc, p, sfb_off[p], kb + j + 1 == num_kb ? tail : 4, kb + j == kb0);
+                                    if (p == PARTS - 1) mma_commit_pair(empty(st), both);
+                                    if (last) mma_commit_pair(accf(acc), both);
                                     if (++st == kStages) st = 0, sph ^= 1;
                                 }
                                 if (!ok) break;
@@ -345,7 +361,7 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
                             kb += group, s = st, ph = sph;
                         }
                     }
-                    mma_commit_pair(done, 0x1);
+                    mma_commit_pair(done, static_cast<uint16_t>(0x1 << lead_rank));
                     mbar_wait_drain(done, 0, a.timeout_ns, a.status);
                 }
             }
@@ -474,7 +490,11 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
         };
         using std::false_type;
         using std::true_type;
-        if constexpr (GLU) {
+        if constexpr (SPLIT) {
+            if (lane == 0) mbar_wait(accf(0), 0, ctl);  // (a wait that gives up leaves the abort flag)
+            __syncwarp();
+            tc_fence_after_sync();
+        } else if constexpr (GLU) {
             if (a.bias != nullptr) run(true_type(), false_type());
             else run(false_type(), false_type());
         } else {
@@ -483,6 +503,67 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
             else if (a.residual != nullptr) run(false_type(), true_type());
             else run(false_type(), false_type());
             if (lane == 0) bulk_wait();
+        }
+    }
+    if constexpr (SPLIT) {
+        // Each pair finishes its share of the columns: the other pairs send it their sums of
+        // them, which it adds in the order of K.
+        const int q = warp & 3, half = (warp - 4) / 4, row = q * 32 + lane, own = kPN / a.splits;
+        const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        // where four columns of this thread's row lie, of those that the from-th other pair sent
+        auto at = [&](int from, int c) { return static_cast<uint32_t>(((from * own + c) / 4 * kRows + row) * 16); };
+        if (warp >= 4) {
+            uint32_t v[3][32];
+#pragma unroll
+            for (int g = 0; g < 3; ++g) tmem_ld_32x32b_x32(acc + half * 96 + 32 * g, v[g]);
+#pragma unroll
+            for (int g = 0; g < 3; ++g) tmem_wait_ld(v[g]);
+#pragma unroll
+            for (int g = 0; g < 6; ++g) {
+                const int c = half * 96 + 16 * g, owner = (c >= own) + (c >= 2 * own) + (c >= 3 * own);
+                if (owner != share) {
+                    const uint32_t to = mapa_shared(out_s, 2 * owner + rank) + at(share < owner ? share : share - 1, c - owner * own);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        st_cluster_v4(to + i * kRows * 16, make_uint4(v[g / 2][g % 2 * 16 + 4 * i], v[g / 2][g % 2 * 16 + 4 * i + 1],
+                                                                     v[g / 2][g % 2 * 16 + 4 * i + 2], v[g / 2][g % 2 * 16 + 4 * i + 3]));
+                }
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // the sums are there
+        const int m = pair % a.m_tiles * (2 * kRows) + rank * kRows + row;
+        if (warp >= 4 && !*abort_flag) {
+#pragma unroll 1
+            for (int g = half; g < own / 16; g += 2) {
+                uint32_t mine[16];
+                tmem_ld_32x32b_x16(acc + share * own + 16 * g, mine);
+                tmem_wait_ld16(mine);
+                float sum[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sum[i] = 0.f;
+                for (int src = 0; src < a.splits; ++src)
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const uint4 v = src == share ? make_uint4(mine[i], mine[i + 1], mine[i + 2], mine[i + 3])
+                                                     : ld_shared_v4(out_s + at(src < share ? src : src - 1, 16 * g + i));
+                        sum[i] += __uint_as_float(v.x), sum[i + 1] += __uint_as_float(v.y);
+                        sum[i + 2] += __uint_as_float(v.z), sum[i + 3] += __uint_as_float(v.w);
+                    }
+#pragma unroll
+                for (int i = 0; i < 16; i += 8) {
+                    const int n = pair / a.m_tiles * kPN + share * own + 16 * g + i;
+                    if (m >= a.M || n >= a.N) continue;
+                    const int64_t off = static_cast<int64_t>(m) * a.N + n;
+                    uint4 b = make_uint4(0, 0, 0, 0), r = b;
+                    if (a.bias != nullptr) b = __ldg(reinterpret_cast<const uint4 *>(a.bias + n));
+                    if (a.residual != nullptr) r = *reinterpret_cast<const uint4 *>(a.residual + off);
+                    uint32_t bits[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) bits[e] = __float_as_uint(sum[i + e]);
+                    *reinterpret_cast<uint4 *>(a.y + off) = finish8<true, true>(bits, f32x2(a.alpha, a.alpha), b, r);
+                }
+            }
         }
     }
     tc_fence_before_sync();
@@ -494,9 +575,10 @@ fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_cons
     }
 }
 
-template <bool NV, int PARTS, bool GLU>
-cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx) {
-    using C = Cfg<NV, PARTS, GLU>;
+// splits: pairs that share a tile's K
+template <bool NV, int PARTS, bool GLU, bool SPLIT = false>
+cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx, int splits = 1) {
+    using C = Cfg<NV, PARTS, GLU, SPLIT>;
     CUtensorMap mx, mw, mxs, mws, my;
     const int row_bytes = static_cast<int>(g.K / 2);
     const int64_t words = fp4_words(g.K, NV), w_rows = GLU ? 2 * g.N : g.N;
@@ -511,7 +593,7 @@ cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx) {
         my = mx;  // not used
     else if (!tensor_map_2d(&my, g.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.M, g.N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
         return cudaErrorInvalidValue;
-    auto kern = fp4_gemm_pair_kernel<NV, PARTS, GLU>;
+    auto kern = fp4_gemm_pair_kernel<NV, PARTS, GLU, SPLIT>;
     if (cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), static_cast<int>(C::kSmemBytes));
         e != cudaSuccess)
         return e;
@@ -523,13 +605,13 @@ cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx) {
     if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
     const int pairs = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+    cfg.gridDim = dim3(static_cast<unsigned>(SPLIT ? 2 * splits * tiles : 2 * pairs));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::kSmemBytes;
     cfg.stream = ctx.stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(2 * splits);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -539,6 +621,7 @@ cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx) {
     Args a = {};
     a.M = static_cast<int>(g.M), a.N = static_cast<int>(g.N), a.K = static_cast<int>(g.K);
     a.m_tiles = static_cast<int>(m_tiles), a.n_tiles = static_cast<int>(n_tiles);
+    a.splits = splits, a.y = static_cast<__nv_bfloat16 *>(g.y);
     a.alpha = g.alpha;
     a.bias = static_cast<const __nv_bfloat16 *>(g.bias), a.residual = static_cast<const __nv_bfloat16 *>(g.residual);
     a.codes = g.a_codes, a.scales = g.a_scales, a.t = fp4::scale_of(g.a_scale);
@@ -549,6 +632,21 @@ cudaError_t launch_t(const Fp4Gemm &g, const LaunchCtx &ctx) {
 
 }  // namespace
 
+// How many pairs share a tile's K: as many as find room at once, with ten k-blocks each
+// at least, as the exchange takes some 2 us (linears of 64 tokens 16384 -> 2048 14.3 us
+// against 19.6, 12288 -> 4096 17.0 against 18.3, their product alone 11.3 against 13.8;
+// 4096 -> 4096, not split, 7.4 against 8.6 with three pairs).
+template <bool NV>
+int pairs_of_a_tile(const Fp4Gemm &g) {
+    using C = Cfg<NV, 1, false, true>;
+    const void *kern = reinterpret_cast<const void *>(fp4_gemm_pair_kernel<NV, 1, false, true>);
+    const int64_t tiles = (g.M + 2 * kRows - 1) / (2 * kRows) * ((g.N + kPN - 1) / kPN), kbs = (g.K + kStageK - 1) / kStageK;
+    if (kbs < 20 || ensure_dynamic_smem(kern, static_cast<int>(C::kSmemBytes)) != cudaSuccess) return 1;
+    for (int n = 4; n > 1; --n)
+        if (kbs >= 10 * n && tiles <= max_active_clusters(kern, kThreads, C::kSmemBytes, 2 * n)) return n;
+    return 1;
+}
+
 cudaError_t launch_fp4_gemm_pair(const Fp4Gemm &g, const LaunchCtx &ctx) {
     const int64_t pairs = sm_count() / 2;
     if (pairs < 1) return cudaErrorInvalidDevice;
@@ -558,6 +656,9 @@ cudaError_t launch_fp4_gemm_pair(const Fp4Gemm &g, const LaunchCtx &ctx) {
     // against 65 for 4096 x 4096 -> 12288 (7, 14), but 34.3 against 33.5 for 8192 x 1024
     // -> 8192 (10, 19), 67 against 60 for 4096 x 12288 -> 4096 (3, 5) and 19.5 against
     // 15.7 for 2048 x 4096 -> 4096 (2, 3).
+    const int share = g.nv ? pairs_of_a_tile<true>(g) : pairs_of_a_tile<false>(g);
+    if (share > 1)
+        return g.nv ? launch_t<true, 1, false, true>(g, ctx, share) : launch_t<false, 1, false, true>(g, ctx, share);
     auto rounds = [&](int n) { return ((g.M + 2 * kRows - 1) / (2 * kRows) * ((g.N + n - 1) / n) + pairs - 1) / pairs; };
     if (2 * rounds(2 * kPN) <= rounds(kPN))
         return g.nv ? launch_t<true, 2, false>(g, ctx) : launch_t<false, 2, false>(g, ctx);

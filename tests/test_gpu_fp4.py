@@ -204,6 +204,35 @@ def test_gemm_many_tiles(M, K, N, fmt, bias, residual):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,K,N,bias,residual", [(33, 5152, 200, True, True), (256, 7712, 1032, False, False), (300, 10272, 392, True, False),
+                                                 (129, 16384, 2048, False, True), (64, 12288, 4096, True, True), (700, 16416, 328, False, False),
+                                                 (513, 8192, 776, True, True)])
+def test_gemm_few_tiles_long_k(M, K, N, fmt, bias, residual):
+    """K divided between the pairs of a cluster, two, three and four of them."""
+    check_gemm(M, K, N, fmt, bias=bias, residual=residual)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_gemm_long_k_in_place_and_nan(fmt):
+    dev = device()
+    g = ref.gen(77)
+    M, K, N = 70, 10240, 264
+    x = ref.randn(g, M, K).to(dev)
+    x[40, 9000] = float("inf")  # of the last share of K
+    xq, xs = ck.fp4_quantize(x, fmt, scale=T[fmt])
+    wq, ws = ck.fp4_quantize(ref.randn(g, N, K, std=K ** -0.5).to(dev), fmt, scale=T[fmt])
+    r = ref.randn(g, M, N).to(dev)
+    want = ck.fp4_gemm(xq, xs, wq, ws, fmt, alpha=T[fmt] ** 2, residual=r)
+    for _ in range(20):  # the same bits every time
+        again = ck.fp4_gemm(xq, xs, wq, ws, fmt, alpha=T[fmt] ** 2, residual=r)
+        assert torch.equal(again.nan_to_num(), want.nan_to_num())
+    got = ck.fp4_gemm(xq, xs, wq, ws, fmt, alpha=T[fmt] ** 2, residual=r, out=r)
+    poll_ok()
+    assert got is r and torch.equal(got.isnan(), want.isnan()) and torch.equal(got.nan_to_num(), want.nan_to_num())
+    assert bool(want[40].isnan().all()) and not bool(want[:40].isnan().any()) and not bool(want[41:].isnan().any())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("M", [4, 40, 400])
 def test_gemm_nan_scales(M, fmt):
     """A block with a NaN scale makes its row of X, or its row of W, NaN, and nothing else."""
