@@ -32,16 +32,6 @@ __device__ __forceinline__ uint32_t pack2(uint64_t v) {
 __device__ __forceinline__ uint4 pack8(const uint64_t (&v)[4]) {
     return make_uint4(pack2(v[0]), pack2(v[1]), pack2(v[2]), pack2(v[3]));
 }
-// A stream's 16 bytes: read once, so they do not displace the weights in L1 (they may
-// be written later in the kernel, by the thread that reads them).
-__device__ __forceinline__ uint4 load_stream(const uint16_t *p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p)
-                 : "memory");
-    return v;
-}
 // The sum of v over a row's team of `tw` threads (8, 16 or whole warps); every thread of
 // the block takes part.  `red` has the team's slots, a multiple of four floats of which
 // those past its warps hold 0; the caller alternates between two sets of them.
@@ -104,12 +94,12 @@ block_norm_kernel(const __grid_constant__ BlockNorm a, int tw, int rows_per_bloc
     auto fetch = [&]() {
 #pragma unroll
         for (int j = 0; j < V; ++j)
-            if (in[j]) rx[j] = load_stream(px + j * 256);
+            if (in[j]) rx[j] = fp4::load_stream(px + j * 256);
         px += sx;
         if (a.branch) {
 #pragma unroll
             for (int j = 0; j < V; ++j)
-                if (in[j]) rb[j] = load_stream(pb + j * 256);
+                if (in[j]) rb[j] = fp4::load_stream(pb + j * 256);
             pb += sb;
         }
     };
@@ -135,6 +125,17 @@ block_norm_kernel(const __grid_constant__ BlockNorm a, int tw, int rows_per_bloc
                     f(j, w);
                 }
         }
+    };
+    // the same of gate, scale and shift: what a kernel ahead may still have been writing when
+    // this one was let in, so not by loads for data that nobody writes
+    auto each_mod = [&](const uint16_t *p, auto f) {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (in[j]) {
+                uint64_t w[4];
+                unpack8(*reinterpret_cast<const uint4 *>(p + col0 + j * 256), w);
+                f(j, w);
+            }
     };
     if (row < a.T) fetch();
     const uint64_t fx = f32x2(a.x_factor, a.x_factor), fb = f32x2(a.branch_factor, a.branch_factor);
@@ -179,7 +180,7 @@ block_norm_kernel(const __grid_constant__ BlockNorm a, int tw, int rows_per_bloc
             });
         }
         if (a.gate)
-            each(a.gate + mod, false, [&](int j, const uint64_t (&w)[4]) {
+            each_mod(a.gate + mod, [&](int j, const uint64_t (&w)[4]) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) h[j][e] = mul_f32x2(h[j][e], w[e]);
             });
@@ -247,12 +248,12 @@ block_norm_kernel(const __grid_constant__ BlockNorm a, int tw, int rows_per_bloc
                 for (int e = 0; e < 4; ++e) h[j][e] = add_f32x2(h[j][e], w[e]);
             });
         if (a.scale)
-            each(a.scale + mod, false, [&](int j, const uint64_t (&w)[4]) {
+            each_mod(a.scale + mod, [&](int j, const uint64_t (&w)[4]) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) h[j][e] = mul_f32x2(h[j][e], add_f32x2(w[e], one));
             });
         if (a.shift)
-            each(a.shift + mod, false, [&](int j, const uint64_t (&w)[4]) {
+            each_mod(a.shift + mod, [&](int j, const uint64_t (&w)[4]) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) h[j][e] = add_f32x2(h[j][e], w[e]);
             });

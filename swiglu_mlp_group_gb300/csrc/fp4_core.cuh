@@ -45,6 +45,18 @@ __device__ __forceinline__ int64_t scale_word_at(int64_t row, int word, int word
     return ((row >> 7) * words + word) * 512 + (r & 31) * 16 + (r >> 5) * 4;
 }
 
+// 16 bytes that are read once: they do not displace others in L1, and are not taken for
+// data that nobody writes (a kernel ahead may have been writing them when this one was
+// let in, and a norm may write them back in place).
+__device__ __forceinline__ uint4 load_stream(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
 // A pair of bf16 as f32, and as f32 with the signs turned (one operation each).
 __device__ __forceinline__ uint64_t unpack2(uint32_t w) {
     return f32x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));

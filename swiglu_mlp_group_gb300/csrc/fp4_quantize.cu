@@ -46,9 +46,9 @@ fp4_quantize_kernel(const void *__restrict__ x, int64_t M, int K, int64_t ldx, f
     for (int i = 0; i < kRowsPerWarp; ++i) {
         a[i] = b[i] = make_uint4(0, 0, 0, 0);
         if (in && i < rows) {
-            a[i] = __ldg(reinterpret_cast<const uint4 *>(src));
-            if constexpr (IN == In::kF32) b[i] = __ldg(reinterpret_cast<const uint4 *>(src) + 1);
-            if constexpr (IN == In::kSwiglu) b[i] = __ldg(reinterpret_cast<const uint4 *>(src + 2 * K));
+            a[i] = fp4::load_stream(src);
+            if constexpr (IN == In::kF32) b[i] = fp4::load_stream(src + 16);
+            if constexpr (IN == In::kSwiglu) b[i] = fp4::load_stream(src + 2 * K);
         }
         src += src_step;
     }
