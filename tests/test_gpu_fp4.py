@@ -204,6 +204,24 @@ def test_gemm_many_tiles(M, K, N, fmt, bias, residual):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,K,N", [(2041, 96, 3400), (1100, 64, 2056), (700, 5152, 392)])
+def test_gemm_tiles_in_place(M, K, N, fmt):
+    """residual is y, over many tiles of a pair, and where pairs share a tile: a chain of calls, each onto the last one's y."""
+    dev = device()
+    g = ref.gen(M + N)
+    xq, xs, _ = operand(g, M, K, fmt)
+    wq, ws, _ = operand(g, N, K, fmt, std=K ** -0.5)
+    y = ref.randn(g, M, N).to(dev)
+    want = y.clone()
+    for _ in range(4):
+        want = ck.fp4_gemm(xq, xs, wq, ws, fmt, alpha=T[fmt] ** 2, residual=want)
+    for _ in range(4):
+        assert ck.fp4_gemm(xq, xs, wq, ws, fmt, alpha=T[fmt] ** 2, residual=y, out=y) is y
+    poll_ok()
+    assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("M,K,N,bias,residual", [(33, 5152, 200, True, True), (256, 7712, 1032, False, False), (300, 10272, 392, True, False),
                                                  (129, 16384, 2048, False, True), (64, 12288, 4096, True, True), (700, 16416, 328, False, False),
                                                  (513, 8192, 776, True, True)])
