@@ -175,6 +175,29 @@ def lib():
         return _lib
 
 
+_quick_module = False  # not looked for yet
+
+
+def _quick():
+    """The compiled calls (csrc/torch_calls.cpp) of the 4-bit operators and the block norm, or None where they were
+    not built.  Such a call returns None where anything is not in order, and the Python one says what."""
+    global _quick_module
+    if _quick_module is False:
+        from importlib.machinery import ExtensionFileLoader
+        from importlib.util import module_from_spec, spec_from_file_location
+
+        from . import _build
+        _torch()
+        lib()
+        path, module = _build.calls_path(), None
+        if path is not None and os.path.exists(path):
+            spec = spec_from_file_location("ck_torch_calls", path, loader=ExtensionFileLoader("ck_torch_calls", path))
+            module = module_from_spec(spec)
+            spec.loader.exec_module(module)
+        _quick_module = module
+    return _quick_module
+
+
 def _make_entry(name):
     def entry(*args):
         return getattr(lib(), name)(*args)
@@ -800,6 +823,10 @@ def fp4_quantize(x, fmt: str, scale: float = 1.0, act: str = "none", codes=None,
     microscaled 4-bit floats -> (codes uint8 [M, K / 2], tiled scales uint8).
 
     fmt "mx": 32 codes share a power of two; "nv": 16 codes share an E4M3 number, the tensor `scale`."""
+    if stream is None and (quick := _quick_module or _quick()) is not None:
+        got = quick.fp4_quantize(x, fmt, scale, act, codes, scales)
+        if got is not None:
+            return got
     torch = _torch()
     f, a = _fp4_format(fmt), _act(act)
     dev = _call_device(x, "x")
@@ -845,6 +872,10 @@ def fp4_gemm(codes, scales, W, w_scales, fmt: str, alpha: float = 1.0, bias=None
              stream=None):
     """y = bf16(alpha X W^T + bias + residual) -> bf16 [M, N], X of codes [M, K / 2] and W of [N, K / 2] with
     tiled scales (fp4_quantize, block_norm_fp4, fp4_tile_scales).  residual may be out."""
+    if stream is None and (quick := _quick_module or _quick()) is not None:
+        got = quick.fp4_gemm(codes, scales, W, w_scales, fmt, alpha, bias, residual, out)
+        if got is not None:
+            return got
     f = _fp4_format(fmt)
     dev = _call_device(codes, "codes")
     M, K, px, pxs = _fp4_operand(codes, scales, f, "codes", dev)
@@ -871,6 +902,10 @@ def fp4_linear(x, W, w_scales, fmt: str, x_scale: float = 1.0, w_scale: float = 
     """Linear on 4-bit weights -> bf16 [M, N]: x [M, K] bf16 (act "swiglu": [gate | up]; rows may lie apart) is
     quantized on the way (tensor scale x_scale); W codes [N, K / 2] with tiled scales, tensor scale w_scale.
     residual [M, N] may be out."""
+    if stream is None and (quick := _quick_module or _quick()) is not None:
+        got = quick.fp4_linear(x, W, w_scales, fmt, x_scale, w_scale, bias, act, out, workspace, residual)
+        if got is not None:
+            return got
     bf16 = _torch().bfloat16
     f, a = _fp4_format(fmt), _act(act)
     dev = _call_device(x, "x")
@@ -904,6 +939,11 @@ def fp4_swiglu_mlp(x, Wgu, gu_scales, Wd, d_scales, fmt: str, x_scale: float = 1
     """SwiGLU MLP on 4-bit weights -> bf16 [M, H]: h = linear(x, Wgu [2I, H / 2]), y = linear(silu(gate) * up,
     Wd [H, I / 2]) + residual.  Tensor scales: x_scale of x, act_scale of silu(gate) * up, the others of the
     weights.  residual may be x or out."""
+    if stream is None and (quick := _quick_module or _quick()) is not None:
+        got = quick.fp4_swiglu_mlp(x, Wgu, gu_scales, Wd, d_scales, fmt, x_scale, gate_up_scale, act_scale, down_scale, bgu,
+                                   bd, residual, out, workspace)
+        if got is not None:
+            return got
     bf16 = _torch().bfloat16
     f = _fp4_format(fmt)
     dev = _call_device(x, "x")
@@ -985,6 +1025,11 @@ def block_norm(x, branch=None, post_weight=None, gate=None, x_factor: float = 1.
     n = norm(h) weight + bias, then n (1 + scale) + shift.  x, branch [T, H] bf16, rows may lie apart; weights
     [H], f32 or bf16 alike; gate, scale, shift bf16 [groups, H], a row for every tokens_per_group tokens (0: one
     row for all).  h_out=x and n_out=branch work in place.  Without a branch and a factor h is x."""
+    if stream is None and (quick := _quick_module or _quick()) is not None:
+        got = quick.block_norm(x, branch, post_weight, gate, x_factor, branch_factor, norm, weight, bias, scale, shift,
+                               tokens_per_group, eps, h_out, n_out)
+        if got is not None:
+            return got
     args, h, dev = _norm_call(x, branch, post_weight, gate, scale, shift, tokens_per_group, x_factor, branch_factor,
                               norm, weight, bias, eps, h_out, stream)
     if n_out is None:
@@ -1002,6 +1047,11 @@ def block_norm_fp4(x, branch=None, fmt: str = "nv", n_scale: float = 1.0, post_w
                    scale=None, shift=None, tokens_per_group: int = 0, eps: float = 1e-6, h_out=None, codes=None,
                    scales=None, stream=None):
     """block_norm whose n is quantized as by fp4_quantize (tensor scale n_scale) -> (h, codes, tiled scales)."""
+    if stream is None and (quick := _quick_module or _quick()) is not None:
+        got = quick.block_norm_fp4(x, branch, fmt, n_scale, post_weight, gate, x_factor, branch_factor, norm, weight, bias,
+                                   scale, shift, tokens_per_group, eps, h_out, codes, scales)
+        if got is not None:
+            return got
     u8 = _torch().uint8
     f = _fp4_format(fmt)
     args, h, dev = _norm_call(x, branch, post_weight, gate, scale, shift, tokens_per_group, x_factor, branch_factor,
