@@ -49,8 +49,11 @@ def _calls_dirs() -> tuple[str, str, str] | None:
     spec = importlib.util.find_spec("torch")
     if spec is None or spec.origin is None or calls_path() is None or shutil.which("g++") is None:
         return None
-    dirs = (os.path.dirname(spec.origin), sysconfig.get_paths()["include"],
-            os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include"))
+    try:
+        cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    except RuntimeError:
+        return None
+    dirs = (os.path.dirname(spec.origin), sysconfig.get_paths()["include"], os.path.join(cuda, "include"))
     heads = (os.path.join(dirs[0], "include", "torch", "csrc", "autograd", "python_variable.h"),
              os.path.join(dirs[1], "Python.h"), os.path.join(dirs[2], "cuda_runtime_api.h"))
     return dirs if all(os.path.exists(h) for h in heads) else None

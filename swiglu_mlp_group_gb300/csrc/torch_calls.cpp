@@ -233,7 +233,7 @@ struct NormArgs {
         norm = r.choice(norm_i, "rms", "layer") ? CK_NORM_LAYER : CK_NORM_RMS;
         per_group = r.integer(group);
         if (!r.ok) return;
-        const int64_t groups = per_group > 0 ? (T + per_group - 1) / per_group : 1;
+        const int64_t groups = per_group > 0 && per_group < T ? (T + per_group - 1) / per_group : 1;
         ldm = groups > 1 ? 0 : H;
         const int mods[3] = {gate, scale, shift};
         for (int i = 0; i < 3; ++i)

@@ -103,3 +103,15 @@ def test_a_shape_that_does_not_fit(call, name, shape, calls):
     with pytest.raises(ValueError):
         getattr(ck, call)(**a)
     assert not calls
+
+
+def test_compiled_calls_take_no_host_tensors():
+    """They hand tensors of the host, stand-ins and wrong counts back to Python."""
+    quick = ck._quick()
+    if quick is None:
+        pytest.skip("torch's headers are not there")
+    x = torch.zeros(M, K, dtype=torch.bfloat16)
+    for name, n in (("fp4_quantize", 6), ("fp4_gemm", 9), ("fp4_linear", 11), ("fp4_swiglu_mlp", 15), ("block_norm", 15),
+                    ("block_norm_fp4", 18)):
+        call = getattr(quick, name)
+        assert call() is None and call(*[None] * n) is None and call(*[x] * n) is None and call(*[vec(M, K)] * n) is None

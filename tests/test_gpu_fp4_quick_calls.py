@@ -121,6 +121,13 @@ def test_what_is_not_in_order_goes_to_python(fmt):
     b = c.branch
     ok = [x, b, None, None, 1.0, 1.0, "rms", c.w16, None, None, None, 0, 1e-6, None, None]
     assert q.block_norm(*ok) is not None
+    assert q.block_norm(*ok[:11], -1, *ok[12:]) is None
+    # groups of more tokens than there are: one, which a row of gate is enough for
+    one = list(ok)
+    one[3], one[11] = b[:1], 1 << 62
+    wide = q.block_norm(*one)
+    one[11] = 0
+    assert all(torch.equal(u, v) for u, v in zip(wide, q.block_norm(*one)))
     for at, bad in [(0, x[:, :100]), (1, b[:3]), (2, c.w32), (3, b[:0]), (3, b[:1, :8]), (4, float("inf")), (6, "batch"), (7, c.w16[:3]),
                     (8, c.w32), (9, x.float()), (11, 2.0), (11, 1 << 70), (12, -1.0), (13, x.float()), (14, x[:3])]:
         args = list(ok)
