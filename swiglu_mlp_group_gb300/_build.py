@@ -128,7 +128,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     if dirs:
         tmp = calls_path() + f".tmp{os.getpid()}"
         cmd = ["g++", "-shared", "-o", tmp, calls_obj, "-L", BUILD_DIR, f"-l:{LIB_NAME}", "-L", os.path.join(dirs[0], "lib"),
-               "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+               "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda", "-ltorch_cuda", "-Wl,-rpath,$ORIGIN"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")

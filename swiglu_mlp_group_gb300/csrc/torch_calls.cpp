@@ -8,7 +8,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -116,8 +116,9 @@ struct Reader {
 
 ck_stream_t stream_of(int dev) { return reinterpret_cast<ck_stream_t>(c10::cuda::getCurrentCUDAStream(dev).stream()); }
 
+// A new tensor, from the allocator without the dispatcher (0.3 us of 1.2).
 Tensor fresh(const Tensor &like, at::ScalarType type, at::IntArrayRef shape) {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
+    return Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
 
 int64_t tiled_bytes(int format, int64_t rows, int64_t K) {
