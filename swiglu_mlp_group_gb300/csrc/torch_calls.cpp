@@ -235,16 +235,21 @@ struct NormArgs {
         per_group = r.integer(group);
         if (!r.ok) return;
         const int64_t groups = per_group > 0 && per_group < T ? (T + per_group - 1) / per_group : 1;
-        ldm = groups > 1 ? 0 : H;
+        // several groups: rows of gate, scale and shift at one stride, each row's own memory (an
+        // expanded one's stride is 0); else only the first row is read
+        ldm = H;
+        bool first_mod = true;
         const int mods[3] = {gate, scale, shift};
         for (int i = 0; i < 3; ++i)
             if (const Tensor *t = r.tensor(mods[i])) {
                 const int64_t ld = r.rows(*t, kBf16);
-                r.want(r.ok && t->size(0) >= groups && t->size(1) == H && (groups <= 1 || ldm == 0 || ldm == ld));
-                if (groups > 1) ldm = ld;
+                r.want(r.ok && t->size(0) >= groups && t->size(1) == H);
+                if (groups > 1) {
+                    r.want(ld >= H && (first_mod || ld == ldm));
+                    ldm = ld, first_mod = false;
+                }
                 mod[i] = t->const_data_ptr();
             }
-        if (ldm == 0) ldm = H;
         const int ws[3] = {weight, bias, post};
         at::ScalarType type = kBf16;
         bool seen = false;
