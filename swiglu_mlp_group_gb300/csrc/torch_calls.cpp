@@ -83,11 +83,19 @@ struct Reader {
     }
     void want(bool c) { ok = ok && c; }
 
-    // Data of contiguous tensors of a type and shape (n < 0: any), or null.
+    // Data of contiguous tensors of a type and shape, or null.
     const void *flat(const Tensor *t, at::ScalarType type) {
         if (!t) return nullptr;
         want(t->scalar_type() == type && t->is_contiguous());
         return t->const_data_ptr();
+    }
+    // The same of a tensor that is written: memory that it still shares with the tensor it
+    // was lazily cloned from becomes its own.  (What may be the same tensor, x or a
+    // residual, is asked for its address after it.)
+    void *written(const Tensor *t, at::ScalarType type) {
+        if (!t) return nullptr;
+        want(t->scalar_type() == type && t->is_contiguous());
+        return ok ? t->mutable_data_ptr() : nullptr;
     }
     const void *vector(int i, at::ScalarType type, int64_t n) {
         const Tensor *t = tensor(i);
@@ -136,7 +144,9 @@ Out out_matrix(Reader &r, int i, const Tensor &like, at::ScalarType type, int64_
     Out o;
     if (r.object(i) != Py_None) {
         o.given = r.object(i);
-        o.data = const_cast<void *>(r.matrix(i, type, rows, cols));
+        const Tensor *t = r.tensor(i);
+        if (t) r.want(t->dim() == 2 && t->size(0) == rows && t->size(1) == cols);
+        o.data = r.written(t, type);
     } else if (r.ok) {
         o.keep = fresh(like, type, {rows, cols});
         o.data = o.keep.mutable_data_ptr();
@@ -148,8 +158,8 @@ Out out_scales(Reader &r, int i, const Tensor &like, int64_t bytes) {
     if (r.object(i) != Py_None) {
         o.given = r.object(i);
         const Tensor *t = r.tensor(i);
-        o.data = const_cast<void *>(r.flat(t, kU8));
         if (t) r.want(t->numel() >= bytes);
+        o.data = r.written(t, kU8);
     } else if (r.ok) {
         o.keep = fresh(like, kU8, {bytes});
         o.data = o.keep.mutable_data_ptr();
@@ -164,7 +174,7 @@ Out out_rows(Reader &r, int i, const Tensor &like, int64_t rows, int64_t cols, i
         const Tensor *t = r.tensor(i);
         if (t) {
             ld = r.rows(*t, kBf16, rows, cols);
-            o.data = t->data_ptr();
+            if (r.ok) o.data = t->mutable_data_ptr();
         }
     } else if (r.ok) {
         ld = cols;
@@ -203,11 +213,12 @@ Workspace workspace(Reader &r, int i, const Tensor &like, size_t need) {
     if (!r.ok) return w;
     if (t) {
         r.want(t->is_contiguous());
+        if (!r.ok) return w;
     } else {
         w.keep = fresh(like, kU8, {static_cast<int64_t>(need > 16 ? need : 16)});
         t = &w.keep;
     }
-    w.data = t->data_ptr(), w.bytes = t->nbytes();
+    w.data = t->mutable_data_ptr(), w.bytes = t->nbytes();
     return w;
 }
 
@@ -332,8 +343,9 @@ PyObject *fp4_gemm(PyObject *, PyObject *const *args, Py_ssize_t n) {
         const Operand a = operand(r, 0, 1, f), w = operand(r, 2, 3, f);
         const double alpha = r.number(5);
         if (!r.ok || a.K != w.K) Py_RETURN_NONE;
-        const void *bias = r.vector(6, kBf16, w.rows), *residual = r.matrix(7, kBf16, a.rows, w.rows);
+        const void *bias = r.vector(6, kBf16, w.rows);
         Out y = out_matrix(r, 8, *x, kBf16, a.rows, w.rows);
+        const void *residual = r.matrix(7, kBf16, a.rows, w.rows);
         if (!r.ok) Py_RETURN_NONE;
         const ck_stream_t s = stream_of(r.dev);
         CK_CALL(ck_fp4_gemm(a.codes, a.scales, a.rows, a.K, static_cast<ck_fp4_format>(f), w.codes, w.scales, w.rows,
@@ -356,8 +368,9 @@ PyObject *fp4_linear(PyObject *, PyObject *const *args, Py_ssize_t n) {
         if (!r.ok) Py_RETURN_NONE;
         const int64_t M = x->size(0), K = act == CK_ACT_SWIGLU ? x->size(1) / 2 : x->size(1);
         r.want(K == w.K);
-        const void *bias = r.vector(6, kBf16, w.rows), *residual = r.matrix(10, kBf16, M, w.rows);
+        const void *bias = r.vector(6, kBf16, w.rows);
         Out y = out_matrix(r, 8, *x, kBf16, M, w.rows);
+        const void *residual = r.matrix(10, kBf16, M, w.rows);
         const Workspace ws = workspace(r, 9, *x, ck_fp4_linear_workspace_bytes(M, K, static_cast<ck_fp4_format>(f)));
         if (!r.ok) Py_RETURN_NONE;
         const ck_stream_t s = stream_of(r.dev);
@@ -378,12 +391,12 @@ PyObject *fp4_swiglu_mlp(PyObject *, PyObject *const *args, Py_ssize_t n) {
         double t[4];
         for (int i = 0; i < 4; ++i) t[i] = r.number(6 + i);
         const Operand gu = operand(r, 1, 2, f), d = operand(r, 3, 4, f);
-        const void *px = r.flat(x, kBf16);
         if (!r.ok || x->dim() != 2) Py_RETURN_NONE;
         const int64_t M = x->size(0), H = x->size(1), I = d.K;
         r.want(gu.K == H && d.rows == H && gu.rows == 2 * I);
-        const void *bgu = r.vector(10, kBf16, 2 * I), *bd = r.vector(11, kBf16, H), *residual = r.matrix(12, kBf16, M, H);
+        const void *bgu = r.vector(10, kBf16, 2 * I), *bd = r.vector(11, kBf16, H);
         Out y = out_matrix(r, 13, *x, kBf16, M, H);
+        const void *px = r.flat(x, kBf16), *residual = r.matrix(12, kBf16, M, H);
         const Workspace ws = workspace(r, 14, *x, ck_fp4_swiglu_mlp_workspace_bytes(M, H, I, static_cast<ck_fp4_format>(f)));
         if (!r.ok) Py_RETURN_NONE;
         const ck_stream_t s = stream_of(r.dev);

@@ -38,3 +38,44 @@ def test_expanded_modulation_is_refused():
     args[3], args[9] = own, one
     assert q.block_norm(*args) is None
     poll_ok()
+
+
+@pytest.mark.parametrize("M", [3, 70])
+def test_outputs_that_share_their_memory(M):
+    """Outputs that are lazy clones: the tensors behind them keep their values, the results are those of a call with
+    outputs of its own."""
+    dev = device()
+    g = ref.gen(M)
+    H, I, fmt, t = 256, 192, "nv", 0.004
+    x, b = ref.randn(g, M, H).to(dev), ref.randn(g, M, H).to(dev)
+    w = ck.fp4_quantize(ref.randn(g, H, H, std=H ** -0.5).to(dev), fmt, scale=t)
+    gu = ck.fp4_quantize(ref.randn(g, 2 * I, H, std=H ** -0.5).to(dev), fmt, scale=t)
+    d = ck.fp4_quantize(ref.randn(g, H, I, std=I ** -0.5).to(dev), fmt, scale=t)
+    codes, scales = ck.fp4_quantize(x, fmt, scale=t)
+    four = dict(x_scale=t, gate_up_scale=t, act_scale=t, down_scale=t)
+    c0, s0 = torch.full_like(codes, 0xa5), torch.full_like(scales, 0xa5)
+
+    def row_scales(s):  # those of rows that are there
+        return torch.from_numpy(ref.untile(s.cpu().numpy(), M, H, fmt))
+    for given, call in [
+        ((b,), lambda out=None: ck.fp4_gemm(codes, scales, *w, fmt, alpha=t * t, residual=b if out is None else out, out=out)),
+        ((b,), lambda out=None: ck.fp4_linear(x, *w, fmt, x_scale=t, w_scale=t, out=out)),
+        ((x,), lambda out=None: ck.fp4_linear(x if out is None else out, *w, fmt, x_scale=t, w_scale=t,
+                                              residual=x if out is None else out, out=out)),
+        ((x,), lambda out=None: ck.fp4_swiglu_mlp(x if out is None else out, *gu, *d, fmt, residual=x, out=out, **four)),
+        ((c0, s0), lambda c=None, s=None: ck.fp4_quantize(x, fmt, scale=t, codes=c, scales=s)),
+        ((x, b), lambda h=None, n=None: ck.block_norm(x, b, h_out=h, n_out=n)),
+        ((x, b), lambda h=None, n=None: ck.block_norm(x if h is None else h, b if n is None else n, h_out=h, n_out=n)),
+        ((x, c0, s0), lambda h=None, c=None, s=None: ck.block_norm_fp4(x, b, fmt, t, h_out=h, codes=c, scales=s)),
+    ]:
+        want = call()
+        kept = [k.clone() for k in given]
+        got = call(*[torch._lazy_clone(k) for k in given])
+        for k, k0 in zip(given, kept):
+            assert torch.equal(k, k0)
+        want, got = (v if isinstance(v, tuple) else (v,) for v in (want, got))
+        for a, e in zip(got, want):
+            if a.dtype is torch.uint8 and a.dim() == 1:
+                a, e = row_scales(a), row_scales(e)
+            assert torch.equal(a, e)
+    poll_ok()

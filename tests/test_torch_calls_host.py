@@ -82,3 +82,40 @@ def test_modulation_rows(check, fp4):
     for per in (0, T, 100):
         assert check.taken(*norm_args(x, b, one, scale, short, per, fp4)) and check.so.check_ldm() == H
     assert check.taken(*norm_args(rows(4, H), rows(4, H), one, one, one, 4, fp4))
+
+
+MARK = 0x5a
+U8 = torch.uint8
+
+
+def bytes_of(t):
+    return t.contiguous().view(U8)
+
+
+def test_outputs_that_share_their_memory(check):
+    """An output that still shares its memory with the tensor it was lazily cloned from gets its own before it is
+    written: the other tensor keeps its values, and the call's are in the output."""
+    N = 32
+    x, b = rows(T, H), rows(T, H)
+    w, ws = rows(N, H // 2, dtype=U8), rows(512, dtype=U8)
+    codes, scales = rows(T, H // 2, dtype=U8), rows(512, dtype=U8)
+    gu, gus = rows(4 * H, H // 2, dtype=U8), rows(2 * 512, dtype=U8)
+    d, ds = rows(H, H, dtype=U8), rows(2 * 512, dtype=U8)
+    y, h, n, c, s = rows(T, N), rows(T, H), rows(T, H), codes.clone(), scales.clone()
+    for given, call in [
+        ((y,), lambda y: ("fp4_gemm", codes, scales, w, ws, "nv", 1.0, None, None, y)),
+        ((y,), lambda y: ("fp4_gemm", codes, scales, w, ws, "nv", 1.0, None, y, y)),
+        ((y,), lambda y: ("fp4_linear", x, w, ws, "nv", 1.0, 1.0, None, "none", y, None, None)),
+        ((h,), lambda h: ("fp4_swiglu_mlp", h, gu, gus, d, ds, "nv", 1.0, 1.0, 1.0, 1.0, None, None, h, h, None)),
+        ((c, s), lambda c, s: ("fp4_quantize", x, "nv", 1.0, "none", c, s)),
+        ((h, n), lambda h, n: norm_args(x, b, h_out=h, n_out=n)),
+        ((h, n), lambda h, n: norm_args(h, n, h_out=h, n_out=n)),
+        ((h, c, s), lambda h, c, s: norm_args(x, b, fp4=True, h_out=h, codes=c, scales=s)),
+    ]:
+        kept = [t.clone() for t in given]
+        clones = [torch._lazy_clone(t) for t in given]
+        args = call(*clones)
+        assert check.taken(*args), args[0]
+        for t, k, o in zip(given, kept, clones):
+            assert torch.equal(t, k), f"{args[0]}: the tensor behind an output was written"
+            assert (bytes_of(o) == MARK).all(), f"{args[0]}: the output was not written"
