@@ -613,7 +613,8 @@ CK_API ck_status ck_fp4_tile_scales(const void *scales, int64_t rows, int64_t K,
  * tensors' scales (finite).
  *   codes, scales : of X [M, K], tiled;  W, w_scales : of W [N, K], tiled.
  *   bias : bf16 [N] or NULL;  residual : bf16 [M, N] or NULL, may be y;
- *   y    : out, bf16 [M, N];  N a multiple of 8.
+ *   y    : out, bf16 [M, N];  N a multiple of 8, for more than 32 tokens at most
+ *          2^31 - 384.
  * A NaN scale makes its row of X, or its row of W, NaN in y.  Errors: CK_ERR_NULL,
  * CK_ERR_INVALID, CK_ERR_SHAPE, CK_ERR_ALIGN, CK_ERR_UNSUPPORTED_DEVICE, CK_ERR_CUDA.
  */

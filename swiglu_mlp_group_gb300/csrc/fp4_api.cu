@@ -24,6 +24,11 @@ bool known(ck_fp4_format f) { return f == CK_FP4_MX || f == CK_FP4_NV; }
 // and codes are normal f32 numbers.
 bool scale_ok(ck_fp4_format f, float s) { return f == CK_FP4_MX ? s == 1.f : s >= 0x1p-60f && s <= 0x1p60f; }
 bool codes_shape(int64_t rows, int64_t K) { return rows >= 1 && rows <= kMaxRows && K >= 32 && K <= kMaxK && K % 32 == 0; }
+// Columns of y.  Tiles of many tokens have up to 384 of them, and count those past N in
+// 32 bits, too.
+bool columns_ok(int64_t M, int64_t N) {
+    return N >= 1 && N % 8 == 0 && N <= (M > ck::kFp4Few ? kMaxRows - 383 : kMaxRows);
+}
 
 ck::LaunchCtx context(ck_stream_t stream, unsigned int *status) {
     ck::LaunchCtx c;
@@ -197,7 +202,7 @@ CK_API ck_status ck_fp4_gemm(const void *codes, const void *scales, int64_t M, i
     CK_TRACE("ck_fp4_gemm");
     if (!codes || !scales || !W || !w_scales || !y) return CK_ERR_NULL;
     if (!known(format) || !isfinite(alpha)) return CK_ERR_INVALID;
-    if (!codes_shape(M, K) || N < 1 || N > kMaxRows || N % 8 != 0) return CK_ERR_SHAPE;
+    if (!codes_shape(M, K) || !columns_ok(M, N)) return CK_ERR_SHAPE;
     if (!aligned16(codes) || !aligned16(scales) || !aligned16(W) || !aligned16(w_scales) || !aligned16(y) ||
         !aligned16(bias) || !aligned16(residual))
         return CK_ERR_ALIGN;
@@ -221,7 +226,7 @@ CK_API ck_status ck_fp4_linear(const void *x, int64_t M, int64_t K, int64_t ldx,
     if (!x || !W || !w_scales || !y) return CK_ERR_NULL;
     if (!known(format) || !scale_ok(format, x_scale) || !scale_ok(format, w_scale)) return CK_ERR_INVALID;
     if (ck_status st = check_rows(x, M, K, ldx, act, 8); st != CK_OK) return st;
-    if (N < 1 || N > kMaxRows || N % 8 != 0) return CK_ERR_SHAPE;
+    if (!columns_ok(M, N)) return CK_ERR_SHAPE;
     if (!aligned16(W) || !aligned16(w_scales) || !aligned16(y) || !aligned16(bias) || !aligned16(residual))
         return CK_ERR_ALIGN;
     const bool nv = format == CK_FP4_NV;
