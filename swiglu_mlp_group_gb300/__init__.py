@@ -780,6 +780,16 @@ def _act(act: str) -> int:
     return a
 
 
+def _tokens(x, act: int):
+    """(M, K) of a call's x [M, K], or of its [gate | up], 2K columns."""
+    M, K = x.shape
+    if act != CK_ACT_SWIGLU:
+        return M, K
+    if K % 2 != 0:
+        raise ValueError("x must hold [gate | up], an even number of columns")
+    return M, K // 2
+
+
 def _tiled_bytes(f: int, rows: int, K: int) -> int:
     """ck_fp4_scale_bytes, without its refusals (a call's own come before a tensor is used)."""
     return (rows + 127) // 128 * ((K + 63) // 64 if f == CK_FP4_NV else (K + 127) // 128) * 512
@@ -832,9 +842,7 @@ def fp4_quantize(x, fmt: str, scale: float = 1.0, act: str = "none", codes=None,
     dev = _call_device(x, "x")
     f32 = x.dtype is torch.float32
     ldx = _row_stride(x, torch.float32 if f32 else torch.bfloat16, "x", dev)
-    M, K = x.shape
-    if a == CK_ACT_SWIGLU:
-        K //= 2
+    M, K = _tokens(x, a)
     n = int(lib().ck_fp4_scale_bytes(f, M, K))
     if n == 0:
         raise CkError(CK_ERR_SHAPE, "ck_fp4_quantize")
@@ -910,9 +918,7 @@ def fp4_linear(x, W, w_scales, fmt: str, x_scale: float = 1.0, w_scale: float = 
     f, a = _fp4_format(fmt), _act(act)
     dev = _call_device(x, "x")
     ldx = _row_stride(x, bf16, "x", dev)
-    M, K = x.shape
-    if a == CK_ACT_SWIGLU:
-        K //= 2
+    M, K = _tokens(x, a)
     N, Kw, pw, pws = _fp4_operand(W, w_scales, f, "W", dev)
     if Kw != K:
         raise ValueError("x and W must have the same columns")

@@ -366,6 +366,7 @@ PyObject *fp4_linear(PyObject *, PyObject *const *args, Py_ssize_t n) {
         const int64_t ldx = r.rows(*x, kBf16);
         const Operand w = operand(r, 1, 2, f);
         if (!r.ok) Py_RETURN_NONE;
+        if (act == CK_ACT_SWIGLU && x->size(1) % 2 != 0) Py_RETURN_NONE;
         const int64_t M = x->size(0), K = act == CK_ACT_SWIGLU ? x->size(1) / 2 : x->size(1);
         r.want(K == w.K);
         const void *bias = r.vector(6, kBf16, w.rows);
@@ -419,6 +420,7 @@ PyObject *fp4_quantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
         const bool f32 = x->scalar_type() == at::kFloat;
         const int64_t ldx = r.rows(*x, f32 ? at::kFloat : kBf16);
         if (!r.ok) Py_RETURN_NONE;
+        if (act == CK_ACT_SWIGLU && x->size(1) % 2 != 0) Py_RETURN_NONE;
         const int64_t M = x->size(0), K = act == CK_ACT_SWIGLU ? x->size(1) / 2 : x->size(1);
         const int64_t bytes = static_cast<int64_t>(ck_fp4_scale_bytes(static_cast<ck_fp4_format>(f), M, K));
         if (bytes == 0) Py_RETURN_NONE;

@@ -79,3 +79,14 @@ def test_outputs_that_share_their_memory(M):
                 a, e = row_scales(a), row_scales(e)
             assert torch.equal(a, e)
     poll_ok()
+
+
+def test_odd_columns_are_not_halved():
+    dev = device()
+    x = torch.zeros(4, 256, dtype=torch.bfloat16, device=dev)
+    w = ck.fp4_quantize(torch.ones(16, 64, dtype=torch.bfloat16, device=dev), "nv")
+    for call in (lambda x: ck.fp4_quantize(x, "nv", act="swiglu"), lambda x: ck.fp4_linear(x, *w, "nv", act="swiglu")):
+        call(x[:, :128])
+        with pytest.raises(ValueError):
+            call(x[:, :129])
+    poll_ok()

@@ -119,3 +119,13 @@ def test_outputs_that_share_their_memory(check):
         for t, k, o in zip(given, kept, clones):
             assert torch.equal(t, k), f"{args[0]}: the tensor behind an output was written"
             assert (bytes_of(o) == MARK).all(), f"{args[0]}: the output was not written"
+
+
+def test_odd_columns_are_not_halved(check):
+    """[gate | up] has an even number of columns; of 2K + 1 the last would be left out without a word."""
+    wide = rows(T, 4 * H)
+    w, ws = rows(32, H // 2, dtype=U8), rows(512, dtype=U8)
+    for cols, ok in ((2 * H, True), (2 * H + 1, False)):
+        x = wide[:, :cols]
+        assert check.taken("fp4_quantize", x, "nv", 1.0, "swiglu", None, None) == ok
+        assert check.taken("fp4_linear", x, w, ws, "nv", 1.0, 1.0, None, "swiglu", None, None, None) == ok
