@@ -20,6 +20,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+import warnings
 
 __all__ = [
     "CkError", "lib", "library_path", "build",
@@ -180,7 +181,7 @@ _quick_module = False  # not looked for yet
 
 def _quick():
     """The compiled calls (csrc/torch_calls.cpp) of the 4-bit operators and the block norm, or None where they were
-    not built.  Such a call returns None where anything is not in order, and the Python one says what."""
+    not built or do not load.  Such a call returns None where anything is not in order, and the Python one says what."""
     global _quick_module
     if _quick_module is False:
         from importlib.machinery import ExtensionFileLoader
@@ -192,8 +193,12 @@ def _quick():
         path, module = _build.calls_path(), None
         if path is not None and os.path.exists(path):
             spec = spec_from_file_location("ck_torch_calls", path, loader=ExtensionFileLoader("ck_torch_calls", path))
-            module = module_from_spec(spec)
-            spec.loader.exec_module(module)
+            try:
+                module = module_from_spec(spec)
+                spec.loader.exec_module(module)
+            except ImportError as e:  # of another build of torch
+                module = None
+                warnings.warn(f"the compiled calls do not load, and go through ctypes: {e}", RuntimeWarning, stacklevel=3)
         _quick_module = module
     return _quick_module
 

@@ -6,8 +6,10 @@ library under ``swiglu_mlp_group_gb300/_build/``.  nvcc cross-compiles, so the
 build also runs on machines without a GPU.
 
 ``csrc/torch_calls.cpp``, the Python binding's quick calls, is compiled by g++
-beside it where torch's and Python's headers are there, for that torch; without
-it the same calls go through ctypes.
+beside it where torch's and Python's headers are there, for that torch and that
+Python.  It uses what torch keeps to itself, which another torch may have
+otherwise: where it does not compile or link, the build warns and goes on, and
+the same calls go through ctypes.
 """
 from __future__ import annotations
 
@@ -19,6 +21,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -37,15 +40,26 @@ CALLS_SOURCE = os.path.join(CSRC, "torch_calls.cpp")
 
 
 def calls_path() -> str | None:
-    """Where the quick calls for the installed torch belong; None without torch."""
+    """Where the quick calls for the installed torch and this Python belong; None without torch."""
     try:
-        return os.path.join(BUILD_DIR, f"ck_torch_calls-{importlib.metadata.version('torch')}.so")
+        version = importlib.metadata.version("torch")
     except importlib.metadata.PackageNotFoundError:
         return None
+    return os.path.join(BUILD_DIR, f"ck_torch_calls-{version}{sysconfig.get_config_var('EXT_SUFFIX') or '.so'}")
+
+
+def _calls_failed() -> str:
+    """The file that says why the quick calls could not be built."""
+    return calls_path() + ".failed"
+
+
+def _remove(path: str) -> None:
+    if os.path.exists(path):
+        os.remove(path)
 
 
 def _calls_dirs() -> tuple[str, str, str] | None:
-    """(torch's folder, Python's headers, CUDA's headers), or None if one of them is missing."""
+    """(torch's folder, Python's headers, CUDA's headers), or None if one of them or torch's CUDA part is missing."""
     spec = importlib.util.find_spec("torch")
     if spec is None or spec.origin is None or calls_path() is None or shutil.which("g++") is None:
         return None
@@ -55,6 +69,7 @@ def _calls_dirs() -> tuple[str, str, str] | None:
         return None
     dirs = (os.path.dirname(spec.origin), sysconfig.get_paths()["include"], os.path.join(cuda, "include"))
     heads = (os.path.join(dirs[0], "include", "torch", "csrc", "autograd", "python_variable.h"),
+             os.path.join(dirs[0], "lib", "libc10_cuda.so"),
              os.path.join(dirs[1], "Python.h"), os.path.join(dirs[2], "cuda_runtime_api.h"))
     return dirs if all(os.path.exists(h) for h in heads) else None
 
@@ -76,15 +91,40 @@ def _deps() -> list[str]:
 
 
 def up_to_date() -> bool:
-    built = [LIB_PATH] + ([calls_path()] if _calls_dirs() else [])
+    built = [LIB_PATH]
+    if _calls_dirs():
+        built.append(calls_path() if os.path.exists(calls_path()) else _calls_failed())
     if not all(os.path.exists(b) for b in built):
         return False
     t = min(os.path.getmtime(b) for b in built)
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def _compile_calls(dirs: tuple[str, str, str], obj: str) -> str | None:
+    """Compile the quick calls; the compiler's messages if it fails."""
+    torch_dir, python_inc, cuda_inc = dirs
+    includes = [INCLUDE, os.path.join(torch_dir, "include"),
+                os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), python_inc, cuda_inc]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", CALLS_SOURCE, "-o", obj]
+    r = subprocess.run(cmd + [f"-I{i}" for i in includes], capture_output=True, text=True)
+    return None if r.returncode == 0 else f"g++ failed for {CALLS_SOURCE}:\n{r.stdout}\n{r.stderr}"
+
+
+def _link_calls(dirs: tuple[str, str, str], obj: str) -> str | None:
+    """Link the quick calls against the library; the linker's messages if it fails."""
+    tmp = calls_path() + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", os.path.dirname(LIB_PATH), f"-l:{LIB_NAME}", "-L",
+           os.path.join(dirs[0], "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda", "-ltorch_cuda",
+           "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        return f"link failed:\n{r.stdout}\n{r.stderr}"
+    os.replace(tmp, calls_path())
+    return None
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
-    """Compile and link the library; returns its path.  Raises on any failure."""
+    """Compile and link the library; returns its path.  Raises on any failure but one of the quick calls."""
     if not force and up_to_date():
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -104,35 +144,26 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     dirs = _calls_dirs()
     calls_obj = os.path.join(BUILD_DIR, "torch_calls.o")
 
-    def compile_calls() -> None:
-        torch_dir, python_inc, cuda_inc = dirs
-        includes = [INCLUDE, os.path.join(torch_dir, "include"),
-                    os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), python_inc, cuda_inc]
-        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", CALLS_SOURCE, "-o", calls_obj]
-        r = subprocess.run(cmd + [f"-I{i}" for i in includes], capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"g++ failed for {CALLS_SOURCE}:\n{r.stdout}\n{r.stderr}")
-
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
-        calls = ex.submit(compile_calls) if dirs else None
+        calls = ex.submit(_compile_calls, dirs, calls_obj) if dirs else None
         objs = list(ex.map(compile_one, srcs))
-        if calls:
-            calls.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [cc] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcuda"] * 0
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    if dirs:
-        tmp = calls_path() + f".tmp{os.getpid()}"
-        cmd = ["g++", "-shared", "-o", tmp, calls_obj, "-L", BUILD_DIR, f"-l:{LIB_NAME}", "-L", os.path.join(dirs[0], "lib"),
-               "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda", "-ltorch_cuda", "-Wl,-rpath,$ORIGIN"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, calls_path())
+    if calls:
+        why = calls.result() or _link_calls(dirs, calls_obj)
+        if why:
+            with open(_calls_failed(), "w") as f:
+                f.write(why)
+            warnings.warn(f"the compiled calls were not built, and go through ctypes: {why}", RuntimeWarning, stacklevel=2)
+    if calls_path() and (not calls or why):  # one of an older library
+        _remove(calls_path())
+    elif calls:
+        _remove(_calls_failed())
     return LIB_PATH
 
 
