@@ -6,6 +6,7 @@ import torch
 import fp4_reference as ref
 import swiglu_mlp_group_gb300 as ck
 from gpu_helpers import device, poll_ok
+from test_gpu_fp4_quick_calls import H, M, Calls
 
 pytestmark = pytest.mark.gpu
 
@@ -89,4 +90,41 @@ def test_odd_columns_are_not_halved():
         call(x[:, :128])
         with pytest.raises(ValueError):
             call(x[:, :129])
+    poll_ok()
+
+
+def poison(t):
+    """NaN in bf16, 0xA5 in bytes: what no call here leaves."""
+    t.fill_(float("nan") if t.is_floating_point() else 0xa5)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_everything_is_written_and_nothing_else(fmt):
+    """Each call into poisoned outputs: given ones (and the rows' neighbours, which stay), and the memory that made
+    ones will get; the Python call's results stay alive meanwhile, so that none of them is handed on."""
+    c = Calls(fmt)
+    assert ck._quick() is not None, "the compiled calls were not built"
+    for name, args, kw in c.calls:
+        given = [kw[k] for k in ("out", "h_out", "n_out", "codes", "scales") if k in kw]
+        fresh = {k: torch.empty_strided(v.shape, v.stride(), dtype=v.dtype, device=v.device) if any(v is o for o in given) else v
+                 for k, v in kw.items()}
+        kept = getattr(ck, name)(*args, **fresh, stream=torch.cuda.current_stream())
+        kept = kept if isinstance(kept, tuple) else (kept,)
+        for o in given:
+            poison(o if o._base is None else o._base)
+        made = [torch.empty_like(k) for k in kept for _ in range(3)]
+        for m in made:
+            poison(m)
+        del made
+        got = getattr(ck, name)(*args, **kw)
+        want, got = c.outputs(name, kept, fmt), c.outputs(name, got, fmt)
+        for a, b in zip(got, want):
+            assert a.shape == b.shape and a.dtype == b.dtype and torch.equal(a, b), f"{name} {list(kw)}"
+        for o in given:
+            if o._base is not None:  # the columns beside the rows
+                beside = o._base[:, H:] if o.storage_offset() == 0 else o._base[:, :H]
+                assert torch.isnan(beside).all(), name
+        if "scales" in kw:  # words of rows that are not there
+            rows = kw["scales"].view(-1, 32, 4, 4).permute(0, 2, 1, 3).flatten(1, 2)
+            assert (rows[:, M:] == 0xa5).all(), name
     poll_ok()
