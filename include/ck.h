@@ -586,9 +586,10 @@ CK_API size_t ck_fp4_scale_bytes(ck_fp4_format format, int64_t rows, int64_t K);
  *   MX: s = 2^e, e = max(floor(log2(amax)) - 2, -127);
  *   NV: s = E4M3(amax / (6 t)) to nearest even, at most 448;
  *   code = E2M1(x / s) (NV: x / f32(s t)) to nearest, ties to the even code, at most 6
- *   in magnitude, with x's sign; all codes of a block 0 where its s is 0.
- * Divisions and products in f32, each correctly rounded.  A block with a NaN or an
- * infinity gets the NaN scale.
+ *   in magnitude, with x's sign; all codes of a block zeros where its s is 0.
+ * Products in f32, correctly rounded.  Quotients in f32, to nearest; of NV one that is
+ * within 2^-43 of itself from the middle of two f32 numbers may go to either (MX: exact).
+ * A block with a NaN or an infinity gets the NaN scale.
  *   x   : [M, ldx] of type xdt (act NONE: bf16 or f32; act SWIGLU: bf16 [gate | up],
  *         2K columns, silu(gate) * up formed in f32 first); ldx a multiple of 8 (f32: 4).
  *   tensor_scale : t, 2^-60 .. 2^60; MX: 1.
@@ -647,6 +648,9 @@ CK_API size_t ck_fp4_linear_workspace_bytes(int64_t M, int64_t K, ck_fp4_format 
  *       of the weights;  bgu bf16 [2I], bd bf16 [H], residual bf16 [M, H]: or NULL;
  *   residual may be x or y, x may be y;
  *   ws : ck_fp4_swiglu_mlp_workspace_bytes(M, H, I, format) bytes.
+ * For more than 32 tokens and I a multiple of 64 the first product quantizes itself, and
+ * h is never stored (ws has room for it all the same); else h passes through ws, which
+ * for many tokens costs about half as much again (the same results).
  * Errors: as ck_fp4_linear.
  */
 CK_API ck_status ck_fp4_swiglu_mlp(const void *x, int64_t M, int64_t H, int64_t I,

@@ -151,9 +151,11 @@ __device__ __forceinline__ void quantize_glu(const uint4 (&gate)[COLS / 8], cons
 
 // What bounds it.  The MMAs of a part's stage (256 columns of K) take 384 clocks, 9.5
 // PFLOP/s in all, with or without the scales' copies between them (timed alone, from
-// shared memory).  Their operands: 81 (MX) and 89 (NV) bytes a clock and SM with one
-// part, of which some 70 come in, 59 and 65 with two, which then wait for the issue
-// (28 instructions a k-block, NV, at some 30 clocks each, MX 18) and between tiles.
+// shared memory; of the instruction's K = 64 form, the one used: sm_103a has a K = 96 form,
+// too, by the chip's published rate half as fast again, which is not measured here).  Their
+// operands: 81 (MX) and 89 (NV) bytes a clock and SM with one part, of which some 70 come
+// in, 59 and 65 with two, which then wait for the issue (28 instructions a k-block, NV, at
+// some 30 clocks each, MX 18) and between tiles.
 // Random codes draw so much power that the clock gives another 5 %.  16384 x 4096 ->
 // 12288: 223 us (NV) and 217 (MX), on zeros 213 and 208 (7.7 and 7.9 PFLOP/s), with a
 // residual 272 and 264; gate and up of as many tokens with 6144 rows each, where no y is
@@ -169,7 +171,15 @@ __device__ __forceinline__ void quantize_glu(const uint4 (&gate)[COLS / 8], cons
 // shared memory (a lane its own row: 300 us against 265), with two parts more registers
 // for the epilogue than for the rest (222 us against 218; one part does not need them:
 // 247 against 242), the k-blocks' order at a tile's ends (gate and up 206 us without, MX;
-// for every k-block NV 205 against 196), in a loop that is not unrolled (278).
+// for every k-block NV 205 against 196), in a loop that is not unrolled (278).  With two
+// parts and a y the epilogue spills 48 bytes a thread (132 loaded), with gate and up NV 8
+// (20); with one part, and with gate and up MX, nothing.
+//
+// Few tokens (33 to 256): a tile has 256 rows, most of them zeros, and there are as many
+// tiles as for 256 tokens: 64 x 4096 -> 12288 10.2 us NV and 9.7 MX, 256 10.9 and 10.4,
+// where the weight's bytes take 4.2 of HBM.  64 tiles for 76 pairs, a tile each, so a
+// call is one tile's chain: beginning, 16 k-blocks, epilogue.  1000 x 2080 -> 1544 8.0 and
+// 7.6: 36 tiles of nine k-blocks, too short a K to split.
 // Tried and slower, one part: 512 tokens x 192 rows (252 us against 240), the issuer's
 // stages unrolled, tiles in bands of 8 and 16 rows of tiles, y in pieces of 64 columns
 // (250), the next tile's first k-blocks prefetched to L2 (264 against 249); two parts, the

@@ -17,7 +17,9 @@ constexpr int kRowsPerWarp = 4;
 // 512 bytes in a row; a warp takes 256 columns of 4 rows, whose loads are on
 // their way together and whose scales lie next to each other.  What counts then is
 // instructions, of the ALU above all: addresses are worked out once for the four
-// rows, and each block's first lane stores its scale byte itself.
+// rows, and each block's first lane stores its scale byte itself.  16384 x 4096: bf16
+// 30.7 us NV (5.6 TB/s) and 27 MX (6.3 to 6.6), f32 45.7 (6.7) and 44.9 (6.8), silu(gate)
+// * up 49.5 (6.2) and 45.4 (6.7): with twice the bytes to load, HBM.
 enum class In : int { kBf16, kF32, kSwiglu };
 
 template <bool NV, In IN>
